@@ -351,6 +351,128 @@ pkv_status pkv_prefill_workspace_size(int32_t num_seqs, int32_t max_query_len, i
                                       int32_t num_kv_heads, int32_t head_dim, int32_t num_splits, size_t* bytes);
 
 /*
+ * Rotate q and k at their tokens' positions and append k and v to the cache, in one pass: what a layer does
+ * between its projections and the attention of a prompt (pkv_decode_step does it inside a decode step).
+ *
+ * For every token t in [0, num_tokens) with s = slot_mapping[t] >= 0 and every frequency i < D / 2, with
+ * pos = positions[a][t], a = freq_axes[i], c = cos_sin[pos][i] and n = cos_sin[pos][D / 2 + i]:
+ *   x'[i] = x[i] c - x[i + D / 2] n,   x'[i + D / 2] = x[i + D / 2] c + x[i] n
+ * for x = q[t][h] into q_out[t][h], and for x = k[t][h] into k_cache[s / 16][h][s % 16]; v[t][h] is copied into
+ * v_cache[s / 16][h][s % 16].  Each product, difference and sum is one fp32 operation rounded to nearest, then
+ * one rounding to bf16: the same bits as pkv_decode_step gives.  A token with a negative slot is padding: its q_out row
+ * and its positions are not touched.  Slots must be distinct, as for pkv_kv_append.
+ *
+ * With one axis this is the usual rotation.  With several (time, height and width of an image token, say) each
+ * frequency turns by its own axis' position.
+ *
+ *   q, k, v, q_out  device, bf16: row t starts t * (stride) elements behind the first and holds [heads][head_dim]
+ *                   contiguously; a stride is a multiple of 8, so rows may be slices of one projection's output.
+ *                   q_out may be q itself with q's stride (rotated in place); no other overlap of outputs with
+ *                   inputs.  q_out_stride is at least num_q_heads * head_dim
+ *   positions       device, int64, axis a's num_tokens positions axis_stride elements behind axis a - 1's
+ *   num_axes        1..PKV_MAX_POSITION_AXES
+ *   freq_axes       HOST, [head_dim / 2] axes, each below num_axes, read before the call returns; ignored (may be
+ *                   NULL) with one axis
+ *   cos_sin         device, fp32 [max_position][head_dim]
+ * num_tokens == 0 is a no-op.  Device-side: a position outside [0, max_position) sets
+ * PKV_DEVERR_POSITION_OUT_OF_TABLE and uses the nearest row of the table; a slot >= 16 * num_blocks sets
+ * PKV_DEVERR_SLOT_OUT_OF_RANGE and the token's k and v are skipped (its q is rotated).
+ */
+#define PKV_MAX_POSITION_AXES 4
+pkv_status pkv_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, const int64_t* positions, int32_t num_axes, int64_t axis_stride,
+                           const uint8_t* freq_axes, const float* cos_sin, int64_t max_position,
+                           const int64_t* slot_mapping, int64_t num_tokens, int32_t num_q_heads,
+                           int32_t num_kv_heads, int32_t head_dim, void* q_out, int64_t q_out_stride, void* k_cache,
+                           void* v_cache, int64_t num_blocks, int32_t block_size, pkv_stream_t stream);
+
+/*
+ * Paged decode attention with a sliding window and sinks.  The query token of sequence b, at position
+ * P = context_lens[b] - 1, sees the cached tokens j <= P with j > P - window or j < num_sink_tokens:
+ *
+ *   out[b][h][:] = sum_j softmax_j(scale * <q[b][h], K_j>) * V_j   over those j
+ *
+ * otherwise as pkv_paged_decode_attention_split with every phase.  Table entries of blocks that hold no visible
+ * token are not read (they may be -1, so that a sequence's blocks can be freed once its window has passed them),
+ * and what the other rows of a block hold does not matter.
+ *
+ *   window           >= 1: the newest tokens that are seen, the query's own among them
+ *   num_sink_tokens  >= 0: the first tokens that stay visible
+ *   workspace        at least pkv_window_decode_workspace_size(..., num_partitions, ...) bytes
+ */
+pkv_status pkv_paged_window_decode_attention(const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                             const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
+                                             int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks,
+                                             int32_t block_size, float scale, int32_t window, int32_t num_sink_tokens,
+                                             void* out, void* workspace, size_t workspace_bytes,
+                                             int32_t num_partitions, pkv_stream_t stream);
+/* Its workspace; num_partitions as for pkv_decode_workspace_size (0: the default, needs a device). */
+pkv_status pkv_window_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                            int32_t head_dim, int32_t max_blocks_per_seq, int32_t window,
+                                            int32_t num_sink_tokens, int32_t num_partitions, size_t* bytes);
+
+/*
+ * Chunked paged prefill attention with a sliding window and sinks: query row i of sequence b's chunk, at position
+ * P = P_b + i, sees the cached tokens j <= P with j > P - window or j < num_sink_tokens.  Otherwise as
+ * pkv_paged_prefill_attention_split (num_splits 1: no workspace), with scale > 0.
+ *
+ * Table entries of blocks that no row of the sequence's chunk sees are not read, and tokens that no row of the
+ * chunk sees do not matter, whatever they hold.  A token that some rows see has to be finite: rows of the same
+ * 128-row tile that do not see it weight it with 0, and 0 times infinity is no number.  (A CTA takes 256 / G
+ * chunk tokens; it reads the blocks that its own rows see.)
+ */
+pkv_status pkv_paged_window_prefill_attention(const void* q, const void* k_cache, const void* v_cache,
+                                              const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                              const int32_t* context_lens, const int32_t* query_start,
+                                              int32_t max_query_len, int32_t num_seqs, int32_t num_q_heads,
+                                              int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks,
+                                              int32_t block_size, float scale, int32_t window,
+                                              int32_t num_sink_tokens, void* out, int32_t num_splits, void* workspace,
+                                              size_t workspace_bytes, pkv_stream_t stream);
+/* A split count for it: pkv_prefill_default_splits, but no more than leaves every split two steps of 128 keys.
+   The workspace of a count is pkv_prefill_workspace_size. */
+pkv_status pkv_window_prefill_default_splits(int32_t num_seqs, int32_t max_query_len, int32_t num_q_heads,
+                                             int32_t num_kv_heads, int32_t window, int32_t num_sink_tokens,
+                                             int32_t* num_splits);
+
+/*
+ * Paged decode attention for groups of sequences that share a prefix (forks of one prompt, requests behind one
+ * system prompt).  The result is that of pkv_paged_decode_attention; the blocks that a group shares are read once
+ * for the group, on the tensor cores with the group's query rows as the rows of the product, and only what
+ * follows them once per sequence.
+ *
+ *   group_start   device, int32 [num_groups + 1], non-decreasing, group_start[0] >= 0 and group_start[num_groups]
+ *                 <= num_seqs: group g is the sequences [group_start[g], group_start[g + 1]).  Sequences outside
+ *                 every group share nothing.  A group may be empty or a single sequence
+ *   prefix_lens   device, int32 [num_groups]: leading tokens that group g shares.  The first prefix_lens[g] / 16
+ *                 block-table entries (whole blocks; a partly shared block is each sequence's own business) of its
+ *                 first sequence are read for all its sequences, whose own entries there are not.  A sequence with
+ *                 fewer tokens than that sees only its own context_lens[b]
+ *   num_seqs      at most PKV_MAX_SEQS, num_groups in [0, PKV_MAX_SEQS]
+ *   scale         > 0
+ *   workspace     device, 16-byte aligned, at least pkv_prefix_decode_workspace_size bytes, scratch as for
+ *                 pkv_paged_decode_attention
+ * num_blocks * num_kv_heads * 16 must be below 2^31.  Three launches.  Shared tokens have to be finite when a
+ * sequence of the group is shorter than the prefix (see pkv_paged_window_prefill_attention).  Arithmetic: the
+ * shared part as pkv_paged_prefill_attention (P rounded to bf16), the rest as pkv_paged_decode_attention, joined in
+ * fp32.  Device-side: group_start out of order sets PKV_DEVERR_CONTEXT_LEN_TOO_LONG (the outputs are unspecified);
+ * prefix_lens[g] < 0 or > 16 * max_blocks_per_seq (of a group that is not empty) sets PKV_DEVERR_CONTEXT_LEN_NEGATIVE or ..._TOO_LONG and is
+ * clamped.
+ */
+pkv_status pkv_paged_prefix_decode_attention(const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                             const int32_t* context_lens, const int32_t* group_start,
+                                             const int32_t* prefix_lens, int32_t num_groups, int32_t num_seqs,
+                                             int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                             int64_t num_blocks, int32_t block_size, float scale, void* out,
+                                             void* workspace, size_t workspace_bytes, pkv_stream_t stream);
+/* Its workspace (needs a device: it holds the partial states of one CTA per SM, or of whole waves of them). */
+pkv_status pkv_prefix_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                            int32_t head_dim, int32_t max_blocks_per_seq, int32_t num_groups,
+                                            size_t* bytes);
+
+/*
  * Copy whole KV blocks inside the pool: the copy half of copy-on-write for
  * blocks shared between sequences.  The pages let requests share a prompt's
  * KV blocks ("v0版本介绍", section "为什么需要推理框架") and plan a prefix

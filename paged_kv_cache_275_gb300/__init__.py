@@ -11,7 +11,9 @@ from ._capi import (BLOCK_SIZE, DEVERR_BLOCK_ID_OUT_OF_RANGE, DEVERR_COPY_OUT_OF
                     DEVERR_CONTEXT_LEN_TOO_LONG, DEVERR_PIPELINE_TIMEOUT, DEVERR_SLOT_OUT_OF_RANGE, EXPORTS,
                     LIB_PATH, MAX_SEQS, PHASE_ALL, PHASE_MERGE, PHASE_PARTITION, PagedKVError, default_partitions,
                     get_and_clear_device_error, kernel_launch_count, kv_append, load, paged_decode_attention,
-                    selftest_wait_timeout, workspace_size)
+                    selftest_wait_timeout, workspace_size, MAX_POSITION_AXES, paged_prefix_decode_attention,
+                    paged_window_decode_attention, paged_window_prefill_attention, prefix_decode_workspace_size,
+                    rope_append, rope_freq_axes, window_decode_workspace_size, window_prefill_default_splits)
 
 __all__ = [
     "BLOCK_SIZE", "MAX_SEQS", "EXPORTS", "LIB_PATH", "PagedKVError", "PHASE_ALL", "PHASE_MERGE", "PHASE_PARTITION",
@@ -22,4 +24,7 @@ __all__ = [
     "DEVERR_POSITION_OUT_OF_TABLE", "paged_prefill_attention", "prefill_workspace_size", "prefill_default_splits",
     "DEVERR_SMEM_ALIGNMENT",
     "selftest_wait_timeout",
+    "MAX_POSITION_AXES", "rope_append", "rope_freq_axes", "paged_window_decode_attention",
+    "window_decode_workspace_size", "paged_window_prefill_attention", "window_prefill_default_splits",
+    "paged_prefix_decode_attention", "prefix_decode_workspace_size",
 ]

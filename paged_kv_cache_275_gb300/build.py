@@ -23,8 +23,9 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 BUILD = PKG / "_build"
 LIB = PKG / "libpagedkv.so"
-SOURCES = ["capi.cu", "kv_append.cu", "paged_decode.cu", "static_workspace.cu", "copy_blocks.cu",
-           "block_manager.cpp", "paged_prefill.cu"]
+SOURCES = ["capi.cu", "kv_append.cu", "rope_append.cu", "paged_decode.cu", "window_decode.cu", "prefix_decode.cu",
+           "static_workspace.cu", "copy_blocks.cu", "block_manager.cpp", "paged_prefill.cu", "window_prefill.cu",
+           "shared_prefix.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -44,7 +45,7 @@ def _nvcc() -> str:
 
 
 def _inputs() -> list[Path]:
-    return [CSRC / s for s in SOURCES] + list(CSRC.glob("*.h")) + list(INCLUDE.glob("*.h")) + [Path(__file__)]
+    return [CSRC / s for s in SOURCES] + list(CSRC.glob("*.h")) + list(CSRC.glob("*.cuh")) + list(INCLUDE.glob("*.h")) + [Path(__file__)]
 
 
 STAMP = BUILD / "flags.txt"

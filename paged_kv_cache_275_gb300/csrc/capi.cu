@@ -105,13 +105,42 @@ pkv_status check_decode_shapes(int32_t num_seqs, int32_t num_q_heads, int32_t nu
 
 constexpr int32_t kMaxPartitions = 1 << 20;
 
+// A sliding window and sinks; window 0: neither.
+struct Window {
+  int32_t window = 0;
+  int32_t sinks = 0;
+};
+pkv_status check_window(int32_t window, int32_t sinks) {
+  if (window <= 0) return fail(PKV_ERR_INVALID_ARGUMENT, "window must be positive (got %d)", window);
+  if (sinks < 0) return fail(PKV_ERR_INVALID_ARGUMENT, "num_sink_tokens must be >= 0 (got %d)", sinks);
+  return PKV_OK;
+}
+// Both within the table, so that the kernels' sums stay within 32 bits (a window of the table's length is
+// no window, and so many sinks are every token).
+Window within_table(Window w, int32_t max_blocks_per_seq) {
+  const int32_t cap = max_blocks_per_seq * PKV_BLOCK_SIZE;
+  if (w.window > cap) w.window = cap;
+  if (w.sinks > cap) w.sinks = cap;
+  return w;
+}
+// Blocks of one sequence that a query token can see.
+int32_t visible_blocks(Window w, int32_t max_blocks_per_seq) {
+  if (w.window == 0) return max_blocks_per_seq;
+  w = within_table(w, max_blocks_per_seq);
+  const int64_t n = (static_cast<int64_t>(w.sinks) + PKV_BLOCK_SIZE - 1) / PKV_BLOCK_SIZE +
+                    (static_cast<int64_t>(w.window) + 2 * PKV_BLOCK_SIZE - 2) / PKV_BLOCK_SIZE;
+  return n < max_blocks_per_seq ? static_cast<int32_t>(n) : max_blocks_per_seq;
+}
+
 pkv_status default_partitions(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int32_t group,
-                              int32_t max_blocks_per_seq, int32_t* out) {
+                              int32_t max_blocks_per_seq, const Window& window, int32_t* out) {
   int pieces = 0;
-  const cudaError_t e = pkv::resident_partition_pieces(head_dim, group, num_seqs, &pieces);
+  const cudaError_t e = window.window ? pkv::resident_window_pieces(head_dim, group, num_seqs, &pieces)
+                                      : pkv::resident_partition_pieces(head_dim, group, num_seqs, &pieces);
   if (e != cudaSuccess) return cuda_fail(e, "occupancy query");
   // Never more pieces than the block stream can have items.
-  const int64_t bound = static_cast<int64_t>(num_seqs) * num_kv_heads * max_blocks_per_seq;
+  const int64_t bound =
+      static_cast<int64_t>(num_seqs) * num_kv_heads * visible_blocks(window, max_blocks_per_seq);
   int64_t n = pieces;
   if (n > bound) n = bound;
   if (n > kMaxPartitions) n = kMaxPartitions;
@@ -130,14 +159,15 @@ size_t workspace_bytes_for(int32_t num_seqs, int32_t num_kv_heads, int32_t head_
 // when the batch does not divide evenly, the shorter last one; each at its own default partition
 // count unless one is given).
 pkv_status decode_workspace_need(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int32_t group,
-                                 int32_t max_blocks_per_seq, int32_t num_partitions, size_t* need) {
+                                 int32_t max_blocks_per_seq, const Window& window, int32_t num_partitions,
+                                 size_t* need) {
   *need = 0;
   const int32_t sizes[2] = {launch_seqs(num_seqs), num_seqs > PKV_MAX_SEQS ? num_seqs % PKV_MAX_SEQS : 0};
   for (int32_t n : sizes) {
     if (n == 0) continue;
     int32_t parts = num_partitions;
     if (parts == 0)
-      if (pkv_status st = default_partitions(n, num_kv_heads, head_dim, group, max_blocks_per_seq, &parts);
+      if (pkv_status st = default_partitions(n, num_kv_heads, head_dim, group, max_blocks_per_seq, window, &parts);
           st != PKV_OK)
         return st;
     const size_t b = workspace_bytes_for(n, num_kv_heads, head_dim, group, parts);
@@ -160,7 +190,8 @@ static pkv_status decode_impl(const void* q, const void* k_cache, const void* v_
                               int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t num_seqs,
                               int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks,
                               int32_t block_size, float scale, void* out, void* workspace, size_t workspace_bytes,
-                              int32_t num_partitions, int32_t phases, pkv_stream_t stream, const FusedStep* fused) {
+                              int32_t num_partitions, int32_t phases, pkv_stream_t stream, const FusedStep* fused,
+                              const Window& window) {
   if (pkv_status st = check_decode_shapes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq);
       st != PKV_OK)
     return st;
@@ -183,7 +214,7 @@ static pkv_status decode_impl(const void* q, const void* k_cache, const void* v_
     return fail(PKV_ERR_UNSUPPORTED, "phases other than PKV_PHASE_ALL need num_seqs <= PKV_MAX_SEQS (%d)",
                 PKV_MAX_SEQS);
   size_t need = 0;
-  if (pkv_status st = decode_workspace_need(num_seqs, num_kv_heads, head_dim, group, max_blocks_per_seq,
+  if (pkv_status st = decode_workspace_need(num_seqs, num_kv_heads, head_dim, group, max_blocks_per_seq, window,
                                             num_partitions, &need);
       st != PKV_OK)
     return st;
@@ -202,7 +233,7 @@ static pkv_status decode_impl(const void* q, const void* k_cache, const void* v_
     const int32_t n = launch_seqs(num_seqs - s0);
     int32_t parts = num_partitions;
     if (parts == 0)
-      if (pkv_status st = default_partitions(n, num_kv_heads, head_dim, group, max_blocks_per_seq, &parts);
+      if (pkv_status st = default_partitions(n, num_kv_heads, head_dim, group, max_blocks_per_seq, window, &parts);
           st != PKV_OK)
         return st;
     pkv::DecodeParams p{};
@@ -229,6 +260,15 @@ static pkv_status decode_impl(const void* q, const void* k_cache, const void* v_
       p.v_new = static_cast<const unsigned char*>(fused->v_new) + s0 * kv_row;
       p.cos_sin = fused->cos_sin;
       p.max_position = fused->max_position;
+    }
+    if (window.window) {
+      const Window w = within_table(window, max_blocks_per_seq);
+      p.window = w.window;
+      p.sinks = w.sinks;
+      const cudaError_t e = pkv::launch_window_decode(p, head_dim, group, s);
+      if (e != cudaSuccess) return cuda_fail(e, "window decode launch");
+      g_launches.fetch_add(2);
+      continue;
     }
     if (phases & PKV_PHASE_PARTITION) {
       const cudaError_t e = pkv::launch_decode_partition(p, head_dim, group, s);
@@ -335,11 +375,23 @@ pkv_status pkv_selftest_wait_timeout(uint64_t limit_ns, pkv_stream_t stream) {
 namespace {
 constexpr int32_t kMaxPrefillSplits = 32;  // the merge reads one split per lane
 
+// The most splits that keep every CTA of the call in one wave (one CTA per SM), at most 32, and
+// within the 65535 grid rows; 1 when the call already fills the GPU.
+int32_t one_wave_splits(int32_t num_seqs, int32_t max_query_len, int32_t num_q_heads, int32_t num_kv_heads, int sms) {
+  const int64_t cta = pkv::prefill_cta_tokens(num_q_heads / num_kv_heads);
+  const int64_t ctas = static_cast<int64_t>(num_seqs) * num_kv_heads * ((max_query_len + cta - 1) / cta);
+  int64_t n = ctas > 0 ? sms / ctas : 1;
+  if (n > kMaxPrefillSplits) n = kMaxPrefillSplits;
+  if (num_seqs > 0 && n > 65535 / num_seqs) n = 65535 / num_seqs;
+  return static_cast<int32_t>(n < 1 ? 1 : n);
+}
+
 pkv_status prefill_impl(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                         int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* query_start,
                         int32_t max_query_len, int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                         int32_t head_dim, int64_t num_blocks, int32_t block_size, float scale, void* out,
-                        int32_t num_splits, void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+                        int32_t num_splits, void* workspace, size_t workspace_bytes, pkv_stream_t stream,
+                        const Window& window) {
   if (num_splits < 1 || num_splits > kMaxPrefillSplits)
     return fail(PKV_ERR_INVALID_ARGUMENT, "num_splits must be in [1, %d] (got %d)", kMaxPrefillSplits, num_splits);
   if (static_cast<int64_t>(num_seqs) * num_splits > 65535)
@@ -396,8 +448,12 @@ pkv_status prefill_impl(const void* q, const void* k_cache, const void* v_cache,
     p.num_splits = num_splits;
     p.ws = static_cast<float*>(workspace);
   }
-  const cudaError_t e = pkv::launch_paged_prefill(p, head_dim, num_q_heads / num_kv_heads, max_query_len,
-                                                  reinterpret_cast<cudaStream_t>(stream));
+  const Window w = within_table(window, max_blocks_per_seq);
+  p.window = w.window;
+  p.sinks = w.sinks;
+  const cudaError_t e =
+      (window.window ? pkv::launch_window_prefill : pkv::launch_paged_prefill)(
+          p, head_dim, num_q_heads / num_kv_heads, max_query_len, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "prefill kernel launch");
   g_launches.fetch_add(num_splits > 1 ? 2 : 1);
   return ok();
@@ -412,7 +468,7 @@ pkv_status pkv_paged_prefill_attention(const void* q, const void* k_cache, const
                                        float scale, void* out, pkv_stream_t stream) {
   return prefill_impl(q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, query_start, max_query_len,
                       num_seqs, num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, scale, out, 1, nullptr, 0,
-                      stream);
+                      stream, Window{});
 }
 
 pkv_status pkv_paged_prefill_attention_split(const void* q, const void* k_cache, const void* v_cache,
@@ -424,7 +480,7 @@ pkv_status pkv_paged_prefill_attention_split(const void* q, const void* k_cache,
                                              void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
   return prefill_impl(q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, query_start, max_query_len,
                       num_seqs, num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, scale, out, num_splits,
-                      workspace, workspace_bytes, stream);
+                      workspace, workspace_bytes, stream, Window{});
 }
 
 pkv_status pkv_prefill_default_splits(int32_t num_seqs, int32_t max_query_len, int32_t num_q_heads,
@@ -434,15 +490,7 @@ pkv_status pkv_prefill_default_splits(int32_t num_seqs, int32_t max_query_len, i
   if (pkv_status st = check_shapes(num_seqs, num_seqs, num_q_heads, num_kv_heads, 128, 1); st != PKV_OK) return st;
   int sms = 0;
   if (pkv_status st = device_state(nullptr, &sms); st != PKV_OK) return st;
-  // The most splits that keep every CTA of the call in one wave (one CTA per SM), at most 32, and
-  // within the 65535 grid rows; 1 when the call already fills the GPU.
-  const int64_t cta = pkv::prefill_cta_tokens(num_q_heads / num_kv_heads);
-  const int64_t ctas = static_cast<int64_t>(num_seqs) * num_kv_heads * ((max_query_len + cta - 1) / cta);
-  int64_t n = ctas > 0 ? sms / ctas : 1;
-  if (n > kMaxPrefillSplits) n = kMaxPrefillSplits;
-  if (num_seqs > 0 && n > 65535 / num_seqs) n = 65535 / num_seqs;
-  if (n < 1) n = 1;
-  *num_splits = static_cast<int32_t>(n);
+  *num_splits = one_wave_splits(num_seqs, max_query_len, num_q_heads, num_kv_heads, sms);
   return ok();
 }
 
@@ -464,7 +512,7 @@ pkv_status pkv_decode_default_partitions(int32_t num_seqs, int32_t num_q_heads, 
       st != PKV_OK)
     return st;
   if (pkv_status st = default_partitions(launch_seqs(num_seqs), num_kv_heads, head_dim, num_q_heads / num_kv_heads,
-                                         max_blocks_per_seq, num_partitions);
+                                         max_blocks_per_seq, Window{}, num_partitions);
       st != PKV_OK)
     return st;
   return ok();
@@ -480,7 +528,7 @@ pkv_status pkv_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int3
     return fail(PKV_ERR_INVALID_ARGUMENT, "num_partitions out of range (got %d)", num_partitions);
   size_t need = 0;
   if (pkv_status st = decode_workspace_need(num_seqs, num_kv_heads, head_dim, num_q_heads / num_kv_heads,
-                                            max_blocks_per_seq, num_partitions, &need);
+                                            max_blocks_per_seq, Window{}, num_partitions, &need);
       st != PKV_OK)
     return st;
   *bytes = need;
@@ -496,7 +544,7 @@ pkv_status pkv_paged_decode_attention_split(const void* q, const void* k_cache, 
                                             pkv_stream_t stream) {
   return decode_impl(q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
                      num_kv_heads, head_dim, num_blocks, block_size, scale, out, workspace, workspace_bytes,
-                     num_partitions, phases, stream, nullptr);
+                     num_partitions, phases, stream, nullptr, Window{});
 }
 
 pkv_status pkv_decode_step(const void* q, const void* k_new, const void* v_new, const float* cos_sin,
@@ -516,7 +564,7 @@ pkv_status pkv_decode_step(const void* q, const void* k_new, const void* v_new, 
   const FusedStep fused{k_new, v_new, cos_sin, cos_sin ? max_position : 0};
   return decode_impl(q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
                      num_kv_heads, head_dim, num_blocks, block_size, scale, out, workspace, workspace_bytes, 0,
-                     PKV_PHASE_ALL, stream, &fused);
+                     PKV_PHASE_ALL, stream, &fused, Window{});
 }
 
 pkv_status pkv_paged_decode_attention(const void* q, const void* k_cache, const void* v_cache,
@@ -528,6 +576,316 @@ pkv_status pkv_paged_decode_attention(const void* q, const void* k_cache, const 
   return pkv_paged_decode_attention_split(q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
                                           num_seqs, num_q_heads, num_kv_heads, head_dim, num_blocks, block_size,
                                           scale, out, workspace, workspace_bytes, 0, PKV_PHASE_ALL, stream);
+}
+
+pkv_status pkv_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, const int64_t* positions, int32_t num_axes, int64_t axis_stride,
+                           const uint8_t* freq_axes, const float* cos_sin, int64_t max_position,
+                           const int64_t* slot_mapping, int64_t num_tokens, int32_t num_q_heads,
+                           int32_t num_kv_heads, int32_t head_dim, void* q_out, int64_t q_out_stride, void* k_cache,
+                           void* v_cache, int64_t num_blocks, int32_t block_size, pkv_stream_t stream) {
+  if (num_tokens < 0) return fail(PKV_ERR_INVALID_ARGUMENT, "num_tokens must be >= 0 (got %lld)", (long long)num_tokens);
+  if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads > (1 << 20) || num_kv_heads > (1 << 20))
+    return fail(PKV_ERR_INVALID_ARGUMENT, "head counts must be in [1, 2^20] (q %d, kv %d)", num_q_heads, num_kv_heads);
+  if (head_dim != 64 && head_dim != 128)
+    return fail(PKV_ERR_UNSUPPORTED, "head_dim %d not built (64 or 128)", head_dim);
+  if (block_size != PKV_BLOCK_SIZE)
+    return fail(PKV_ERR_UNSUPPORTED, "block_size must be %d (got %d)", PKV_BLOCK_SIZE, block_size);
+  if (num_blocks <= 0 || num_blocks > (int64_t{1} << 40))
+    return fail(PKV_ERR_INVALID_ARGUMENT, "num_blocks out of range (got %lld)", (long long)num_blocks);
+  if (num_tokens > (int64_t{1} << 32))
+    return fail(PKV_ERR_UNSUPPORTED, "num_tokens %lld too large", (long long)num_tokens);
+  if (num_axes < 1 || num_axes > pkv::kMaxPositionAxes)
+    return fail(PKV_ERR_INVALID_ARGUMENT, "num_axes must be in [1, %d] (got %d)", pkv::kMaxPositionAxes, num_axes);
+  if (max_position <= 0)
+    return fail(PKV_ERR_INVALID_ARGUMENT, "max_position must be positive (got %lld)", (long long)max_position);
+  if (num_axes > 1) {
+    if (axis_stride < 0) return fail(PKV_ERR_INVALID_ARGUMENT, "axis_stride must be >= 0 (got %lld)", (long long)axis_stride);
+    if (!freq_axes) return fail(PKV_ERR_INVALID_ARGUMENT, "freq_axes is null with %d axes", num_axes);
+    for (int i = 0; i < head_dim / 2; ++i)
+      if (freq_axes[i] >= num_axes)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "freq_axes[%d] = %d, with %d axes", i, freq_axes[i], num_axes);
+  }
+  const struct {
+    const char* name;
+    int64_t stride, least;
+  } strides[] = {{"q_stride", q_stride, 0},
+                 {"k_stride", k_stride, 0},
+                 {"v_stride", v_stride, 0},
+                 {"q_out_stride", q_out_stride, static_cast<int64_t>(num_q_heads) * head_dim}};
+  for (const auto& x : strides)
+    if (x.stride < x.least || x.stride % 8 || x.stride > (int64_t{1} << 40))
+      return fail(PKV_ERR_INVALID_ARGUMENT, "%s must be a multiple of 8 elements and at least %lld (got %lld)", x.name,
+                  (long long)x.least, (long long)x.stride);
+  if (num_tokens == 0) return ok();
+  if (!q || !k || !v || !positions || !cos_sin || !slot_mapping || !q_out || !k_cache || !v_cache)
+    return fail(PKV_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_cache) ||
+      !aligned16(v_cache) || !aligned16(cos_sin) || (reinterpret_cast<uintptr_t>(positions) & 7u) ||
+      (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+    return fail(PKV_ERR_INVALID_ARGUMENT,
+                "q, k, v, q_out, cos_sin and the caches must be 16-byte aligned, positions and slot_mapping 8-byte");
+  unsigned* err = nullptr;
+  int sms = 0;
+  if (pkv_status st = device_state(&err, &sms); st != PKV_OK) return st;
+  pkv::RopeAppendParams p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_out = q_out;
+  p.q_stride = q_stride / 8;
+  p.k_stride = k_stride / 8;
+  p.v_stride = v_stride / 8;
+  p.q_out_stride = q_out_stride / 8;
+  p.positions = positions;
+  p.axis_stride = axis_stride;
+  p.cos_sin = cos_sin;
+  p.max_position = max_position;
+  p.slot_mapping = slot_mapping;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.err = err;
+  p.num_tokens = num_tokens;
+  p.num_slots = num_blocks * PKV_BLOCK_SIZE;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.num_axes = num_axes;
+  if (num_axes > 1) memcpy(p.freq_axis, freq_axes, head_dim / 2);
+  const cudaError_t e = pkv::launch_rope_append(p, head_dim, sms, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rope_append launch");
+  g_launches.fetch_add(1);
+  return ok();
+}
+
+pkv_status pkv_window_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                            int32_t head_dim, int32_t max_blocks_per_seq, int32_t window,
+                                            int32_t num_sink_tokens, int32_t num_partitions, size_t* bytes) {
+  if (!bytes) return fail(PKV_ERR_INVALID_ARGUMENT, "bytes is null");
+  if (pkv_status st = check_decode_shapes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq);
+      st != PKV_OK)
+    return st;
+  if (pkv_status st = check_window(window, num_sink_tokens); st != PKV_OK) return st;
+  if (num_partitions < 0 || num_partitions > kMaxPartitions)
+    return fail(PKV_ERR_INVALID_ARGUMENT, "num_partitions out of range (got %d)", num_partitions);
+  size_t need = 0;
+  if (pkv_status st = decode_workspace_need(num_seqs, num_kv_heads, head_dim, num_q_heads / num_kv_heads,
+                                            max_blocks_per_seq, Window{window, num_sink_tokens}, num_partitions, &need);
+      st != PKV_OK)
+    return st;
+  *bytes = need;
+  return ok();
+}
+
+pkv_status pkv_paged_window_decode_attention(const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                             const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
+                                             int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks,
+                                             int32_t block_size, float scale, int32_t window, int32_t num_sink_tokens,
+                                             void* out, void* workspace, size_t workspace_bytes,
+                                             int32_t num_partitions, pkv_stream_t stream) {
+  if (pkv_status st = check_window(window, num_sink_tokens); st != PKV_OK) return st;
+  return decode_impl(q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
+                     num_kv_heads, head_dim, num_blocks, block_size, scale, out, workspace, workspace_bytes,
+                     num_partitions, PKV_PHASE_ALL, stream, nullptr, Window{window, num_sink_tokens});
+}
+
+pkv_status pkv_window_prefill_default_splits(int32_t num_seqs, int32_t max_query_len, int32_t num_q_heads,
+                                             int32_t num_kv_heads, int32_t window, int32_t num_sink_tokens,
+                                             int32_t* num_splits) {
+  if (!num_splits) return fail(PKV_ERR_INVALID_ARGUMENT, "num_splits is null");
+  if (num_seqs < 0 || max_query_len < 0) return fail(PKV_ERR_INVALID_ARGUMENT, "num_seqs and max_query_len must be >= 0");
+  if (pkv_status st = check_shapes(num_seqs, num_seqs, num_q_heads, num_kv_heads, 128, 1); st != PKV_OK) return st;
+  if (pkv_status st = check_window(window, num_sink_tokens); st != PKV_OK) return st;
+  int sms = 0;
+  if (pkv_status st = device_state(nullptr, &sms); st != PKV_OK) return st;
+  int32_t n = one_wave_splits(num_seqs, max_query_len, num_q_heads, num_kv_heads, sms);
+  // At least two key steps a split: a CTA's rows see at most its tokens' windows and the sinks.
+  const int64_t keys = static_cast<int64_t>(window) + num_sink_tokens + pkv::prefill_cta_tokens(num_q_heads / num_kv_heads);
+  const int64_t most = (keys + 255) / 256;
+  if (n > most) n = static_cast<int32_t>(most);
+  *num_splits = n;
+  return ok();
+}
+
+pkv_status pkv_paged_window_prefill_attention(const void* q, const void* k_cache, const void* v_cache,
+                                              const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                              const int32_t* context_lens, const int32_t* query_start,
+                                              int32_t max_query_len, int32_t num_seqs, int32_t num_q_heads,
+                                              int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks,
+                                              int32_t block_size, float scale, int32_t window,
+                                              int32_t num_sink_tokens, void* out, int32_t num_splits, void* workspace,
+                                              size_t workspace_bytes, pkv_stream_t stream) {
+  if (pkv_status st = check_window(window, num_sink_tokens); st != PKV_OK) return st;
+  if (!(scale > 0.f)) return fail(PKV_ERR_INVALID_ARGUMENT, "scale must be positive");
+  return prefill_impl(q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, query_start, max_query_len,
+                      num_seqs, num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, scale, out, num_splits,
+                      workspace, workspace_bytes, stream, Window{window, num_sink_tokens});
+}
+
+namespace {
+// Shared-prefix decode: its grid, partition count and workspace (byte offsets of the parts).
+struct PrefixPlan {
+  int32_t ctas = 0, parts = 0;
+  size_t pairs = 0, shared = 0, plan_ok = 0, records = 0, whole = 0, pieces = 0, prefix = 0, bytes = 0;
+};
+
+pkv_status plan_prefix_decode(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t max_blocks_per_seq, int32_t num_groups, PrefixPlan* plan) {
+  if (pkv_status st = check_shapes(num_seqs, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq);
+      st != PKV_OK)
+    return st;
+  if (num_seqs > PKV_MAX_SEQS)
+    return fail(PKV_ERR_UNSUPPORTED, "num_seqs %d exceeds PKV_MAX_SEQS (%d)", num_seqs, PKV_MAX_SEQS);
+  if (num_groups < 0 || num_groups > PKV_MAX_SEQS)
+    return fail(PKV_ERR_INVALID_ARGUMENT, "num_groups must be in [0, %d] (got %d)", PKV_MAX_SEQS, num_groups);
+  const int group = num_q_heads / num_kv_heads;
+  int sms = 0;
+  if (pkv_status st = device_state(nullptr, &sms); st != PKV_OK) return st;
+  // The most (tile pair, kv head) units the groups can make, and from there whole waves of one CTA per SM.
+  const int64_t tiles = (num_groups < num_seqs ? num_groups : num_seqs) +
+                        static_cast<int64_t>(num_seqs) / pkv::prefill_cta_tokens(group);
+  const int64_t waves = (tiles * num_kv_heads + sms - 1) / sms;
+  const int64_t ctas = (waves < 1 ? 1 : waves) * sms;
+  if (ctas * 256 >= (int64_t{1} << 31))
+    return fail(PKV_ERR_UNSUPPORTED, "too many groups, sequences and kv heads for one launch (%lld CTAs)", (long long)ctas);
+  int pieces = 0;
+  const cudaError_t e = pkv::resident_tail_pieces(head_dim, group, num_seqs, &pieces);
+  if (e != cudaSuccess) return cuda_fail(e, "occupancy query");
+  const int64_t bound = static_cast<int64_t>(num_seqs) * num_kv_heads * max_blocks_per_seq;
+  plan->ctas = static_cast<int32_t>(ctas);
+  plan->parts = pieces < bound ? pieces : static_cast<int32_t>(bound < 1 ? 1 : bound);
+  const size_t state = static_cast<size_t>(pkv::piece_floats(head_dim, group)) * sizeof(float);
+  const size_t pair_count = static_cast<size_t>(num_seqs) * num_kv_heads;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t from = at;
+    at += (bytes + 255) & ~size_t(255);
+    return from;
+  };
+  take(pkv::workspace_prefix_bytes(num_seqs));
+  plan->pairs = take(pair_count * 8);
+  plan->shared = take(static_cast<size_t>(num_seqs) * 4);
+  plan->plan_ok = take(4);
+  plan->records = take(pair_count * 8);
+  plan->whole = take(pair_count * state);
+  plan->pieces = take(static_cast<size_t>(plan->parts) * 2 * state);
+  plan->prefix = take(static_cast<size_t>(ctas) * 256 * (head_dim + 2) * sizeof(float));
+  plan->bytes = at;
+  return PKV_OK;
+}
+}  // namespace
+
+pkv_status pkv_prefix_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                            int32_t head_dim, int32_t max_blocks_per_seq, int32_t num_groups,
+                                            size_t* bytes) {
+  if (!bytes) return fail(PKV_ERR_INVALID_ARGUMENT, "bytes is null");
+  PrefixPlan plan;
+  if (pkv_status st = plan_prefix_decode(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, num_groups,
+                                         &plan);
+      st != PKV_OK)
+    return st;
+  *bytes = plan.bytes;
+  return ok();
+}
+
+pkv_status pkv_paged_prefix_decode_attention(const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                             const int32_t* context_lens, const int32_t* group_start,
+                                             const int32_t* prefix_lens, int32_t num_groups, int32_t num_seqs,
+                                             int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                             int64_t num_blocks, int32_t block_size, float scale, void* out,
+                                             void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+  if (pkv_status st = check_shapes(num_seqs, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq);
+      st != PKV_OK)
+    return st;
+  if (block_size != PKV_BLOCK_SIZE)
+    return fail(PKV_ERR_UNSUPPORTED, "block_size must be %d (got %d)", PKV_BLOCK_SIZE, block_size);
+  if (num_blocks <= 0 || num_blocks > (int64_t{1} << 40) ||
+      num_blocks * num_kv_heads * PKV_BLOCK_SIZE >= (int64_t{1} << 31))
+    return fail(PKV_ERR_UNSUPPORTED, "num_blocks * num_kv_heads * 16 must be in (0, 2^31) (got %lld blocks)",
+                (long long)num_blocks);
+  if (!std::isfinite(scale) || scale <= 0.f) return fail(PKV_ERR_INVALID_ARGUMENT, "scale must be finite and positive");
+  if (num_seqs > PKV_MAX_SEQS)
+    return fail(PKV_ERR_UNSUPPORTED, "num_seqs %d exceeds PKV_MAX_SEQS (%d)", num_seqs, PKV_MAX_SEQS);
+  if (num_groups < 0 || num_groups > PKV_MAX_SEQS)
+    return fail(PKV_ERR_INVALID_ARGUMENT, "num_groups must be in [0, %d] (got %d)", PKV_MAX_SEQS, num_groups);
+  if (num_seqs == 0) return ok();
+  if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out || !workspace ||
+      (num_groups > 0 && (!group_start || !prefix_lens)))
+    return fail(PKV_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned16(workspace) ||
+      ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens) |
+        reinterpret_cast<uintptr_t>(group_start) | reinterpret_cast<uintptr_t>(prefix_lens)) &
+       3u))
+    return fail(PKV_ERR_INVALID_ARGUMENT, "q, caches, out and workspace must be 16-byte aligned");
+  PrefixPlan plan;
+  if (pkv_status st = plan_prefix_decode(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, num_groups,
+                                         &plan);
+      st != PKV_OK)
+    return st;
+  if (workspace_bytes < plan.bytes)
+    return fail(PKV_ERR_INVALID_ARGUMENT, "workspace too small: %zu bytes given, %zu needed", workspace_bytes,
+                plan.bytes);
+  unsigned* err = nullptr;
+  if (pkv_status st = device_state(&err, nullptr); st != PKV_OK) return st;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int group = num_q_heads / num_kv_heads;
+  pkv::PrefillParams f{};
+  f.q = q;
+  f.k_cache = k_cache;
+  f.v_cache = v_cache;
+  f.block_tables = block_tables;
+  f.context_lens = context_lens;
+  f.out = out;
+  f.err = err;
+  f.num_blocks = num_blocks;
+  f.num_seqs = num_seqs;
+  f.num_q_heads = num_q_heads;
+  f.num_kv_heads = num_kv_heads;
+  f.max_blocks_per_seq = max_blocks_per_seq;
+  f.max_query_len = 1;
+  f.scale = scale;
+  f.ws = reinterpret_cast<float*>(ws + plan.prefix);
+  f.group_start = group_start;
+  f.prefix_lens = prefix_lens;
+  f.num_groups = num_groups;
+  f.shared_ctas = plan.ctas;
+  f.ws_records = reinterpret_cast<int2*>(ws + plan.records);
+  f.ws_plan_ok = reinterpret_cast<int32_t*>(ws + plan.plan_ok);
+  cudaError_t e = pkv::launch_shared_prefix(f, head_dim, group, s);
+  if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
+  pkv::DecodeParams p{};
+  p.q = q;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.out = out;
+  p.ws_prefix = reinterpret_cast<int32_t*>(ws);
+  p.ws_pairs = reinterpret_cast<int32_t*>(ws + plan.pairs);
+  p.ws_pieces = reinterpret_cast<float*>(ws + plan.pieces);
+  p.err = err;
+  p.num_blocks = num_blocks;
+  p.num_seqs = num_seqs;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.num_partitions = plan.parts;
+  p.qscale = scale * 1.4426950408889634f;
+  p.group_start = group_start;
+  p.prefix_lens = prefix_lens;
+  p.num_groups = num_groups;
+  p.ws_shared = reinterpret_cast<int32_t*>(ws + plan.shared);
+  p.ws_whole = reinterpret_cast<float*>(ws + plan.whole);
+  p.ws_plan_ok = f.ws_plan_ok;
+  p.ws_records = f.ws_records;
+  p.ws_prefix_o = f.ws;
+  p.ws_prefix_ml = reinterpret_cast<const float2*>(f.ws + static_cast<size_t>(plan.ctas) * 256 * head_dim);
+  if ((e = pkv::launch_tail_partition(p, head_dim, group, s)) != cudaSuccess) return cuda_fail(e, "tail partition launch");
+  if ((e = pkv::launch_prefix_merge(p, head_dim, group, s)) != cudaSuccess) return cuda_fail(e, "prefix merge launch");
+  g_launches.fetch_add(3);
+  return ok();
 }
 
 pkv_status pkv_get_and_clear_device_error(uint32_t* bits, pkv_stream_t stream) {

@@ -27,11 +27,26 @@ struct PrefillParams {
   int num_splits = 1;
   int ws_rows = 0;     // chunk rows per sequence in ws (the grid's tiles x chunk tokens per CTA)
   float* ws = nullptr;  // [split][seq][ws_rows][num_q_heads]: D floats of O; then the same index: (m, l)
+  // Window: a row sees its last `window` tokens and the first `sinks` (both at most 16 * max_blocks_per_seq).
+  int window = 0;
+  int sinks = 0;
+  // Shared prefixes (one query token a sequence; q and out rows are sequences): groups of consecutive
+  // sequences and the tokens they share.  ws: [CTA][256 rows]: D floats of O; then the same index: (m, l).
+  const int32_t* group_start = nullptr;  // [num_groups + 1]
+  const int32_t* prefix_lens = nullptr;  // [num_groups]
+  int num_groups = 0;
+  int shared_ctas = 0;               // grid
+  int2* ws_records = nullptr;        // [num_seqs][num_kv_heads]: (first row in ws, splits 256 rows apart)
+  int32_t* ws_plan_ok = nullptr;     // whether group_start is in order (records are valid)
 };
 
 // Chunked prefill attention (tensor cores); grid covers max_query_len rows per sequence.
 cudaError_t launch_paged_prefill(const PrefillParams& p, int head_dim, int group, int max_query_len,
                                  cudaStream_t stream);
+// The same for rows with a window and sinks (num_splits as above), and for shared prefixes (partial states).
+cudaError_t launch_window_prefill(const PrefillParams& p, int head_dim, int group, int max_query_len,
+                                  cudaStream_t stream);
+cudaError_t launch_shared_prefix(const PrefillParams& p, int head_dim, int group, cudaStream_t stream);
 // Chunk tokens one CTA covers (two 128-row tiles of 128 / group tokens).
 inline int prefill_cta_tokens(int group) { return 256 / group; }
 // Workspace bytes of a split call: partial states of every split.

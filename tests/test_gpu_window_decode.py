@@ -1,0 +1,182 @@
+"""Windowed decode attention on the GPU against the definition in 64 bits (tolerances: plain64.attend)."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_275_gb300 as pkv
+from gpu_util import device_errors
+from plain64 import BLOCK, Pages, assert_within, attend, f64, sees
+
+pytestmark = pytest.mark.gpu
+
+
+def exact(pages, q, lens, window, sinks, scale):
+    qf, kf, vf = f64(q), f64(pages.k), f64(pages.v)
+    rows = [attend(qf[b], kf, vf, pages.table[b], sees(n - 1, window, sinks) if n > 0 else [], scale, 0.0)
+            for b, n in enumerate(lens)]
+    return np.stack([r[0] for r in rows]), np.stack([r[1] for r in rows])
+
+
+def hide(pages, window, sinks):
+    """NaN in every token that is not seen, and -1 for every block that holds none that is."""
+    for b, n in enumerate(pages.lens):
+        seen = set(sees(n - 1, window, sinks).tolist()) if n else set()
+        pages.poison(b, [t for t in range(-(-n // BLOCK) * BLOCK) if t not in seen])
+        for blk in range(-(-n // BLOCK)):
+            if not any(t in seen for t in range(blk * BLOCK, blk * BLOCK + BLOCK)):
+                pages.table[b, blk] = -1
+
+
+def run(lens, hq, hkv, d, window, sinks, seed=0, scale=None, **kw):
+    pages = Pages(lens, hkv, d, seed)
+    hide(pages, window, sinks)
+    q = pages.randn(len(lens), hq, d)
+    scale = d ** -0.5 if scale is None else scale
+    kc, vc, table, cl = pages.cuda()
+    out = torch.full((len(lens), hq, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    got = pkv.paged_window_decode_attention(q.cuda(), kc, vc, table, cl, scale, out, window, sinks, **kw)
+    assert got is out
+    ref, allowed = exact(pages, q, lens, window, sinks, scale)
+    assert_within(out, ref, allowed, f"{hq}/{hkv} D{d} window {window} sinks {sinks} {kw}")
+    assert device_errors() == 0
+    return out
+
+
+LENS = (0, 1, 2, 15, 16, 17, 31, 33, 64, 100, 257, 700)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (4, 2), (8, 2), (16, 2), (8, 8), (3, 3)])
+def test_layouts(hq, hkv, d):
+    run(LENS, hq, hkv, d, 50, 4, seed=hq)
+
+
+@pytest.mark.parametrize("hq", [4, 16])
+@pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 100, 700, 5000, 0x7fffffff])
+@pytest.mark.parametrize("sinks", [0, 1, 16, 20])
+def test_windows(hq, window, sinks):
+    run(LENS, hq, 2, 64, window, sinks, seed=window % 1000 + sinks)
+
+
+@pytest.mark.parametrize("hq", [4, 16])
+@pytest.mark.parametrize("sinks", [99, 690, 0x7fffffff])
+def test_many_sinks(hq, sinks):
+    run(LENS, hq, 2, 128, 3, sinks, seed=1)
+
+
+@pytest.mark.parametrize("hq", [4, 16])
+@pytest.mark.parametrize("parts", [1, 2, 7, 64, 1000])
+def test_partition_counts(hq, parts):
+    run((300, 0, 1, 77, 1000), hq, 2, 128, 130, 5, seed=2, num_partitions=parts)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.05, 1.0])
+@pytest.mark.parametrize("hq", [4, 16])
+def test_scales(hq, scale):
+    run((40, 90), hq, 2, 64, 30, 3, seed=4, scale=scale)
+
+
+def test_window_as_long_as_the_sequences_is_plain_decode():
+    lens = (5, 16, 40, 333)
+    pages = Pages(lens, 2, 128, 8)
+    q = pages.randn(4, 8, 128).cuda()
+    kc, vc, table, cl = pages.cuda()
+    a, b = torch.empty_like(q), torch.empty_like(q)
+    pkv.paged_window_decode_attention(q, kc, vc, table, cl, 0.1, a, 400, 0, num_partitions=9)
+    pkv.paged_decode_attention(q, kc, vc, table, cl, 0.1, b, num_partitions=9)
+    assert torch.equal(a, b)
+
+
+def test_more_sequences_than_one_launch():
+    lens = np.random.RandomState(0).randint(0, 40, 4096 + 200)
+    run(lens, 2, 1, 64, 9, 2, seed=6)
+
+
+def test_bad_lengths_and_blocks_are_flagged():
+    pages = Pages((20, 40), 1, 64, 3)
+    q = pages.randn(2, 2, 64).cuda()
+    kc, vc, table, cl = pages.cuda()
+    out = torch.empty_like(q)
+    assert device_errors() == 0
+    for bad, bit in ((-5, pkv.DEVERR_CONTEXT_LEN_NEGATIVE), (49, pkv.DEVERR_CONTEXT_LEN_TOO_LONG)):
+        lens = cl.clone()
+        lens[0] = bad
+        pkv.paged_window_decode_attention(q, kc, vc, table, lens, 0.1, out, 10, 1)
+        assert device_errors() & bit
+    table[1, 2] = 1 << 20
+    pkv.paged_window_decode_attention(q, kc, vc, table, cl, 0.1, out, 10, 1)
+    assert device_errors() == pkv.DEVERR_BLOCK_ID_OUT_OF_RANGE
+
+
+def test_graphs_without_a_given_workspace_do_not_share_it():
+    """Two captured calls of different sizes, then eager ones that make the eager workspace grow."""
+    cases = []
+    for lens, hq in (((40, 300), 4), ((700,) * 9, 16)):
+        pages = Pages(lens, 2, 128, len(lens))
+        q = pages.randn(len(lens), hq, 128)
+        ref = exact(pages, q, lens, 64, 4, 0.09)
+        cases.append((pages.cuda(), q.cuda(), torch.empty(len(lens), hq, 128, dtype=torch.bfloat16, device="cuda"), ref))
+
+    def call(c):
+        (kc, vc, table, cl), q, out, _ = c
+        pkv.paged_window_decode_attention(q, kc, vc, table, cl, 0.09, out, 64, 4)
+
+    for c in cases:
+        call(c)
+    torch.cuda.synchronize()
+    graphs = []
+    for c in cases:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call(c)
+    run(LENS * 20, 16, 2, 128, 2000, 4, seed=11)
+    for _ in range(2):
+        for g, c in zip(graphs, cases):
+            c[2].zero_()
+            g.replay()
+        torch.cuda.synchronize()
+        for _, _, out, (ref, allowed) in cases:
+            assert_within(out, ref, allowed, "replayed")
+    assert device_errors() == 0
+
+
+def test_two_streams_at_once():
+    lens = (900, 20, 400)
+    pages = Pages(lens, 4, 128, 21)
+    q = pages.randn(3, 16, 128)
+    ref, allowed = exact(pages, q, lens, 200, 4, 0.09)
+    kc, vc, table, cl = pages.cuda()
+    qg = q.cuda()
+    outs = [torch.zeros_like(qg) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, out in zip(streams, outs):
+            pkv.paged_window_decode_attention(qg, kc, vc, table, cl, 0.09, out, 200, 4, stream=s)
+    torch.cuda.synchronize()
+    for out in outs:
+        assert_within(out, ref, allowed, "two streams")
+    assert device_errors() == 0
+
+
+def test_refusals():
+    pages = Pages((20, 40), 1, 64, 3)
+    q = pages.randn(2, 2, 64).cuda()
+    kc, vc, table, cl = pages.cuda()
+    out = torch.empty_like(q)
+    call = pkv.paged_window_decode_attention
+    with pytest.raises(pkv.PagedKVError, match="window"):
+        call(q, kc, vc, table, cl, 0.1, out, 0)
+    with pytest.raises(pkv.PagedKVError, match="num_sink_tokens"):
+        call(q, kc, vc, table, cl, 0.1, out, 5, -1)
+    with pytest.raises(ValueError, match="32 bits"):
+        call(q, kc, vc, table, cl, 0.1, out, (1 << 32) + 5)
+    with pytest.raises(ValueError, match="batch"):
+        call(q, kc, vc, table[:1], cl, 0.1, out, 5)
+    with pytest.raises(ValueError, match="workspace"):
+        call(q, kc, vc, table, cl, 0.1, out, 5, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(TypeError, match="bfloat16"):
+        call(q.float(), kc, vc, table, cl, 0.1, out, 5)
+    with pytest.raises(ValueError, match="contiguous"):
+        call(q, kc, vc, table.t().contiguous().t(), cl, 0.1, out, 5)
+    assert device_errors() == 0
