@@ -8,7 +8,6 @@ library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
-import functools
 import threading
 from pathlib import Path
 
@@ -490,44 +489,10 @@ def paged_prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
 MAX_POSITION_AXES = 4
 
 
-def _require_on(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int, device: torch.device) -> None:
-    """_require without its cost when nothing is wrong (these calls can be shorter than their checks)."""
-    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != ndim or t.get_device() != device.index
-            or not t.is_contiguous()):
-        _require(t, name, dtype, ndim, device)
-
-
-def _device_of(t: torch.Tensor, name: str) -> torch.device:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    return t.device
-
-
-def _stream_on(device: torch.device, stream: torch.cuda.Stream | None) -> int:
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    if stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    return stream.cuda_stream
-
-
-def _run_on(device: torch.device, call, *args) -> None:
-    """call(*args) with the tensors' device current."""
-    if torch.cuda.current_device() == device.index:
-        status = call(*args)
-    else:
-        with torch.cuda.device(device):
-            status = call(*args)
-    if status != OK:
-        _check(status)
-
-
 _scratch = threading.local()
 
 
-def _temporary(device: torch.device, stream: torch.cuda.Stream | None, handle: int, nbytes: int) -> torch.Tensor:
+def _temporary(device: int, stream: torch.cuda.Stream | None, handle: int, nbytes: int) -> torch.Tensor:
     """A workspace of a call that was given none.
 
     One buffer per host thread, device and stream: calls that share it run in order (two threads' calls on one
@@ -535,99 +500,64 @@ def _temporary(device: torch.device, stream: torch.cuda.Stream | None, handle: i
     graph's memory, which lives as long as the graph does and is shared with nothing outside it.
     """
     buffers = _scratch.__dict__
-    if stream is None and torch.cuda.current_device() == device.index:
-        ws = buffers.get((device.index, handle))
-        if ws is not None and ws.numel() >= nbytes and not torch.cuda.is_current_stream_capturing():
-            return ws
-    with torch.cuda.device(device), torch.cuda.stream(stream):
+    with torch.cuda.stream(stream):  # (no stream: the current one; the caller has made the device current)
         if torch.cuda.is_current_stream_capturing():
             return torch.empty(nbytes, dtype=torch.uint8, device=device)
-        ws = buffers.get((device.index, handle))
+        ws = buffers.get((device, handle))
         if ws is None or ws.numel() < nbytes:
-            ws = buffers[(device.index, handle)] = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+            ws = buffers[(device, handle)] = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
         return ws
 
 
-def _given(workspace: torch.Tensor | None, device: torch.device, stream: torch.cuda.Stream | None, handle: int,
-           nbytes: int) -> torch.Tensor:
-    if workspace is None:
-        return _temporary(device, stream, handle, nbytes)
-    _require(workspace, "workspace", torch.uint8, 1, device)
-    if workspace.numel() < nbytes:
-        raise ValueError(f"workspace must hold {nbytes} bytes (got {workspace.numel()})")
-    return workspace
+_binding = None
 
 
-def _query(ctype, call, device_index: int, *args) -> int:
+def _native():
+    """The compiled binding (csrc/binding.cpp) of the calls below."""
+    global _binding
+    if _binding is None:
+        load()
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise ImportError("the compiled binding is missing: build it with `python -m paged_kv_cache_275_gb300.build` "
+                              "(there is no fallback path)") from e
+        module.register(_check, _temporary)
+        _binding = module
+    return _binding
+
+
+def _query(ctype, call, *args) -> int:
     out = ctype(0)
-    _run_on(torch.device("cuda", device_index), call, *args, ctypes.byref(out))
+    _check(call(*args, ctypes.byref(out)))
     return int(out.value)
-
-
-@functools.lru_cache(maxsize=1024)
-def _window_decode_workspace(device_index: int, *shape: int) -> int:
-    return _query(ctypes.c_size_t, load().pkv_window_decode_workspace_size, device_index, *shape)
-
-
-@functools.lru_cache(maxsize=1024)
-def _prefix_decode_workspace(device_index: int, *shape: int) -> int:
-    return _query(ctypes.c_size_t, load().pkv_prefix_decode_workspace_size, device_index, *shape)
-
-
-@functools.lru_cache(maxsize=1024)
-def _window_prefill_splits(device_index: int, *shape: int) -> int:
-    return _query(ctypes.c_int32, load().pkv_window_prefill_default_splits, device_index, *shape)
 
 
 def window_decode_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
                                  max_blocks_per_seq: int, window: int, num_sink_tokens: int = 0,
                                  num_partitions: int = 0) -> int:
     """Bytes of the workspace of a windowed decode call on the current device."""
-    return _window_decode_workspace(torch.cuda.current_device(), num_seqs, num_q_heads, num_kv_heads, head_dim,
-                                    max_blocks_per_seq, window, num_sink_tokens, num_partitions)
+    return _query(ctypes.c_size_t, load().pkv_window_decode_workspace_size, num_seqs, num_q_heads, num_kv_heads,
+                  head_dim, max_blocks_per_seq, window, num_sink_tokens, num_partitions)
 
 
 def prefix_decode_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
                                  max_blocks_per_seq: int, num_groups: int) -> int:
     """Bytes of the workspace of a shared-prefix decode call on the current device."""
-    return _prefix_decode_workspace(torch.cuda.current_device(), num_seqs, num_q_heads, num_kv_heads, head_dim,
-                                    max_blocks_per_seq, num_groups)
+    return _query(ctypes.c_size_t, load().pkv_prefix_decode_workspace_size, num_seqs, num_q_heads, num_kv_heads,
+                  head_dim, max_blocks_per_seq, num_groups)
 
 
 def window_prefill_default_splits(num_seqs: int, max_query_len: int, num_q_heads: int, num_kv_heads: int,
                                   window: int, num_sink_tokens: int = 0) -> int:
     """The split count of a windowed prefill call with num_splits = 0 on the current device."""
-    return _window_prefill_splits(torch.cuda.current_device(), num_seqs, max_query_len, num_q_heads, num_kv_heads,
-                                  window, num_sink_tokens)
+    return _query(ctypes.c_int32, load().pkv_window_prefill_default_splits, num_seqs, max_query_len, num_q_heads,
+                  num_kv_heads, window, num_sink_tokens)
 
 
 def rope_freq_axes(sections) -> bytes:
     """freq_axes of rope_append for frequencies dealt to the axes in order: sections[a] of them turn by axis a."""
     return b"".join(bytes([axis]) * count for axis, count in enumerate(sections))
-
-
-def _int32(value: int, name: str) -> int:
-    """ctypes would drop the upper bits of a wider value."""
-    if not -0x80000000 <= value <= 0x7fffffff:
-        raise ValueError(f"{name} does not fit in 32 bits (got {value})")
-    return value
-
-
-def _token_stride(t: torch.Tensor, name: str, shape: tuple, device: torch.device) -> int:
-    """Elements between token rows of a [tokens, heads, head_dim] tensor whose rows are contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.get_device() != device.index:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    tokens, heads, head_dim = shape
-    per_token, per_head, per_dim = t.stride()
-    if per_dim != 1 or (heads > 1 and per_head != head_dim):
-        raise ValueError(f"{name}[token] must be contiguous (got strides {t.stride()})")
-    return per_token if tokens > 1 else heads * head_dim
 
 
 def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
@@ -640,58 +570,8 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
     ``rope_freq_axes``).  cos_sin: [max_position, D] fp32.  q, k, v and q_out may be slices of wider rows, as of one
     projection's output: only a token's own [heads, D] has to be contiguous, 16-byte aligned rows.
     """
-    dev = _device_of(k_cache, "k_cache")
-    _require_on(k_cache, "k_cache", torch.bfloat16, 4, dev)
-    _require_on(v_cache, "v_cache", torch.bfloat16, 4, dev)
-    _require_on(slot_mapping, "slot_mapping", torch.int64, 1, dev)
-    _require_on(cos_sin, "cos_sin", torch.float32, 2, dev)
-    nb, hkv, bs, d = k_cache.shape
-    n = slot_mapping.shape[0]
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache shapes differ")
-    if cos_sin.shape[1] != d:
-        raise ValueError("cos_sin must be [max_position, head_dim]")
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be [tokens, heads, head_dim]")
-    hq = q.shape[1]
-    strides = [_token_stride(t, name, (n, heads, d), dev)
-               for t, name, heads in ((q, "q", hq), (k, "k", hkv), (v, "v", hkv), (q_out, "q_out", hq))]
-    if (not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int64
-            or positions.get_device() != dev.index or positions.dim() not in (1, 2) or positions.shape[-1] != n
-            or (n > 1 and positions.stride(-1) != 1)):
-        raise ValueError(f"positions must be int64 [{n}] or [axes, {n}] on {dev}, with contiguous rows")
-    axes, axis_stride = (1, 0) if positions.dim() == 1 else (positions.shape[0], positions.stride(0))
-    axis_of = None
-    if axes > 1:
-        if freq_axes is None:
-            raise ValueError("positions of several axes need freq_axes")
-        axis_of = bytes(freq_axes)
-        if len(axis_of) != d // 2:
-            raise ValueError(f"freq_axes must hold head_dim / 2 = {d // 2} axes (got {len(axis_of)})")
-    _run_on(dev, load().pkv_rope_append, q.data_ptr(), strides[0], k.data_ptr(), strides[1], v.data_ptr(), strides[2],
-            positions.data_ptr(), axes, axis_stride, axis_of, cos_sin.data_ptr(), cos_sin.shape[0],
-            slot_mapping.data_ptr(), n, hq, hkv, d, q_out.data_ptr(), strides[3], k_cache.data_ptr(),
-            v_cache.data_ptr(), nb, bs, _stream_on(dev, stream))
-    return q_out
-
-
-def _attention_shapes(q, k_cache, v_cache, block_tables, context_lens, out):
-    """Checks the tensors that every paged attention call takes; returns (device, q shape, cache shape, W)."""
-    dev = _device_of(q, "q")
-    _require_on(q, "q", torch.bfloat16, 3, dev)
-    _require_on(k_cache, "k_cache", torch.bfloat16, 4, dev)
-    _require_on(v_cache, "v_cache", torch.bfloat16, 4, dev)
-    _require_on(block_tables, "block_tables", torch.int32, 2, dev)
-    _require_on(context_lens, "context_lens", torch.int32, 1, dev)
-    _require_on(out, "out", torch.bfloat16, 3, dev)
-    shape, cache = q.shape, k_cache.shape
-    if v_cache.shape != cache or cache[3] != shape[2]:
-        raise ValueError("cache shapes do not match q")
-    if out.shape != shape:
-        raise ValueError("out must have the shape of q")
-    if block_tables.shape[0] != context_lens.shape[0]:
-        raise ValueError("block_tables / context_lens batch mismatch")
-    return dev, shape, cache, block_tables.shape[1]
+    return (_binding or _native()).rope_append(q, k, v, positions, slot_mapping, cos_sin, k_cache, v_cache, q_out,
+                                               freq_axes, stream)
 
 
 def paged_window_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -703,19 +583,8 @@ def paged_window_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cach
 
     Block-table entries of blocks that hold none of them are not read.  Returns ``out``.
     """
-    dev, (B, hq, d), (nb, hkv, bs, _), W = _attention_shapes(q, k_cache, v_cache, block_tables, context_lens, out)
-    if block_tables.shape[0] != B:
-        raise ValueError("block_tables / context_lens batch mismatch")
-    if B == 0:
-        return out
-    _int32(window, "window"), _int32(num_sink_tokens, "num_sink_tokens"), _int32(num_partitions, "num_partitions")
-    handle = _stream_on(dev, stream)
-    nbytes = _window_decode_workspace(dev.index, B, hq, hkv, d, W, window, num_sink_tokens, num_partitions)
-    ws = _given(workspace, dev, stream, handle, nbytes)
-    _run_on(dev, load().pkv_paged_window_decode_attention, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            block_tables.data_ptr(), W, context_lens.data_ptr(), B, hq, hkv, d, nb, bs, scale, window, num_sink_tokens,
-            out.data_ptr(), ws.data_ptr(), ws.numel(), num_partitions, handle)
-    return out
+    return (_binding or _native()).window_decode(q, k_cache, v_cache, block_tables, context_lens, scale, out, window,
+                                                 num_sink_tokens, num_partitions, workspace, stream)
 
 
 def paged_window_prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -729,24 +598,9 @@ def paged_window_prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cac
     ``num_splits`` 0 takes ``window_prefill_default_splits``; a count above 1 needs a workspace of
     ``prefill_workspace_size`` bytes, allocated here if not given.  Returns ``out``.
     """
-    dev, (_, hq, d), (nb, hkv, bs, _), W = _attention_shapes(q, k_cache, v_cache, block_tables, context_lens, out)
-    _require_on(query_start, "query_start", torch.int32, 1, dev)
-    B = context_lens.shape[0]
-    if query_start.shape[0] != B + 1:
-        raise ValueError(f"query_start must hold {B + 1} rows' starts")
-    _int32(window, "window"), _int32(num_sink_tokens, "num_sink_tokens")
-    _int32(max_query_len, "max_query_len"), _int32(num_splits, "num_splits")
-    handle = _stream_on(dev, stream)
-    if num_splits == 0:
-        num_splits = _window_prefill_splits(dev.index, B, max_query_len, hq, hkv, window, num_sink_tokens)
-    ws_ptr = ws_bytes = 0
-    if num_splits > 1:
-        ws = _given(workspace, dev, stream, handle, prefill_workspace_size(B, max_query_len, hq, hkv, d, num_splits))
-        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
-    _run_on(dev, load().pkv_paged_window_prefill_attention, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            block_tables.data_ptr(), W, context_lens.data_ptr(), query_start.data_ptr(), max_query_len, B, hq, hkv, d,
-            nb, bs, scale, window, num_sink_tokens, out.data_ptr(), num_splits, ws_ptr, ws_bytes, handle)
-    return out
+    return (_binding or _native()).window_prefill(q, k_cache, v_cache, block_tables, context_lens, query_start,
+                                                  max_query_len, scale, out, window, num_sink_tokens, num_splits,
+                                                  workspace, stream)
 
 
 def paged_prefix_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -759,19 +613,5 @@ def paged_prefix_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cach
     Group g is the sequences group_start[g] .. group_start[g + 1] - 1 (int32 [groups + 1]); the whole blocks of its
     first prefix_lens[g] tokens (int32 [groups]) are taken from its first sequence's table.  Returns ``out``.
     """
-    dev, (B, hq, d), (nb, hkv, bs, _), W = _attention_shapes(q, k_cache, v_cache, block_tables, context_lens, out)
-    _require_on(group_start, "group_start", torch.int32, 1, dev)
-    _require_on(prefix_lens, "prefix_lens", torch.int32, 1, dev)
-    groups = prefix_lens.shape[0]
-    if block_tables.shape[0] != B:
-        raise ValueError("block_tables / context_lens batch mismatch")
-    if group_start.shape[0] != groups + 1:
-        raise ValueError(f"group_start must hold {groups + 1} rows' starts")
-    if B == 0:
-        return out
-    handle = _stream_on(dev, stream)
-    ws = _given(workspace, dev, stream, handle, _prefix_decode_workspace(dev.index, B, hq, hkv, d, W, groups))
-    _run_on(dev, load().pkv_paged_prefix_decode_attention, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            block_tables.data_ptr(), W, context_lens.data_ptr(), group_start.data_ptr(), prefix_lens.data_ptr(), groups,
-            B, hq, hkv, d, nb, bs, scale, out.data_ptr(), ws.data_ptr(), ws.numel(), handle)
-    return out
+    return (_binding or _native()).prefix_decode(q, k_cache, v_cache, block_tables, context_lens, group_start,
+                                                 prefix_lens, scale, out, workspace, stream)

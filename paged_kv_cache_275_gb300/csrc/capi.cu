@@ -123,6 +123,12 @@ Window within_table(Window w, int32_t max_blocks_per_seq) {
   if (w.sinks > cap) w.sinks = cap;
   return w;
 }
+#ifndef PKV_MIN_PIECE_BLOCKS
+#define PKV_MIN_PIECE_BLOCKS 2
+#endif
+#ifndef PKV_TAIL_WAVES
+#define PKV_TAIL_WAVES 1
+#endif
 // Blocks of one sequence that a query token can see.
 int32_t visible_blocks(Window w, int32_t max_blocks_per_seq) {
   if (w.window == 0) return max_blocks_per_seq;
@@ -139,8 +145,8 @@ pkv_status default_partitions(int32_t num_seqs, int32_t num_kv_heads, int32_t he
                                       : pkv::resident_partition_pieces(head_dim, group, num_seqs, &pieces);
   if (e != cudaSuccess) return cuda_fail(e, "occupancy query");
   // Never more pieces than the block stream can have items.
-  const int64_t bound =
-      static_cast<int64_t>(num_seqs) * num_kv_heads * visible_blocks(window, max_blocks_per_seq);
+  int64_t bound = static_cast<int64_t>(num_seqs) * num_kv_heads * visible_blocks(window, max_blocks_per_seq);
+  if (window.window) bound = (bound + PKV_MIN_PIECE_BLOCKS - 1) / PKV_MIN_PIECE_BLOCKS;
   int64_t n = pieces;
   if (n > bound) n = bound;
   if (n > kMaxPartitions) n = kMaxPartitions;
@@ -263,9 +269,12 @@ static pkv_status decode_impl(const void* q, const void* k_cache, const void* v_
     }
     if (window.window) {
       const Window w = within_table(window, max_blocks_per_seq);
-      p.window = w.window;
-      p.sinks = w.sinks;
-      const cudaError_t e = pkv::launch_window_decode(p, head_dim, group, s);
+      pkv::DecodeViewParams v{};
+      static_cast<pkv::DecodeParams&>(v) = p;
+      v.window = w.window;
+      v.sinks = w.sinks;
+      v.min_piece_blocks = num_partitions == 0 ? PKV_MIN_PIECE_BLOCKS : 1;
+      const cudaError_t e = pkv::launch_window_decode(v, head_dim, group, s);
       if (e != cudaSuccess) return cuda_fail(e, "window decode launch");
       g_launches.fetch_add(2);
       continue;
@@ -725,7 +734,7 @@ pkv_status pkv_paged_window_prefill_attention(const void* q, const void* k_cache
 namespace {
 // Shared-prefix decode: its grid, partition count and workspace (byte offsets of the parts).
 struct PrefixPlan {
-  int32_t ctas = 0, parts = 0;
+  int32_t ctas = 0, parts = 0, sms = 0;
   size_t pairs = 0, shared = 0, plan_ok = 0, records = 0, whole = 0, pieces = 0, prefix = 0, bytes = 0;
 };
 
@@ -751,8 +760,11 @@ pkv_status plan_prefix_decode(int32_t num_seqs, int32_t num_q_heads, int32_t num
   int pieces = 0;
   const cudaError_t e = pkv::resident_tail_pieces(head_dim, group, num_seqs, &pieces);
   if (e != cudaSuccess) return cuda_fail(e, "occupancy query");
-  const int64_t bound = static_cast<int64_t>(num_seqs) * num_kv_heads * max_blocks_per_seq;
+  const int64_t bound = (static_cast<int64_t>(num_seqs) * num_kv_heads * max_blocks_per_seq + PKV_MIN_PIECE_BLOCKS - 1) /
+                        PKV_MIN_PIECE_BLOCKS;
   plan->ctas = static_cast<int32_t>(ctas);
+  plan->sms = sms;
+  pieces *= PKV_TAIL_WAVES;
   plan->parts = pieces < bound ? pieces : static_cast<int32_t>(bound < 1 ? 1 : bound);
   const size_t state = static_cast<size_t>(pkv::piece_floats(head_dim, group)) * sizeof(float);
   const size_t pair_count = static_cast<size_t>(num_seqs) * num_kv_heads;
@@ -851,11 +863,12 @@ pkv_status pkv_paged_prefix_decode_attention(const void* q, const void* k_cache,
   f.prefix_lens = prefix_lens;
   f.num_groups = num_groups;
   f.shared_ctas = plan.ctas;
+  f.num_sms = plan.sms;
   f.ws_records = reinterpret_cast<int2*>(ws + plan.records);
   f.ws_plan_ok = reinterpret_cast<int32_t*>(ws + plan.plan_ok);
   cudaError_t e = pkv::launch_shared_prefix(f, head_dim, group, s);
   if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
-  pkv::DecodeParams p{};
+  pkv::DecodeViewParams p{};
   p.q = q;
   p.k_cache = k_cache;
   p.v_cache = v_cache;
@@ -872,6 +885,7 @@ pkv_status pkv_paged_prefix_decode_attention(const void* q, const void* k_cache,
   p.num_kv_heads = num_kv_heads;
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.num_partitions = plan.parts;
+  p.min_piece_blocks = PKV_MIN_PIECE_BLOCKS;
   p.qscale = scale * 1.4426950408889634f;
   p.group_start = group_start;
   p.prefix_lens = prefix_lens;

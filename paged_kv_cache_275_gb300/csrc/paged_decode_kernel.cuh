@@ -73,6 +73,9 @@ enum class View {
   kTail,    // blocks behind the ones its group shares; every state goes to the workspace
 };
 
+template <View kView>
+using ParamsOf = std::conditional_t<kView == View::kAll, DecodeParams, DecodeViewParams>;
+
 // Rows of one 16-token block that the query sees.
 struct SeesBelow {  // rows below `end`
   int end;
@@ -168,15 +171,20 @@ struct Geo {
 #endif
 static_assert(PKV_MMA_MIN_G == 4 || PKV_MMA_MIN_G == 8,
               "groups of eight always take the tensor cores; four may (their p tile holds the two 256-byte P tiles)");
-template <int G>
+template <int G, View kView>
 struct Split {
-  static constexpr bool kMma = G >= PKV_MMA_MIN_G;
+  static constexpr bool kMma = kView != View::kAll || G >= PKV_MMA_MIN_G;
 };
 // One ring stage: K tile | V tile | q rows.  The tensor-core path copies K and V as
 // 128-byte-swizzled tensor tiles, whose stages start on 1024-byte boundaries.
-template <int D, int G>
+template <int D, int G, View kView>
 constexpr int stage_bytes() {
-  return Split<G>::kMma ? (Geo<D, G>::kStageBytes + 1023) / 1024 * 1024 : Geo<D, G>::kStageBytes;
+  return Split<G, kView>::kMma ? (Geo<D, G>::kStageBytes + 1023) / 1024 * 1024 : Geo<D, G>::kStageBytes;
+}
+// A warp's p tile; the tensor-core path keeps two 256-byte P tiles there.
+template <int D, int G, View kView>
+constexpr int ptile_bytes() {
+  return Split<G, kView>::kMma && Geo<D, G>::kPTileBytes < 512 ? 512 : Geo<D, G>::kPTileBytes;
 }
 
 // Launch shape per (head_dim, group): warps per CTA and stages per warp's ring.  At
@@ -193,37 +201,48 @@ constexpr int stage_bytes() {
 #ifndef PKV_D64_STAGES
 #define PKV_D64_STAGES 4
 #endif
-template <int D, int G>
+template <int D, int G, View kView>
 struct Shape;
-template <int G>
-struct Shape<128, G> {
+template <int G, View kView>
+struct Shape<128, G, kView> {
 #ifdef PKV_D128_WARPS
   static constexpr int kWarps = PKV_D128_WARPS;
 #else
-  static constexpr int kWarps = G == 4 ? 4 : 8;
+  static constexpr int kWarps = G == 4 && !Split<G, kView>::kMma ? 4 : 8;
 #endif
 #ifdef PKV_D128_STAGES
   static constexpr int kStages = PKV_D128_STAGES;
 #else
-  static constexpr int kStages = G == 4 ? 3 : 2;
+  static constexpr int kStages = G == 4 && !Split<G, kView>::kMma ? 3 : 2;
 #endif
 };
 template <int G>
-struct Shape<64, G> {
+struct Shape<64, G, View::kAll> {
   static constexpr int kWarps = PKV_D64_WARPS;
   static constexpr int kStages = PKV_D64_STAGES;
+};
+#ifndef PKV_D64_VIEW_WARPS
+#define PKV_D64_VIEW_WARPS 8
+#endif
+#ifndef PKV_D64_VIEW_STAGES
+#define PKV_D64_VIEW_STAGES 2
+#endif
+template <int G, View kView>
+struct Shape<64, G, kView> {
+  static constexpr int kWarps = PKV_D64_VIEW_WARPS;
+  static constexpr int kStages = PKV_D64_VIEW_STAGES;
 };
 
 // Shared memory of one CTA: a ring and a p tile per warp, a barrier per stage (and, on
 // the tensor-core path, up to 1024 bytes to align the first stage).
-template <int D, int G, int NW, int S>
+template <int D, int G, int NW, int S, View kView>
 constexpr size_t ring_smem_bytes() {
-  return (Split<G>::kMma ? 1024 : 0) + size_t(NW) * S * stage_bytes<D, G>() + size_t(NW) * Geo<D, G>::kPTileBytes +
-         size_t(NW) * S * 8;
+  return (Split<G, kView>::kMma ? 1024 : 0) + size_t(NW) * S * stage_bytes<D, G, kView>() +
+         size_t(NW) * ptile_bytes<D, G, kView>() + size_t(NW) * S * 8;
 }
-template <int D, int G>
+template <int D, int G, View kView>
 constexpr size_t static_smem_bytes() {
-  return ring_smem_bytes<D, G, Shape<D, G>::kWarps, Shape<D, G>::kStages>();
+  return ring_smem_bytes<D, G, Shape<D, G, kView>::kWarps, Shape<D, G, kView>::kStages, kView>();
 }
 // Per sequence: its length, its block prefix and, in the tail view, its shared blocks.
 template <View kView>
@@ -232,12 +251,13 @@ constexpr size_t sequence_words(size_t num_seqs) {
 }
 template <int D, int G, View kView>
 size_t partition_smem_bytes(int num_seqs) {
-  return (static_smem_bytes<D, G>() + sequence_words<kView>(num_seqs) * 4 + 15) & ~size_t(15);
+  return (static_smem_bytes<D, G, kView>() + sequence_words<kView>(num_seqs) * 4 + 15) & ~size_t(15);
 }
 // Every instance fits the 227 KB a CTA may opt in to, with the largest batch's lengths and prefix.
 template <int D, int G>
 constexpr bool fits_largest_batch() {
-  return static_smem_bytes<D, G>() + sequence_words<View::kTail>(PKV_MAX_SEQS) * 4 + 16 <= 227u * 1024u;
+  return static_smem_bytes<D, G, View::kAll>() + sequence_words<View::kAll>(PKV_MAX_SEQS) * 4 + 16 <= 227u * 1024u &&
+         static_smem_bytes<D, G, View::kTail>() + sequence_words<View::kTail>(PKV_MAX_SEQS) * 4 + 16 <= 227u * 1024u;
 }
 static_assert(fits_largest_batch<64, 1>() && fits_largest_batch<64, 2>() && fits_largest_batch<64, 4>() &&
                   fits_largest_batch<64, 8>() && fits_largest_batch<128, 1>() && fits_largest_batch<128, 2>() &&
@@ -594,7 +614,7 @@ __device__ __forceinline__ uint4 rope_chunk(uint4 x, uint4 y, const float* cs_ro
 }
 
 // Tail view: leading blocks of sequence `row` that its group shares, 0 outside every group.
-__device__ __forceinline__ int shared_blocks_of_row(const DecodeParams& p, int row) {
+__device__ __forceinline__ int shared_blocks_of_row(const DecodeViewParams& p, int row) {
   int lo = 0, hi = p.num_groups;  // the last group that starts at or before the row
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -603,6 +623,13 @@ __device__ __forceinline__ int shared_blocks_of_row(const DecodeParams& p, int r
   }
   if (lo == 0 || row >= __ldg(p.group_start + lo)) return 0;
   return shared_prefix_blocks(__ldg(p.prefix_lens + lo - 1), p.max_blocks_per_seq);
+}
+
+// Window and tail views: pieces that a stream of `total` items is cut into, at least min_piece_blocks items each
+// while there are so many, so that a short stream leaves few states to merge.
+__device__ __forceinline__ int pieces_of(const DecodeViewParams& p, long long total) {
+  const long long most = (total + p.min_piece_blocks - 1) / p.min_piece_blocks;
+  return most < p.num_partitions ? static_cast<int>(most) : p.num_partitions;
 }
 
 // Walk of the flat (sequence, kv head, block) stream.
@@ -622,13 +649,14 @@ __device__ __forceinline__ void advance(Cursor& cur, const int* s_prefix, int nu
 
 template <int D, int G, int NW, int S, View kView>
 __global__ void __launch_bounds__(NW * 32)
-    paged_decode_partition_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap map_k,
+    paged_decode_partition_kernel(const ParamsOf<kView> p, const __grid_constant__ CUtensorMap map_k,
                                   const __grid_constant__ CUtensorMap map_v) {
   using T = Geo<D, G>;
-  constexpr bool kMma = Split<G>::kMma;  // q.K and p.V on the tensor cores
-  constexpr int kStage = stage_bytes<D, G>();
+  constexpr bool kMma = Split<G, kView>::kMma;  // q.K and p.V on the tensor cores
+  constexpr int kStage = stage_bytes<D, G, kView>();
+  constexpr int kPTile = ptile_bytes<D, G, kView>();
   static_assert(kMma || T::valid(), "unsupported (head_dim, group) geometry");
-  static_assert(!kMma || T::kPTileBytes >= 512, "the tensor-core path keeps two 256-byte P tiles per warp");
+  static_assert(!kMma || kPTile >= 512, "the tensor-core path keeps two 256-byte P tiles per warp");
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_wsum[32];
 
@@ -640,7 +668,7 @@ __global__ void __launch_bounds__(NW * 32)
     stages = smem + (((a + 1023u) & ~1023u) - a);
   }
   float2* ptiles = reinterpret_cast<float2*>(stages + size_t(NW) * S * kStage);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<unsigned char*>(ptiles) + NW * T::kPTileBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<unsigned char*>(ptiles) + NW * kPTile);
   int* s_prefix = reinterpret_cast<int*>(bars + NW * S);
   int* s_len = s_prefix + (B + 1);
   int* s_shared = s_len + B;  // tail view only
@@ -652,9 +680,13 @@ __global__ void __launch_bounds__(NW * 32)
   pdl_trigger();
   // The tail view runs beside the shared-prefix kernel launched just before it, whose output it
   // does not read: that kernel lets this one start only after its own wait, so everything earlier
-  // in the stream is complete here.  The wait moves to the end, so that the merge behind this
-  // kernel also finds the prefix states complete.
+  // in the stream is complete here.  Its first CTA waits for that kernel before it leaves, so that the
+  // join behind this kernel also finds the prefix states complete (a wait in every CTA would keep the
+  // SMs that the prefix kernel left free occupied instead of handing them to the next CTAs).
   if constexpr (kView != View::kTail) pdl_wait();
+  auto leave = [&] {
+    if (kView == View::kTail && blockIdx.x == 0) pdl_wait();
+  };
 
   // --- CTA prologue: clamp lengths, block prefix over sequences -------------
   if (tid == 0) s_prefix[0] = 0;
@@ -713,7 +745,7 @@ __global__ void __launch_bounds__(NW * 32)
   unsigned char* ring_ptr = stages + size_t(warp) * S * kStage;
   const uint32_t ring = smem_addr(ring_ptr);
   const uint32_t bar0 = smem_addr(bars + warp * S);
-  float2* ptile = ptiles + warp * (T::kPTileBytes / 8);
+  float2* ptile = ptiles + warp * (kPTile / 8);
   if (producer) {
 #pragma unroll
     for (int s = 0; s < S; ++s) mbar_init(bar0 + 8 * s, 1);
@@ -723,16 +755,15 @@ __global__ void __launch_bounds__(NW * 32)
 
   const long long total = static_cast<long long>(hkv) * s_prefix[B];
   const int gw = blockIdx.x * NW + warp;  // this warp's piece
-  if (gw >= p.num_partitions || total == 0) {
-    if constexpr (kView == View::kTail) pdl_wait();
+  int num_pieces = p.num_partitions;
+  if constexpr (kView != View::kAll) num_pieces = pieces_of(p, total);
+  if (gw >= num_pieces || total == 0) {
+    leave();
     return;
   }
-  const long long begin = gw * total / p.num_partitions;
-  const long long end = (gw + 1) * total / p.num_partitions;
-  if (begin == end) {
-    if constexpr (kView == View::kTail) pdl_wait();
-    return;
-  }
+  const long long begin = gw * total / num_pieces;
+  const long long end = (gw + 1) * total / num_pieces;
+  if (begin == end) return;  // (no piece of the other views is empty)
   const int n = static_cast<int>(end - begin);
 
   // Locate the first item: largest b with hkv * prefix[b] <= begin.
@@ -838,7 +869,7 @@ __global__ void __launch_bounds__(NW * 32)
       // Give up on this piece: flag it, let the copies already in flight land, leave.
       if (lane == 0) atomicOr(p.err, kErrTimeout);
       for (int x = i; x < n && x < i + S; ++x) mbar_wait(bar0 + 8 * (x % S), (x / S) & 1, kDrainTimeoutNs);
-      if constexpr (kView == View::kTail) pdl_wait();
+      leave();
       return;
     }
     const int seq_len = s_len[cc.b];
@@ -992,8 +1023,9 @@ __global__ void __launch_bounds__(NW * 32)
     // Where the pair's state goes: the piece's first or later slot, or in the tail view, where a pair
     // that lies whole in the piece is merged too, the pair's own slot.
     auto state_of = [&](bool whole_pair) -> float* {
-      if (kView == View::kTail && whole_pair)
-        return p.ws_whole + (static_cast<size_t>(cc.b) * hkv + cc.kvh) * T::kPieceFloats;
+      if constexpr (kView == View::kTail) {
+        if (whole_pair) return p.ws_whole + (static_cast<size_t>(cc.b) * hkv + cc.kvh) * T::kPieceFloats;
+      }
       return p.ws_pieces + (static_cast<size_t>(gw) * 2 + (first_pair ? 0 : 1)) * T::kPieceFloats;
     };
     if (last_of_pair && lane == 0) p.ws_pairs[2 * (static_cast<size_t>(cc.b) * hkv + cc.kvh) + 1] = gw;
@@ -1112,7 +1144,7 @@ __global__ void __launch_bounds__(NW * 32)
       phase ^= 1u;
     }
   }
-  if constexpr (kView == View::kTail) pdl_wait();
+  leave();
 }
 
 // ---------------------------------------------------------------------------
@@ -1120,6 +1152,9 @@ __global__ void __launch_bounds__(NW * 32)
 // write zeros for empty sequences.  One CTA per (sequence, kv head), one warp
 // per q head of the group.
 // ---------------------------------------------------------------------------
+#ifndef PKV_JOIN_FEW_PAIRS
+#define PKV_JOIN_FEW_PAIRS 304
+#endif
 #ifndef PKV_MERGE_AHEAD
 #define PKV_MERGE_AHEAD 8
 #endif
@@ -1149,7 +1184,6 @@ __global__ void __launch_bounds__(G * 32) paged_decode_merge_kernel(const Decode
   }
   const int wa = rec_a >> 1;
   if (wa == wb) return;  // whole pair in one piece: already written
-  if (wa < 0 || wa > wb || wb >= p.num_partitions) return;  // a piece timed out and recorded nothing (flagged)
   // With more pieces than items some pieces are empty and hold no state: only then are piece
   // bounds needed (piece w covers items [w N / P, (w + 1) N / P)).
   const long long total = static_cast<long long>(hkv) * total_blocks;
@@ -1211,12 +1245,136 @@ __global__ void __launch_bounds__(G * 32) paged_decode_merge_kernel(const Decode
 }
 
 // ---------------------------------------------------------------------------
+// Join of the window and tail views: one softmax over the states that a pair's pieces left and, in the tail
+// view, those of its shared prefix:
+//   out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s,  M = max_s m_s.
+// One CTA per (sequence, kv head).  A short stream can leave tens of states a pair: with few pairs kSlices
+// warps share a q head's states and combine through shared memory.  A warp fetches kAhead states before it
+// combines any, a lane D / 32 dims of each.
+// ---------------------------------------------------------------------------
+template <int D, int G, View kView, int kSlices>
+__global__ void __launch_bounds__(G * kSlices * 32) join_states_kernel(const DecodeViewParams p) {
+  constexpr int kPieceFloats = Geo<D, G>::kPieceFloats;
+  constexpr int kPer = D / 32;
+  constexpr int kAhead = 4;
+  __shared__ float2 s_ml[kSlices][G];
+  __shared__ float s_o[kSlices][G][D];
+  const int hkv = p.num_kv_heads;
+  const int b = blockIdx.x / hkv;
+  const int kvh = blockIdx.x - b * hkv;
+  const int warp = threadIdx.x >> 5;
+  const int g = warp % G, slice = warp / G;
+  const int lane = threadIdx.x & 31;
+  const size_t pair = blockIdx.x;
+  pdl_trigger();
+  pdl_wait();
+  // Everything that says where the states are, requested together.
+  const int len = min(p.context_lens[b], p.max_blocks_per_seq * kBlockTokens);
+  const int2 rec = *reinterpret_cast<const int2*>(p.ws_pairs + 2 * pair);
+  const long long total = static_cast<long long>(hkv) * p.ws_prefix[p.num_seqs];
+  int shared = 0;
+  int2 prefix = make_int2(0, 0);  // the prefix states' first row and count
+  if constexpr (kView == View::kTail) {
+    shared = p.ws_shared[b];
+    const int ok = *p.ws_plan_ok;
+    prefix = p.ws_records[pair];
+    if (!ok || shared == 0 || len <= 0) prefix.y = 0;
+  }
+  const bool has_pieces = len > shared * kBlockTokens;
+  int wa = rec.x >> 1;
+  int count = has_pieces ? rec.y - wa + 1 : 0;  // states that the partition left
+  // A piece that timed out recorded nothing (its error is flagged): read no states then.
+  if (has_pieces && (wa < 0 || count < 1 || rec.y >= pieces_of(p, total))) count = 0;
+  if (kView == View::kWindow && count == 1) return;  // the pair lies whole in one piece, which wrote it
+  const int states = prefix.y + count;
+
+  float M = -INFINITY, l = 0.f;
+  float acc[kPer];
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
+  for (int u0 = slice; u0 < states; u0 += kSlices * kAhead) {
+    float2 s[kAhead];
+    float a[kAhead][kPer];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int u = u0 + k * kSlices;
+      s[k] = make_float2(-INFINITY, 0.f);
+      if (u >= states) continue;
+      const float* o;
+      if (kView == View::kTail && u < prefix.y) {
+        const size_t row = static_cast<size_t>(prefix.x) + g + static_cast<size_t>(u) * 256;
+        o = p.ws_prefix_o + row * D;
+        s[k] = p.ws_prefix_ml[row];
+      } else {
+        const int w = wa + u - prefix.y;
+        const float* state = kView == View::kTail && count == 1
+                                 ? p.ws_whole + pair * kPieceFloats
+                                 : p.ws_pieces + (static_cast<size_t>(w) * 2 + (w == wa ? (rec.x & 1) : 0)) * kPieceFloats;
+        o = state + g * D;
+        s[k] = make_float2(state[G * D + g], state[G * D + G + g]);
+      }
+      o += lane * kPer;
+      if constexpr (kPer == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(o);
+        a[k][0] = v.x; a[k][1] = v.y; a[k][2] = v.z; a[k][3] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(o);
+        a[k][0] = v.x; a[k][1] = v.y;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (s[k].x == -INFINITY) continue;  // none, or one that saw no key
+      const float mn = fmaxf(M, s[k].x);
+      const float alpha = exp2f(M - mn), beta = exp2f(s[k].x - mn);
+      l = l * alpha + s[k].y * beta;
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) acc[x] = acc[x] * alpha + a[k][x] * beta;
+      M = mn;
+    }
+  }
+  if constexpr (kSlices > 1) {
+    if (states > 1) {  // uniform for the CTA
+      if (lane == 0) s_ml[slice][g] = make_float2(M, l);
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) s_o[slice][g][lane * kPer + x] = acc[x];
+      __syncthreads();
+      if (slice > 0) return;
+#pragma unroll
+      for (int k = 1; k < kSlices; ++k) {
+        const float2 s = s_ml[k][g];
+        if (s.x == -INFINITY) continue;
+        const float mn = fmaxf(M, s.x);
+        const float alpha = exp2f(M - mn), beta = exp2f(s.x - mn);
+        l = l * alpha + s.y * beta;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) acc[x] = acc[x] * alpha + s_o[k][g][lane * kPer + x] * beta;
+        M = mn;
+      }
+    }
+    if (slice > 0) return;
+  }
+  const float inv = l > 0.f ? 1.0f / l : 0.f;  // no token: zeros
+  __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) +
+                        (static_cast<size_t>(b) * p.num_q_heads + kvh * G + g) * D + lane * kPer;
+  if constexpr (kPer == 4) {
+    uint2 o;
+    o.x = float2_to_bf16x2(acc[0] * inv, acc[1] * inv);
+    o.y = float2_to_bf16x2(acc[2] * inv, acc[3] * inv);
+    *reinterpret_cast<uint2*>(orow) = o;
+  } else {
+    *reinterpret_cast<uint32_t*>(orow) = float2_to_bf16x2(acc[0] * inv, acc[1] * inv);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Host side: per-instance launch helpers.
 // ---------------------------------------------------------------------------
 template <int D, int G, View kView>
 struct Instance {
-  static constexpr int NW = Shape<D, G>::kWarps;
-  static constexpr int S = Shape<D, G>::kStages;
+  static constexpr int NW = Shape<D, G, kView>::kWarps;
+  static constexpr int S = Shape<D, G, kView>::kStages;
+  static constexpr int kManySlices = 16 / G;
   static constexpr auto kPartition = &paged_decode_partition_kernel<D, G, NW, S, kView>;
 
   static cudaError_t prepare(int dev) {
@@ -1243,23 +1401,35 @@ struct Instance {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if ((e = prepare(dev)) != cudaSuccess) return e;
+    // The answer goes by the shared memory, which goes by the number of sequences: the last one is kept per device.
+    static std::mutex mu;
+    static struct { size_t smem; int pieces; } last[64];
+    const size_t smem = partition_smem_bytes<D, G, kView>(num_seqs);
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 64 && last[dev].smem == smem) {
+      *pieces = last[dev].pieces;
+      return cudaSuccess;
+    }
     int sms = 0, per_sm = 0;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kPartition,
-                                                      NW * 32, partition_smem_bytes<D, G, kView>(num_seqs));
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kPartition, NW * 32, smem);
     if (e != cudaSuccess) return e;
     *pieces = sms * (per_sm > 0 ? per_sm : 1) * NW;
+    if (dev < 64) {
+      last[dev].smem = smem;
+      last[dev].pieces = *pieces;
+    }
     return cudaSuccess;
   }
 
-  static cudaError_t partition(const DecodeParams& p, cudaStream_t stream) {
+  static cudaError_t partition(const ParamsOf<kView>& p, cudaStream_t stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if ((e = prepare(dev)) != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>((p.num_partitions + NW - 1) / NW);
     CUtensorMap mk{}, mv{};
-    if constexpr (Split<G>::kMma) {  // the caches as swizzled tensor tiles
+    if constexpr (Split<G, kView>::kMma) {  // the caches as swizzled tensor tiles
       const int64_t rows = p.num_blocks * p.num_kv_heads * kBlockTokens;
       if (rows > INT32_MAX) return cudaErrorInvalidValue;  // tensor-copy row coordinates are 32-bit
       if ((e = encode_cache_map(&mk, p.k_cache, rows, D)) != cudaSuccess) return e;
@@ -1269,9 +1439,15 @@ struct Instance {
                       partition_smem_bytes<D, G, kView>(p.num_seqs), stream, p, mk, mv);
   }
 
-  static cudaError_t merge(const DecodeParams& p, cudaStream_t stream) {
+  static cudaError_t merge(const ParamsOf<kView>& p, cudaStream_t stream) {
     const unsigned grid = static_cast<unsigned>(p.num_seqs) * static_cast<unsigned>(p.num_kv_heads);
-    return launch_pdl(paged_decode_merge_kernel<D, G>, dim3(grid), dim3(G * 32), 0, stream, p);
+    if constexpr (kView == View::kAll)
+      return launch_pdl(paged_decode_merge_kernel<D, G>, dim3(grid), dim3(G * 32), 0, stream, p);
+    else if (grid > PKV_JOIN_FEW_PAIRS)
+      return launch_pdl(join_states_kernel<D, G, kView, 1>, dim3(grid), dim3(G * 32), 0, stream, p);
+    else
+      return launch_pdl(join_states_kernel<D, G, kView, kManySlices>, dim3(grid), dim3(G * kManySlices * 32), 0, stream,
+                        p);
   }
 };
 

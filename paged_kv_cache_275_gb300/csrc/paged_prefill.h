@@ -35,7 +35,8 @@ struct PrefillParams {
   const int32_t* group_start = nullptr;  // [num_groups + 1]
   const int32_t* prefix_lens = nullptr;  // [num_groups]
   int num_groups = 0;
-  int shared_ctas = 0;               // grid
+  int shared_ctas = 0;               // grid: whole waves of num_sms
+  int num_sms = 0;
   int2* ws_records = nullptr;        // [num_seqs][num_kv_heads]: (first row in ws, splits 256 rows apart)
   int32_t* ws_plan_ok = nullptr;     // whether group_start is in order (records are valid)
 };

@@ -80,6 +80,15 @@ constexpr int kTmemCols = 512;  // per tile t: S at [256 t, 256 t + 128), O at [
 __host__ __device__ constexpr int col_s(int t) { return 256 * t; }  // P (bf16 pairs) over the first 64 of S
 __host__ __device__ constexpr int col_o(int t) { return 256 * t + 128; }
 constexpr int kTmemSlotOffset = 384;  // in the 512-byte barrier area: barriers below, TMEM slot and sequence pick here
+#ifndef PKV_SHARED_CTA_US
+#define PKV_SHARED_CTA_US 7.f
+#endif
+#ifndef PKV_SHARED_STEP_US
+#define PKV_SHARED_STEP_US 1.9f
+#endif
+#ifndef PKV_SHARED_SM_RATE
+#define PKV_SHARED_SM_RATE 1e5f
+#endif
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;
 constexpr unsigned long long kWaitNs = 2000000000ull;
@@ -343,19 +352,29 @@ struct SharedJob {
   int tile, kv_head, split, num_splits;
 };
 
-// The work of group g is tile pairs x kv heads units of ceil(keys / 128) key steps each.  All groups' units
-// are cut into splits of at most s steps, with the least s that needs no more CTAs than the grid has (the
-// host sizes the grid at no less than one CTA a unit), so that the CTAs finish together whatever the
-// groups' sizes and lengths.  CTA numbers run over the groups, their tile pairs, kv heads and splits.
-// Every warp finds the CTA's job by itself, a group per lane at a time.  False: no job for this CTA.
-// group_start has to start at 0 or above, not fall, and end at num_seqs or below; otherwise no group is
-// used, which ws_plan_ok tells the merge.
-template <int G>
+// The work of group g is tile pairs x kv heads units of ceil(keys / 128) key steps each.  All groups' units are
+// cut into splits of at most s steps, so that the CTAs finish about together whatever the groups' sizes and
+// lengths (the host sizes the grid at no less than one CTA a unit, so some s always fits).  The tail's kernel runs
+// beside this one on the SMs that it leaves free, so s is not the least that fits but the one with the least
+// estimated time for both: few long splits give the tail more SMs, and the join fewer states.
+// CTA numbers run over the groups, their tile pairs, kv heads and splits.  One warp finds the CTA's job, a group or
+// a candidate s per lane.  False: no job for this CTA.  group_start has to start at 0 or above, not fall, and end at
+// num_seqs or below; otherwise no group is used, which ws_plan_ok tells the join.
+template <int D, int G>
 __device__ __forceinline__ bool find_shared_job(const PrefillParams& p, SharedJob& job) {
   constexpr int kCtaTokens = kTiles * kRows / G;
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31;
-  const bool reporter = blockIdx.x == 0 && threadIdx.x < 32;
+  const bool reporter = blockIdx.x == 0;
+  // The sequences' lengths, of at most 256 of them: about how much there is behind the shared blocks.
+  const int every = (p.num_seqs + 255) / 256;
+  int lens[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int b = (lane + 32 * i) * every;
+    lens[i] = b < p.num_seqs ? __ldg(p.context_lens + b) : 0;
+  }
+
   struct Group {
     int first, rows, keys;
     bool fine;
@@ -364,13 +383,11 @@ __device__ __forceinline__ bool find_shared_job(const PrefillParams& p, SharedJo
     Group x{0, 0, 0, true};
     if (g < p.num_groups) {
       const int a = __ldg(p.group_start + g), e = __ldg(p.group_start + g + 1);
+      const int len = __ldg(p.prefix_lens + g);
       x.fine = a >= 0 && a <= e && e <= p.num_seqs;
-      if (x.fine) {
+      if (x.fine && a < e) {  // an empty group's length says nothing
         x.first = a;
         x.rows = e - a;
-      }
-      if (x.rows > 0) {  // an empty group's length says nothing
-        const int len = __ldg(p.prefix_lens + g);
         x.keys = shared_prefix_blocks(len, p.max_blocks_per_seq) * kBlockTokens;
         if (reporter && len < 0) atomicOr(p.err, kErrLenNegative);
         if (reporter && len > p.max_blocks_per_seq * kBlockTokens) atomicOr(p.err, kErrLenTooLong);
@@ -382,46 +399,71 @@ __device__ __forceinline__ bool find_shared_job(const PrefillParams& p, SharedJo
   auto steps = [&](const Group& x) { return (x.keys + kKeys - 1) / kKeys; };
 
   const Group mine = group(lane);  // the first 32 groups stay in registers
-  bool fine = true;
-  int most = 1;  // the longest unit's steps
+  float tokens = 0.f;              // behind the shared blocks, over all sequences
+#pragma unroll
+  for (int i = 0; i < 8; ++i) tokens += max(0, lens[i]);
+  tokens *= every;
+  bool fine = true, two_tiles = false;
+  int most = 1;   // the longest unit's steps
+  float work = 0.f;  // unit steps
   for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
     const Group x = g0 == 0 ? mine : group(g0 + lane);
     fine = fine && x.fine;
     most = max(most, steps(x));
+    work += static_cast<float>(units(x)) * static_cast<float>(steps(x));
+    two_tiles = two_tiles || x.rows * G > kRows;
+    tokens -= static_cast<float>(x.rows) * static_cast<float>(x.keys);
   }
   fine = __all_sync(kAll, fine);
+  two_tiles = __any_sync(kAll, two_tiles);
   most = __reduce_max_sync(kAll, most);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    work += __shfl_xor_sync(kAll, work, off);
+    tokens += __shfl_xor_sync(kAll, tokens, off);
+  }
   if (reporter && lane == 0) {
     *p.ws_plan_ok = fine;
     if (!fine) atomicOr(p.err, kErrLenTooLong);
   }
-  if (!fine) return false;
-  auto ctas = [&](int s) -> int {  // CTAs that splits of at most s steps need
-    int n = 0;
-    for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
-      const Group x = g0 == 0 ? mine : group(g0 + lane);
-      n += units(x) * ((steps(x) + s - 1) / s);
-    }
-    return __reduce_add_sync(kAll, n);
-  };
-  int lo = 1, hi = most;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (ctas(mid) <= static_cast<int>(gridDim.x)) hi = mid;
-    else lo = mid + 1;
+  if (!fine || work == 0.f) return false;
+
+  // Candidate s of the lane: from the least that could fit on, an eighth of it apart; the last is the longest unit.
+  const int least_s = max(1, static_cast<int>(work / gridDim.x));
+  const int s = lane == 31 ? most : min(most, least_s + lane * ((least_s + 7) / 8));
+  int n = 0;  // its CTAs
+  for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
+    const Group x = g0 == 0 ? mine : group(g0 + lane);
+    const int u = units(x), t = steps(x);
+    for (int k = 0; k < min(32, p.num_groups - g0); ++k)
+      n += __shfl_sync(kAll, u, k) * ((__shfl_sync(kAll, t, k) + s - 1) / s);
   }
+  // Microseconds: a CTA costs kCtaUs and a step of two tiles (or one) kStepUs; an SM streams the tail at kSmRate
+  // bytes a microsecond, all of them together at kAllRate.
+  constexpr float kCtaUs = PKV_SHARED_CTA_US, kSmRate = PKV_SHARED_SM_RATE, kAllRate = 6.4e6f;
+  const float tail = fmaxf(tokens, 0.f) * (4.f * D) * p.num_kv_heads;
+  const int waves = (n + p.num_sms - 1) / p.num_sms;
+  const float us = waves * (kCtaUs + s * (two_tiles ? PKV_SHARED_STEP_US : 1.2f));
+  const float beside = fminf(max(p.num_sms - n, 0) * kSmRate, kAllRate) * us;
+  float cost = us + fmaxf(tail - beside, 0.f) * (1.f / kAllRate);
+  if (n > static_cast<int>(gridDim.x)) cost = INFINITY;  // does not fit
+  float best = cost;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) best = fminf(best, __shfl_xor_sync(kAll, best, off));
+  const int split_steps = __shfl_sync(kAll, s, __ffs(__ballot_sync(kAll, cost == best)) - 1);
+
   int base = 0;  // CTAs of the groups before g0
   for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
     const Group x = g0 == 0 ? mine : group(g0 + lane);
-    const int splits = (steps(x) + lo - 1) / lo, n = units(x) * splits;
-    int end = n;
+    const int splits = (steps(x) + split_steps - 1) / split_steps, count = units(x) * splits;
+    int end = count;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int y = __shfl_up_sync(kAll, end, off);
       if (lane >= off) end += y;
     }
-    const int at = static_cast<int>(blockIdx.x) - base - (end - n);  // this CTA's place in the lane's group
-    const unsigned owner = __ballot_sync(kAll, at >= 0 && at < n);
+    const int at = static_cast<int>(blockIdx.x) - base - (end - count);  // this CTA's place in the lane's group
+    const unsigned owner = __ballot_sync(kAll, at >= 0 && at < count);
     if (owner) {
       const int src = __ffs(owner) - 1;
       job.first_row = __shfl_sync(kAll, x.first, src);
@@ -483,8 +525,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   int b = zrank;
   int q0, C, L;
   if constexpr (kMask == Mask::kShared) {
-    SharedJob job;
-    if (!find_shared_job<G>(p, job)) return;  // uniform for the CTA
+    SharedJob& job = *reinterpret_cast<SharedJob*>(smem + T::kOffBar + kTmemSlotOffset + 16);
+    if (warp == 0) {
+      SharedJob mine{};
+      if (!find_shared_job<D, G>(p, mine)) mine.num_splits = 0;
+      if (lane == 0) job = mine;
+    }
+    __syncthreads();
+    if (job.num_splits == 0) return;  // uniform for the CTA
     b = job.first_row;
     q0 = job.first_row;
     C = job.rows;

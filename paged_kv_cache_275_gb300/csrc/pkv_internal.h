@@ -63,6 +63,11 @@ struct DecodeParams {
   const void* v_new;     // bf16 [num_seqs][num_kv_heads][head_dim]
   const float* cos_sin;  // fp32 [max_position][head_dim] (cos | sin) or null: no RoPE
   int64_t max_position;
+};
+
+// What the views of a sequence other than the whole of it need besides.
+struct DecodeViewParams : DecodeParams {
+  int min_piece_blocks;  // window and tail views: the least blocks a piece is cut to
   // Window view: a sequence's last `window` tokens and its first `sinks` (both at most 16 * max_blocks_per_seq).
   int window;
   int sinks;
@@ -105,6 +110,7 @@ struct RopeAppendParams {
   int num_q_heads;
   int num_kv_heads;
   int num_axes;
+  int parts;  // warps that share a token's rows
   uint8_t freq_axis[64];  // position axis of each of the head_dim / 2 frequencies
 };
 
@@ -162,9 +168,9 @@ cudaError_t launch_decode_partition(const DecodeParams& p, int head_dim, int gro
 cudaError_t launch_decode_merge(const DecodeParams& p, int head_dim, int group, cudaStream_t stream);
 // The same over a window and sinks (window_decode.cu) and over what follows shared prefixes (prefix_decode.cu).
 cudaError_t resident_window_pieces(int head_dim, int group, int num_seqs, int* pieces);
-cudaError_t launch_window_decode(const DecodeParams& p, int head_dim, int group, cudaStream_t stream);
+cudaError_t launch_window_decode(const DecodeViewParams& p, int head_dim, int group, cudaStream_t stream);
 cudaError_t resident_tail_pieces(int head_dim, int group, int num_seqs, int* pieces);
-cudaError_t launch_tail_partition(const DecodeParams& p, int head_dim, int group, cudaStream_t stream);
-cudaError_t launch_prefix_merge(const DecodeParams& p, int head_dim, int group, cudaStream_t stream);
+cudaError_t launch_tail_partition(const DecodeViewParams& p, int head_dim, int group, cudaStream_t stream);
+cudaError_t launch_prefix_merge(const DecodeViewParams& p, int head_dim, int group, cudaStream_t stream);
 
 }  // namespace pkv

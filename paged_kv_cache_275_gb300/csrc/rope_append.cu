@@ -17,7 +17,16 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 256;
+#ifndef PKV_ROPE_THREADS
+#define PKV_ROPE_THREADS 128
+#endif
+#ifndef PKV_ROPE_AHEAD
+#define PKV_ROPE_AHEAD 2
+#endif
+constexpr int kThreads = PKV_ROPE_THREADS;
+#ifndef PKV_ROPE_CTAS
+#define PKV_ROPE_CTAS 8
+#endif
 
 __device__ __forceinline__ uint4 load_once(const uint4* p) {
   uint4 r;
@@ -55,54 +64,92 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendP
   constexpr int kLanes = D / 16;          // lanes of a row
   constexpr int kRowsAtOnce = 32 / kLanes;
   constexpr int kChunks = D / 8;          // 16-byte chunks of a row
+  constexpr int kAhead = PKV_ROPE_AHEAD;  // rows of a lane in flight
   const int lane = threadIdx.x & 31;
   const int c = lane % kLanes, sub = lane / kLanes;
   const int rows = p.num_q_heads + 2 * p.num_kv_heads;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); t < p.num_tokens; t += warps) {
+  const int64_t items = p.num_tokens * p.parts;  // a token's rows in `parts` parts
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); item < items;
+       item += warps) {
+    const int64_t t = item / p.parts;
+    const int part = static_cast<int>(item - t * p.parts);
+    const int first = part * kRowsAtOnce + sub, step = p.parts * kRowsAtOnce;
+    uint4 a[kAhead], b[kAhead];
+    auto fetch = [&](int r0) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int r = r0 + k * step;
+        if (r >= rows) continue;
+        const int kr = r - p.num_q_heads, vr = kr - p.num_kv_heads;
+        const uint4* src = kr < 0 ? static_cast<const uint4*>(p.q) + t * p.q_stride + r * kChunks
+                           : vr < 0 ? static_cast<const uint4*>(p.k) + t * p.k_stride + kr * kChunks
+                                    : static_cast<const uint4*>(p.v) + t * p.v_stride + vr * kChunks;
+        a[k] = load_once(src + c);
+        b[k] = load_once(src + c + kLanes);
+      }
+    };
+    // The first rows are on their way while the position and then its table row are looked up.
+    fetch(first);
     const int64_t slot = p.slot_mapping[t];
     if (slot < 0) continue;  // padding
     const bool stored = slot < p.num_slots;
-    if (!stored && lane == 0) atomicOr(p.err, kErrSlot);
-    float cs[8], sn[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int f = 8 * c + e;
-      int64_t pos = p.positions[p.freq_axis[f] * p.axis_stride + t];
+    if (!stored && lane == 0 && part == 0) atomicOr(p.err, kErrSlot);
+    auto row_of = [&](int axis) -> const float* {
+      int64_t pos = p.positions[axis * p.axis_stride + t];
       if (pos < 0 || pos >= p.max_position) {
         atomicOr(p.err, kErrPosition);
         pos = pos < 0 ? 0 : p.max_position - 1;
       }
-      cs[e] = __ldg(p.cos_sin + pos * D + f);
-      sn[e] = __ldg(p.cos_sin + pos * D + D / 2 + f);
+      return p.cos_sin + pos * D;
+    };
+    float cs[8], sn[8];
+    if (p.num_axes == 1) {
+      const float4* row = reinterpret_cast<const float4*>(row_of(0)) + 2 * c;
+      const float4 c0 = __ldg(row), c1 = __ldg(row + 1), s0 = __ldg(row + D / 8), s1 = __ldg(row + D / 8 + 1);
+      cs[0] = c0.x; cs[1] = c0.y; cs[2] = c0.z; cs[3] = c0.w; cs[4] = c1.x; cs[5] = c1.y; cs[6] = c1.z; cs[7] = c1.w;
+      sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w; sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int f = 8 * c + e;
+        const float* row = row_of(p.freq_axis[f]);
+        cs[e] = __ldg(row + f);
+        sn[e] = __ldg(row + D / 2 + f);
+      }
     }
-    for (int r = sub; r < rows; r += kRowsAtOnce) {
-      const bool is_q = r < p.num_q_heads;
-      const int head = is_q ? r : (r - p.num_q_heads) % p.num_kv_heads;
-      const bool is_v = r >= p.num_q_heads + p.num_kv_heads;
-      if (!is_q && !stored) continue;
-      const uint4* src = is_q ? static_cast<const uint4*>(p.q) + t * p.q_stride
-                              : is_v ? static_cast<const uint4*>(p.v) + t * p.v_stride
-                                     : static_cast<const uint4*>(p.k) + t * p.k_stride;
-      uint4* dst = is_q ? static_cast<uint4*>(p.q_out) + t * p.q_out_stride + static_cast<int64_t>(head) * kChunks
-                        : static_cast<uint4*>(is_v ? p.v_cache : p.k_cache) +
-                              (((slot / kBlockTokens) * p.num_kv_heads + head) * kBlockTokens + slot % kBlockTokens) *
-                                  kChunks;
-      uint4 a = load_once(src + head * kChunks + c);
-      uint4 b = load_once(src + head * kChunks + c + kLanes);
-      if (!is_v) rotate(a, b, cs, sn);
-      dst[c] = a;
-      dst[c + kLanes] = b;
+    const int64_t cache_row = (slot / kBlockTokens) * p.num_kv_heads * kBlockTokens + slot % kBlockTokens;
+    for (int r0 = first; r0 < rows; r0 += kAhead * step) {
+      if (r0 != first) fetch(r0);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int r = r0 + k * step;
+        if (r >= rows) continue;
+        const int kr = r - p.num_q_heads, vr = kr - p.num_kv_heads;
+        if (vr < 0) rotate(a[k], b[k], cs, sn);
+        if (kr >= 0 && !stored) continue;
+        uint4* dst = kr < 0 ? static_cast<uint4*>(p.q_out) + t * p.q_out_stride + static_cast<int64_t>(r) * kChunks
+                            : static_cast<uint4*>(vr < 0 ? p.k_cache : p.v_cache) +
+                                  (cache_row + static_cast<int64_t>(vr < 0 ? kr : vr) * kBlockTokens) * kChunks;
+        dst[c] = a[k];
+        dst[c + kLanes] = b[k];
+      }
     }
   }
 }
 
 template <int D>
 cudaError_t launch(const RopeAppendParams& p, int num_sms, cudaStream_t stream) {
-  int64_t blocks = (p.num_tokens + kThreads / 32 - 1) / (kThreads / 32);
-  const int64_t cap = static_cast<int64_t>(num_sms) * 8;
+  constexpr int kRowsAtOnce = 512 / D;
+  const int rounds = (p.num_q_heads + 2 * p.num_kv_heads + kRowsAtOnce - 1) / kRowsAtOnce;
+  const int64_t cap = static_cast<int64_t>(num_sms) * PKV_ROPE_CTAS * (256 / kThreads);
+  // Few tokens: a token's rows over several warps, as long as that leaves one CTA per SM at most.
+  RopeAppendParams q = p;
+  const int64_t parts = num_sms * static_cast<int64_t>(kThreads / 32) / p.num_tokens;
+  q.parts = static_cast<int>(parts < 1 ? 1 : parts > rounds ? rounds : parts);
+  int64_t blocks = (p.num_tokens * q.parts + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > cap) blocks = cap;
-  return launch_pdl(rope_append_kernel<D>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, p);
+  return launch_pdl(rope_append_kernel<D>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, q);
 }
 
 }  // namespace

@@ -11,7 +11,7 @@ cudaError_t resident_window_pieces(int head_dim, int group, int num_seqs, int* p
                                  [&](auto inst) { return decltype(inst)::resident_pieces(num_seqs, pieces); });
 }
 
-cudaError_t launch_window_decode(const DecodeParams& p, int head_dim, int group, cudaStream_t stream) {
+cudaError_t launch_window_decode(const DecodeViewParams& p, int head_dim, int group, cudaStream_t stream) {
   return dispatch<View::kWindow>(head_dim, group, [&](auto inst) {
     const cudaError_t e = decltype(inst)::partition(p, stream);
     return e != cudaSuccess ? e : decltype(inst)::merge(p, stream);
