@@ -58,9 +58,9 @@ L2_BYTES = 126 * 2 ** 20
 
 
 KERNEL_SOURCES = {
-    "paged_decode_partition_kernel": ("paged_kv_cache_275_gb300/csrc/paged_decode.cu",
+    "paged_decode_partition_kernel": ("paged_kv_cache_275_gb300/csrc/paged_decode_kernel.cuh",
                                       "paged_kv_cache_275_gb300/csrc/pkv_internal.h"),
-    "paged_prefill_kernel": ("paged_kv_cache_275_gb300/csrc/paged_prefill.cu",
+    "paged_prefill_kernel": ("paged_kv_cache_275_gb300/csrc/paged_prefill_kernel.cuh",
                              "paged_kv_cache_275_gb300/csrc/paged_prefill.h",
                              "paged_kv_cache_275_gb300/csrc/pkv_internal.h"),
     "kv_append_kernel": ("paged_kv_cache_275_gb300/csrc/kv_append.cu",

@@ -15,8 +15,10 @@
 
 #include "pagedkv.h"
 #include "copy_blocks.h"
+#include "decode_views.h"
 #include "paged_prefill.h"
 #include "pkv_internal.h"
+#include "rope_append.h"
 
 // Sticky device error word; one instance per device (module-scope __device__).
 static __device__ unsigned int g_pkv_device_error;
@@ -123,12 +125,16 @@ Window within_table(Window w, int32_t max_blocks_per_seq) {
   if (w.sinks > cap) w.sinks = cap;
   return w;
 }
-#ifndef PKV_MIN_PIECE_BLOCKS
-#define PKV_MIN_PIECE_BLOCKS 2
-#endif
-#ifndef PKV_TAIL_WAVES
-#define PKV_TAIL_WAVES 1
-#endif
+// Window and tail streams are cut into pieces of no less than this many blocks: a piece is a state to join, and a block
+// more a piece is a block's time (one sequence, window 1024, two heads: 9.3 us a call with 2, 9.4 with 1, 11.7 with 4,
+// 16.2 with 8).
+constexpr int32_t kMinPieceBlocks = 2;
+// Pieces a warp of the tail view, which runs beside the prefix kernel on the SMs that are free at the time: 128 sequences
+// behind one prefix 53.9 us with 2, 57.7 with 1, 58.3 with 3; 150 behind five 73.4, 71.6, 77.7.
+constexpr int32_t kTailWaves = 2;
+// Least key steps of a split of a windowed prefill (one chunk of 512, window 1024: 19.4 us with 1 to 3, 20.2 with 4,
+// 21.6 with 5).
+constexpr int32_t kMinSplitSteps = 2;
 // Blocks of one sequence that a query token can see.
 int32_t visible_blocks(Window w, int32_t max_blocks_per_seq) {
   if (w.window == 0) return max_blocks_per_seq;
@@ -146,7 +152,7 @@ pkv_status default_partitions(int32_t num_seqs, int32_t num_kv_heads, int32_t he
   if (e != cudaSuccess) return cuda_fail(e, "occupancy query");
   // Never more pieces than the block stream can have items.
   int64_t bound = static_cast<int64_t>(num_seqs) * num_kv_heads * visible_blocks(window, max_blocks_per_seq);
-  if (window.window) bound = (bound + PKV_MIN_PIECE_BLOCKS - 1) / PKV_MIN_PIECE_BLOCKS;
+  if (window.window) bound = (bound + kMinPieceBlocks - 1) / kMinPieceBlocks;
   int64_t n = pieces;
   if (n > bound) n = bound;
   if (n > kMaxPartitions) n = kMaxPartitions;
@@ -273,7 +279,7 @@ static pkv_status decode_impl(const void* q, const void* k_cache, const void* v_
       static_cast<pkv::DecodeParams&>(v) = p;
       v.window = w.window;
       v.sinks = w.sinks;
-      v.min_piece_blocks = num_partitions == 0 ? PKV_MIN_PIECE_BLOCKS : 1;
+      v.min_piece_blocks = num_partitions == 0 ? kMinPieceBlocks : 1;
       const cudaError_t e = pkv::launch_window_decode(v, head_dim, group, s);
       if (e != cudaSuccess) return cuda_fail(e, "window decode launch");
       g_launches.fetch_add(2);
@@ -710,7 +716,7 @@ pkv_status pkv_window_prefill_default_splits(int32_t num_seqs, int32_t max_query
   int32_t n = one_wave_splits(num_seqs, max_query_len, num_q_heads, num_kv_heads, sms);
   // At least two key steps a split: a CTA's rows see at most its tokens' windows and the sinks.
   const int64_t keys = static_cast<int64_t>(window) + num_sink_tokens + pkv::prefill_cta_tokens(num_q_heads / num_kv_heads);
-  const int64_t most = (keys + 255) / 256;
+  const int64_t most = (keys + 128 * kMinSplitSteps - 1) / (128 * kMinSplitSteps);
   if (n > most) n = static_cast<int32_t>(most);
   *num_splits = n;
   return ok();
@@ -760,11 +766,11 @@ pkv_status plan_prefix_decode(int32_t num_seqs, int32_t num_q_heads, int32_t num
   int pieces = 0;
   const cudaError_t e = pkv::resident_tail_pieces(head_dim, group, num_seqs, &pieces);
   if (e != cudaSuccess) return cuda_fail(e, "occupancy query");
-  const int64_t bound = (static_cast<int64_t>(num_seqs) * num_kv_heads * max_blocks_per_seq + PKV_MIN_PIECE_BLOCKS - 1) /
-                        PKV_MIN_PIECE_BLOCKS;
+  const int64_t bound = (static_cast<int64_t>(num_seqs) * num_kv_heads * max_blocks_per_seq + kMinPieceBlocks - 1) /
+                        kMinPieceBlocks;
   plan->ctas = static_cast<int32_t>(ctas);
   plan->sms = sms;
-  pieces *= PKV_TAIL_WAVES;
+  pieces *= kTailWaves;
   plan->parts = pieces < bound ? pieces : static_cast<int32_t>(bound < 1 ? 1 : bound);
   const size_t state = static_cast<size_t>(pkv::piece_floats(head_dim, group)) * sizeof(float);
   const size_t pair_count = static_cast<size_t>(num_seqs) * num_kv_heads;
@@ -885,7 +891,7 @@ pkv_status pkv_paged_prefix_decode_attention(const void* q, const void* k_cache,
   p.num_kv_heads = num_kv_heads;
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.num_partitions = plan.parts;
-  p.min_piece_blocks = PKV_MIN_PIECE_BLOCKS;
+  p.min_piece_blocks = kMinPieceBlocks;
   p.qscale = scale * 1.4426950408889634f;
   p.group_start = group_start;
   p.prefix_lens = prefix_lens;
@@ -897,7 +903,7 @@ pkv_status pkv_paged_prefix_decode_attention(const void* q, const void* k_cache,
   p.ws_prefix_o = f.ws;
   p.ws_prefix_ml = reinterpret_cast<const float2*>(f.ws + static_cast<size_t>(plan.ctas) * 256 * head_dim);
   if ((e = pkv::launch_tail_partition(p, head_dim, group, s)) != cudaSuccess) return cuda_fail(e, "tail partition launch");
-  if ((e = pkv::launch_prefix_merge(p, head_dim, group, s)) != cudaSuccess) return cuda_fail(e, "prefix merge launch");
+  if ((e = pkv::launch_prefix_join(p, head_dim, group, s)) != cudaSuccess) return cuda_fail(e, "prefix join launch");
   g_launches.fetch_add(3);
   return ok();
 }

@@ -53,7 +53,7 @@
 #include <type_traits>
 
 #include "pagedkv.h"
-#include "pkv_internal.h"
+#include "decode_views.h"
 
 namespace pkv {
 namespace {
@@ -171,6 +171,11 @@ struct Geo {
 #endif
 static_assert(PKV_MMA_MIN_G == 4 || PKV_MMA_MIN_G == 8,
               "groups of eight always take the tensor cores; four may (their p tile holds the two 256-byte P tiles)");
+// The window and tail views take them for every group, the columns past it zero: a tail shares the GPU with the
+// shared prefix's kernel, where it is an SM's own speed that counts, and 64-dim heads and four heads gain alone
+// (prefix of 4096, tails of 16..1024 tokens, 64 sequences of 8 kv heads, D 128, us a call with the CUDA cores and with
+// these: one head 32.5, 31.5; two 34.2, 32.4; four 44.7, 36.5; window of 4096 at four heads 141.6, 132.4, at one and two
+// 128.4, 129.4 and 129.1, 131.0; at D 64 one head 80.8, 69.8, four 108.8, 72.0).
 template <int G, View kView>
 struct Split {
   static constexpr bool kMma = kView != View::kAll || G >= PKV_MMA_MIN_G;
@@ -203,6 +208,14 @@ constexpr int ptile_bytes() {
 #endif
 template <int D, int G, View kView>
 struct Shape;
+// The tail view's CTAs come and go beside the prefix kernel's, so small ones pack better: 128 sequences behind 8192
+// tokens take 53.9 us a call with 4 warps, 54.9 with 2, 55.9 with 1, 60.8 with 8 (all with the partition count of two
+// waves; 56.8 with 8 in one wave).
+template <int G>
+struct Shape<128, G, View::kTail> {
+  static constexpr int kWarps = 4;
+  static constexpr int kStages = 2;
+};
 template <int G, View kView>
 struct Shape<128, G, kView> {
 #ifdef PKV_D128_WARPS
@@ -221,16 +234,12 @@ struct Shape<64, G, View::kAll> {
   static constexpr int kWarps = PKV_D64_WARPS;
   static constexpr int kStages = PKV_D64_STAGES;
 };
-#ifndef PKV_D64_VIEW_WARPS
-#define PKV_D64_VIEW_WARPS 8
-#endif
-#ifndef PKV_D64_VIEW_STAGES
-#define PKV_D64_VIEW_STAGES 2
-#endif
+// Blocks of 64 dims are small: warps in flight count more than stages (61 sequences with a window of 4095, eight heads:
+// 47.0 us with 8 warps of 2 stages, 57.6 with 8 x 4, 56.5 with 4 x 4, 57.0 with 8 x 3, 46.9 with 16 x 2, 50.5 with 12 x 2).
 template <int G, View kView>
 struct Shape<64, G, kView> {
-  static constexpr int kWarps = PKV_D64_VIEW_WARPS;
-  static constexpr int kStages = PKV_D64_VIEW_STAGES;
+  static constexpr int kWarps = 8;
+  static constexpr int kStages = 2;
 };
 
 // Shared memory of one CTA: a ring and a p tile per warp, a barrier per stage (and, on
@@ -361,12 +370,12 @@ __device__ __forceinline__ uint32_t float2_to_bf16x2(float lo, float hi) {
 // ---------------------------------------------------------------------------
 // One 16-token block: scores, online-softmax update, p.V accumulation.
 // ---------------------------------------------------------------------------
-template <int D, int G, bool kMasked, class Sees>
+template <int D, int G, bool kMasked>
 __device__ __forceinline__ void process_block(const unsigned char* sK, const unsigned char* sV, float2* ptile, const float2 (&q)[G][4],
                                               float2 (&acc)[G][4], float (&m_ref)[G],
                                               float (&m_mine)[Geo<D, G>::kFinal],
                                               float (&l_mine)[Geo<D, G>::kFinal], int c, int half, int mask,
-                                              const Sees& sees) {
+                                              int valid) {
   using T = Geo<D, G>;
   constexpr int kFinal = T::kFinal;
   const int mj = mask / G;  // token-step part of the swizzle
@@ -407,7 +416,7 @@ __device__ __forceinline__ void process_block(const unsigned char* sK, const uns
     const int item = mask + k;
     tok_of[k] = T::kTokensPerStep * (item / G) + half;
     s[k] = part[k];
-    if (kMasked) s[k] = sees(tok_of[k]) ? s[k] : -INFINITY;
+    if (kMasked) s[k] = tok_of[k] < valid ? s[k] : -INFINITY;
   }
   // The running max of a head is raised only when some score of the block beats it by more
   // than the slack; one vote decides, and the per-head block max is formed only then.
@@ -455,7 +464,7 @@ __device__ __forceinline__ void process_block(const unsigned char* sK, const uns
   for (int j = 0; j < T::kSteps; ++j) {
     const int tok = T::kTokensPerStep * j + half;
     uint4 w = lds128(sV + tok * kRowBytes + c * 16);
-    if (kMasked && !sees(tok)) w = make_uint4(0u, 0u, 0u, 0u);  // never multiply a stale row
+    if (kMasked && tok >= valid) w = make_uint4(0u, 0u, 0u, 0u);  // never multiply a stale row
     const float2 v0 = bf16x2_to_float2(w.x), v1 = bf16x2_to_float2(w.y);
     const float2 v2 = bf16x2_to_float2(w.z), v3 = bf16x2_to_float2(w.w);
     const float2* pp = ptile + tok * G;
@@ -763,7 +772,10 @@ __global__ void __launch_bounds__(NW * 32)
   }
   const long long begin = gw * total / num_pieces;
   const long long end = (gw + 1) * total / num_pieces;
-  if (begin == end) return;  // (no piece of the other views is empty)
+  if (begin >= end) {
+    leave();
+    return;
+  }
   const int n = static_cast<int>(end - begin);
 
   // Locate the first item: largest b with hkv * prefix[b] <= begin.
@@ -982,17 +994,17 @@ __global__ void __launch_bounds__(NW * 32)
       }
       __syncwarp();
     }
-    typename SeesOf<kView>::type sees;
-    sees.end = valid;
-    bool whole = valid >= kBlockTokens;  // every row of the block is seen
-    if constexpr (kView == View::kWindow) {
-      sees.first = valid - p.window;
-      sees.sinks = p.sinks - col * kBlockTokens;
-      whole = whole && (sees.first <= 0 || sees.sinks >= kBlockTokens);
-    }
     if constexpr (kMma) {
       const uint32_t sk = ring + stage * kStage;
       unsigned char* sv_ptr = ring_ptr + stage * kStage + T::kTileBytes;
+      typename SeesOf<kView>::type sees;
+      sees.end = valid;
+      bool whole = valid >= kBlockTokens;  // every row of the block is seen
+      if constexpr (kView == View::kWindow) {
+        sees.first = valid - p.window;
+        sees.sinks = p.sinks - col * kBlockTokens;
+        whole = whole && (sees.first <= 0 || sees.sinks >= kBlockTokens);
+      }
       if (whole)
         process_block_mma<D, false>(sk, sv_ptr, sk + T::kTileBytes, smem_addr(ptile), qf, o_t, m2, l2, qscale, lane,
                                     sees);
@@ -1000,12 +1012,12 @@ __global__ void __launch_bounds__(NW * 32)
         process_block_mma<D, true>(sk, sv_ptr, sk + T::kTileBytes, smem_addr(ptile), qf, o_t, m2, l2, qscale, lane,
                                    sees);
     } else {
-      if (whole)
+      if (valid >= kBlockTokens)
         process_block<D, G, false>(st_ptr, st_ptr + T::kTileBytes, ptile, q, acc, m_ref, m_mine, l_mine, c, half,
-                                    mask, sees);
+                                    mask, kBlockTokens);
       else
         process_block<D, G, true>(st_ptr, st_ptr + T::kTileBytes, ptile, q, acc, m_ref, m_mine, l_mine, c, half,
-                                   mask, sees);
+                                   mask, valid);
     }
     __syncwarp();
 
@@ -1152,9 +1164,6 @@ __global__ void __launch_bounds__(NW * 32)
 // write zeros for empty sequences.  One CTA per (sequence, kv head), one warp
 // per q head of the group.
 // ---------------------------------------------------------------------------
-#ifndef PKV_JOIN_FEW_PAIRS
-#define PKV_JOIN_FEW_PAIRS 304
-#endif
 #ifndef PKV_MERGE_AHEAD
 #define PKV_MERGE_AHEAD 8
 #endif
@@ -1256,7 +1265,7 @@ template <int D, int G, View kView, int kSlices>
 __global__ void __launch_bounds__(G * kSlices * 32) join_states_kernel(const DecodeViewParams p) {
   constexpr int kPieceFloats = Geo<D, G>::kPieceFloats;
   constexpr int kPer = D / 32;
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 4;  // (150 sequences of eight heads behind prefixes: 73.4 us a call; with 2 76.6, with 8 77.2)
   __shared__ float2 s_ml[kSlices][G];
   __shared__ float s_o[kSlices][G][D];
   const int hkv = p.num_kv_heads;
@@ -1324,7 +1333,7 @@ __global__ void __launch_bounds__(G * kSlices * 32) join_states_kernel(const Dec
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      if (s[k].x == -INFINITY) continue;  // none, or one that saw no key
+      if (s[k].x == -INFINITY && s[k].y == 0.f) continue;  // none, or one that saw no key
       const float mn = fmaxf(M, s[k].x);
       const float alpha = exp2f(M - mn), beta = exp2f(s[k].x - mn);
       l = l * alpha + s[k].y * beta;
@@ -1343,7 +1352,7 @@ __global__ void __launch_bounds__(G * kSlices * 32) join_states_kernel(const Dec
 #pragma unroll
       for (int k = 1; k < kSlices; ++k) {
         const float2 s = s_ml[k][g];
-        if (s.x == -INFINITY) continue;
+        if (s.x == -INFINITY && s.y == 0.f) continue;
         const float mn = fmaxf(M, s.x);
         const float alpha = exp2f(M - mn), beta = exp2f(s.x - mn);
         l = l * alpha + s.y * beta;
@@ -1354,7 +1363,7 @@ __global__ void __launch_bounds__(G * kSlices * 32) join_states_kernel(const Dec
     }
     if (slice > 0) return;
   }
-  const float inv = l > 0.f ? 1.0f / l : 0.f;  // no token: zeros
+  const float inv = l != 0.f ? 1.0f / l : 0.f;  // no token: zeros
   __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) +
                         (static_cast<size_t>(b) * p.num_q_heads + kvh * G + g) * D + lane * kPer;
   if constexpr (kPer == 4) {
@@ -1374,6 +1383,10 @@ template <int D, int G, View kView>
 struct Instance {
   static constexpr int NW = Shape<D, G, kView>::kWarps;
   static constexpr int S = Shape<D, G, kView>::kStages;
+  // Join: up to so many (sequence, kv head) pairs get 16 warps each, more get one a head.  Few pairs of a short stream
+  // have tens of states each (one sequence, window 1024: 12.5 us a call with one warp a head, 9.3 with sixteen); with
+  // many pairs the extra warps only fill the SMs (1024 pairs, window 2048: 140.6 us with one a head, 144.7 with sixteen).
+  static constexpr unsigned kFewPairs = 304;
   static constexpr int kManySlices = 16 / G;
   static constexpr auto kPartition = &paged_decode_partition_kernel<D, G, NW, S, kView>;
 
@@ -1443,7 +1456,7 @@ struct Instance {
     const unsigned grid = static_cast<unsigned>(p.num_seqs) * static_cast<unsigned>(p.num_kv_heads);
     if constexpr (kView == View::kAll)
       return launch_pdl(paged_decode_merge_kernel<D, G>, dim3(grid), dim3(G * 32), 0, stream, p);
-    else if (grid > PKV_JOIN_FEW_PAIRS)
+    else if (grid > kFewPairs)
       return launch_pdl(join_states_kernel<D, G, kView, 1>, dim3(grid), dim3(G * 32), 0, stream, p);
     else
       return launch_pdl(join_states_kernel<D, G, kView, kManySlices>, dim3(grid), dim3(G * kManySlices * 32), 0, stream,

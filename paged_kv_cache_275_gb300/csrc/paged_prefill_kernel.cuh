@@ -57,6 +57,7 @@
 #include <mutex>
 
 #include "paged_prefill.h"
+#include "shared_plan.cuh"
 
 namespace pkv {
 namespace {
@@ -80,15 +81,6 @@ constexpr int kTmemCols = 512;  // per tile t: S at [256 t, 256 t + 128), O at [
 __host__ __device__ constexpr int col_s(int t) { return 256 * t; }  // P (bf16 pairs) over the first 64 of S
 __host__ __device__ constexpr int col_o(int t) { return 256 * t + 128; }
 constexpr int kTmemSlotOffset = 384;  // in the 512-byte barrier area: barriers below, TMEM slot and sequence pick here
-#ifndef PKV_SHARED_CTA_US
-#define PKV_SHARED_CTA_US 7.f
-#endif
-#ifndef PKV_SHARED_STEP_US
-#define PKV_SHARED_STEP_US 1.9f
-#endif
-#ifndef PKV_SHARED_SM_RATE
-#define PKV_SHARED_SM_RATE 1e5f
-#endif
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;
 constexpr unsigned long long kWaitNs = 2000000000ull;
@@ -299,6 +291,12 @@ __device__ __forceinline__ float ex2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// max(a, b, c), not a number if one of them is none.
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
@@ -352,110 +350,37 @@ struct SharedJob {
   int tile, kv_head, split, num_splits;
 };
 
-// The work of group g is tile pairs x kv heads units of ceil(keys / 128) key steps each.  All groups' units are
-// cut into splits of at most s steps, so that the CTAs finish about together whatever the groups' sizes and
-// lengths (the host sizes the grid at no less than one CTA a unit, so some s always fits).  The tail's kernel runs
-// beside this one on the SMs that it leaves free, so s is not the least that fits but the one with the least
-// estimated time for both: few long splits give the tail more SMs, and the join fewer states.
-// CTA numbers run over the groups, their tile pairs, kv heads and splits.  One warp finds the CTA's job, a group or
-// a candidate s per lane.  False: no job for this CTA.  group_start has to start at 0 or above, not fall, and end at
-// num_seqs or below; otherwise no group is used, which ws_plan_ok tells the join.
+// The CTA's job of the plan (shared_plan.cuh).  CTA numbers run over the groups, their tile pairs, kv heads and
+// splits.  False: no job for this CTA.  Called by one warp; CTA 0 reports what is wrong with the groups, and whether
+// they are in order at all (else no group is used) to the join.
 template <int D, int G>
 __device__ __forceinline__ bool find_shared_job(const PrefillParams& p, SharedJob& job) {
-  constexpr int kCtaTokens = kTiles * kRows / G;
+  static_assert(kPlanRows == kTiles * kRows && kPlanKeys == kKeys, "the plan's units are this kernel's");
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31;
-  const bool reporter = blockIdx.x == 0;
-  // The sequences' lengths, of at most 256 of them: about how much there is behind the shared blocks.
-  const int every = (p.num_seqs + 255) / 256;
-  int lens[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int b = (lane + 32 * i) * every;
-    lens[i] = b < p.num_seqs ? __ldg(p.context_lens + b) : 0;
-  }
-
-  struct Group {
-    int first, rows, keys;
-    bool fine;
-  };
-  auto group = [&](int g) -> Group {
-    Group x{0, 0, 0, true};
-    if (g < p.num_groups) {
-      const int a = __ldg(p.group_start + g), e = __ldg(p.group_start + g + 1);
-      const int len = __ldg(p.prefix_lens + g);
-      x.fine = a >= 0 && a <= e && e <= p.num_seqs;
-      if (x.fine && a < e) {  // an empty group's length says nothing
-        x.first = a;
-        x.rows = e - a;
-        x.keys = shared_prefix_blocks(len, p.max_blocks_per_seq) * kBlockTokens;
-        if (reporter && len < 0) atomicOr(p.err, kErrLenNegative);
-        if (reporter && len > p.max_blocks_per_seq * kBlockTokens) atomicOr(p.err, kErrLenTooLong);
-      }
+  const SharedPlanner<D, G> planner{p.group_start,  p.prefix_lens,        p.context_lens, p.num_groups,
+                                    p.num_seqs,     p.num_kv_heads,       p.max_blocks_per_seq, p.num_sms,
+                                    static_cast<int>(gridDim.x)};
+  const SharedGroup mine = planner.group(lane);  // the first 32 groups stay in registers
+  const SharedPlan plan = planner.plan(lane, mine);
+  if (blockIdx.x == 0) {
+    if (lane == 0) {
+      *p.ws_plan_ok = plan.fine;
+      if (!plan.fine) atomicOr(p.err, kErrLenTooLong);
     }
-    return x;
-  };
-  auto units = [&](const Group& x) { return x.keys > 0 ? (x.rows + kCtaTokens - 1) / kCtaTokens * p.num_kv_heads : 0; };
-  auto steps = [&](const Group& x) { return (x.keys + kKeys - 1) / kKeys; };
-
-  const Group mine = group(lane);  // the first 32 groups stay in registers
-  float tokens = 0.f;              // behind the shared blocks, over all sequences
-#pragma unroll
-  for (int i = 0; i < 8; ++i) tokens += max(0, lens[i]);
-  tokens *= every;
-  bool fine = true, two_tiles = false;
-  int most = 1;   // the longest unit's steps
-  float work = 0.f;  // unit steps
-  for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
-    const Group x = g0 == 0 ? mine : group(g0 + lane);
-    fine = fine && x.fine;
-    most = max(most, steps(x));
-    work += static_cast<float>(units(x)) * static_cast<float>(steps(x));
-    two_tiles = two_tiles || x.rows * G > kRows;
-    tokens -= static_cast<float>(x.rows) * static_cast<float>(x.keys);
+    for (int g = lane; g < p.num_groups; g += 32)
+      if (planner.group(g).rows > 0) {
+        const int len = __ldg(p.prefix_lens + g);
+        if (len < 0) atomicOr(p.err, kErrLenNegative);
+        if (len > p.max_blocks_per_seq * kBlockTokens) atomicOr(p.err, kErrLenTooLong);
+      }
   }
-  fine = __all_sync(kAll, fine);
-  two_tiles = __any_sync(kAll, two_tiles);
-  most = __reduce_max_sync(kAll, most);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    work += __shfl_xor_sync(kAll, work, off);
-    tokens += __shfl_xor_sync(kAll, tokens, off);
-  }
-  if (reporter && lane == 0) {
-    *p.ws_plan_ok = fine;
-    if (!fine) atomicOr(p.err, kErrLenTooLong);
-  }
-  if (!fine || work == 0.f) return false;
-
-  // Candidate s of the lane: from the least that could fit on, an eighth of it apart; the last is the longest unit.
-  const int least_s = max(1, static_cast<int>(work / gridDim.x));
-  const int s = lane == 31 ? most : min(most, least_s + lane * ((least_s + 7) / 8));
-  int n = 0;  // its CTAs
-  for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
-    const Group x = g0 == 0 ? mine : group(g0 + lane);
-    const int u = units(x), t = steps(x);
-    for (int k = 0; k < min(32, p.num_groups - g0); ++k)
-      n += __shfl_sync(kAll, u, k) * ((__shfl_sync(kAll, t, k) + s - 1) / s);
-  }
-  // Microseconds: a CTA costs kCtaUs and a step of two tiles (or one) kStepUs; an SM streams the tail at kSmRate
-  // bytes a microsecond, all of them together at kAllRate.
-  constexpr float kCtaUs = PKV_SHARED_CTA_US, kSmRate = PKV_SHARED_SM_RATE, kAllRate = 6.4e6f;
-  const float tail = fmaxf(tokens, 0.f) * (4.f * D) * p.num_kv_heads;
-  const int waves = (n + p.num_sms - 1) / p.num_sms;
-  const float us = waves * (kCtaUs + s * (two_tiles ? PKV_SHARED_STEP_US : 1.2f));
-  const float beside = fminf(max(p.num_sms - n, 0) * kSmRate, kAllRate) * us;
-  float cost = us + fmaxf(tail - beside, 0.f) * (1.f / kAllRate);
-  if (n > static_cast<int>(gridDim.x)) cost = INFINITY;  // does not fit
-  float best = cost;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) best = fminf(best, __shfl_xor_sync(kAll, best, off));
-  const int split_steps = __shfl_sync(kAll, s, __ffs(__ballot_sync(kAll, cost == best)) - 1);
-
+  if (plan.split_steps == 0) return false;
   int base = 0;  // CTAs of the groups before g0
   for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
-    const Group x = g0 == 0 ? mine : group(g0 + lane);
-    const int splits = (steps(x) + split_steps - 1) / split_steps, count = units(x) * splits;
+    const SharedGroup x = g0 == 0 ? mine : planner.group(g0 + lane);
+    const int splits = (planner.steps(x) + plan.split_steps - 1) / plan.split_steps;
+    const int count = planner.units(x) * splits;
     int end = count;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -960,20 +885,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // Row max: eight chains of three-input maxima, then their maximum.
       static_assert(kKeys % 8 == 0 && kKeys >= 24, "row max layout");
+      auto max3 = [](float a, float b, float c) { return kMask == Mask::kCausal ? fmax3(a, b, c) : fmax3_nan(a, b, c); };
       float mc[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) mc[k] = fmax3(s[k], s[k + 8], s[k + 16]);
+      for (int k = 0; k < 8; ++k) mc[k] = max3(s[k], s[k + 8], s[k + 16]);
       constexpr int kPairsEnd = 24 + ((kKeys - 24) / 16) * 16;
 #pragma unroll
       for (int x = 24; x < kPairsEnd; x += 16)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mc[k] = fmax3(mc[k], s[x + k], s[x + 8 + k]);
+        for (int k = 0; k < 8; ++k) mc[k] = max3(mc[k], s[x + k], s[x + 8 + k]);
       if constexpr (kPairsEnd < kKeys) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mc[k] = fmaxf(mc[k], s[kPairsEnd + k]);
+        for (int k = 0; k < 8; ++k)
+          mc[k] = kMask == Mask::kCausal ? fmaxf(mc[k], s[kPairsEnd + k]) : max3(mc[k], mc[k], s[kPairsEnd + k]);
       }
-      const float row_max = fmax3(fmax3(mc[0], mc[1], mc[2]), fmax3(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7]));
-      const float bm = row_max * qk;  // the scale is positive: the max of the scaled scores
+      float row_max;
+      if constexpr (kMask == Mask::kCausal)
+        row_max = fmax3(fmax3(mc[0], mc[1], mc[2]), fmax3(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7]));
+      else
+        row_max = max3(max3(mc[0], mc[1], mc[2]), max3(mc[3], mc[4], mc[5]), max3(mc[6], mc[7], mc[7]));
+      float bm = row_max * qk;  // the scale is positive: the max of the scaled scores
+      bool bad = false;         // a score that is not a number, or infinite: so is the row's result
+      if constexpr (kMask != Mask::kCausal) {
+        bad = !(bm < INFINITY);
+        if (bad) bm = m_used == -INFINITY ? 0.f : m_used;
+      }
       if constexpr (kMask == Mask::kWindow) sees = bm > -INFINITY || m_used > -INFINITY;  // a key of the window yet
       const bool raise = sees && bm > m_used + kSlack;
       const float m_new = raise ? bm : m_used;
@@ -995,6 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float2 a01 = __fadd2_rn(acc4[0], acc4[1]), a23 = __fadd2_rn(acc4[2], acc4[3]);
       const float2 a = __fadd2_rn(a01, a23);
       l = l * alpha + (a.x + a.y);
+      if (bad) l = __int_as_float(0x7fffffff);
       m_used = m_new;
       // O is rescaled in place (its previous P.V has retired: see the wait above).
       if (j >= 1 && __any_sync(0xffffffffu, raise)) {
@@ -1059,7 +996,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       unsigned char* ot = smem + T::kOffQ + t * T::kQTile;
       if (!failed && __all_sync(0xffffffffu, bar_wait(o_full + 8 * t, 0))) {
         tc_after_sync();
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        // (Without a key l is 0; it is not a number where a score was none.)
+        const float inv = (kMask == Mask::kCausal ? l > 0.f : l != 0.f) ? 1.f / l : 0.f;
   #pragma unroll
         for (int c0 = 0; c0 < D; c0 += 32) {
           float o[32];
@@ -1198,6 +1136,86 @@ __global__ void __launch_bounds__(256) paged_prefill_merge_kernel(const PrefillP
   }
 }
 
+// The merge of a windowed split call: the same sum, a warp two rows at a time, a lane D / 32 dims.  These calls are
+// small (few tiles, short windows), so it is latency that counts: the first kFirst splits' O are requested before
+// their (m, l) say which of them saw a key.
+template <int D>
+__global__ void __launch_bounds__(256, 4) window_prefill_merge_kernel(const PrefillParams p) {
+  constexpr int kCols = D / 32, kRowsPerWarp = 2, kFirst = 4;
+  const int b = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_trigger();
+  pdl_wait();
+  const int q0 = p.query_start[b];
+  const int C = p.query_start[b + 1] - q0;
+  const int L = p.context_lens[b];
+  if (C < 0 || L < C || L > p.max_blocks_per_seq * kBlockTokens) return;  // flagged by the attention kernel
+  const int rows = min(C, p.ws_rows) * p.num_q_heads;
+  const size_t split_stride = static_cast<size_t>(p.num_seqs) * p.ws_rows * p.num_q_heads;  // rows per split
+  const float2* ml = reinterpret_cast<const float2*>(p.ws + static_cast<size_t>(p.num_splits) * split_stride * D);
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
+  auto load = [&](size_t row, float (&o)[kCols]) {
+    const float* src = p.ws + row * D + lane * kCols;
+    if constexpr (kCols == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(src);
+      o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(src);
+      o[0] = v.x; o[1] = v.y;
+    }
+  };
+  for (int row2 = (blockIdx.x * 8 + warp) * kRowsPerWarp; row2 < rows; row2 += gridDim.x * 8 * kRowsPerWarp) {
+    const size_t r0 = static_cast<size_t>(b) * p.ws_rows * p.num_q_heads + row2;  // the first row in split 0
+    float2 s[kRowsPerWarp];
+    float o[kRowsPerWarp][kFirst][kCols];
+#pragma unroll
+    for (int k = 0; k < kRowsPerWarp; ++k) {
+      s[k] = make_float2(-INFINITY, 0.f);
+      if (lane < p.num_splits && row2 + k < rows) s[k] = ml[lane * split_stride + r0 + k];
+    }
+#pragma unroll
+    for (int k = 0; k < kRowsPerWarp; ++k)
+#pragma unroll
+      for (int f = 0; f < kFirst; ++f)
+        if (f < p.num_splits && row2 + k < rows) load(f * split_stride + r0 + k, o[k][f]);
+#pragma unroll
+    for (int k = 0; k < kRowsPerWarp; ++k) {
+      if (row2 + k >= rows) break;
+      float mx = s[k].x;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      const float w = s[k].x == -INFINITY ? 0.f : exp2f(s[k].x - mx);
+      float den = w * s[k].y;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
+      const float inv = den != 0.f ? 1.f / den : 0.f;
+      float acc[kCols];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
+#pragma unroll
+      for (int f = 0; f < kFirst; ++f) {
+        const float wf = __shfl_sync(0xffffffffu, w, f);
+        if (wf == 0.f) continue;  // no such split, or one that saw no key and wrote no O
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) acc[c] += wf * o[k][f][c];
+      }
+      for (int f = kFirst; f < p.num_splits; ++f) {
+        const float wf = __shfl_sync(0xffffffffu, w, f);
+        if (wf == 0.f) continue;
+        float v[kCols];
+        load(f * split_stride + r0 + k, v);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) acc[c] += wf * v[c];
+      }
+      const int i = (row2 + k) / p.num_q_heads, h = (row2 + k) % p.num_q_heads;
+      __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(
+          out + (static_cast<size_t>(q0 + i) * p.num_q_heads + h) * D + lane * kCols);
+#pragma unroll
+      for (int c = 0; c < kCols; c += 2) dst[c / 2] = __floats2bfloat162_rn(acc[c] * inv, acc[c + 1] * inv);
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
@@ -1315,9 +1333,15 @@ cudaError_t launch_t(const PrefillParams& p, int max_query_len, cudaStream_t str
     const dim3 grid(p.num_kv_heads, tiles, p.num_seqs * p.num_splits);
     e = launch_pdl(paged_prefill_kernel<D, G, true, kMask>, grid, dim3(kThreads), Pf<D>::kSmem, stream, q, mk, mv, mo);
     if (e != cudaSuccess) return e;
-    const int64_t row_blocks = (static_cast<int64_t>(q.ws_rows) * p.num_q_heads + 31) / 32;  // 8 warps x 4 rows
-    const dim3 mgrid(static_cast<unsigned>(row_blocks < 65535 ? row_blocks : 65535), p.num_seqs);
-    return launch_pdl(paged_prefill_merge_kernel<D>, mgrid, dim3(256), 0, stream, q);
+    if constexpr (kMask == Mask::kWindow) {
+      const int64_t blocks = (static_cast<int64_t>(q.ws_rows) * p.num_q_heads + 15) / 16;  // 8 warps x 2 rows
+      return launch_pdl(window_prefill_merge_kernel<D>,
+                        dim3(static_cast<unsigned>(blocks < 65535 ? blocks : 65535), p.num_seqs), dim3(256), 0, stream, q);
+    } else {
+      const int64_t row_blocks = (static_cast<int64_t>(q.ws_rows) * p.num_q_heads + 31) / 32;  // 8 warps x 4 rows
+      const dim3 mgrid(static_cast<unsigned>(row_blocks < 65535 ? row_blocks : 65535), p.num_seqs);
+      return launch_pdl(paged_prefill_merge_kernel<D>, mgrid, dim3(256), 0, stream, q);
+    }
   }
 }
 

@@ -65,55 +65,6 @@ struct DecodeParams {
   int64_t max_position;
 };
 
-// What the views of a sequence other than the whole of it need besides.
-struct DecodeViewParams : DecodeParams {
-  int min_piece_blocks;  // window and tail views: the least blocks a piece is cut to
-  // Window view: a sequence's last `window` tokens and its first `sinks` (both at most 16 * max_blocks_per_seq).
-  int window;
-  int sinks;
-  // Tail view: groups of consecutive sequences whose first prefix_lens[g] / 16 blocks are shared.
-  const int32_t* group_start;  // [num_groups + 1]
-  const int32_t* prefix_lens;  // [num_groups]
-  int num_groups;
-  int32_t* ws_shared;          // workspace: int32 [num_seqs], each sequence's shared blocks
-  float* ws_whole;             // workspace: fp32 states of pairs that lie whole in a piece, [num_seqs * num_kv_heads]
-  const int32_t* ws_plan_ok;   // workspace: whether the groups are in order (0: the records are not to be used)
-  const int2* ws_records;      // workspace: [num_seqs * num_kv_heads]: (first row, splits) of a pair's prefix states
-  const float* ws_prefix_o;    // workspace: prefix states, rows of D floats (a pair's splits 256 rows apart)
-  const float2* ws_prefix_ml;  // workspace: their (m, l)
-};
-
-// Blocks of a shared prefix of len tokens: whole blocks only, within the table.
-__host__ __device__ __forceinline__ int shared_prefix_blocks(int len, int max_blocks_per_seq) {
-  const int blocks = len > 0 ? len / kBlockTokens : 0;
-  return blocks < max_blocks_per_seq ? blocks : max_blocks_per_seq;
-}
-
-// Rotation and append of a batch of tokens (rope_append.cu).
-constexpr int kMaxPositionAxes = 4;
-struct RopeAppendParams {
-  const void* q;  // rows of [heads][head_dim] bf16, `stride` 16-byte chunks apart
-  const void* k;
-  const void* v;
-  void* q_out;
-  int64_t q_stride, k_stride, v_stride, q_out_stride;
-  const int64_t* positions;  // [num_axes][num_tokens], axes axis_stride apart
-  int64_t axis_stride;
-  const float* cos_sin;      // fp32 [max_position][head_dim]
-  int64_t max_position;
-  const int64_t* slot_mapping;
-  void* k_cache;
-  void* v_cache;
-  unsigned* err;
-  int64_t num_tokens;
-  int64_t num_slots;  // 16 * num_blocks
-  int num_q_heads;
-  int num_kv_heads;
-  int num_axes;
-  int parts;  // warps that share a token's rows
-  uint8_t freq_axis[64];  // position axis of each of the head_dim / 2 frequencies
-};
-
 // Programmatic dependent launch.  Every kernel of this library is launched with
 // programmatic stream serialization: it may start (and run its prologue) while
 // the previous kernel in the stream drains, and it executes pdl_wait() before
@@ -148,8 +99,6 @@ void set_error_message(const char* message);
 // kv_append kernel launch.
 cudaError_t launch_kv_append(const AppendParams& p, int num_sms, cudaStream_t stream);
 
-cudaError_t launch_rope_append(const RopeAppendParams& p, int head_dim, int num_sms, cudaStream_t stream);
-
 // Number of fp32 values in one partial-state piece for these shapes.
 int piece_floats(int head_dim, int group);
 // Bytes of the workspace header (block prefix, then the pair records) for num_seqs sequences.
@@ -166,11 +115,5 @@ cudaError_t launch_bounded_wait_selftest(unsigned* err, unsigned long long limit
 // Decode kernels.  `group` = num_q_heads / num_kv_heads.
 cudaError_t launch_decode_partition(const DecodeParams& p, int head_dim, int group, cudaStream_t stream);
 cudaError_t launch_decode_merge(const DecodeParams& p, int head_dim, int group, cudaStream_t stream);
-// The same over a window and sinks (window_decode.cu) and over what follows shared prefixes (prefix_decode.cu).
-cudaError_t resident_window_pieces(int head_dim, int group, int num_seqs, int* pieces);
-cudaError_t launch_window_decode(const DecodeViewParams& p, int head_dim, int group, cudaStream_t stream);
-cudaError_t resident_tail_pieces(int head_dim, int group, int num_seqs, int* pieces);
-cudaError_t launch_tail_partition(const DecodeViewParams& p, int head_dim, int group, cudaStream_t stream);
-cudaError_t launch_prefix_merge(const DecodeViewParams& p, int head_dim, int group, cudaStream_t stream);
 
 }  // namespace pkv

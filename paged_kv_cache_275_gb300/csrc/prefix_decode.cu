@@ -17,7 +17,7 @@ cudaError_t launch_tail_partition(const DecodeViewParams& p, int head_dim, int g
   return dispatch<View::kTail>(head_dim, group, [&](auto inst) { return decltype(inst)::partition(p, stream); });
 }
 
-cudaError_t launch_prefix_merge(const DecodeViewParams& p, int head_dim, int group, cudaStream_t stream) {
+cudaError_t launch_prefix_join(const DecodeViewParams& p, int head_dim, int group, cudaStream_t stream) {
   return dispatch<View::kTail>(head_dim, group, [&](auto inst) { return decltype(inst)::merge(p, stream); });
 }
 

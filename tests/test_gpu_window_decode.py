@@ -91,6 +91,21 @@ def test_window_as_long_as_the_sequences_is_plain_decode():
     assert device_errors() == 0
 
 
+@pytest.mark.parametrize("hq", [1, 4, 8])
+@pytest.mark.parametrize("parts", [1, 9])
+def test_a_key_that_is_not_a_number_spoils_the_row_that_sees_it(hq, parts):
+    pages = Pages((200, 40, 300), 1, 128, 9)
+    q = pages.randn(3, hq, 128)
+    pages.poison(0, [190])
+    ref, allowed = exact(pages, q, (200, 40, 300), 64, 2, 0.09)
+    kc, vc, table, cl = pages.cuda()
+    out = torch.zeros(q.shape, dtype=torch.bfloat16, device="cuda")
+    pkv.paged_window_decode_attention(q.cuda(), kc, vc, table, cl, 0.09, out, 64, 2, num_partitions=parts)
+    assert torch.isnan(out[0].float()).all()
+    assert_within(out[1:], ref[1:], allowed[1:], "the others")
+    assert device_errors() == 0
+
+
 def test_more_sequences_than_one_launch():
     lens = np.random.RandomState(0).randint(0, 40, 4096 + 200)
     run(lens, 2, 1, 64, 9, 2, seed=6)

@@ -102,13 +102,37 @@ def test_long_past_is_not_read():
 
 
 def test_window_longer_than_everything_is_plain_prefill():
+    """Both within their bound of the exact result (their exponentials are computed differently)."""
     pages, lens, start, q = make(CHUNKS[:5], PASTS[:5], 8, 2, 128, 10000, 0, 5, hidden=False)
+    ref, allowed = exact(pages, q, start, lens, None, 0, 0.09)
     kc, vc, table, cl = pages.cuda()
     qs, qg = torch.tensor(start, dtype=torch.int32, device="cuda"), q.cuda()
     a, b = torch.empty_like(qg), torch.empty_like(qg)
     pkv.paged_window_prefill_attention(qg, kc, vc, table, cl, qs, 130, 0.09, a, 10000, 0, num_splits=1)
     pkv.paged_prefill_attention(qg, kc, vc, table, cl, qs, 130, 0.09, b)
-    assert torch.equal(a, b)
+    assert_within(a, ref, allowed, "window")
+    assert_within(b, ref, allowed, "plain")
+    assert device_errors() == 0
+
+
+@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_key_that_is_not_finite_spoils_the_rows_that_see_it(value, splits):
+    """Row i of the chunk is at position 300 + i; key 280 is in the windows of the rows up to 280 + 63."""
+    pages, lens, start, q = make((100,), (300,), 4, 1, 128, 64, 0, 6, hidden=False)
+    pages.k[int(pages.table[0, 280 // BLOCK]), 0, 280 % BLOCK] = value
+    kc, vc, table, cl = pages.cuda()
+    out = torch.zeros(q.shape, dtype=torch.bfloat16, device="cuda")
+    pkv.paged_window_prefill_attention(q.cuda(), kc, vc, table, cl, torch.tensor(start, dtype=torch.int32, device="cuda"),
+                                       100, 0.09, out, 64, 0, num_splits=splits)
+    finite = torch.isfinite(out.float()).all(-1).cpu()
+    if value != value:
+        assert not finite[:44].any()
+    assert finite[44:].all()
+    pages.k[int(pages.table[0, 280 // BLOCK]), 0, 280 % BLOCK] = 0.0
+    ref, allowed = exact(pages, q, start, lens, 64, 0, 0.09)
+    assert_within(out[44:], ref[44:], allowed[44:], "rows that do not see it")
+    assert device_errors() == 0
 
 
 def test_rows_behind_the_last_sequence_are_left_alone():
