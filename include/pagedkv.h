@@ -407,7 +407,8 @@ pkv_status pkv_paged_window_decode_attention(const void* q, const void* k_cache,
                                              int32_t block_size, float scale, int32_t window, int32_t num_sink_tokens,
                                              void* out, void* workspace, size_t workspace_bytes,
                                              int32_t num_partitions, pkv_stream_t stream);
-/* Its workspace; num_partitions as for pkv_decode_workspace_size (0: the default, needs a device). */
+/* Its workspace; num_partitions as for pkv_decode_workspace_size (0: the default, needs a device).  It can be 0 bytes
+   (few sequences and a short window: one launch that joins through shared memory); the workspace may be NULL then. */
 pkv_status pkv_window_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                             int32_t head_dim, int32_t max_blocks_per_seq, int32_t window,
                                             int32_t num_sink_tokens, int32_t num_partitions, size_t* bytes);
@@ -453,7 +454,7 @@ pkv_status pkv_window_prefill_default_splits(int32_t num_seqs, int32_t max_query
  *   scale         > 0
  *   workspace     device, 16-byte aligned, at least pkv_prefix_decode_workspace_size bytes, scratch as for
  *                 pkv_paged_decode_attention
- * num_blocks * num_kv_heads * 16 must be below 2^31.  Three launches.  Shared tokens have to be finite when a
+ * num_blocks * num_kv_heads * 16 must be below 2^31.  One or three launches.  Shared tokens have to be finite when a
  * sequence of the group is shorter than the prefix (see pkv_paged_window_prefill_attention).  Arithmetic: the
  * shared part as pkv_paged_prefill_attention (P rounded to bf16), the rest as pkv_paged_decode_attention, joined in
  * fp32.  Device-side: group_start out of order sets PKV_DEVERR_CONTEXT_LEN_TOO_LONG (the outputs are unspecified);
@@ -467,7 +468,9 @@ pkv_status pkv_paged_prefix_decode_attention(const void* q, const void* k_cache,
                                              int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                              int64_t num_blocks, int32_t block_size, float scale, void* out,
                                              void* workspace, size_t workspace_bytes, pkv_stream_t stream);
-/* Its workspace (needs a device: it holds the partial states of one CTA per SM, or of whole waves of them). */
+/* Its workspace (needs a device: it holds the partial states of one CTA per SM, or of whole waves of them).  It can be 0
+   bytes (few sequences and a narrow table: one launch, in which each sequence reads the shared blocks for itself); the
+   workspace may be NULL then. */
 pkv_status pkv_prefix_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                             int32_t head_dim, int32_t max_blocks_per_seq, int32_t num_groups,
                                             size_t* bytes);

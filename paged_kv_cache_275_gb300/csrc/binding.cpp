@@ -321,7 +321,7 @@ PyObject* window_decode(PyObject*, PyObject* const* a, Py_ssize_t) {
       size_t need = 0;
       check(pkv_window_decode_workspace_size(t.rows, t.hq, t.hkv, t.d, t.width, window, sinks, parts, &need));
       Workspace ws;
-      ws.take(a[10], t.dev, a[11], stream, need);
+      if (need > 0) ws.take(a[10], t.dev, a[11], stream, need);
       run([&] {
         return pkv_paged_window_decode_attention(t.q, t.kc, t.vc, t.table, t.width, t.lens, t.rows, t.hq, t.hkv, t.d,
                                                  t.blocks, t.block, static_cast<float>(scale), window, sinks, t.out,
@@ -381,7 +381,7 @@ PyObject* prefix_decode(PyObject*, PyObject* const* a, Py_ssize_t) {
       size_t need = 0;
       check(pkv_prefix_decode_workspace_size(t.rows, t.hq, t.hkv, t.d, t.width, groups, &need));
       Workspace ws;
-      ws.take(a[9], t.dev, a[10], stream, need);
+      if (need > 0) ws.take(a[9], t.dev, a[10], stream, need);
       run([&] {
         return pkv_paged_prefix_decode_attention(t.q, t.kc, t.vc, t.table, t.width, t.lens,
                                                  static_cast<const int32_t*>(start.data_ptr()),

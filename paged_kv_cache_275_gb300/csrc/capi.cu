@@ -144,6 +144,17 @@ int32_t visible_blocks(Window w, int32_t max_blocks_per_seq) {
   return n < max_blocks_per_seq ? static_cast<int32_t>(n) : max_blocks_per_seq;
 }
 
+// CTAs a (sequence, kv head) of a windowed call in its form for few pairs; 0: the call takes the other form, as it
+// does whenever a partition count is given.
+pkv_status cluster_ctas(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int32_t group,
+                        int32_t max_blocks_per_seq, const Window& window, int32_t num_partitions, int* ctas) {
+  *ctas = 0;
+  if (num_partitions != 0 || num_seqs == 0 || num_seqs > PKV_MAX_SEQS) return PKV_OK;
+  const cudaError_t e = pkv::window_cluster_ctas(head_dim, group, num_seqs, num_kv_heads,
+                                                 visible_blocks(window, max_blocks_per_seq), ctas);
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "cluster occupancy query");
+}
+
 pkv_status default_partitions(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int32_t group,
                               int32_t max_blocks_per_seq, const Window& window, int32_t* out) {
   int pieces = 0;
@@ -216,7 +227,13 @@ static pkv_status decode_impl(const void* q, const void* k_cache, const void* v_
   if (num_partitions < 0 || num_partitions > kMaxPartitions)
     return fail(PKV_ERR_INVALID_ARGUMENT, "num_partitions out of range (got %d)", num_partitions);
   if (num_seqs == 0) return ok();
-  if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out || !workspace)
+  int cluster = 0;  // CTAs a (sequence, kv head) of the form without a workspace
+  if (window.window)
+    if (pkv_status st = cluster_ctas(num_seqs, num_kv_heads, head_dim, num_q_heads / num_kv_heads,
+                                       max_blocks_per_seq, window, num_partitions, &cluster);
+        st != PKV_OK)
+      return st;
+  if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out || (!workspace && !cluster))
     return fail(PKV_ERR_INVALID_ARGUMENT, "null pointer argument");
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned16(workspace) ||
       (reinterpret_cast<uintptr_t>(block_tables) & 3u) || (reinterpret_cast<uintptr_t>(context_lens) & 3u))
@@ -226,10 +243,11 @@ static pkv_status decode_impl(const void* q, const void* k_cache, const void* v_
     return fail(PKV_ERR_UNSUPPORTED, "phases other than PKV_PHASE_ALL need num_seqs <= PKV_MAX_SEQS (%d)",
                 PKV_MAX_SEQS);
   size_t need = 0;
-  if (pkv_status st = decode_workspace_need(num_seqs, num_kv_heads, head_dim, group, max_blocks_per_seq, window,
-                                            num_partitions, &need);
-      st != PKV_OK)
-    return st;
+  if (!cluster)
+    if (pkv_status st = decode_workspace_need(num_seqs, num_kv_heads, head_dim, group, max_blocks_per_seq, window,
+                                              num_partitions, &need);
+        st != PKV_OK)
+      return st;
   if (workspace_bytes < need)
     return fail(PKV_ERR_INVALID_ARGUMENT, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, need);
 
@@ -244,7 +262,7 @@ static pkv_status decode_impl(const void* q, const void* k_cache, const void* v_
   for (int32_t s0 = 0; s0 < num_seqs; s0 += PKV_MAX_SEQS) {
     const int32_t n = launch_seqs(num_seqs - s0);
     int32_t parts = num_partitions;
-    if (parts == 0)
+    if (parts == 0 && !cluster)
       if (pkv_status st = default_partitions(n, num_kv_heads, head_dim, group, max_blocks_per_seq, window, &parts);
           st != PKV_OK)
         return st;
@@ -255,10 +273,12 @@ static pkv_status decode_impl(const void* q, const void* k_cache, const void* v_
     p.block_tables = block_tables + static_cast<size_t>(s0) * max_blocks_per_seq;
     p.context_lens = context_lens + s0;
     p.out = static_cast<unsigned char*>(out) + s0 * q_row;
-    p.ws_prefix = static_cast<int32_t*>(workspace);
-    p.ws_pairs = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(workspace) + pkv::workspace_prefix_bytes(n));
-    p.ws_pieces = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
-                                           pkv::workspace_header_bytes(n, num_kv_heads));
+    if (workspace) {
+      p.ws_prefix = static_cast<int32_t*>(workspace);
+      p.ws_pairs = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(workspace) + pkv::workspace_prefix_bytes(n));
+      p.ws_pieces = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
+                                             pkv::workspace_header_bytes(n, num_kv_heads));
+    }
     p.err = err;
     p.num_blocks = num_blocks;
     p.num_seqs = n;
@@ -280,9 +300,10 @@ static pkv_status decode_impl(const void* q, const void* k_cache, const void* v_
       v.window = w.window;
       v.sinks = w.sinks;
       v.min_piece_blocks = num_partitions == 0 ? kMinPieceBlocks : 1;
-      const cudaError_t e = pkv::launch_window_decode(v, head_dim, group, s);
+      const cudaError_t e = cluster ? pkv::launch_window_cluster(v, head_dim, group, cluster, s)
+                                    : pkv::launch_window_decode(v, head_dim, group, s);
       if (e != cudaSuccess) return cuda_fail(e, "window decode launch");
-      g_launches.fetch_add(2);
+      g_launches.fetch_add(cluster ? 1 : 2);
       continue;
     }
     if (phases & PKV_PHASE_PARTITION) {
@@ -683,10 +704,16 @@ pkv_status pkv_window_decode_workspace_size(int32_t num_seqs, int32_t num_q_head
   if (num_partitions < 0 || num_partitions > kMaxPartitions)
     return fail(PKV_ERR_INVALID_ARGUMENT, "num_partitions out of range (got %d)", num_partitions);
   size_t need = 0;
-  if (pkv_status st = decode_workspace_need(num_seqs, num_kv_heads, head_dim, num_q_heads / num_kv_heads,
-                                            max_blocks_per_seq, Window{window, num_sink_tokens}, num_partitions, &need);
-      st != PKV_OK)
+  const Window w{window, num_sink_tokens};
+  int cluster = 0;
+  if (pkv_status st = cluster_ctas(num_seqs, num_kv_heads, head_dim, num_q_heads / num_kv_heads,
+                                     max_blocks_per_seq, w, num_partitions, &cluster); st != PKV_OK)
     return st;
+  if (!cluster)
+    if (pkv_status st = decode_workspace_need(num_seqs, num_kv_heads, head_dim, num_q_heads / num_kv_heads,
+                                              max_blocks_per_seq, w, num_partitions, &need);
+        st != PKV_OK)
+      return st;
   *bytes = need;
   return ok();
 }
@@ -740,6 +767,7 @@ pkv_status pkv_paged_window_prefill_attention(const void* q, const void* k_cache
 namespace {
 // Shared-prefix decode: its grid, partition count and workspace (byte offsets of the parts).
 struct PrefixPlan {
+  int cluster = 0;  // CTAs a (sequence, kv head) of the form for few pairs, which needs none of the rest
   int32_t ctas = 0, parts = 0, sms = 0;
   size_t pairs = 0, shared = 0, plan_ok = 0, records = 0, whole = 0, pieces = 0, prefix = 0, bytes = 0;
 };
@@ -754,6 +782,11 @@ pkv_status plan_prefix_decode(int32_t num_seqs, int32_t num_q_heads, int32_t num
   if (num_groups < 0 || num_groups > PKV_MAX_SEQS)
     return fail(PKV_ERR_INVALID_ARGUMENT, "num_groups must be in [0, %d] (got %d)", PKV_MAX_SEQS, num_groups);
   const int group = num_q_heads / num_kv_heads;
+  if (num_seqs > 0) {
+    const cudaError_t e = pkv::prefix_cluster_ctas(head_dim, group, num_seqs, num_kv_heads, max_blocks_per_seq, &plan->cluster);
+    if (e != cudaSuccess) return cuda_fail(e, "cluster occupancy query");
+    if (plan->cluster) return PKV_OK;
+  }
   int sms = 0;
   if (pkv_status st = device_state(nullptr, &sms); st != PKV_OK) return st;
   // The most (tile pair, kv head) units the groups can make, and from there whole waves of one CTA per SM.
@@ -828,7 +861,7 @@ pkv_status pkv_paged_prefix_decode_attention(const void* q, const void* k_cache,
   if (num_groups < 0 || num_groups > PKV_MAX_SEQS)
     return fail(PKV_ERR_INVALID_ARGUMENT, "num_groups must be in [0, %d] (got %d)", PKV_MAX_SEQS, num_groups);
   if (num_seqs == 0) return ok();
-  if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out || !workspace ||
+  if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out ||
       (num_groups > 0 && (!group_start || !prefix_lens)))
     return fail(PKV_ERR_INVALID_ARGUMENT, "null pointer argument");
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned16(workspace) ||
@@ -841,14 +874,37 @@ pkv_status pkv_paged_prefix_decode_attention(const void* q, const void* k_cache,
                                          &plan);
       st != PKV_OK)
     return st;
-  if (workspace_bytes < plan.bytes)
-    return fail(PKV_ERR_INVALID_ARGUMENT, "workspace too small: %zu bytes given, %zu needed", workspace_bytes,
-                plan.bytes);
+  if (workspace_bytes < plan.bytes || (!workspace && plan.bytes))
+    return fail(PKV_ERR_INVALID_ARGUMENT, "workspace too small: %zu bytes given, %zu needed",
+                workspace ? workspace_bytes : size_t{0}, plan.bytes);
   unsigned* err = nullptr;
   if (pkv_status st = device_state(&err, nullptr); st != PKV_OK) return st;
-  unsigned char* ws = static_cast<unsigned char*>(workspace);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int group = num_q_heads / num_kv_heads;
+  pkv::DecodeViewParams p{};
+  p.q = q;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.out = out;
+  p.err = err;
+  p.num_blocks = num_blocks;
+  p.num_seqs = num_seqs;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.qscale = scale * 1.4426950408889634f;
+  p.group_start = group_start;
+  p.prefix_lens = prefix_lens;
+  p.num_groups = num_groups;
+  if (plan.cluster) {
+    const cudaError_t e = pkv::launch_prefix_cluster(p, head_dim, group, plan.cluster, s);
+    if (e != cudaSuccess) return cuda_fail(e, "prefix decode launch");
+    g_launches.fetch_add(1);
+    return ok();
+  }
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
   pkv::PrefillParams f{};
   f.q = q;
   f.k_cache = k_cache;
@@ -874,28 +930,11 @@ pkv_status pkv_paged_prefix_decode_attention(const void* q, const void* k_cache,
   f.ws_plan_ok = reinterpret_cast<int32_t*>(ws + plan.plan_ok);
   cudaError_t e = pkv::launch_shared_prefix(f, head_dim, group, s);
   if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
-  pkv::DecodeViewParams p{};
-  p.q = q;
-  p.k_cache = k_cache;
-  p.v_cache = v_cache;
-  p.block_tables = block_tables;
-  p.context_lens = context_lens;
-  p.out = out;
   p.ws_prefix = reinterpret_cast<int32_t*>(ws);
   p.ws_pairs = reinterpret_cast<int32_t*>(ws + plan.pairs);
   p.ws_pieces = reinterpret_cast<float*>(ws + plan.pieces);
-  p.err = err;
-  p.num_blocks = num_blocks;
-  p.num_seqs = num_seqs;
-  p.num_q_heads = num_q_heads;
-  p.num_kv_heads = num_kv_heads;
-  p.max_blocks_per_seq = max_blocks_per_seq;
   p.num_partitions = plan.parts;
   p.min_piece_blocks = kMinPieceBlocks;
-  p.qscale = scale * 1.4426950408889634f;
-  p.group_start = group_start;
-  p.prefix_lens = prefix_lens;
-  p.num_groups = num_groups;
   p.ws_shared = reinterpret_cast<int32_t*>(ws + plan.shared);
   p.ws_whole = reinterpret_cast<float*>(ws + plan.whole);
   p.ws_plan_ok = f.ws_plan_ok;

@@ -33,6 +33,13 @@ __host__ __device__ __forceinline__ int shared_prefix_blocks(int len, int max_bl
 // Pieces the partition kernel keeps in flight on the current device, as resident_partition_pieces.
 cudaError_t resident_window_pieces(int head_dim, int group, int num_seqs, int* pieces);
 cudaError_t resident_tail_pieces(int head_dim, int group, int num_seqs, int* pieces);
+// Windowed decode, a cluster of `ctas` CTAs a (sequence, kv head): how many suit a call (0: it is too large for this
+// form), and the launch (no workspace).
+cudaError_t window_cluster_ctas(int head_dim, int group, int num_seqs, int num_kv_heads, int visible_blocks, int* ctas);
+cudaError_t launch_window_cluster(const DecodeViewParams& p, int head_dim, int group, int ctas, cudaStream_t stream);
+// The same for sequences that share prefixes (each pair reads its group's blocks for itself).
+cudaError_t prefix_cluster_ctas(int head_dim, int group, int num_seqs, int num_kv_heads, int visible_blocks, int* ctas);
+cudaError_t launch_prefix_cluster(const DecodeViewParams& p, int head_dim, int group, int ctas, cudaStream_t stream);
 // Windowed decode (partition, then join).
 cudaError_t launch_window_decode(const DecodeViewParams& p, int head_dim, int group, cudaStream_t stream);
 // What follows shared prefixes: the partition (behind launch_shared_prefix), and the join of both.

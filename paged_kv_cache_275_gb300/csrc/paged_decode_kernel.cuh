@@ -622,16 +622,36 @@ __device__ __forceinline__ uint4 rope_chunk(uint4 x, uint4 y, const float* cs_ro
   return make_uint4(ow[0], ow[1], ow[2], ow[3]);
 }
 
-// Tail view: leading blocks of sequence `row` that its group shares, 0 outside every group.
-__device__ __forceinline__ int shared_blocks_of_row(const DecodeViewParams& p, int row) {
+// Tail view: the leading blocks of sequence `row` that its group shares (0 outside every group), and the group's first
+// sequence.
+struct SharedRow {
+  int blocks, first_row;
+};
+__device__ __forceinline__ SharedRow shared_blocks_of_row(const DecodeViewParams& p, int row) {
   int lo = 0, hi = p.num_groups;  // the last group that starts at or before the row
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (__ldg(p.group_start + mid) <= row) lo = mid + 1;
     else hi = mid;
   }
-  if (lo == 0 || row >= __ldg(p.group_start + lo)) return 0;
-  return shared_prefix_blocks(__ldg(p.prefix_lens + lo - 1), p.max_blocks_per_seq);
+  if (lo == 0) return {0, 0};
+  const int first = __ldg(p.group_start + lo - 1);
+  if (first < 0 || row >= __ldg(p.group_start + lo)) return {0, 0};
+  return {shared_prefix_blocks(__ldg(p.prefix_lens + lo - 1), p.max_blocks_per_seq), first};
+}
+
+// Flags what is wrong with a call's groups: bounds out of order, and lengths outside the table of groups that are not
+// empty.  Called by a CTA's threads together.
+__device__ __forceinline__ void report_groups(const DecodeViewParams& p) {
+  for (int g = threadIdx.x; g < p.num_groups; g += blockDim.x) {
+    const int a = __ldg(p.group_start + g), e = __ldg(p.group_start + g + 1), len = __ldg(p.prefix_lens + g);
+    if (a < 0 || a > e || e > p.num_seqs) {
+      atomicOr(p.err, kErrLenTooLong);
+    } else if (a < e) {
+      if (len < 0) atomicOr(p.err, kErrLenNegative);
+      if (len > p.max_blocks_per_seq * kBlockTokens) atomicOr(p.err, kErrLenTooLong);
+    }
+  }
 }
 
 // Window and tail views: pieces that a stream of `total` items is cut into, at least min_piece_blocks items each
@@ -719,7 +739,7 @@ __global__ void __launch_bounds__(NW * 32)
     int x = (L + kBlockTokens - 1) / kBlockTokens;
     if constexpr (kView == View::kWindow) x -= WindowBlocks(L, p.window, p.sinks).skip;
     if constexpr (kView == View::kTail) {
-      const int shared = idx < B ? shared_blocks_of_row(p, idx) : 0;
+      const int shared = idx < B ? shared_blocks_of_row(p, idx).blocks : 0;
       if (idx < B) s_shared[idx] = shared;
       x = x > shared ? x - shared : 0;
     }

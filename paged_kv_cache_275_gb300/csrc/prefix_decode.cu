@@ -5,9 +5,23 @@
 // a group's query rows are the rows of a tensor-core product with the prefix's keys, which are read once for
 // the group (once per 256 rows) instead of once per sequence.  What follows the shared blocks is each
 // sequence's own and streams through the partition kernel (View::kTail).
-#include "paged_decode_kernel.cuh"
+#include "cluster_decode.cuh"
 
 namespace pkv {
+cudaError_t prefix_cluster_ctas(int head_dim, int group, int num_seqs, int num_kv_heads, int visible_blocks, int* ctas) {
+  // What the three kernels take depends on lengths that only the device knows: 10 us at least, 14 to 15 where a warp here
+  // has 8 blocks (which takes 12), and less than here where it has 16 (16 sequences of 8 kv heads behind 2048 tokens: 15.2
+  // and 18.7 us).
+  return dispatch_cluster<View::kTail>(head_dim, group, [&](auto form) {
+    return decltype(form)::ctas(num_seqs, num_kv_heads, visible_blocks, 13.2f, false, ctas);
+  });
+}
+
+cudaError_t launch_prefix_cluster(const DecodeViewParams& p, int head_dim, int group, int ctas, cudaStream_t stream) {
+  return dispatch_cluster<View::kTail>(
+      head_dim, group, [&](auto form) { return decltype(form)::launch(p, ctas, stream); });
+}
+
 cudaError_t resident_tail_pieces(int head_dim, int group, int num_seqs, int* pieces) {
   return dispatch<View::kTail>(head_dim, group,
                                [&](auto inst) { return decltype(inst)::resident_pieces(num_seqs, pieces); });

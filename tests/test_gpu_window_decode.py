@@ -1,4 +1,7 @@
-"""Windowed decode attention on the GPU against the definition in 64 bits (tolerances: plain64.attend)."""
+"""Windowed decode attention on the GPU against the definition in 64 bits (tolerances: plain64.attend).
+
+A call with few (sequence, kv head) pairs and no partition count given joins through shared memory; others, and all with
+a count, through the workspace.  Most tests run both."""
 import numpy as np
 import pytest
 import torch
@@ -47,15 +50,25 @@ LENS = (0, 1, 2, 15, 16, 17, 31, 33, 64, 100, 257, 700)
 
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("hq,hkv", [(2, 2), (4, 2), (8, 2), (16, 2), (8, 8), (3, 3)])
-def test_layouts(hq, hkv, d):
-    run(LENS, hq, hkv, d, 50, 4, seed=hq)
+@pytest.mark.parametrize("parts", [0, 37])
+def test_layouts(hq, hkv, d, parts):
+    run(LENS, hq, hkv, d, 50, 4, seed=hq, num_partitions=parts)
+
+
+@pytest.mark.parametrize("seqs,window", [(1, 1000), (1, 40), (2, 1000), (9, 1000), (9, 100), (19, 200), (70, 300), (160, 60)])
+@pytest.mark.parametrize("hq,hkv", [(8, 8), (8, 1), (32, 4)])
+def test_either_side_of_the_forms(seqs, window, hq, hkv):
+    """Clusters of one to eight CTAs a pair, from one block a warp to several, and calls too large for them."""
+    lens = np.random.RandomState(seqs + window).randint(0, 1500, seqs)
+    run(lens, hq, hkv, 64, window, 5, seed=seqs)
 
 
 @pytest.mark.parametrize("hq", [4, 16])
 @pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 100, 700, 5000, 0x7fffffff])
 @pytest.mark.parametrize("sinks", [0, 1, 16, 20])
-def test_windows(hq, window, sinks):
-    run(LENS, hq, 2, 64, window, sinks, seed=window % 1000 + sinks)
+@pytest.mark.parametrize("parts", [0, 37])
+def test_windows(hq, window, sinks, parts):
+    run(LENS, hq, 2, 64, window, sinks, seed=window % 1000 + sinks, num_partitions=parts)
 
 
 @pytest.mark.parametrize("hq", [4, 16])
@@ -72,8 +85,9 @@ def test_partition_counts(hq, parts):
 
 @pytest.mark.parametrize("scale", [0.0, -0.05, 1.0])
 @pytest.mark.parametrize("hq", [4, 16])
-def test_scales(hq, scale):
-    run((40, 90), hq, 2, 64, 30, 3, seed=4, scale=scale)
+@pytest.mark.parametrize("parts", [0, 5])
+def test_scales(hq, scale, parts):
+    run((40, 90), hq, 2, 64, 30, 3, seed=4, scale=scale, num_partitions=parts)
 
 
 def test_window_as_long_as_the_sequences_is_plain_decode():
@@ -92,7 +106,7 @@ def test_window_as_long_as_the_sequences_is_plain_decode():
 
 
 @pytest.mark.parametrize("hq", [1, 4, 8])
-@pytest.mark.parametrize("parts", [1, 9])
+@pytest.mark.parametrize("parts", [0, 1, 9])
 def test_a_key_that_is_not_a_number_spoils_the_row_that_sees_it(hq, parts):
     pages = Pages((200, 40, 300), 1, 128, 9)
     q = pages.randn(3, hq, 128)
@@ -111,7 +125,8 @@ def test_more_sequences_than_one_launch():
     run(lens, 2, 1, 64, 9, 2, seed=6)
 
 
-def test_bad_lengths_and_blocks_are_flagged():
+@pytest.mark.parametrize("parts", [0, 3])
+def test_bad_lengths_and_blocks_are_flagged(parts):
     pages = Pages((20, 40), 1, 64, 3)
     q = pages.randn(2, 2, 64).cuda()
     kc, vc, table, cl = pages.cuda()
@@ -120,14 +135,15 @@ def test_bad_lengths_and_blocks_are_flagged():
     for bad, bit in ((-5, pkv.DEVERR_CONTEXT_LEN_NEGATIVE), (49, pkv.DEVERR_CONTEXT_LEN_TOO_LONG)):
         lens = cl.clone()
         lens[0] = bad
-        pkv.paged_window_decode_attention(q, kc, vc, table, lens, 0.1, out, 10, 1)
+        pkv.paged_window_decode_attention(q, kc, vc, table, lens, 0.1, out, 10, 1, num_partitions=parts)
         assert device_errors() & bit
     table[1, 2] = 1 << 20
-    pkv.paged_window_decode_attention(q, kc, vc, table, cl, 0.1, out, 10, 1)
+    pkv.paged_window_decode_attention(q, kc, vc, table, cl, 0.1, out, 10, 1, num_partitions=parts)
     assert device_errors() == pkv.DEVERR_BLOCK_ID_OUT_OF_RANGE
 
 
-def test_graphs_without_a_given_workspace_do_not_share_it():
+@pytest.mark.parametrize("parts", [0, 40])
+def test_graphs_without_a_given_workspace_do_not_share_it(parts):
     """Two captured calls of different sizes, then eager ones that make the eager workspace grow."""
     cases = []
     for lens, hq in (((40, 300), 4), ((700,) * 9, 16)):
@@ -138,7 +154,7 @@ def test_graphs_without_a_given_workspace_do_not_share_it():
 
     def call(c):
         (kc, vc, table, cl), q, out, _ = c
-        pkv.paged_window_decode_attention(q, kc, vc, table, cl, 0.09, out, 64, 4)
+        pkv.paged_window_decode_attention(q, kc, vc, table, cl, 0.09, out, 64, 4, num_partitions=parts)
 
     for c in cases:
         call(c)
@@ -148,7 +164,7 @@ def test_graphs_without_a_given_workspace_do_not_share_it():
         graphs.append(torch.cuda.CUDAGraph())
         with torch.cuda.graph(graphs[-1]):
             call(c)
-    run(LENS * 20, 16, 2, 128, 2000, 4, seed=11)
+    run(LENS * 20, 16, 2, 128, 2000, 4, seed=11, num_partitions=parts and 5000)
     for _ in range(2):
         for g, c in zip(graphs, cases):
             c[2].zero_()
@@ -159,7 +175,8 @@ def test_graphs_without_a_given_workspace_do_not_share_it():
     assert device_errors() == 0
 
 
-def test_two_streams_at_once():
+@pytest.mark.parametrize("parts", [0, 40])
+def test_two_streams_at_once(parts):
     lens = (900, 20, 400)
     pages = Pages(lens, 4, 128, 21)
     q = pages.randn(3, 16, 128)
@@ -171,7 +188,7 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for _ in range(20):
         for s, out in zip(streams, outs):
-            pkv.paged_window_decode_attention(qg, kc, vc, table, cl, 0.09, out, 200, 4, stream=s)
+            pkv.paged_window_decode_attention(qg, kc, vc, table, cl, 0.09, out, 200, 4, stream=s, num_partitions=parts)
     torch.cuda.synchronize()
     for out in outs:
         assert_within(out, ref, allowed, "two streams")
@@ -193,7 +210,8 @@ def test_refusals():
     with pytest.raises(ValueError, match="batch"):
         call(q, kc, vc, table[:1], cl, 0.1, out, 5)
     with pytest.raises(ValueError, match="workspace"):
-        call(q, kc, vc, table, cl, 0.1, out, 5, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        call(q, kc, vc, table, cl, 0.1, out, 5, num_partitions=2,
+             workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(TypeError, match="bfloat16"):
         call(q.float(), kc, vc, table, cl, 0.1, out, 5)
     with pytest.raises(ValueError, match="contiguous"):

@@ -118,7 +118,7 @@ def prefix_decode(lib, **kw):
 
 @pytest.mark.parametrize("kw,status,says", [
     (dict(B=-1), 1, "num_seqs"), (dict(B=4097), 2, "PKV_MAX_SEQS"), (dict(groups=-1), 1, "num_groups"),
-    (dict(groups=4097), 1, "num_groups"), (dict(gs=None), 1, "null"), (dict(pl=None), 1, "null"), (dict(ws=None), 1, "null"),
+    (dict(groups=4097), 1, "num_groups"), (dict(gs=None), 1, "null"), (dict(pl=None), 1, "null"), (dict(q=None), 1, "null"),
     (dict(gs=FAKE + 2), 1, "aligned"), (dict(out=FAKE + 8), 1, "aligned"), (dict(scale=0.0), 1, "scale"),
     (dict(scale=-0.1), 1, "scale"), (dict(scale=float("nan")), 1, "scale"), (dict(nb=0), 2, "num_blocks"),
     (dict(nb=1 << 24), 2, "2^31"), (dict(bs=32), 2, "block_size"), (dict(d=80), 2, "head_dim"), (dict(hq=20), 1, "multiple"),
