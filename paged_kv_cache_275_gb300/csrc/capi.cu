@@ -129,9 +129,6 @@ Window within_table(Window w, int32_t max_blocks_per_seq) {
 // more a piece is a block's time (one sequence, window 1024, two heads: 9.3 us a call with 2, 9.4 with 1, 11.7 with 4,
 // 16.2 with 8).
 constexpr int32_t kMinPieceBlocks = 2;
-// Pieces a warp of the tail view, which runs beside the prefix kernel on the SMs that are free at the time: 128 sequences
-// behind one prefix 53.9 us with 2, 57.7 with 1, 58.3 with 3; 150 behind five 73.4, 71.6, 77.7.
-constexpr int32_t kTailWaves = 2;
 // Least key steps of a split of a windowed prefill (one chunk of 512, window 1024: 19.4 us with 1 to 3, 20.2 with 4,
 // 21.6 with 5).
 constexpr int32_t kMinSplitSteps = 2;
@@ -803,7 +800,6 @@ pkv_status plan_prefix_decode(int32_t num_seqs, int32_t num_q_heads, int32_t num
                         kMinPieceBlocks;
   plan->ctas = static_cast<int32_t>(ctas);
   plan->sms = sms;
-  pieces *= kTailWaves;
   plan->parts = pieces < bound ? pieces : static_cast<int32_t>(bound < 1 ? 1 : bound);
   const size_t state = static_cast<size_t>(pkv::piece_floats(head_dim, group)) * sizeof(float);
   const size_t pair_count = static_cast<size_t>(num_seqs) * num_kv_heads;

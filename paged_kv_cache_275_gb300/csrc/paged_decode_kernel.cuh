@@ -209,8 +209,7 @@ constexpr int ptile_bytes() {
 template <int D, int G, View kView>
 struct Shape;
 // The tail view's CTAs come and go beside the prefix kernel's, so small ones pack better: 128 sequences behind 8192
-// tokens take 53.9 us a call with 4 warps, 54.9 with 2, 55.9 with 1, 60.8 with 8 (all with the partition count of two
-// waves; 56.8 with 8 in one wave).
+// tokens take 51.5 us a call with 4 warps, 51.9 with 2, 52.7 with 8.
 template <int G>
 struct Shape<128, G, View::kTail> {
   static constexpr int kWarps = 4;
@@ -661,6 +660,16 @@ __device__ __forceinline__ int pieces_of(const DecodeViewParams& p, long long to
   return most < p.num_partitions ? static_cast<int>(most) : p.num_partitions;
 }
 
+// Tail view: where piece w of a stream of `total` items begins.  CTAs start in their order, as SMs become free of the
+// prefix kernel, so the pieces get smaller, from 1.6 to 0.4 of their mean: the CTAs that start last are soon done (128
+// sequences behind one prefix 51.5 us, 150 behind five 70.8; from 1.5 51.9 and 70.5, from 1.9 53.5 and 73.2, all alike 57.7
+// and 71.6, and half as large and all alike 53.9 and 73.4).  With a mean of 6 items no piece is empty.
+__device__ __forceinline__ long long shrinking_bound(int w, long long total, int pieces) {
+  if (w >= pieces) return total;
+  const float x = static_cast<float>(w) / static_cast<float>(pieces);
+  return static_cast<long long>(static_cast<float>(total) * (x * (1.6f - 0.6f * x)));
+}
+
 // Walk of the flat (sequence, kv head, block) stream.
 struct Cursor {
   int b, kvh, blk, nblk;
@@ -790,8 +799,14 @@ __global__ void __launch_bounds__(NW * 32)
     leave();
     return;
   }
-  const long long begin = gw * total / num_pieces;
-  const long long end = (gw + 1) * total / num_pieces;
+  long long begin, end;
+  if (kView == View::kTail && total >= 6ll * num_pieces) {
+    begin = shrinking_bound(gw, total, num_pieces);
+    end = shrinking_bound(gw + 1, total, num_pieces);
+  } else {
+    begin = gw * total / num_pieces;
+    end = (gw + 1) * total / num_pieces;
+  }
   if (begin >= end) {
     leave();
     return;

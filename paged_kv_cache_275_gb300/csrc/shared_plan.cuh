@@ -14,7 +14,8 @@ constexpr int kPlanRows = 256;  // query rows of a unit (a tile pair)
 // Microseconds of a prefix CTA besides its steps and of a step, with two query tiles and with one, and bytes a
 // microsecond that an SM streams of a tail, beside busy neighbours and when all SMs stream; as measured (globaltimer
 // stamps in every CTA) with 128 sequences of 32 q / 8 kv heads behind 8192 shared tokens and with 150 of 64 / 8 in five
-// groups.  The times of these calls hardly depend on them: with half or twice the early rate 55.8 and 56.4 us against 54.9.
+// groups.  (The first call's time hardly depends on the step's, 52.0 us with 1.5 as with 2.3 against 51.9, but on the early
+// rate: 60.4 with 3e4, 54.0 with 8e4.)
 constexpr float kSharedCtaUs = 6.2f, kSharedStepUs = 1.85f, kSharedOneTileStepUs = 1.2f;
 constexpr float kTailEarlyRate = 5.4e4f, kTailLateRate = 4.2e4f;
 
