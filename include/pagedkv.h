@@ -394,7 +394,7 @@ pkv_status pkv_rope_append(const void* q, int64_t q_stride, const void* k, int64
  *
  * otherwise as pkv_paged_decode_attention_split with every phase.  Table entries of blocks that hold no visible
  * token are not read (they may be -1, so that a sequence's blocks can be freed once its window has passed them),
- * and what the other rows of a block hold does not matter.
+ * and what the other rows of a block hold does not matter.  num_blocks * num_kv_heads * 16 must be below 2^31.
  *
  *   window           >= 1: the newest tokens that are seen, the query's own among them
  *   num_sink_tokens  >= 0: the first tokens that stay visible
@@ -419,16 +419,17 @@ pkv_status pkv_window_decode_workspace_size(int32_t num_seqs, int32_t num_q_head
  * pkv_paged_prefill_attention_split (num_splits 1: no workspace), with scale > 0.
  *
  * Table entries of blocks that no row of the sequence's chunk sees are not read, and tokens that no row of the
- * chunk sees do not matter, whatever they hold.  A token that some rows see has to be finite: rows of the same
+ * chunk sees do not matter, whatever they hold.  num_query_tokens is the number of rows of q and out; a sequence whose
+ * chunk reaches outside them sets PKV_DEVERR_CONTEXT_LEN_TOO_LONG and is skipped.  A token that some rows see has to be finite: rows of the same
  * 128-row tile that do not see it weight it with 0, and 0 times infinity is no number.  (A CTA takes 256 / G
  * chunk tokens; it reads the blocks that its own rows see.)
  */
 pkv_status pkv_paged_window_prefill_attention(const void* q, const void* k_cache, const void* v_cache,
                                               const int32_t* block_tables, int32_t max_blocks_per_seq,
                                               const int32_t* context_lens, const int32_t* query_start,
-                                              int32_t max_query_len, int32_t num_seqs, int32_t num_q_heads,
-                                              int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks,
-                                              int32_t block_size, float scale, int32_t window,
+                                              int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs,
+                                              int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                              int64_t num_blocks, int32_t block_size, float scale, int32_t window,
                                               int32_t num_sink_tokens, void* out, int32_t num_splits, void* workspace,
                                               size_t workspace_bytes, pkv_stream_t stream);
 /* A split count for it: pkv_prefill_default_splits, but no more than leaves every split two steps of 128 keys.

@@ -123,7 +123,7 @@ def load(path: Path | str | None = None) -> ctypes.CDLL:
         lib.pkv_paged_window_decode_attention.argtypes = [V, V, V, V, I32, V, I32, I32, I32, I32, I64, I32, F32, I32,
                                                           I32, V, V, SZ, I32, V]
         lib.pkv_window_decode_workspace_size.argtypes = [I32] * 8 + [ctypes.POINTER(SZ)]
-        lib.pkv_paged_window_prefill_attention.argtypes = [V, V, V, V, I32, V, V, I32, I32, I32, I32, I32, I64, I32,
+        lib.pkv_paged_window_prefill_attention.argtypes = [V, V, V, V, I32, V, V, I64, I32, I32, I32, I32, I32, I64, I32,
                                                            F32, I32, I32, V, I32, V, SZ, V]
         lib.pkv_window_prefill_default_splits.argtypes = [I32] * 6 + [ctypes.POINTER(I32)]
         lib.pkv_paged_prefix_decode_attention.argtypes = [V, V, V, V, I32, V, V, V, I32, I32, I32, I32, I32, I64, I32,

@@ -355,7 +355,7 @@ PyObject* window_prefill(PyObject*, PyObject* const* a, Py_ssize_t) {
     }
     run([&] {
       return pkv_paged_window_prefill_attention(t.q, t.kc, t.vc, t.table, t.width, t.lens,
-                                                static_cast<const int32_t*>(start.data_ptr()), most, t.batch, t.hq,
+                                                static_cast<const int32_t*>(start.data_ptr()), t.rows, most, t.batch, t.hq,
                                                 t.hkv, t.d, t.blocks, t.block, static_cast<float>(scale), window, sinks,
                                                 t.out, splits, ws.data, ws.bytes, stream);
     });

@@ -223,6 +223,9 @@ static pkv_status decode_impl(const void* q, const void* k_cache, const void* v_
   if (phases < 1 || phases > PKV_PHASE_ALL) return fail(PKV_ERR_INVALID_ARGUMENT, "phases must be 1, 2 or 3");
   if (num_partitions < 0 || num_partitions > kMaxPartitions)
     return fail(PKV_ERR_INVALID_ARGUMENT, "num_partitions out of range (got %d)", num_partitions);
+  if (window.window && num_blocks * num_kv_heads * PKV_BLOCK_SIZE >= (int64_t{1} << 31))
+    return fail(PKV_ERR_UNSUPPORTED, "num_blocks * num_kv_heads * 16 must be below 2^31 (got %lld blocks)",
+                (long long)num_blocks);
   if (num_seqs == 0) return ok();
   int cluster = 0;  // CTAs a (sequence, kv head) of the form without a workspace
   if (window.window)
@@ -424,7 +427,7 @@ pkv_status prefill_impl(const void* q, const void* k_cache, const void* v_cache,
                         int32_t max_query_len, int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                         int32_t head_dim, int64_t num_blocks, int32_t block_size, float scale, void* out,
                         int32_t num_splits, void* workspace, size_t workspace_bytes, pkv_stream_t stream,
-                        const Window& window) {
+                        const Window& window, int64_t query_rows) {
   if (num_splits < 1 || num_splits > kMaxPrefillSplits)
     return fail(PKV_ERR_INVALID_ARGUMENT, "num_splits must be in [1, %d] (got %d)", kMaxPrefillSplits, num_splits);
   if (static_cast<int64_t>(num_seqs) * num_splits > 65535)
@@ -484,6 +487,7 @@ pkv_status prefill_impl(const void* q, const void* k_cache, const void* v_cache,
   const Window w = within_table(window, max_blocks_per_seq);
   p.window = w.window;
   p.sinks = w.sinks;
+  p.query_rows = query_rows;
   const cudaError_t e =
       (window.window ? pkv::launch_window_prefill : pkv::launch_paged_prefill)(
           p, head_dim, num_q_heads / num_kv_heads, max_query_len, reinterpret_cast<cudaStream_t>(stream));
@@ -501,7 +505,7 @@ pkv_status pkv_paged_prefill_attention(const void* q, const void* k_cache, const
                                        float scale, void* out, pkv_stream_t stream) {
   return prefill_impl(q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, query_start, max_query_len,
                       num_seqs, num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, scale, out, 1, nullptr, 0,
-                      stream, Window{});
+                      stream, Window{}, 0);
 }
 
 pkv_status pkv_paged_prefill_attention_split(const void* q, const void* k_cache, const void* v_cache,
@@ -513,7 +517,7 @@ pkv_status pkv_paged_prefill_attention_split(const void* q, const void* k_cache,
                                              void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
   return prefill_impl(q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, query_start, max_query_len,
                       num_seqs, num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, scale, out, num_splits,
-                      workspace, workspace_bytes, stream, Window{});
+                      workspace, workspace_bytes, stream, Window{}, 0);
 }
 
 pkv_status pkv_prefill_default_splits(int32_t num_seqs, int32_t max_query_len, int32_t num_q_heads,
@@ -749,16 +753,18 @@ pkv_status pkv_window_prefill_default_splits(int32_t num_seqs, int32_t max_query
 pkv_status pkv_paged_window_prefill_attention(const void* q, const void* k_cache, const void* v_cache,
                                               const int32_t* block_tables, int32_t max_blocks_per_seq,
                                               const int32_t* context_lens, const int32_t* query_start,
-                                              int32_t max_query_len, int32_t num_seqs, int32_t num_q_heads,
-                                              int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks,
-                                              int32_t block_size, float scale, int32_t window,
+                                              int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs,
+                                              int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                              int64_t num_blocks, int32_t block_size, float scale, int32_t window,
                                               int32_t num_sink_tokens, void* out, int32_t num_splits, void* workspace,
                                               size_t workspace_bytes, pkv_stream_t stream) {
   if (pkv_status st = check_window(window, num_sink_tokens); st != PKV_OK) return st;
   if (!(scale > 0.f)) return fail(PKV_ERR_INVALID_ARGUMENT, "scale must be positive");
+  if (num_query_tokens < 0)
+    return fail(PKV_ERR_INVALID_ARGUMENT, "num_query_tokens must be >= 0 (got %lld)", (long long)num_query_tokens);
   return prefill_impl(q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, query_start, max_query_len,
                       num_seqs, num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, scale, out, num_splits,
-                      workspace, workspace_bytes, stream, Window{window, num_sink_tokens});
+                      workspace, workspace_bytes, stream, Window{window, num_sink_tokens}, num_query_tokens);
 }
 
 namespace {

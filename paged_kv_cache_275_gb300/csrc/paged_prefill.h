@@ -30,6 +30,7 @@ struct PrefillParams {
   // Window: a row sees its last `window` tokens and the first `sinks` (both at most 16 * max_blocks_per_seq).
   int window = 0;
   int sinks = 0;
+  int64_t query_rows = 0;  // rows of q and out: no chunk may reach past them
   // Shared prefixes (one query token a sequence; q and out rows are sequences): groups of consecutive
   // sequences and the tokens they share.  ws: [CTA][256 rows]: D floats of O; then the same index: (m, l).
   const int32_t* group_start = nullptr;  // [num_groups + 1]

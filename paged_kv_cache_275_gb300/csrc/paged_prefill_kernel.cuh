@@ -497,7 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if constexpr (kMask != Mask::kShared) {
     const int cap = p.max_blocks_per_seq * kBlockTokens;
-    if (C < 0 || L < C || L > cap) {
+    const bool outside = kMask == Mask::kWindow && (q0 < 0 || static_cast<int64_t>(q0) + C > p.query_rows);
+    if (C < 0 || L < C || L > cap || outside) {
       if (tid == 0 && tile == 0) atomicOr(p.err, kErrLenTooLong);
       return;
     }
@@ -1149,7 +1150,8 @@ __global__ void __launch_bounds__(256, 4) window_prefill_merge_kernel(const Pref
   const int q0 = p.query_start[b];
   const int C = p.query_start[b + 1] - q0;
   const int L = p.context_lens[b];
-  if (C < 0 || L < C || L > p.max_blocks_per_seq * kBlockTokens) return;  // flagged by the attention kernel
+  if (C < 0 || L < C || L > p.max_blocks_per_seq * kBlockTokens || q0 < 0 || static_cast<int64_t>(q0) + C > p.query_rows)
+    return;  // flagged by the attention kernel
   const int rows = min(C, p.ws_rows) * p.num_q_heads;
   const size_t split_stride = static_cast<size_t>(p.num_seqs) * p.ws_rows * p.num_q_heads;  // rows per split
   const float2* ml = reinterpret_cast<const float2*>(p.ws + static_cast<size_t>(p.num_splits) * split_stride * D);

@@ -28,9 +28,6 @@ struct SharedPlan {
   bool fine;        // every group's bounds are in order: group_start starts at 0 or above, does not fall, and ends at
                     // num_seqs or below
   int split_steps;  // most key steps of a split; 0: nothing is shared
-  int ctas;         // CTAs that takes
-  float us;         // about how long they run
-  float tail;       // about how many bytes of K and V follow the shared blocks
 };
 
 // One instance a head dim and group size: the plan of a call, worked out by a whole warp.
@@ -97,30 +94,39 @@ struct SharedPlanner {
       work += __shfl_xor_sync(kAll, work, off);
       tokens += __shfl_xor_sync(kAll, tokens, off);
     }
-    r.tail = fmaxf(tokens, 0.f) * (4.f * D) * num_kv_heads;
+    const float tail = fmaxf(tokens, 0.f) * (4.f * D) * num_kv_heads;  // about how many bytes follow the shared blocks
     if (!r.fine || work == 0.f) return r;
-    // The lane's candidate s: from the least that could fit on, an eighth of it apart; the last is the longest unit.
-    const int least_s = max(1, static_cast<int>(work / grid));
-    const int s = lane == 31 ? most : min(most, least_s + lane * ((least_s + 7) / 8));
-    int n = 0;  // its CTAs
-    for (int g0 = 0; g0 < num_groups; g0 += 32) {
-      const SharedGroup x = g0 == 0 ? mine : group(g0 + lane);
-      const int u = units(x), t = steps(x);
-      for (int k = 0; k < min(32, num_groups - g0); ++k)
-        n += __shfl_sync(kAll, u, k) * ((__shfl_sync(kAll, t, k) + s - 1) / s);
+    const int least_s = min(most, max(1, static_cast<int>(work / grid)));
+    if (num_groups > 32) {  // many groups: the least s that fits, with a group a lane at a time (the longest unit's does)
+      int lo = least_s, hi = most;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        int n = 0;
+        for (int g0 = 0; g0 < num_groups; g0 += 32) {
+          const SharedGroup x = group(g0 + lane);
+          n += units(x) * ((steps(x) + mid - 1) / mid);
+        }
+        if (__reduce_add_sync(kAll, n) <= grid) hi = mid;
+        else lo = mid + 1;
+      }
+      r.split_steps = lo;
+      return r;
     }
+    // The lane's candidate s: from the least that could fit on, an eighth of it apart; the last is the longest unit.
+    const int s = lane == 31 ? most : min(most, least_s + lane * ((least_s + 7) / 8));
+    const int u = units(mine), t = steps(mine);
+    int n = 0;  // its CTAs
+    for (int k = 0; k < num_groups; ++k)
+      n += __shfl_sync(kAll, u, k) * ((__shfl_sync(kAll, t, k) + s - 1) / s);
     const int waves = (n + num_sms - 1) / num_sms;
     const float us = waves * (kSharedCtaUs + s * (two_tiles ? kSharedStepUs : kSharedOneTileStepUs));
     const float beside = max(num_sms - n, 0) * kTailEarlyRate * us;
-    float cost = us + fmaxf(r.tail - beside, 0.f) / (num_sms * kTailLateRate);
+    float cost = us + fmaxf(tail - beside, 0.f) / (num_sms * kTailLateRate);
     if (n > grid) cost = INFINITY;  // does not fit
     float best = cost;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) best = fminf(best, __shfl_xor_sync(kAll, best, off));
-    const int winner = __ffs(__ballot_sync(kAll, cost == best)) - 1;
-    r.split_steps = __shfl_sync(kAll, s, winner);
-    r.ctas = __shfl_sync(kAll, n, winner);
-    r.us = __shfl_sync(kAll, us, winner);
+    r.split_steps = __shfl_sync(kAll, s, __ffs(__ballot_sync(kAll, cost == best)) - 1);
     return r;
   }
 };

@@ -95,7 +95,7 @@ def test_no_groups_is_plain_decode(width):
     run([], (50, 0, 140), 8, 2, 64, width, seed=5)
 
 
-@pytest.mark.parametrize("count", [31, 33, 70])
+@pytest.mark.parametrize("count", [31, 32, 33, 70, 400])
 @both_forms
 def test_many_groups(count, width):
     """More groups than a warp has lanes, of all lengths."""
@@ -210,6 +210,28 @@ def test_back_to_back_calls_graphs_and_streams(width):
         for g in graphs:
             g.replay()
     check("replayed")
+    assert device_errors() == 0
+
+
+@both_forms
+def test_blocks_at_the_end_of_a_large_cache(width):
+    """Element offsets past 32 bits: 2.3e9 elements a cache, every block used near its end."""
+    groups, lens = [(0, 3, 100)], (130, 101, 115)
+    pages, real = make(groups, lens, 8, 128, 31, width)
+    q = pages.randn(3, 16, 128)
+    ref, allowed = exact(pages, real, q, lens, 0.1)
+    kc, vc, table, cl = pages.cuda()
+    blocks = 140_000
+    big = [torch.empty(blocks, 8, BLOCK, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    shift = blocks - pages.pool
+    for b, c in zip(big, (kc, vc)):
+        b[shift:] = c
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = torch.empty(q.shape, dtype=q.dtype, device="cuda")
+    moved = torch.where(table >= 0, table + shift, table)
+    pkv.paged_prefix_decode_attention(q.cuda(), *big, moved, cl, torch.tensor([0, 3], **i32), torch.tensor([100], **i32),
+                                      0.1, out)
+    assert_within(out, ref, allowed, "large cache")
     assert device_errors() == 0
 
 

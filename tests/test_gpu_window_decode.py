@@ -195,6 +195,54 @@ def test_two_streams_at_once(parts):
     assert device_errors() == 0
 
 
+@pytest.mark.parametrize("parts", [0, 20])
+@pytest.mark.parametrize("hq", [8, 32])
+def test_blocks_at_the_end_of_a_large_cache(parts, hq):
+    """Element offsets past 32 bits: 2.3e9 elements a cache."""
+    lens = (300, 20)
+    pages = Pages(lens, 8, 128, 23)
+    q = pages.randn(2, hq, 128)
+    ref, allowed = exact(pages, q, lens, 100, 4, 0.09)
+    kc, vc, table, cl = pages.cuda()
+    blocks = 140_000
+    big = [torch.empty(blocks, 8, BLOCK, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for b, c in zip(big, (kc, vc)):
+        b[blocks - pages.pool:] = c
+    out = torch.empty(q.shape, dtype=q.dtype, device="cuda")
+    pkv.paged_window_decode_attention(q.cuda(), *big, torch.where(table >= 0, table + (blocks - pages.pool), table), cl,
+                                      0.09, out, 100, 4, num_partitions=parts)
+    assert_within(out, ref, allowed, "large cache")
+    assert device_errors() == 0
+
+
+def test_threads_on_one_stream_keep_their_workspaces_apart():
+    """Host threads whose calls interleave on one stream: each has a workspace of its own."""
+    import threading
+    cases = []
+    for k in range(3):
+        lens = (500 + k, 40, 300 - k)
+        pages = Pages(lens, 2, 64, 40 + k)
+        q = pages.randn(3, 8, 64)
+        cases.append((exact(pages, q, lens, 200, 4, 0.09), q.cuda(), pages.cuda(),
+                      torch.zeros(q.shape, dtype=q.dtype, device="cuda")))
+
+    def work(case):
+        _, q, (kc, vc, table, cl), out = case
+        for _ in range(50):
+            pkv.paged_window_decode_attention(q, kc, vc, table, cl, 0.09, out, 200, 4, num_partitions=30)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(c,)) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for (ref, allowed), _, _, out in cases:
+        assert_within(out, ref, allowed, "threads")
+    assert device_errors() == 0
+
+
 def test_refusals():
     pages = Pages((20, 40), 1, 64, 3)
     q = pages.randn(2, 2, 64).cuda()

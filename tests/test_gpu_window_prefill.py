@@ -161,6 +161,40 @@ def test_bad_lengths_and_blocks_are_flagged():
     assert device_errors() == pkv.DEVERR_BLOCK_ID_OUT_OF_RANGE
 
 
+@pytest.mark.parametrize("splits", [1, 2])
+@pytest.mark.parametrize("start", [[0, 20, 41], [0, 41, 20], [-1, 20, 40], [20, 40, 60]])
+def test_chunks_outside_the_query_rows_are_flagged_and_skipped(start, splits):
+    pages, lens, _, q = make((20, 20), (50, 60), 4, 2, 64, 16, 2, 9, hidden=False)
+    kc, vc, table, cl = pages.cuda()
+    out = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+    assert device_errors() == 0
+    pkv.paged_window_prefill_attention(q.cuda(), kc, vc, table, cl, torch.tensor(start, dtype=torch.int32, device="cuda"),
+                                       41, 0.1, out, 16, 2, num_splits=splits)
+    assert device_errors() == pkv.DEVERR_CONTEXT_LEN_TOO_LONG
+    if start == [0, 20, 41]:  # the first chunk is in order
+        ref, allowed = exact(pages, q, [0, 20, 40], lens, 16, 2, 0.1)
+        assert_within(out[:20], ref[:20], allowed[:20], "the other chunk")
+        assert (out[20:] == 5.0).all()
+
+
+@pytest.mark.parametrize("splits", [1, 3])
+def test_blocks_at_the_end_of_a_large_cache(splits):
+    """Element offsets past 32 bits: 2.3e9 elements a cache."""
+    pages, lens, start, q = make((40,), (150,), 16, 8, 128, 100, 4, 17)
+    ref, allowed = exact(pages, q, start, lens, 100, 4, 0.1)
+    kc, vc, table, cl = pages.cuda()
+    blocks = 140_000
+    big = [torch.empty(blocks, 8, BLOCK, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for b, c in zip(big, (kc, vc)):
+        b[blocks - pages.pool:] = c
+    out = torch.empty(q.shape, dtype=q.dtype, device="cuda")
+    pkv.paged_window_prefill_attention(q.cuda(), *big, torch.where(table >= 0, table + (blocks - pages.pool), table), cl,
+                                       torch.tensor(start, dtype=torch.int32, device="cuda"), 40, 0.1, out, 100, 4,
+                                       num_splits=splits)
+    assert_within(out, ref, allowed, "large cache")
+    assert device_errors() == 0
+
+
 @pytest.mark.parametrize("splits", [1, 0])
 def test_graph_and_stream(splits):
     pages, lens, start, q = make((64, 9), (300, 80), 8, 2, 128, 100, 4, 13)

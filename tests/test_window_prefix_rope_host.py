@@ -56,6 +56,7 @@ def window_decode(lib, **kw):
     (dict(hq=30), 1, "multiple"), (dict(hq=24, hkv=2), 2, "group"), (dict(d=256), 2, "head_dim"), (dict(bs=8), 2, "block_size"),
     (dict(B=-1), 1, "num_seqs"), (dict(W=0), 1, "max_blocks"), (dict(nb=0), 1, "num_blocks"),
     (dict(scale=float("nan")), 1, "scale"), (dict(parts=-1), 1, "num_partitions"), (dict(out=None), 1, "null"),
+    (dict(nb=1 << 24), 2, "2^31"),
     (dict(q=FAKE + 2), 1, "aligned"), (dict(), 1, "workspace too small"), (dict(B=5000), 1, "workspace too small"),
 ])
 def test_window_decode_refuses(lib, kw, status, says):
@@ -79,7 +80,7 @@ def test_window_decode_workspace_size(lib):
 
 
 def window_prefill(lib, **kw):
-    a = dict(q=FAKE, kc=FAKE, vc=FAKE, bt=FAKE, W=8, cl=FAKE, qs=FAKE, mql=512, B=4, hq=32, hkv=8, d=128, nb=100,
+    a = dict(q=FAKE, kc=FAKE, vc=FAKE, bt=FAKE, W=8, cl=FAKE, qs=FAKE, T=2048, mql=512, B=4, hq=32, hkv=8, d=128, nb=100,
              bs=16, scale=0.088, window=64, sinks=4, out=FAKE, S=1, ws=None, wsb=0, stream=None)
     assert set(kw) <= set(a)
     return lib.pkv_paged_window_prefill_attention(*{**a, **kw}.values())
@@ -91,7 +92,7 @@ def window_prefill(lib, **kw):
     (dict(B=65536), 2, "65535"), (dict(mql=65535 * 64 + 1), 2, "max_query_len"), (dict(mql=-1), 1, "max_query_len"),
     (dict(S=0), 1, "num_splits"), (dict(S=33), 1, "num_splits"), (dict(S=2), 1, "workspace too small"),
     (dict(S=2, ws=FAKE, wsb=16), 1, "workspace too small"), (dict(S=2, ws=FAKE + 8, wsb=1 << 40), 1, "aligned"),
-    (dict(q=None), 1, "null"), (dict(d=32), 2, "head_dim"), (dict(hq=48, hkv=3), 2, "group"),
+    (dict(q=None), 1, "null"), (dict(d=32), 2, "head_dim"), (dict(hq=48, hkv=3), 2, "group"), (dict(T=-1), 1, "num_query_tokens"),
 ])
 def test_window_prefill_refuses(lib, kw, status, says):
     assert window_prefill(lib, **kw) == status and says in msg(lib)
