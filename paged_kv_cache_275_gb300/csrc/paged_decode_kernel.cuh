@@ -47,7 +47,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <climits>
 #include <cstdint>
 #include <mutex>
 #include <type_traits>

@@ -11,13 +11,15 @@ namespace {
 constexpr int kPlanKeys = 128;  // keys of a step
 constexpr int kPlanRows = 256;  // query rows of a unit (a tile pair)
 
-// Microseconds of a prefix CTA besides its steps and of a step, with two query tiles and with one, and bytes a
-// microsecond that an SM streams of a tail, beside busy neighbours and when all SMs stream; as measured (globaltimer
-// stamps in every CTA) with 128 sequences of 32 q / 8 kv heads behind 8192 shared tokens and with 150 of 64 / 8 in five
-// groups.  (The first call's time hardly depends on the step's, 52.0 us with 1.5 as with 2.3 against 51.9, but on the early
-// rate: 60.4 with 3e4, 54.0 with 8e4.)
-constexpr float kSharedCtaUs = 6.2f, kSharedStepUs = 1.85f, kSharedOneTileStepUs = 1.2f;
-constexpr float kTailEarlyRate = 5.4e4f, kTailLateRate = 4.2e4f;
+// The plan's estimate: microseconds of a prefix CTA besides its steps and of a step, with two query tiles and with one;
+// bytes a microsecond that an SM streams of a tail, beside the prefix and when all SMs stream; and microseconds that a
+// tail which outlasts the prefix takes to get going.  Chosen so that the splits they lead to are near the best of all
+// splits, measured over twelve calls (32 to 128 sequences, one to six groups, prefixes of 500 to 16384 tokens, 1 to 8 kv
+// heads), and tried on twelve others: 42.6 us in the geometric mean of the 24, against 43.4 with the times and rates that
+// globaltimer stamps in the CTAs gave (6.2, 1.85, 1.2, 5.4e4, 4.2e4, 0), 42.8 with (6.2, 1.6, 1.1, 3.6e4, 3.6e4, 0) and
+// 42.5, but up to 10 % more for single calls, with (4, 2.1, 1.4, 3e4, 2.8e4, 4).
+constexpr float kSharedCtaUs = 4.f, kSharedStepUs = 1.85f, kSharedOneTileStepUs = 1.f;
+constexpr float kTailEarlyRate = 3.8e4f, kTailLateRate = 3.6e4f, kTailLateUs = 2.f;
 
 struct SharedGroup {
   int first, rows, keys;  // its sequences, and the tokens of its shared blocks
@@ -120,8 +122,8 @@ struct SharedPlanner {
       n += __shfl_sync(kAll, u, k) * ((__shfl_sync(kAll, t, k) + s - 1) / s);
     const int waves = (n + num_sms - 1) / num_sms;
     const float us = waves * (kSharedCtaUs + s * (two_tiles ? kSharedStepUs : kSharedOneTileStepUs));
-    const float beside = max(num_sms - n, 0) * kTailEarlyRate * us;
-    float cost = us + fmaxf(tail - beside, 0.f) / (num_sms * kTailLateRate);
+    const float behind = tail - max(num_sms - n, 0) * kTailEarlyRate * us;
+    float cost = us + (behind > 0.f ? kTailLateUs + behind / (num_sms * kTailLateRate) : 0.f);
     if (n > grid) cost = INFINITY;  // does not fit
     float best = cost;
 #pragma unroll
