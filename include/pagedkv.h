@@ -416,13 +416,18 @@ pkv_status pkv_window_decode_workspace_size(int32_t num_seqs, int32_t num_q_head
 /*
  * Chunked paged prefill attention with a sliding window and sinks: query row i of sequence b's chunk, at position
  * P = P_b + i, sees the cached tokens j <= P with j > P - window or j < num_sink_tokens.  Otherwise as
- * pkv_paged_prefill_attention_split (num_splits 1: no workspace), with scale > 0.
+ * pkv_paged_prefill_attention, with scale > 0.
+ *
+ * A CTA takes a tile pair (256 / G tokens of a chunk, G = num_q_heads / num_kv_heads) and a kv head.  With num_splits > 1
+ * a call that leaves half the SMs or more without one has a tile pair's keys split over up to num_splits CTAs, in fp32
+ * states that a second kernel joins; that needs the workspace.  (Calls of more than 320 sequences are not split, and need
+ * none.)
  *
  * Table entries of blocks that no row of the sequence's chunk sees are not read, and tokens that no row of the
  * chunk sees do not matter, whatever they hold.  num_query_tokens is the number of rows of q and out; a sequence whose
  * chunk reaches outside them sets PKV_DEVERR_CONTEXT_LEN_TOO_LONG and is skipped.  A token that some rows see has to be finite: rows of the same
- * 128-row tile that do not see it weight it with 0, and 0 times infinity is no number.  (A CTA takes 256 / G
- * chunk tokens; it reads the blocks that its own rows see.)
+ * 128-row tile that do not see it weight it with 0, and 0 times infinity is no number.  (A CTA reads the
+ * blocks that its own rows see.)
  */
 pkv_status pkv_paged_window_prefill_attention(const void* q, const void* k_cache, const void* v_cache,
                                               const int32_t* block_tables, int32_t max_blocks_per_seq,
@@ -432,11 +437,12 @@ pkv_status pkv_paged_window_prefill_attention(const void* q, const void* k_cache
                                               int64_t num_blocks, int32_t block_size, float scale, int32_t window,
                                               int32_t num_sink_tokens, void* out, int32_t num_splits, void* workspace,
                                               size_t workspace_bytes, pkv_stream_t stream);
-/* A split count for it: pkv_prefill_default_splits, but no more than leaves every split two steps of 128 keys.
-   The workspace of a count is pkv_prefill_workspace_size. */
+/* A split count for it: as many as leave every split two steps of 128 keys, 32 at most. */
 pkv_status pkv_window_prefill_default_splits(int32_t num_seqs, int32_t max_query_len, int32_t num_q_heads,
                                              int32_t num_kv_heads, int32_t window, int32_t num_sink_tokens,
                                              int32_t* num_splits);
+/* Its workspace: the same for every count above 1, whatever the call's size; 0 for a count of 1. */
+pkv_status pkv_window_prefill_workspace_size(int32_t head_dim, int32_t num_splits, size_t* bytes);
 
 /*
  * Paged decode attention for groups of sequences that share a prefix (forks of one prompt, requests behind one

@@ -59,6 +59,7 @@ EXPORTS = (
     "pkv_window_decode_workspace_size",
     "pkv_paged_window_prefill_attention",
     "pkv_window_prefill_default_splits",
+    "pkv_window_prefill_workspace_size",
     "pkv_paged_prefix_decode_attention",
     "pkv_prefix_decode_workspace_size",
     "pkv_bm_create",
@@ -126,6 +127,7 @@ def load(path: Path | str | None = None) -> ctypes.CDLL:
         lib.pkv_paged_window_prefill_attention.argtypes = [V, V, V, V, I32, V, V, I64, I32, I32, I32, I32, I32, I64, I32,
                                                            F32, I32, I32, V, I32, V, SZ, V]
         lib.pkv_window_prefill_default_splits.argtypes = [I32] * 6 + [ctypes.POINTER(I32)]
+        lib.pkv_window_prefill_workspace_size.argtypes = [I32, I32, ctypes.POINTER(SZ)]
         lib.pkv_paged_prefix_decode_attention.argtypes = [V, V, V, V, I32, V, V, V, I32, I32, I32, I32, I32, I64, I32,
                                                           F32, V, V, SZ, V]
         lib.pkv_prefix_decode_workspace_size.argtypes = [I32] * 6 + [ctypes.POINTER(SZ)]
@@ -149,7 +151,8 @@ def load(path: Path | str | None = None) -> ctypes.CDLL:
                      "pkv_bm_append_slots", "pkv_bm_fork", "pkv_bm_free_sequence", "pkv_bm_block_tables",
                      "pkv_bm_ref_count", "pkv_rope_append", "pkv_paged_window_decode_attention",
                      "pkv_window_decode_workspace_size", "pkv_paged_window_prefill_attention",
-                     "pkv_window_prefill_default_splits", "pkv_paged_prefix_decode_attention",
+                     "pkv_window_prefill_default_splits", "pkv_window_prefill_workspace_size",
+                     "pkv_paged_prefix_decode_attention",
                      "pkv_prefix_decode_workspace_size"):
             getattr(lib, name).restype = ctypes.c_int
         lib.pkv_last_error_message.argtypes = []
@@ -555,6 +558,11 @@ def window_prefill_default_splits(num_seqs: int, max_query_len: int, num_q_heads
                   num_kv_heads, window, num_sink_tokens)
 
 
+def window_prefill_workspace_size(head_dim: int, num_splits: int) -> int:
+    """Bytes of the workspace of a windowed prefill call, of any size."""
+    return _query(ctypes.c_size_t, load().pkv_window_prefill_workspace_size, head_dim, num_splits)
+
+
 def rope_freq_axes(sections) -> bytes:
     """freq_axes of rope_append for frequencies dealt to the axes in order: sections[a] of them turn by axis a."""
     return b"".join(bytes([axis]) * count for axis, count in enumerate(sections))
@@ -595,8 +603,9 @@ def paged_window_prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cac
                                    stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """paged_prefill_attention where a row sees its last ``window`` tokens and the first ``num_sink_tokens``.
 
-    ``num_splits`` 0 takes ``window_prefill_default_splits``; a count above 1 needs a workspace of
-    ``prefill_workspace_size`` bytes, allocated here if not given.  Returns ``out``.
+    ``num_splits`` is the most CTAs that a tile pair's keys are split over when the call has few of them; 0 takes
+    ``window_prefill_default_splits``.  Above 1 it needs a workspace of ``window_prefill_workspace_size`` bytes, allocated
+    here if not given.  Returns ``out``.
     """
     return (_binding or _native()).window_prefill(q, k_cache, v_cache, block_tables, context_lens, query_start,
                                                   max_query_len, scale, out, window, num_sink_tokens, num_splits,

@@ -350,7 +350,7 @@ PyObject* window_prefill(PyObject*, PyObject* const* a, Py_ssize_t) {
     Workspace ws;
     if (splits > 1) {
       size_t need = 0;
-      check(pkv_prefill_workspace_size(t.batch, most, t.hq, t.hkv, t.d, splits, &need));
+      check(pkv_window_prefill_workspace_size(t.d, splits, &need));
       ws.take(a[12], t.dev, a[13], stream, need);
     }
     run([&] {

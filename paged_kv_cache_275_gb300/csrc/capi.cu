@@ -455,15 +455,19 @@ pkv_status prefill_impl(const void* q, const void* k_cache, const void* v_cache,
       (reinterpret_cast<uintptr_t>(block_tables) & 3u) || (reinterpret_cast<uintptr_t>(context_lens) & 3u) ||
       (reinterpret_cast<uintptr_t>(query_start) & 3u))
     return fail(PKV_ERR_INVALID_ARGUMENT, "q, caches and out must be 16-byte aligned");
+  if (window.window && num_seqs > pkv::kPrefillRankedSeqs) num_splits = 1;  // its units are not split
+  const pkv::WindowSplitLayout layout(head_dim, num_splits);
   if (num_splits > 1) {
     const size_t need =
-        pkv::prefill_workspace_bytes(num_seqs, max_query_len, num_q_heads, num_kv_heads, head_dim, num_splits);
+        window.window ? layout.bytes
+                      : pkv::prefill_workspace_bytes(num_seqs, max_query_len, num_q_heads, num_kv_heads, head_dim, num_splits);
     if (!workspace || workspace_bytes < need)
       return fail(PKV_ERR_INVALID_ARGUMENT, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, need);
     if (!aligned16(workspace)) return fail(PKV_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
   }
   unsigned* err = nullptr;
-  if (pkv_status st = device_state(&err, nullptr); st != PKV_OK) return st;
+  int sms = 0;
+  if (pkv_status st = device_state(&err, &sms); st != PKV_OK) return st;
   pkv::PrefillParams p{};
   p.q = q;
   p.k_cache = k_cache;
@@ -483,7 +487,10 @@ pkv_status prefill_impl(const void* q, const void* k_cache, const void* v_cache,
   if (num_splits > 1) {
     p.num_splits = num_splits;
     p.ws = static_cast<float*>(workspace);
+    p.ws_units = reinterpret_cast<int4*>(static_cast<unsigned char*>(workspace) + layout.units);
+    p.ws_count = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(workspace) + layout.count);
   }
+  p.num_sms = sms < pkv::kWindowSplitCtas ? sms : pkv::kWindowSplitCtas;
   const Window w = within_table(window, max_blocks_per_seq);
   p.window = w.window;
   p.sinks = w.sinks;
@@ -492,7 +499,13 @@ pkv_status prefill_impl(const void* q, const void* k_cache, const void* v_cache,
       (window.window ? pkv::launch_window_prefill : pkv::launch_paged_prefill)(
           p, head_dim, num_q_heads / num_kv_heads, max_query_len, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "prefill kernel launch");
-  g_launches.fetch_add(num_splits > 1 ? 2 : 1);
+  if (window.window) {
+    g_launches.fetch_add(pkv::window_splits(p, num_q_heads / num_kv_heads, max_query_len)
+                             ? 2
+                             : (num_seqs + pkv::kPrefillRankedSeqs - 1) / pkv::kPrefillRankedSeqs);
+  } else {
+    g_launches.fetch_add(num_splits > 1 ? 2 : 1);
+  }
   return ok();
 }
 }  // namespace
@@ -739,14 +752,19 @@ pkv_status pkv_window_prefill_default_splits(int32_t num_seqs, int32_t max_query
   if (num_seqs < 0 || max_query_len < 0) return fail(PKV_ERR_INVALID_ARGUMENT, "num_seqs and max_query_len must be >= 0");
   if (pkv_status st = check_shapes(num_seqs, num_seqs, num_q_heads, num_kv_heads, 128, 1); st != PKV_OK) return st;
   if (pkv_status st = check_window(window, num_sink_tokens); st != PKV_OK) return st;
-  int sms = 0;
-  if (pkv_status st = device_state(nullptr, &sms); st != PKV_OK) return st;
-  int32_t n = one_wave_splits(num_seqs, max_query_len, num_q_heads, num_kv_heads, sms);
   // At least two key steps a split: a CTA's rows see at most its tokens' windows and the sinks.
   const int64_t keys = static_cast<int64_t>(window) + num_sink_tokens + pkv::prefill_cta_tokens(num_q_heads / num_kv_heads);
   const int64_t most = (keys + 128 * kMinSplitSteps - 1) / (128 * kMinSplitSteps);
-  if (n > most) n = static_cast<int32_t>(most);
-  *num_splits = n;
+  *num_splits = num_seqs > pkv::kPrefillRankedSeqs ? 1 : static_cast<int32_t>(most < kMaxPrefillSplits ? most : kMaxPrefillSplits);
+  return ok();
+}
+
+pkv_status pkv_window_prefill_workspace_size(int32_t head_dim, int32_t num_splits, size_t* bytes) {
+  if (!bytes) return fail(PKV_ERR_INVALID_ARGUMENT, "bytes is null");
+  if (pkv_status st = check_shapes(1, 1, 1, 1, head_dim, 1); st != PKV_OK) return st;
+  if (num_splits < 1 || num_splits > kMaxPrefillSplits)
+    return fail(PKV_ERR_INVALID_ARGUMENT, "num_splits must be in [1, %d] (got %d)", kMaxPrefillSplits, num_splits);
+  *bytes = pkv::WindowSplitLayout(head_dim, num_splits).bytes;
   return ok();
 }
 

@@ -83,6 +83,21 @@ def test_splits(splits):
     run((70, 1, 300), (900, 40, 0), 4, 1, 128, 333, 9, seed=splits, num_splits=splits)
 
 
+@pytest.mark.parametrize("splits", [0, 1, 5])
+@pytest.mark.parametrize("tiles", [19, 20, 28, 29, 38])
+def test_last_waves(tiles, splits):
+    """Eight kv heads and chunks of `tiles` tile pairs (32 tokens each) in all, the first and last rows of them ragged:
+    152 SMs are full, have 8, 72 and 80 units in a second wave, and are full twice."""
+    a = tiles // 3
+    run((32 * a - 5, 3, 32 * (tiles - a - 1) - 31), (100, 700, 0), 64, 8, 64, 300, 4, seed=tiles, num_splits=splits)
+
+
+@pytest.mark.parametrize("splits", [0, 3])
+def test_more_sequences_than_are_ranked(splits):
+    for n in (320, 321):
+        run([1 + i % 3 for i in range(n)], [(7 * i) % 60 for i in range(n)], 2, 1, 64, 20, 2, seed=n, num_splits=splits)
+
+
 @pytest.mark.parametrize("seed", range(6))
 def test_random_shapes(seed):
     import random

@@ -110,6 +110,25 @@ def test_window_prefill_default_splits_checks_arguments_before_the_device(lib):
     assert splits(-1, 512, 32, 8, 64, 4, ctypes.byref(n)) == 1
 
 
+@pytest.mark.parametrize("window,sinks,want", [(1, 0, 1), (192, 0, 1), (193, 0, 2), (192, 1, 2), (1024, 0, 5), (1 << 30, 0, 32)])
+def test_window_prefill_default_splits(lib, window, sinks, want):
+    """Two steps of 128 keys each for the window, the sinks and the 64 tokens of a tile pair."""
+    n = ctypes.c_int32(0)
+    assert lib.pkv_window_prefill_default_splits(1, 512, 32, 8, window, sinks, ctypes.byref(n)) == 0 and n.value == want
+    assert lib.pkv_window_prefill_default_splits(321, 512, 32, 8, window, sinks, ctypes.byref(n)) == 0 and n.value == 1
+
+
+def test_window_prefill_workspace_size(lib):
+    n = ctypes.c_size_t(0)
+    size = lib.pkv_window_prefill_workspace_size
+    assert size(128, 1, ctypes.byref(n)) == 0 and n.value == 0
+    for d in (64, 128):
+        for splits in (2, 32):
+            assert size(d, splits, ctypes.byref(n)) == 0 and n.value == 160 * 256 * (d + 2) * 4 + 80 * 16 + 16
+    assert size(96, 2, ctypes.byref(n)) == 2 and size(128, 0, ctypes.byref(n)) == 1 and size(128, 33, ctypes.byref(n)) == 1
+    assert size(128, 2, None) == 1
+
+
 def prefix_decode(lib, **kw):
     a = dict(q=FAKE, kc=FAKE, vc=FAKE, bt=FAKE, W=8, cl=FAKE, gs=FAKE, pl=FAKE, groups=2, B=4, hq=32, hkv=8, d=128,
              nb=100, bs=16, scale=0.088, out=FAKE, ws=FAKE, wsb=16, stream=None)
