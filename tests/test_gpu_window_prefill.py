@@ -92,6 +92,13 @@ def test_last_waves(tiles, splits):
     run((32 * a - 5, 3, 32 * (tiles - a - 1) - 31), (100, 700, 0), 64, 8, 64, 300, 4, seed=tiles, num_splits=splits)
 
 
+@pytest.mark.parametrize("d,window,sinks", [(64, 20, 3), (128, 140, 30), (64, 1, 0), (128, 500, 200)])
+def test_many_rounds_of_short_units(d, window, sinks):
+    """100 chunks of one to five tokens and eight kv heads: 800 units, one to six key steps each, five or six a CTA, with keys
+    past the end and between sinks and window in most."""
+    run([1 + i % 5 for i in range(100)], [(37 * i) % 700 for i in range(100)], 8, 8, d, window, sinks, seed=d + window)
+
+
 @pytest.mark.parametrize("splits", [0, 3])
 def test_more_sequences_than_are_ranked(splits):
     for n in (320, 321):
