@@ -425,9 +425,9 @@ pkv_status pkv_window_decode_workspace_size(int32_t num_seqs, int32_t num_q_head
  *
  * Table entries of blocks that no row of the sequence's chunk sees are not read, and tokens that no row of the
  * chunk sees do not matter, whatever they hold.  num_query_tokens is the number of rows of q and out; a sequence whose
- * chunk reaches outside them sets PKV_DEVERR_CONTEXT_LEN_TOO_LONG and is skipped.  A token that some rows see has to be finite: rows of the same
- * 128-row tile that do not see it weight it with 0, and 0 times infinity is no number.  (A CTA reads the
- * blocks that its own rows see.)
+ * chunk reaches outside them sets PKV_DEVERR_CONTEXT_LEN_TOO_LONG and is skipped.  A token that some rows see has to be
+ * finite: rows of the same 128-row tile that do not see it weight it with 0, and 0 times infinity is no number.  (A CTA
+ * reads the blocks that its own rows see.)
  */
 pkv_status pkv_paged_window_prefill_attention(const void* q, const void* k_cache, const void* v_cache,
                                               const int32_t* block_tables, int32_t max_blocks_per_seq,

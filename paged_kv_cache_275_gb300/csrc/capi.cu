@@ -129,8 +129,8 @@ Window within_table(Window w, int32_t max_blocks_per_seq) {
 // more a piece is a block's time (one sequence, window 1024, two heads: 9.3 us a call with 2, 9.4 with 1, 11.7 with 4,
 // 16.2 with 8).
 constexpr int32_t kMinPieceBlocks = 2;
-// Least key steps of a split of a windowed prefill (one chunk of 512, window 1024: 19.4 us with 1 to 3, 20.2 with 4,
-// 21.6 with 5).
+// Least key steps of a split of a windowed prefill (one chunk of 512, window 1024: 18.6 us with 1 to 3, 19.7 with 4,
+// 21.0 with 5).
 constexpr int32_t kMinSplitSteps = 2;
 // Blocks of one sequence that a query token can see.
 int32_t visible_blocks(Window w, int32_t max_blocks_per_seq) {

@@ -208,7 +208,7 @@ constexpr int ptile_bytes() {
 template <int D, int G, View kView>
 struct Shape;
 // The tail view's CTAs come and go beside the prefix kernel's, so small ones pack better: 128 sequences behind 8192
-// tokens take 51.5 us a call with 4 warps, 51.9 with 2, 52.7 with 8.
+// tokens take 47.7 us a call with 4 warps, 47.1 with 2, 49.2 with 8; 150 behind five prompts 70.6, 71.5 and 70.7.
 template <int G>
 struct Shape<128, G, View::kTail> {
   static constexpr int kWarps = 4;
@@ -661,8 +661,8 @@ __device__ __forceinline__ int pieces_of(const DecodeViewParams& p, long long to
 
 // Tail view: where piece w of a stream of `total` items begins.  CTAs start in their order, as SMs become free of the
 // prefix kernel, so the pieces get smaller, from 1.6 to 0.4 of their mean: the CTAs that start last are soon done (128
-// sequences behind one prefix 51.5 us, 150 behind five 70.8; from 1.5 51.9 and 70.5, from 1.9 53.5 and 73.2, all alike 57.7
-// and 71.6, and half as large and all alike 53.9 and 73.4).  With a mean of 6 items no piece is empty.
+// sequences behind one prefix 47.7 us, 150 behind five 70.6; from 1.5 48.1 and 70.5, from 1.7 47.6 and 71.6, from 1.9 48.4
+// and 73.0, all alike 50.1 and 71.2).  With a mean of 6 items no piece is empty.
 __device__ __forceinline__ long long shrinking_bound(int w, long long total, int pieces) {
   if (w >= pieces) return total;
   const float x = static_cast<float>(w) / static_cast<float>(pieces);
@@ -1299,7 +1299,7 @@ template <int D, int G, View kView, int kSlices>
 __global__ void __launch_bounds__(G * kSlices * 32) join_states_kernel(const DecodeViewParams p) {
   constexpr int kPieceFloats = Geo<D, G>::kPieceFloats;
   constexpr int kPer = D / 32;
-  constexpr int kAhead = 4;  // (150 sequences of eight heads behind prefixes: 73.4 us a call; with 2 76.6, with 8 77.2)
+  constexpr int kAhead = 4;  // (150 sequences of eight heads behind prefixes: 70.6 us a call; with 2 the same, with 8 71.3)
   __shared__ float2 s_ml[kSlices][G];
   __shared__ float s_o[kSlices][G][D];
   const int hkv = p.num_kv_heads;

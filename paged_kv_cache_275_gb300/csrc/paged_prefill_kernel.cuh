@@ -113,7 +113,8 @@ struct Pf {
   // At least 120 KB so that one CTA holds the SM: it owns all 512 TMEM columns,
   // and a second CTA's allocation would have to wait.
   static constexpr int kSmem = kRaw > 120 * 1024 ? kRaw : 120 * 1024;
-  // Windowed calls: a table of the call's units and the warps' units behind that (227 KB with D = 128, all that a CTA may have).
+  // Windowed calls: a table of the call's units and the warps' units behind that (227 KB with D = 128, all that a CTA
+  // may have).
   static constexpr int kWindowWarps = kRaw + 2048;
   static constexpr int kWindowSmem = kRaw + 2560 > 120 * 1024 ? kRaw + 2560 : 120 * 1024;
 };
@@ -1320,7 +1321,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             failed = true;
           }
-          // The tile's Q buffer is free for the next unit when all its rows have been read: another phase of the same barrier.
+          // The tile's Q buffer is free for the next unit when all its rows have been read: another phase of the same
+          // barrier.
           if constexpr (kLoop) {
             bar_arrive(o_staged + 8 * t);
             if (!__all_sync(0xffffffffu, !failed && bar_wait(o_staged + 8 * t, 1))) failed = true;
@@ -1618,7 +1620,7 @@ cudaError_t launch_t(const PrefillParams& p, int max_query_len, cudaStream_t str
     e = launch_pdl(paged_prefill_kernel<D, G, kSplit, kMask>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), kSmem, stream,
                    p, mk, mv, mo);
     if (!kSplit || e != cudaSuccess) return e;
-    const unsigned most = static_cast<unsigned>(std::min<int64_t>(units, p.num_sms / 2));  // split units: two CTAs each at least
+    const unsigned most = static_cast<unsigned>(std::min<int64_t>(units, p.num_sms / 2));  // units: two CTAs each at least
     return launch_pdl(window_prefill_merge_kernel<D>, dim3(kTiles * kRows / 16, most), dim3(256), 0, stream, p);
   } else if constexpr (!kSplit) {
     const int tiles = (max_query_len + kCtaTokens - 1) / kCtaTokens;
