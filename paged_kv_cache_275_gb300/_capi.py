@@ -492,26 +492,6 @@ def paged_prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
 MAX_POSITION_AXES = 4
 
 
-_scratch = threading.local()
-
-
-def _temporary(device: int, stream: torch.cuda.Stream | None, handle: int, nbytes: int) -> torch.Tensor:
-    """A workspace of a call that was given none.
-
-    One buffer per host thread, device and stream: calls that share it run in order (two threads' calls on one
-    stream could interleave their launches).  A call that is being captured takes a buffer of its own from the
-    graph's memory, which lives as long as the graph does and is shared with nothing outside it.
-    """
-    buffers = _scratch.__dict__
-    with torch.cuda.stream(stream):  # (no stream: the current one; the caller has made the device current)
-        if torch.cuda.is_current_stream_capturing():
-            return torch.empty(nbytes, dtype=torch.uint8, device=device)
-        ws = buffers.get((device, handle))
-        if ws is None or ws.numel() < nbytes:
-            ws = buffers[(device, handle)] = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-        return ws
-
-
 _binding = None
 
 
@@ -525,7 +505,7 @@ def _native():
         except ImportError as e:
             raise ImportError("the compiled binding is missing: build it with `python -m paged_kv_cache_275_gb300.build` "
                               "(there is no fallback path)") from e
-        module.register(_check, _temporary)
+        module.register(_check)
         _binding = module
     return _binding
 

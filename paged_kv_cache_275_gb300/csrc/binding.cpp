@@ -5,13 +5,17 @@
 // documentation; every function here takes its arguments by position, None where they were not given.
 #include <Python.h>
 
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <cuda_runtime.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <exception>
+#include <memory>
 #include <string>
 #include <vector>
 
@@ -82,9 +86,8 @@ int32_t extent(int64_t v, const char* name) {
   return static_cast<int32_t>(v);
 }
 
-// What _capi.py registered: raises PagedKVError of a status; gives a workspace.
+// What _capi.py registered: raises PagedKVError of a status.
 PyObject* g_check = nullptr;
-PyObject* g_temporary = nullptr;
 
 void check(int status) {
   if (status == PKV_OK) return;
@@ -128,63 +131,80 @@ pkv_stream_t stream_of(PyObject* stream, int device) {
   return static_cast<pkv_stream_t>(p);
 }
 
-// This thread's workspaces, as _temporary last gave them.  The Python side owns the buffers for as long as the
-// thread lives, and replaces one only through a call that updates its entry here.
+// Device memory of torch's allocator, for use on one stream.
+struct Release {
+  void operator()(void* p) const noexcept {
+    try {
+      c10::cuda::CUDACachingAllocator::raw_delete(p);
+    } catch (...) {  // (the allocator is gone: the process is ending)
+    }
+  }
+};
+using Buffer = std::unique_ptr<void, Release>;
+Buffer allocate(size_t bytes, pkv_stream_t stream) {  // on the current device
+  return Buffer(c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(bytes, static_cast<cudaStream_t>(stream)));
+}
+
+// This OS thread's workspaces, one per device and stream, for calls that were given none: calls that share a buffer run in
+// order (two threads' calls on one stream could interleave their launches).  The buffers are owned here and live as long as
+// the thread does.  Nothing of Python's may own them: a thread that Python did not start gets new thread-local storage each
+// time it enters the interpreter.
 struct Scratch {
   int device;
   pkv_stream_t stream;
-  void* data;
   size_t bytes;
+  Buffer data;
 };
 thread_local std::vector<Scratch> t_scratch;
 
 // The caller's workspace (kept alive by `owner`), or one of this thread, device and stream.
 struct Workspace {
   PyObject* owner = nullptr;
+  Buffer own;
   void* data = nullptr;
   size_t bytes = 0;
   Workspace() = default;
   Workspace(const Workspace&) = delete;
   ~Workspace() { Py_XDECREF(owner); }
-  void take(PyObject* given, int device, PyObject* stream, pkv_stream_t handle, size_t need) {
+  void take(PyObject* given, int device, pkv_stream_t handle, size_t need) {  // `device` is the current one
     if (given != Py_None) {
       Py_INCREF(given);
       owner = given;
-      contiguous(given, "workspace", at::kByte, 1, device);
-    } else {
-      cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-      if (cudaStreamIsCapturing(handle, &capture) != cudaSuccess) {
-        (void)cudaGetLastError();
-        capture = cudaStreamCaptureStatusActive;
-      }
-      const bool eager = capture == cudaStreamCaptureStatusNone;
-      Scratch* mine = nullptr;
-      for (Scratch& x : t_scratch)
-        if (x.device == device && x.stream == handle) mine = &x;
-      if (eager && mine && mine->bytes >= need) {
-        data = mine->data;
-        bytes = mine->bytes;
-        return;
-      }
-      owner = PyObject_CallFunction(g_temporary, "iOKn", device, stream,
-                                    static_cast<unsigned long long>(reinterpret_cast<uintptr_t>(handle)),
-                                    static_cast<Py_ssize_t>(need));
-      if (!owner) throw Raised{};
-      if (eager) {
-        const at::Tensor& t = tensor(owner, "workspace");
-        if (!mine) {
-          t_scratch.push_back({device, handle, nullptr, 0});
-          mine = &t_scratch.back();
-        }
-        mine->data = t.data_ptr();
-        mine->bytes = static_cast<size_t>(t.numel());
-      }
+      const at::Tensor& t = contiguous(given, "workspace", at::kByte, 1, device);
+      data = t.data_ptr();
+      bytes = static_cast<size_t>(t.numel());
+      if (bytes < need)
+        raise(PyExc_ValueError, "workspace must hold " + std::to_string(need) + " bytes (got " + std::to_string(bytes) + ")");
+      return;
     }
-    const at::Tensor& t = tensor(owner, "workspace");
-    data = t.data_ptr();
-    bytes = static_cast<size_t>(t.numel());
-    if (bytes < need)
-      raise(PyExc_ValueError, "workspace must hold " + std::to_string(need) + " bytes (got " + std::to_string(bytes) + ")");
+    bytes = std::max<size_t>(need, 256);
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(handle, &capture) != cudaSuccess) {
+      (void)cudaGetLastError();
+      capture = cudaStreamCaptureStatusActive;
+    }
+    // A call that is being captured takes a buffer of its own: the allocator gives it from the memory that torch reserves for
+    // the graph, for as long as the graph lives, and what the graph's later calls are given there comes behind this call.
+    if (capture != cudaStreamCaptureStatusNone) {
+      own = allocate(bytes, handle);
+      data = own.get();
+      return;
+    }
+    Scratch* mine = nullptr;
+    for (Scratch& x : t_scratch)
+      if (x.device == device && x.stream == handle) mine = &x;
+    if (!mine) {
+      t_scratch.push_back({device, handle, 0, nullptr});
+      mine = &t_scratch.back();
+    }
+    if (mine->bytes < need) {  // (the old buffer goes back first, to what runs behind it on its stream)
+      mine->bytes = 0;
+      mine->data.reset();
+      mine->data = allocate(bytes, handle);
+      mine->bytes = bytes;
+    }
+    data = mine->data.get();
+    bytes = mine->bytes;
   }
 };
 
@@ -201,8 +221,8 @@ PyObject* guarded(F&& f) {
   try {
     return f();
   } catch (const Raised&) {
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (const std::exception&) {
+    torch::translate_exception_to_python(std::current_exception());  // (no memory is torch.OutOfMemoryError)
   }
   return nullptr;
 }
@@ -321,7 +341,7 @@ PyObject* window_decode(PyObject*, PyObject* const* a, Py_ssize_t) {
       size_t need = 0;
       check(pkv_window_decode_workspace_size(t.rows, t.hq, t.hkv, t.d, t.width, window, sinks, parts, &need));
       Workspace ws;
-      if (need > 0) ws.take(a[10], t.dev, a[11], stream, need);
+      if (need > 0) ws.take(a[10], t.dev, stream, need);
       run([&] {
         return pkv_paged_window_decode_attention(t.q, t.kc, t.vc, t.table, t.width, t.lens, t.rows, t.hq, t.hkv, t.d,
                                                  t.blocks, t.block, static_cast<float>(scale), window, sinks, t.out,
@@ -351,7 +371,7 @@ PyObject* window_prefill(PyObject*, PyObject* const* a, Py_ssize_t) {
     if (splits > 1) {
       size_t need = 0;
       check(pkv_window_prefill_workspace_size(t.d, splits, &need));
-      ws.take(a[12], t.dev, a[13], stream, need);
+      ws.take(a[12], t.dev, stream, need);
     }
     run([&] {
       return pkv_paged_window_prefill_attention(t.q, t.kc, t.vc, t.table, t.width, t.lens,
@@ -381,7 +401,7 @@ PyObject* prefix_decode(PyObject*, PyObject* const* a, Py_ssize_t) {
       size_t need = 0;
       check(pkv_prefix_decode_workspace_size(t.rows, t.hq, t.hkv, t.d, t.width, groups, &need));
       Workspace ws;
-      if (need > 0) ws.take(a[9], t.dev, a[10], stream, need);
+      if (need > 0) ws.take(a[9], t.dev, stream, need);
       run([&] {
         return pkv_paged_prefix_decode_attention(t.q, t.kc, t.vc, t.table, t.width, t.lens,
                                                  static_cast<const int32_t*>(start.data_ptr()),
@@ -395,18 +415,11 @@ PyObject* prefix_decode(PyObject*, PyObject* const* a, Py_ssize_t) {
   });
 }
 
-// register(check, temporary): the Python side's helpers.
-PyObject* register_helpers(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 2) {
-    PyErr_SetString(PyExc_TypeError, "register(check, temporary)");
-    return nullptr;
-  }
+// register(check): the Python side's helper.
+PyObject* register_helpers(PyObject*, PyObject* const* a, Py_ssize_t) {
   Py_INCREF(a[0]);
-  Py_INCREF(a[1]);
   Py_XDECREF(g_check);
-  Py_XDECREF(g_temporary);
   g_check = a[0];
-  g_temporary = a[1];
   Py_RETURN_NONE;
 }
 
@@ -427,7 +440,7 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef g_methods[] = {
-    method<2, register_helpers>("register"), method<11, rope_append>("rope_append"),
+    method<1, register_helpers>("register"), method<11, rope_append>("rope_append"),
     method<12, window_decode>("window_decode"), method<14, window_prefill>("window_prefill"),
     method<11, prefix_decode>("prefix_decode"), {nullptr, nullptr, 0, nullptr},
 };
