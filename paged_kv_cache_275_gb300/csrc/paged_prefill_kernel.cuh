@@ -443,24 +443,41 @@ struct WindowSteps {
   int steps, tiles, tail, hole0, hole1;
 };
 
-// Called by the whole CTA, with a thread a sequence; `lens` holds kThreads words.  Leaves the table and the number of all
-// tile pairs; CTA 0 reports chunks that are not in order, which have no units.
+// Called by the whole CTA, with a thread a sequence; `scratch` holds 2 kThreads words.  Leaves the table and the number of all
+// tile pairs; CTA 0 reports chunks that are not in order, which have no units.  The chunks that have units do not overlap (one
+// that starts before the end of an earlier one is not in order), which bounds the tile pairs as the host does (window_units).
 template <int G>
-__device__ __forceinline__ void rank_window_units(const PrefillParams& p, int* lens, WindowTable& table, int& total) {
+__device__ __forceinline__ void rank_window_units(const PrefillParams& p, int* scratch, WindowTable& table, int& total) {
   constexpr int kCtaTokens = kTiles * (kRows / G);
   static_assert(kThreads == kPrefillRankedSeqs, "a thread a sequence");
+  int* const lens = scratch;
+  int* const ends = scratch + kThreads;  // where a chunk ends that holds rows and is in order by itself; else 0
   const int tid = threadIdx.x;
-  int len = 0;
+  int len = 0, q0 = 0;
+  bool falls = false;
   if (tid < p.num_seqs) {
-    const int q0 = __ldg(p.query_start + tid), chunk = __ldg(p.query_start + tid + 1) - q0;
+    q0 = __ldg(p.query_start + tid);
+    const int q1 = __ldg(p.query_start + tid + 1), chunk = q1 - q0;
     len = __ldg(p.context_lens + tid);
+    falls = q1 < q0;
     const bool outside = chunk < 0 || len < chunk || len > p.max_blocks_per_seq * kBlockTokens || q0 < 0 ||
                          static_cast<int64_t>(q0) + chunk > p.query_rows;
     if (blockIdx.x == 0 && (outside || chunk > p.max_query_len)) atomicOr(p.err, kErrLenTooLong);
     lens[tid] = len;  // (rows past max_query_len are lost; the host bounds the tile pairs by 65535)
+    ends[tid] = outside || chunk == 0 ? 0 : q1;
     table.tiles[tid] = outside ? 0 : static_cast<unsigned short>((min(chunk, p.max_query_len) + kCtaTokens - 1) / kCtaTokens);
   }
-  __syncthreads();
+  if (__syncthreads_or(falls)) {  // without a fall no chunk starts before the end of another
+    if (tid < p.num_seqs && ends[tid] > 0) {
+      int before = 0;
+      for (int u = 0; u < tid; ++u) before = max(before, ends[u]);
+      if (q0 < before) {
+        if (blockIdx.x == 0) atomicOr(p.err, kErrLenTooLong);
+        table.tiles[tid] = 0;
+      }
+    }
+    __syncthreads();
+  }
   if (tid < p.num_seqs) {
     int before = 0, all = 0;
     for (int u = 0; u < p.num_seqs; ++u) {
