@@ -463,9 +463,9 @@ pkv_status pkv_window_prefill_workspace_size(int32_t head_dim, int32_t num_split
  *   workspace     device, 16-byte aligned, at least pkv_prefix_decode_workspace_size bytes, scratch as for
  *                 pkv_paged_decode_attention
  * num_blocks * num_kv_heads * 16 must be below 2^31.  One or three launches.  Shared tokens have to be finite when a
- * sequence of the group is shorter than the prefix (see pkv_paged_window_prefill_attention).  Arithmetic: the
- * shared part as pkv_paged_prefill_attention (P rounded to bf16), the rest as pkv_paged_decode_attention, joined in
- * fp32.  Device-side: group_start out of order sets PKV_DEVERR_CONTEXT_LEN_TOO_LONG (the outputs are unspecified);
+ * sequence of the group is shorter than the prefix (see pkv_paged_window_prefill_attention).  Arithmetic: as
+ * pkv_paged_decode_attention at eight heads a group, with the weights in two bf16 parts, the shared part and the rest joined
+ * in fp32.  Device-side: group_start out of order sets PKV_DEVERR_CONTEXT_LEN_TOO_LONG (the outputs are unspecified);
  * prefix_lens[g] < 0 or > 16 * max_blocks_per_seq (of a group that is not empty) sets PKV_DEVERR_CONTEXT_LEN_NEGATIVE or ..._TOO_LONG and is
  * clamped.
  */

@@ -529,6 +529,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t s_base = saddr(smem);
   static_assert(kMask != Mask::kShared || kSplit, "a shared prefix leaves partial states");
+  // A decode weight enters P V as two bf16 parts, the high one and the rounded-off rest, so that P V carries the fp32 weights
+  // to within 2^-16, as in the decode kernels: with one part (2^-9) a sequence's result would depend on the running max that
+  // each weight was taken against, so on the splits, which go by the whole batch, and on the form that the call takes.  The
+  // rest stands behind the high parts, over the other half of S.  A step takes 1.3 (two tiles) to 1.4 times as long as with
+  // one part, a call 1.09 times in the geometric mean of 24 (128 sequences of 32 heads behind 8192 tokens 48.0 -> 56.8 us).
+  // With one plan for all, that mean is 47.0 us so, 47.4 with the high parts cut off instead of rounded, and 52.1 with them
+  // handed over before the rest is formed, so that their products run meanwhile.
+  constexpr bool kTwoPartP = kMask == Mask::kShared;
   // A windowed call's work is many short units: its CTAs stay and take unit after unit, so that set-up is paid once and the
   // first copies of a unit overlap the end of the one before.  Every role goes through the units by itself.
   constexpr bool kLoop = kMask == Mask::kWindow && !kSplit;
@@ -1057,6 +1065,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int g = 0; g < kKeys / 64; ++g)  // four pages of 16 keys each: P columns 8 apart
               mma4_ts<kIdPV, 8, T::kPageBytes / 16>(tmem + col_o(t), d_s + g * 32,
                                                     v + static_cast<uint32_t>((g * 4 * T::kPageBytes) >> 4), (j | g) != 0);
+            if constexpr (kTwoPartP) {
+#pragma unroll
+              for (int g = 0; g < kKeys / 64; ++g)
+                mma4_ts<kIdPV, 8, T::kPageBytes / 16>(tmem + col_o(t), d_s + kKeys / 2 + g * 32,
+                                                      v + static_cast<uint32_t>((g * 4 * T::kPageBytes) >> 4), 1);
+            }
             if (last) mma_commit(o_full + 8 * t);
             // The last reader of this V slot is issued: release it as soon as that P.V retires, not
             // after the S of the next step, so that the producer can refill it sooner.
@@ -1198,7 +1212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float neg_m = sees ? -m_new : 0.f;                        // rows seeing no key: all p = 0
           float2 acc4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                             make_float2(0.f, 0.f)};
-          uint32_t packed[kKeys / 2];
+          uint32_t packed[kKeys / 2], rest[kTwoPartP ? kKeys / 2 : 1];
           const float2 qk2 = make_float2(qk, qk), neg_m2 = make_float2(neg_m, neg_m);
 #pragma unroll
           for (int x = 0; x < kKeys; x += 2) {
@@ -1207,6 +1221,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 e = __ffma2_rn(make_float2(s[x], s[x + 1]), qk2, neg_m2);
             const float p0 = ex2_approx(e.x), p1 = ex2_approx(e.y);
             packed[x / 2] = pack_bf16(p0, p1);
+            if constexpr (kTwoPartP)
+              rest[x / 2] = pack_bf16(p0 - __uint_as_float(packed[x / 2] << 16), p1 - __uint_as_float(packed[x / 2] & 0xffff0000u));
             acc4[(x / 2) & 3] = __fadd2_rn(acc4[(x / 2) & 3], make_float2(p0, p1));
           }
           const float2 a01 = __fadd2_rn(acc4[0], acc4[1]), a23 = __fadd2_rn(acc4[2], acc4[3]);
@@ -1229,6 +1245,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           // tensor-memory A operand of O += P V.
           tmem_st32_raw(s_cols, *reinterpret_cast<const uint32_t(*)[32]>(&packed[0]));
           tmem_st32_raw(s_cols + 32, *reinterpret_cast<const uint32_t(*)[32]>(&packed[32]));
+          if constexpr (kTwoPartP) {
+            tmem_st32_raw(s_cols + kKeys / 2, *reinterpret_cast<const uint32_t(*)[32]>(&rest[0]));
+            tmem_st32_raw(s_cols + kKeys / 2 + 32, *reinterpret_cast<const uint32_t(*)[32]>(&rest[32]));
+          }
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           tc_before_sync();
           bar_arrive(p_full + 8 * t);
