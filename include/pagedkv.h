@@ -424,7 +424,7 @@ pkv_status pkv_window_decode_workspace_size(int32_t num_seqs, int32_t num_q_head
  * none.)
  *
  * Table entries of blocks that no row of the sequence's chunk sees are not read, and tokens that no row of the
- * chunk sees do not matter, whatever they hold.  num_query_tokens is the number of rows of q and out; a sequence whose
+ * chunk sees do not matter, whatever they hold.  num_query_tokens is the number of rows of q and out (0: a no-op); a sequence whose
  * chunk reaches outside them sets PKV_DEVERR_CONTEXT_LEN_TOO_LONG and is skipped, and so is one that starts before the end of
  * an earlier sequence's chunk (of its 320, counted from the first).  A token that some rows see has to be
  * finite: rows of the same 128-row tile that do not see it weight it with 0, and 0 times infinity is no number.  (A CTA

@@ -448,7 +448,7 @@ pkv_status prefill_impl(const void* q, const void* k_cache, const void* v_cache,
   if ((static_cast<int64_t>(max_query_len) + cta_tokens - 1) / cta_tokens > 65535)
     return fail(PKV_ERR_UNSUPPORTED, "max_query_len %d exceeds 65535 CTAs of %d chunk tokens", max_query_len,
                 cta_tokens);
-  if (num_seqs == 0 || max_query_len == 0) return ok();
+  if (num_seqs == 0 || max_query_len == 0 || (window.window && query_rows == 0)) return ok();
   if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start || !out)
     return fail(PKV_ERR_INVALID_ARGUMENT, "null pointer argument");
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||

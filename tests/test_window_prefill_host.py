@@ -1,0 +1,13 @@
+"""Host side of the windowed prefill: calls without rows, the split count and the workspace that a call needs (on the
+CPU: what is looked at here returns before any CUDA call; pointers are fake, nothing is dereferenced)."""
+import pytest
+
+from test_window_prefix_rope_host import lib, msg, window_prefill  # noqa: F401  (lib: a fixture)
+
+
+@pytest.mark.parametrize("splits", [1, 2])
+def test_no_query_rows_is_a_noop(lib, splits):  # noqa: F811
+    """Empty chunks under a bound that a caller keeps for a fixed schedule: q and out have no rows, so no address."""
+    assert window_prefill(lib, T=0, q=None, out=None, S=splits) == 0 and msg(lib) == ""
+    assert window_prefill(lib, T=0, S=splits) == 0
+    assert window_prefill(lib, T=0, q=None, window=0) == 1 and "window" in msg(lib)  # (still checked)
