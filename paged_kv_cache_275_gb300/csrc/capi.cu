@@ -430,6 +430,7 @@ pkv_status prefill_impl(const void* q, const void* k_cache, const void* v_cache,
                         const Window& window, int64_t query_rows) {
   if (num_splits < 1 || num_splits > kMaxPrefillSplits)
     return fail(PKV_ERR_INVALID_ARGUMENT, "num_splits must be in [1, %d] (got %d)", kMaxPrefillSplits, num_splits);
+  if (window.window && num_seqs > pkv::kPrefillRankedSeqs) num_splits = 1;  // its units are not split
   if (static_cast<int64_t>(num_seqs) * num_splits > 65535)
     return fail(PKV_ERR_UNSUPPORTED, "num_seqs * num_splits = %lld exceeds 65535 (one grid row of CTAs each)",
                 static_cast<long long>(num_seqs) * num_splits);
@@ -455,7 +456,6 @@ pkv_status prefill_impl(const void* q, const void* k_cache, const void* v_cache,
       (reinterpret_cast<uintptr_t>(block_tables) & 3u) || (reinterpret_cast<uintptr_t>(context_lens) & 3u) ||
       (reinterpret_cast<uintptr_t>(query_start) & 3u))
     return fail(PKV_ERR_INVALID_ARGUMENT, "q, caches and out must be 16-byte aligned");
-  if (window.window && num_seqs > pkv::kPrefillRankedSeqs) num_splits = 1;  // its units are not split
   const pkv::WindowSplitLayout layout(head_dim, num_splits);
   if (num_splits > 1) {
     const size_t need =

@@ -11,3 +11,10 @@ def test_no_query_rows_is_a_noop(lib, splits):  # noqa: F811
     assert window_prefill(lib, T=0, q=None, out=None, S=splits) == 0 and msg(lib) == ""
     assert window_prefill(lib, T=0, S=splits) == 0
     assert window_prefill(lib, T=0, q=None, window=0) == 1 and "window" in msg(lib)  # (still checked)
+
+
+@pytest.mark.parametrize("seqs,splits", [(2048, 32), (32768, 2), (65535, 32)])
+def test_many_sequences_are_not_refused_for_splits_that_they_do_not_take(lib, seqs, splits):  # noqa: F811
+    """Calls of more than 320 sequences are not split, so a count is no reason to refuse them."""
+    assert window_prefill(lib, B=seqs, S=splits, T=0) == 0 and msg(lib) == ""
+    assert window_prefill(lib, B=seqs, S=33, T=0) == 1 and "num_splits" in msg(lib)
