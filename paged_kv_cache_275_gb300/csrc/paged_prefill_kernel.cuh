@@ -1566,19 +1566,29 @@ cudaError_t encoder(EncodeTiled* out) {
   return cudaSuccess;
 }
 
-// The cache viewed as [num_blocks * num_kv_heads * 16 rows][head_dim] bf16; box 16 rows x 64 dims.
-cudaError_t cache_map(CUtensorMap* map, const void* cache, int64_t rows, int head_dim) {
+// A tensor map of the encoder's arguments.  It needs the device's context, which a host thread whose first use of CUDA this is
+// does not have yet (asking for the current device does not bind it): then it is bound and the map encoded once more.
+template <typename... Args>
+cudaError_t encode(Args... args) {
   EncodeTiled enc = nullptr;
   cudaError_t e = encoder(&enc);
   if (e != cudaSuccess) return e;
+  if (enc(args...) == CUDA_SUCCESS) return cudaSuccess;
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaSetDevice(dev)) != cudaSuccess) return e;
+  return enc(args...) == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// The cache viewed as [num_blocks * num_kv_heads * 16 rows][head_dim] bf16; box 16 rows x 64 dims.
+cudaError_t cache_map(CUtensorMap* map, const void* cache, int64_t rows, int head_dim) {
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(head_dim) * 2};
   const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(kBlockTokens)};
   const cuuint32_t elem[2] = {1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(cache), dims, strides, box, elem,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(cache), dims, strides, box, elem,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // The cache as pages for the prefill kernel: 4D [row groups][halves][8 rows][64 dims] bf16
@@ -1586,19 +1596,15 @@ cudaError_t cache_map(CUtensorMap* map, const void* cache, int64_t rows, int hea
 // one copy moves a whole page of one kv head into [group][half][8 rows][128 B], 128-byte
 // swizzle (each half's 8 rows one swizzle atom).
 cudaError_t page_map(CUtensorMap* map, const void* cache, int64_t rows, int head_dim) {
-  EncodeTiled enc = nullptr;
-  cudaError_t e = encoder(&enc);
-  if (e != cudaSuccess) return e;
   const cuuint32_t halves = static_cast<cuuint32_t>(head_dim / 64);
   const cuuint64_t row_bytes = static_cast<cuuint64_t>(head_dim) * 2;
   const cuuint64_t dims[4] = {64, 8, halves, static_cast<cuuint64_t>(rows / 8)};
   const cuuint64_t strides[3] = {row_bytes, 128, 8 * row_bytes};
   const cuuint32_t box[4] = {64, 8, halves, 2};
   const cuuint32_t elem[4] = {1, 1, 1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(cache), dims, strides, box, elem,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(cache), dims, strides, box, elem,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // The output as [tokens][num_q_heads][head_dim] bf16 for tensor stores: box 64 dims x G heads x kTokens
@@ -1606,19 +1612,15 @@ cudaError_t page_map(CUtensorMap* map, const void* cache, int64_t rows, int head
 // that lie in a chunk, below the call's total token count).
 cudaError_t out_map(CUtensorMap* map, void* out, int64_t tokens, int num_q_heads, int head_dim, int group,
                     int tile_tokens) {
-  EncodeTiled enc = nullptr;
-  cudaError_t e = encoder(&enc);
-  if (e != cudaSuccess) return e;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(num_q_heads),
                               static_cast<cuuint64_t>(tokens)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2,
                                  static_cast<cuuint64_t>(num_q_heads) * head_dim * 2};
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(tile_tokens)};
   const cuuint32_t elem[3] = {1, 1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, out, dims, strides, box, elem,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, out, dims, strides, box, elem,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 template <int D, int G, bool kSplit, Mask kMask>
