@@ -420,8 +420,8 @@ pkv_status pkv_window_decode_workspace_size(int32_t num_seqs, int32_t num_q_head
  *
  * A CTA takes a tile pair (256 / G tokens of a chunk, G = num_q_heads / num_kv_heads) and a kv head.  With num_splits > 1
  * a call that leaves half the SMs or more without one has a tile pair's keys split over up to num_splits CTAs, in fp32
- * states that a second kernel joins; that needs the workspace.  (Calls of more than 320 sequences are not split, and need
- * none.)
+ * states that a second kernel joins; that needs the workspace (whether or not the call is split: pkv_window_prefill_splits).
+ * (Calls of more than 320 sequences are not split, and need none.)
  *
  * Table entries of blocks that no row of the sequence's chunk sees are not read, and tokens that no row of the
  * chunk sees do not matter, whatever they hold.  num_query_tokens is the number of rows of q and out (0: a no-op); a sequence whose
@@ -442,6 +442,11 @@ pkv_status pkv_paged_window_prefill_attention(const void* q, const void* k_cache
 pkv_status pkv_window_prefill_default_splits(int32_t num_seqs, int32_t max_query_len, int32_t num_q_heads,
                                              int32_t num_kv_heads, int32_t window, int32_t num_sink_tokens,
                                              int32_t* num_splits);
+/* What a call of these sizes makes of a count on the current device: *used is num_splits if its units are few enough to be
+   split, else 1.  A call that is given *used instead of num_splits does the same, and needs no workspace for a count that it
+   would not use. */
+pkv_status pkv_window_prefill_splits(int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs,
+                                     int32_t num_q_heads, int32_t num_kv_heads, int32_t num_splits, int32_t* used);
 /* Its workspace: the same for every count above 1, whatever the call's size; 0 for a count of 1. */
 pkv_status pkv_window_prefill_workspace_size(int32_t head_dim, int32_t num_splits, size_t* bytes);
 

@@ -14,7 +14,7 @@ from ._capi import (BLOCK_SIZE, DEVERR_BLOCK_ID_OUT_OF_RANGE, DEVERR_COPY_OUT_OF
                     selftest_wait_timeout, workspace_size, MAX_POSITION_AXES, paged_prefix_decode_attention,
                     paged_window_decode_attention, paged_window_prefill_attention, prefix_decode_workspace_size,
                     rope_append, rope_freq_axes, window_decode_workspace_size, window_prefill_default_splits,
-                    window_prefill_workspace_size)
+                    window_prefill_splits, window_prefill_workspace_size)
 
 __all__ = [
     "BLOCK_SIZE", "MAX_SEQS", "EXPORTS", "LIB_PATH", "PagedKVError", "PHASE_ALL", "PHASE_MERGE", "PHASE_PARTITION",
@@ -27,6 +27,6 @@ __all__ = [
     "selftest_wait_timeout",
     "MAX_POSITION_AXES", "rope_append", "rope_freq_axes", "paged_window_decode_attention",
     "window_decode_workspace_size", "paged_window_prefill_attention", "window_prefill_default_splits",
-    "window_prefill_workspace_size",
+    "window_prefill_splits", "window_prefill_workspace_size",
     "paged_prefix_decode_attention", "prefix_decode_workspace_size",
 ]

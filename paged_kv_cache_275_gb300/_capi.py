@@ -59,6 +59,7 @@ EXPORTS = (
     "pkv_window_decode_workspace_size",
     "pkv_paged_window_prefill_attention",
     "pkv_window_prefill_default_splits",
+    "pkv_window_prefill_splits",
     "pkv_window_prefill_workspace_size",
     "pkv_paged_prefix_decode_attention",
     "pkv_prefix_decode_workspace_size",
@@ -127,6 +128,7 @@ def load(path: Path | str | None = None) -> ctypes.CDLL:
         lib.pkv_paged_window_prefill_attention.argtypes = [V, V, V, V, I32, V, V, I64, I32, I32, I32, I32, I32, I64, I32,
                                                            F32, I32, I32, V, I32, V, SZ, V]
         lib.pkv_window_prefill_default_splits.argtypes = [I32] * 6 + [ctypes.POINTER(I32)]
+        lib.pkv_window_prefill_splits.argtypes = [I64] + [I32] * 5 + [ctypes.POINTER(I32)]
         lib.pkv_window_prefill_workspace_size.argtypes = [I32, I32, ctypes.POINTER(SZ)]
         lib.pkv_paged_prefix_decode_attention.argtypes = [V, V, V, V, I32, V, V, V, I32, I32, I32, I32, I32, I64, I32,
                                                           F32, V, V, SZ, V]
@@ -151,8 +153,8 @@ def load(path: Path | str | None = None) -> ctypes.CDLL:
                      "pkv_bm_append_slots", "pkv_bm_fork", "pkv_bm_free_sequence", "pkv_bm_block_tables",
                      "pkv_bm_ref_count", "pkv_rope_append", "pkv_paged_window_decode_attention",
                      "pkv_window_decode_workspace_size", "pkv_paged_window_prefill_attention",
-                     "pkv_window_prefill_default_splits", "pkv_window_prefill_workspace_size",
-                     "pkv_paged_prefix_decode_attention",
+                     "pkv_window_prefill_default_splits", "pkv_window_prefill_splits",
+                     "pkv_window_prefill_workspace_size", "pkv_paged_prefix_decode_attention",
                      "pkv_prefix_decode_workspace_size"):
             getattr(lib, name).restype = ctypes.c_int
         lib.pkv_last_error_message.argtypes = []
@@ -538,6 +540,13 @@ def window_prefill_default_splits(num_seqs: int, max_query_len: int, num_q_heads
                   num_kv_heads, window, num_sink_tokens)
 
 
+def window_prefill_splits(num_query_tokens: int, max_query_len: int, num_seqs: int, num_q_heads: int,
+                          num_kv_heads: int, num_splits: int) -> int:
+    """``num_splits`` if a windowed prefill call of these sizes is split on the current device, else 1 (no workspace)."""
+    return _query(ctypes.c_int32, load().pkv_window_prefill_splits, num_query_tokens, max_query_len, num_seqs,
+                  num_q_heads, num_kv_heads, num_splits)
+
+
 def window_prefill_workspace_size(head_dim: int, num_splits: int) -> int:
     """Bytes of the workspace of a windowed prefill call, of any size."""
     return _query(ctypes.c_size_t, load().pkv_window_prefill_workspace_size, head_dim, num_splits)
@@ -584,8 +593,8 @@ def paged_window_prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cac
     """paged_prefill_attention where a row sees its last ``window`` tokens and the first ``num_sink_tokens``.
 
     ``num_splits`` is the most CTAs that a tile pair's keys are split over when the call has few of them; 0 takes
-    ``window_prefill_default_splits``.  Above 1 it needs a workspace of ``window_prefill_workspace_size`` bytes, allocated
-    here if not given.  Returns ``out``.
+    ``window_prefill_default_splits``.  A call that is split (``window_prefill_splits``) needs a workspace of
+    ``window_prefill_workspace_size`` bytes, allocated here if not given.  Returns ``out``.
     """
     return (_binding or _native()).window_prefill(q, k_cache, v_cache, block_tables, context_lens, query_start,
                                                   max_query_len, scale, out, window, num_sink_tokens, num_splits,

@@ -367,6 +367,7 @@ PyObject* window_prefill(PyObject*, PyObject* const* a, Py_ssize_t) {
     const pkv_stream_t stream = stream_of(a[13], t.dev);
     const OnDevice guard(t.dev);
     if (splits == 0) check(pkv_window_prefill_default_splits(t.batch, most, t.hq, t.hkv, window, sinks, &splits));
+    if (splits != 1) check(pkv_window_prefill_splits(t.rows, most, t.batch, t.hq, t.hkv, splits, &splits));
     Workspace ws;
     if (splits > 1) {
       size_t need = 0;

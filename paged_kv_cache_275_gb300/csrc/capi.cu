@@ -411,6 +411,9 @@ pkv_status pkv_selftest_wait_timeout(uint64_t limit_ns, pkv_stream_t stream) {
 namespace {
 constexpr int32_t kMaxPrefillSplits = 32;  // the merge reads one split per lane
 
+// SMs that a windowed call counts on.
+int32_t window_sms(int sms) { return sms < pkv::kWindowSplitCtas ? sms : pkv::kWindowSplitCtas; }
+
 // The most splits that keep every CTA of the call in one wave (one CTA per SM), at most 32, and
 // within the 65535 grid rows; 1 when the call already fills the GPU.
 int32_t one_wave_splits(int32_t num_seqs, int32_t max_query_len, int32_t num_q_heads, int32_t num_kv_heads, int sms) {
@@ -490,7 +493,7 @@ pkv_status prefill_impl(const void* q, const void* k_cache, const void* v_cache,
     p.ws_units = reinterpret_cast<int4*>(static_cast<unsigned char*>(workspace) + layout.units);
     p.ws_count = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(workspace) + layout.count);
   }
-  p.num_sms = sms < pkv::kWindowSplitCtas ? sms : pkv::kWindowSplitCtas;
+  p.num_sms = window_sms(sms);
   const Window w = within_table(window, max_blocks_per_seq);
   p.window = w.window;
   p.sinks = w.sinks;
@@ -756,6 +759,29 @@ pkv_status pkv_window_prefill_default_splits(int32_t num_seqs, int32_t max_query
   const int64_t keys = static_cast<int64_t>(window) + num_sink_tokens + pkv::prefill_cta_tokens(num_q_heads / num_kv_heads);
   const int64_t most = (keys + 128 * kMinSplitSteps - 1) / (128 * kMinSplitSteps);
   *num_splits = num_seqs > pkv::kPrefillRankedSeqs ? 1 : static_cast<int32_t>(most < kMaxPrefillSplits ? most : kMaxPrefillSplits);
+  return ok();
+}
+
+pkv_status pkv_window_prefill_splits(int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs,
+                                     int32_t num_q_heads, int32_t num_kv_heads, int32_t num_splits, int32_t* used) {
+  if (!used) return fail(PKV_ERR_INVALID_ARGUMENT, "used is null");
+  if (num_query_tokens < 0 || max_query_len < 0 || num_seqs < 0)
+    return fail(PKV_ERR_INVALID_ARGUMENT, "num_query_tokens, max_query_len and num_seqs must be >= 0");
+  if (num_splits < 1 || num_splits > kMaxPrefillSplits)
+    return fail(PKV_ERR_INVALID_ARGUMENT, "num_splits must be in [1, %d] (got %d)", kMaxPrefillSplits, num_splits);
+  if (pkv_status st = check_shapes(num_seqs, num_seqs, num_q_heads, num_kv_heads, 128, 1); st != PKV_OK) return st;
+  *used = 1;
+  if (num_splits == 1 || num_seqs == 0 || num_seqs > pkv::kPrefillRankedSeqs || max_query_len == 0 || num_query_tokens == 0)
+    return ok();
+  int sms = 0;
+  if (pkv_status st = device_state(nullptr, &sms); st != PKV_OK) return st;
+  pkv::PrefillParams p{};
+  p.num_seqs = num_seqs;
+  p.num_kv_heads = num_kv_heads;
+  p.query_rows = num_query_tokens;
+  p.num_splits = num_splits;
+  p.num_sms = window_sms(sms);
+  if (pkv::window_splits(p, num_q_heads / num_kv_heads, max_query_len)) *used = num_splits;
   return ok();
 }
 
