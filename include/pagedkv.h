@@ -407,8 +407,9 @@ pkv_status pkv_paged_window_decode_attention(const void* q, const void* k_cache,
                                              int32_t block_size, float scale, int32_t window, int32_t num_sink_tokens,
                                              void* out, void* workspace, size_t workspace_bytes,
                                              int32_t num_partitions, pkv_stream_t stream);
-/* Its workspace; num_partitions as for pkv_decode_workspace_size (0: the default, needs a device).  It can be 0 bytes
-   (few sequences and a short window: one launch that joins through shared memory); the workspace may be NULL then. */
+/* Its workspace; num_partitions as for pkv_decode_workspace_size (0: the default, needs a device).  What is enough for
+   num_seqs sequences and max_blocks_per_seq is enough for fewer sequences and for narrower tables.  It can be 0 bytes (few
+   sequences and a short window: one launch that joins through shared memory); the workspace may be NULL then. */
 pkv_status pkv_window_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                             int32_t head_dim, int32_t max_blocks_per_seq, int32_t window,
                                             int32_t num_sink_tokens, int32_t num_partitions, size_t* bytes);
@@ -481,9 +482,10 @@ pkv_status pkv_paged_prefix_decode_attention(const void* q, const void* k_cache,
                                              int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                              int64_t num_blocks, int32_t block_size, float scale, void* out,
                                              void* workspace, size_t workspace_bytes, pkv_stream_t stream);
-/* Its workspace (needs a device: it holds the partial states of one CTA per SM, or of whole waves of them).  It can be 0
-   bytes (few sequences and a narrow table: one launch, in which each sequence reads the shared blocks for itself); the
-   workspace may be NULL then. */
+/* Its workspace (needs a device: it holds the partial states of one CTA per SM, or of whole waves of them).  What is enough
+   for num_seqs sequences, max_blocks_per_seq and num_groups is enough for fewer of each.  It can be 0 bytes (few sequences
+   and a narrow table: one launch, in which each sequence reads the shared blocks for itself); the workspace may be NULL
+   then. */
 pkv_status pkv_prefix_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                             int32_t head_dim, int32_t max_blocks_per_seq, int32_t num_groups,
                                             size_t* bytes);

@@ -152,20 +152,23 @@ pkv_status cluster_ctas(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim
   return e == cudaSuccess ? PKV_OK : cuda_fail(e, "cluster occupancy query");
 }
 
+// Pieces of a stream, `resident` if it can have so many: never more than it can have items, or pieces of the least size.
+int32_t most_partitions(int32_t num_seqs, int32_t num_kv_heads, int32_t visible, const Window& window, int resident) {
+  int64_t bound = static_cast<int64_t>(num_seqs) * num_kv_heads * visible;
+  if (window.window) bound = (bound + kMinPieceBlocks - 1) / kMinPieceBlocks;
+  int64_t n = resident;
+  if (n > bound) n = bound;
+  if (n > kMaxPartitions) n = kMaxPartitions;
+  return static_cast<int32_t>(n < 1 ? 1 : n);
+}
+
 pkv_status default_partitions(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int32_t group,
                               int32_t max_blocks_per_seq, const Window& window, int32_t* out) {
   int pieces = 0;
   const cudaError_t e = window.window ? pkv::resident_window_pieces(head_dim, group, num_seqs, &pieces)
                                       : pkv::resident_partition_pieces(head_dim, group, num_seqs, &pieces);
   if (e != cudaSuccess) return cuda_fail(e, "occupancy query");
-  // Never more pieces than the block stream can have items.
-  int64_t bound = static_cast<int64_t>(num_seqs) * num_kv_heads * visible_blocks(window, max_blocks_per_seq);
-  if (window.window) bound = (bound + kMinPieceBlocks - 1) / kMinPieceBlocks;
-  int64_t n = pieces;
-  if (n > bound) n = bound;
-  if (n > kMaxPartitions) n = kMaxPartitions;
-  if (n < 1) n = 1;
-  *out = static_cast<int32_t>(n);
+  *out = most_partitions(num_seqs, num_kv_heads, visible_blocks(window, max_blocks_per_seq), window, pieces);
   return PKV_OK;
 }
 
@@ -720,17 +723,31 @@ pkv_status pkv_window_decode_workspace_size(int32_t num_seqs, int32_t num_q_head
   if (pkv_status st = check_window(window, num_sink_tokens); st != PKV_OK) return st;
   if (num_partitions < 0 || num_partitions > kMaxPartitions)
     return fail(PKV_ERR_INVALID_ARGUMENT, "num_partitions out of range (got %d)", num_partitions);
-  size_t need = 0;
   const Window w{window, num_sink_tokens};
-  int cluster = 0;
-  if (pkv_status st = cluster_ctas(num_seqs, num_kv_heads, head_dim, num_q_heads / num_kv_heads,
-                                     max_blocks_per_seq, w, num_partitions, &cluster); st != PKV_OK)
-    return st;
-  if (!cluster)
-    if (pkv_status st = decode_workspace_need(num_seqs, num_kv_heads, head_dim, num_q_heads / num_kv_heads,
-                                              max_blocks_per_seq, w, num_partitions, &need);
+  const int group = num_q_heads / num_kv_heads;
+  size_t need = 0;
+  if (num_partitions != 0) {
+    if (pkv_status st = decode_workspace_need(num_seqs, num_kv_heads, head_dim, group, max_blocks_per_seq, w, num_partitions,
+                                              &need);
         st != PKV_OK)
       return st;
+  } else if (num_seqs > 0) {
+    // What every call of up to num_seqs sequences can do with: nothing if all of them take the form for few pairs, else the
+    // most pieces that any of them is cut into, which a single sequence's shared memory leaves room for.
+    const int32_t n = launch_seqs(num_seqs);
+    const int32_t visible = visible_blocks(w, max_blocks_per_seq);
+    bool none = false;
+    if (n == num_seqs) {
+      const cudaError_t e = pkv::window_cluster_takes_all(head_dim, group, n, num_kv_heads, visible, &none);
+      if (e != cudaSuccess) return cuda_fail(e, "cluster occupancy query");
+    }
+    if (!none) {
+      int pieces = 0;
+      const cudaError_t e = pkv::resident_window_pieces(head_dim, group, 1, &pieces);
+      if (e != cudaSuccess) return cuda_fail(e, "occupancy query");
+      need = workspace_bytes_for(n, num_kv_heads, head_dim, group, most_partitions(n, num_kv_heads, visible, w, pieces));
+    }
+  }
   *bytes = need;
   return ok();
 }
@@ -812,7 +829,9 @@ pkv_status pkv_paged_window_prefill_attention(const void* q, const void* k_cache
 }
 
 namespace {
-// Shared-prefix decode: its grid, partition count and workspace (byte offsets of the parts).
+// Shared-prefix decode: its grid, partition count and workspace (byte offsets of the parts).  The tail is cut into as many
+// pieces as run at once with `sized_for` sequences: the call's own, or one for the size query (the most of any batch, so
+// that what is enough for a batch is enough for smaller ones).
 struct PrefixPlan {
   int cluster = 0;  // CTAs a (sequence, kv head) of the form for few pairs, which needs none of the rest
   int32_t ctas = 0, parts = 0, sms = 0;
@@ -820,7 +839,7 @@ struct PrefixPlan {
 };
 
 pkv_status plan_prefix_decode(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
-                              int32_t max_blocks_per_seq, int32_t num_groups, PrefixPlan* plan) {
+                              int32_t max_blocks_per_seq, int32_t num_groups, int32_t sized_for, PrefixPlan* plan) {
   if (pkv_status st = check_shapes(num_seqs, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq);
       st != PKV_OK)
     return st;
@@ -844,7 +863,7 @@ pkv_status plan_prefix_decode(int32_t num_seqs, int32_t num_q_heads, int32_t num
   if (ctas * 256 >= (int64_t{1} << 31))
     return fail(PKV_ERR_UNSUPPORTED, "too many groups, sequences and kv heads for one launch (%lld CTAs)", (long long)ctas);
   int pieces = 0;
-  const cudaError_t e = pkv::resident_tail_pieces(head_dim, group, num_seqs, &pieces);
+  const cudaError_t e = pkv::resident_tail_pieces(head_dim, group, sized_for, &pieces);
   if (e != cudaSuccess) return cuda_fail(e, "occupancy query");
   const int64_t bound = (static_cast<int64_t>(num_seqs) * num_kv_heads * max_blocks_per_seq + kMinPieceBlocks - 1) /
                         kMinPieceBlocks;
@@ -878,7 +897,7 @@ pkv_status pkv_prefix_decode_workspace_size(int32_t num_seqs, int32_t num_q_head
   if (!bytes) return fail(PKV_ERR_INVALID_ARGUMENT, "bytes is null");
   PrefixPlan plan;
   if (pkv_status st = plan_prefix_decode(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, num_groups,
-                                         &plan);
+                                         1, &plan);
       st != PKV_OK)
     return st;
   *bytes = plan.bytes;
@@ -917,7 +936,7 @@ pkv_status pkv_paged_prefix_decode_attention(const void* q, const void* k_cache,
     return fail(PKV_ERR_INVALID_ARGUMENT, "q, caches, out and workspace must be 16-byte aligned");
   PrefixPlan plan;
   if (pkv_status st = plan_prefix_decode(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, num_groups,
-                                         &plan);
+                                         num_seqs, &plan);
       st != PKV_OK)
     return st;
   if (workspace_bytes < plan.bytes || (!workspace && plan.bytes))

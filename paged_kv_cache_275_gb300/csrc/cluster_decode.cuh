@@ -340,17 +340,33 @@ struct ClusterForm {
   // call, because the pairs are too many or it would take longer than the other form, which takes `other_us` or, if
   // `streamed`, that and the time of streaming the call's blocks over the whole GPU (of which kUneven are taken to exist, as
   // sequences may be shorter than their tables).
-  static cudaError_t ctas(int num_seqs, int num_kv_heads, int visible_blocks, float other_us, bool streamed, int* out) {
-    const int* counts = nullptr;
-    const cudaError_t e = resident(&counts);
-    if (e != cudaSuccess) return e;
-    const int64_t pairs = static_cast<int64_t>(num_seqs) * num_kv_heads;
+  static int choose(const int* counts, int64_t pairs, int visible_blocks, float other_us, bool streamed) {
     int k = 0;
     while (k < 3 && (kClusterWarps * 2 << k) < visible_blocks && pairs <= counts[k + 1]) ++k;
     const float bytes = static_cast<float>(pairs) * visible_blocks * (2.f * Geo<D, G>::kTileBytes);
     const float mine = kClusterUs + kBlockUs<D> * visible_blocks / (kClusterWarps << k);
     const float other = other_us + (streamed ? kUneven * bytes / kStreamRate : 0.f);
-    *out = pairs <= counts[k] && mine <= other ? 1 << k : 0;
+    return pairs <= counts[k] && mine <= other ? 1 << k : 0;
+  }
+  static cudaError_t ctas(int num_seqs, int num_kv_heads, int visible_blocks, float other_us, bool streamed, int* out) {
+    const int* counts = nullptr;
+    const cudaError_t e = resident(&counts);
+    if (e != cudaSuccess) return e;
+    *out = choose(counts, static_cast<int64_t>(num_seqs) * num_kv_heads, visible_blocks, other_us, streamed);
+    return cudaSuccess;
+  }
+  // Whether a call of every number of sequences up to num_seqs takes this form.  With as many CTAs a pair the smallest batch
+  // is the first not to (its other form streams least), so one batch for each number of CTAs is looked at.
+  static cudaError_t takes_all(int num_seqs, int num_kv_heads, int visible_blocks, float other_us, bool streamed, bool* out) {
+    const int* counts = nullptr;
+    const cudaError_t e = resident(&counts);
+    if (e != cudaSuccess) return e;
+    auto takes = [&](int64_t seqs) { return choose(counts, seqs * num_kv_heads, visible_blocks, other_us, streamed) != 0; };
+    *out = takes(num_seqs) && takes(1);
+    for (int k = 1; k <= 3; ++k) {
+      const int64_t fewer_ctas = counts[k] / num_kv_heads + 1;  // the first batch with so many pairs that they get fewer
+      if (fewer_ctas < num_seqs) *out = *out && takes(fewer_ctas);
+    }
     return cudaSuccess;
   }
 

@@ -36,6 +36,8 @@ cudaError_t resident_tail_pieces(int head_dim, int group, int num_seqs, int* pie
 // Windowed decode, a cluster of `ctas` CTAs a (sequence, kv head): how many suit a call (0: it is too large for this
 // form), and the launch (no workspace).
 cudaError_t window_cluster_ctas(int head_dim, int group, int num_seqs, int num_kv_heads, int visible_blocks, int* ctas);
+// Whether a windowed call of every number of sequences up to num_seqs takes that form.
+cudaError_t window_cluster_takes_all(int head_dim, int group, int num_seqs, int num_kv_heads, int visible_blocks, bool* all);
 cudaError_t launch_window_cluster(const DecodeViewParams& p, int head_dim, int group, int ctas, cudaStream_t stream);
 // The same for sequences that share prefixes (each pair reads its group's blocks for itself).
 cudaError_t prefix_cluster_ctas(int head_dim, int group, int num_seqs, int num_kv_heads, int visible_blocks, int* ctas);

@@ -1448,13 +1448,15 @@ struct Instance {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if ((e = prepare(dev)) != cudaSuccess) return e;
-    // The answer goes by the shared memory, which goes by the number of sequences: the last one is kept per device.
+    // The answer goes by the shared memory, which goes by the number of sequences: those of a single sequence (for which
+    // workspaces are sized) and of the last number asked for are kept per device.
     static std::mutex mu;
-    static struct { size_t smem; int pieces; } last[64];
+    static struct { size_t smem; int pieces; } known[64][2];
     const size_t smem = partition_smem_bytes<D, G, kView>(num_seqs);
     std::lock_guard<std::mutex> lock(mu);
-    if (dev < 64 && last[dev].smem == smem) {
-      *pieces = last[dev].pieces;
+    auto* last = dev < 64 ? &known[dev][num_seqs == 1] : nullptr;
+    if (last && last->smem == smem) {
+      *pieces = last->pieces;
       return cudaSuccess;
     }
     int sms = 0, per_sm = 0;
@@ -1462,9 +1464,9 @@ struct Instance {
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kPartition, NW * 32, smem);
     if (e != cudaSuccess) return e;
     *pieces = sms * (per_sm > 0 ? per_sm : 1) * NW;
-    if (dev < 64) {
-      last[dev].smem = smem;
-      last[dev].pieces = *pieces;
+    if (last) {
+      last->smem = smem;
+      last->pieces = *pieces;
     }
     return cudaSuccess;
   }

@@ -9,11 +9,19 @@
 
 namespace pkv {
 
+// The partition and join kernels take 8.7 us besides streaming if the pairs are many; of few pairs the join has so many
+// states that they lose up to 16 blocks a warp.
+constexpr float kOtherFormUs = 18.4f;
+
 cudaError_t window_cluster_ctas(int head_dim, int group, int num_seqs, int num_kv_heads, int visible_blocks, int* ctas) {
-  // The partition and join kernels take 8.7 us besides streaming if the pairs are many; of few pairs the join has so many
-  // states that they lose up to 16 blocks a warp.
   return dispatch_cluster<View::kWindow>(head_dim, group, [&](auto form) {
-    return decltype(form)::ctas(num_seqs, num_kv_heads, visible_blocks, 18.4f, true, ctas);
+    return decltype(form)::ctas(num_seqs, num_kv_heads, visible_blocks, kOtherFormUs, true, ctas);
+  });
+}
+
+cudaError_t window_cluster_takes_all(int head_dim, int group, int num_seqs, int num_kv_heads, int visible_blocks, bool* all) {
+  return dispatch_cluster<View::kWindow>(head_dim, group, [&](auto form) {
+    return decltype(form)::takes_all(num_seqs, num_kv_heads, visible_blocks, kOtherFormUs, true, all);
   });
 }
 
