@@ -57,14 +57,14 @@ FALLBACK_HBM_GBS = 6800.0
 L2_BYTES = 126 * 2 ** 20
 
 
+# The sources that a traffic record of a kernel stands for: the file that holds it and every header that one includes.
+_CSRC = "paged_kv_cache_275_gb300/csrc/"
 KERNEL_SOURCES = {
-    "paged_decode_partition_kernel": ("paged_kv_cache_275_gb300/csrc/paged_decode_kernel.cuh",
-                                      "paged_kv_cache_275_gb300/csrc/pkv_internal.h"),
-    "paged_prefill_kernel": ("paged_kv_cache_275_gb300/csrc/paged_prefill_kernel.cuh",
-                             "paged_kv_cache_275_gb300/csrc/paged_prefill.h",
-                             "paged_kv_cache_275_gb300/csrc/pkv_internal.h"),
-    "kv_append_kernel": ("paged_kv_cache_275_gb300/csrc/kv_append.cu",
-                         "paged_kv_cache_275_gb300/csrc/pkv_internal.h"),
+    "paged_decode_partition_kernel": tuple(_CSRC + f for f in (
+        "paged_decode_kernel.cuh", "decode_views.h", "pkv_internal.h")),
+    "paged_prefill_kernel": tuple(_CSRC + f for f in (
+        "paged_prefill_kernel.cuh", "paged_prefill.h", "shared_plan.cuh", "decode_views.h", "pkv_internal.h")),
+    "kv_append_kernel": tuple(_CSRC + f for f in ("kv_append.cu", "pkv_internal.h")),
 }
 
 
