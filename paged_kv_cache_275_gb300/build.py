@@ -63,7 +63,9 @@ def extra_flags() -> list[str]:
 
 
 def _stamp() -> str:
-    return " ".join([*extra_flags(), "torch", importlib.metadata.version("torch")])
+    """What the binaries depend on besides the sources; the binding goes by the interpreter's ABI as well as by torch's."""
+    return " ".join([*extra_flags(), "torch", importlib.metadata.version("torch"), "python",
+                     str(sysconfig.get_config_var("SOABI"))])
 
 
 def needs_build() -> bool:
