@@ -491,6 +491,9 @@ def paged_prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
 # ----------------------------------------------------------------------------
 # Rotary append, windowed attention, shared-prefix decode
 # ----------------------------------------------------------------------------
+# A call that needs a workspace and is given none keeps one for its host thread, device and stream until the thread ends.
+# While torch.cuda.graph captures, it takes one from the graph's memory instead; a capture that was begun by other means has
+# no such memory, and its calls need a workspace that lives as long as the graph.
 MAX_POSITION_AXES = 4
 
 

@@ -104,7 +104,7 @@ class OnDevice {
     if (changed_) c10::cuda::set_device(static_cast<c10::DeviceIndex>(device));
   }
   ~OnDevice() {
-    if (changed_) c10::cuda::set_device(static_cast<c10::DeviceIndex>(before_));
+    if (changed_) (void)cudaSetDevice(before_);  // (nothing may be thrown here; the call's own status says what failed)
   }
   OnDevice(const OnDevice&) = delete;
 
