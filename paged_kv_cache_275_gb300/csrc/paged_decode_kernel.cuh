@@ -174,7 +174,7 @@ static_assert(PKV_MMA_MIN_G == 4 || PKV_MMA_MIN_G == 8,
 // shared prefix's kernel, where it is an SM's own speed that counts, and 64-dim heads and four heads gain alone
 // (prefix of 4096, tails of 16..1024 tokens, 64 sequences of 8 kv heads, D 128, us a call with the CUDA cores and with
 // these: one head 32.5, 31.5; two 34.2, 32.4; four 44.7, 36.5; window of 4096 at four heads 141.6, 132.4, at one and two
-// 128.4, 129.4 and 129.1, 131.0; at D 64 one head 80.8, 69.8, four 108.8, 72.0).
+// 128.4, 129.4 and 129.1, 131.0; at D 64 one head 80.8, 69.8, four 108.8, 72.0; the prefix's weights were in one part then).
 template <int G, View kView>
 struct Split {
   static constexpr bool kMma = kView != View::kAll || G >= PKV_MMA_MIN_G;
@@ -207,8 +207,9 @@ constexpr int ptile_bytes() {
 #endif
 template <int D, int G, View kView>
 struct Shape;
-// The tail view's CTAs come and go beside the prefix kernel's, so small ones pack better: 128 sequences behind 8192
-// tokens take 47.7 us a call with 4 warps, 47.1 with 2, 49.2 with 8; 150 behind five prompts 70.6, 71.5 and 70.7.
+// The tail view's CTAs come and go beside the prefix kernel's, so small ones pack better: 24 shared-prefix calls (those of
+// shared_plan.cuh, the join fetching four states ahead) take 46.2 us in the geometric mean with 4 warps, 46.6 with 2, 46.8
+// with 8.
 template <int G>
 struct Shape<128, G, View::kTail> {
   static constexpr int kWarps = 4;
@@ -232,8 +233,9 @@ struct Shape<64, G, View::kAll> {
   static constexpr int kWarps = PKV_D64_WARPS;
   static constexpr int kStages = PKV_D64_STAGES;
 };
-// Blocks of 64 dims are small: warps in flight count more than stages (61 sequences with a window of 4095, eight heads:
-// 47.0 us with 8 warps of 2 stages, 57.6 with 8 x 4, 56.5 with 4 x 4, 57.0 with 8 x 3, 46.9 with 16 x 2, 50.5 with 12 x 2).
+// Blocks of 64 dims are small: warps in flight count more than stages (twelve windowed calls, 30 to 200 sequences, one to
+// eight heads a group, windows of 500 to 8192: 38.9 us in the geometric mean with 8 warps of 2 stages, 43.2 with 8 x 4, 43.0
+// with 4 x 4, 42.9 with 8 x 3, 39.1 with 16 x 2 and with 12 x 2).
 template <int G, View kView>
 struct Shape<64, G, kView> {
   static constexpr int kWarps = 8;
@@ -660,9 +662,8 @@ __device__ __forceinline__ int pieces_of(const DecodeViewParams& p, long long to
 }
 
 // Tail view: where piece w of a stream of `total` items begins.  CTAs start in their order, as SMs become free of the
-// prefix kernel, so the pieces get smaller, from 1.6 to 0.4 of their mean: the CTAs that start last are soon done (128
-// sequences behind one prefix 47.7 us, 150 behind five 70.6; from 1.5 48.1 and 70.5, from 1.7 47.6 and 71.6, from 1.9 48.4
-// and 73.0, all alike 50.1 and 71.2).  With a mean of 6 items no piece is empty.
+// prefix kernel, so the pieces get smaller, from 1.6 to 0.4 of their mean: the CTAs that start last are soon done (24 calls,
+// as for the tail's shape, 46.2 us in the geometric mean; from 1.5 46.3, from 1.7 46.2, all alike 47.9).  With a mean of 6 items no piece is empty.
 __device__ __forceinline__ long long shrinking_bound(int w, long long total, int pieces) {
   if (w >= pieces) return total;
   const float x = static_cast<float>(w) / static_cast<float>(pieces);
@@ -1299,7 +1300,10 @@ template <int D, int G, View kView, int kSlices>
 __global__ void __launch_bounds__(G * kSlices * 32) join_states_kernel(const DecodeViewParams p) {
   constexpr int kPieceFloats = Geo<D, G>::kPieceFloats;
   constexpr int kPer = D / 32;
-  constexpr int kAhead = 4;  // (150 sequences of eight heads behind prefixes: 70.6 us a call; with 2 the same, with 8 71.3)
+  // States fetched before any is combined.  A tail's pairs have the prefix's splits besides (24 calls 44.4 us in the geometric
+  // mean with 8, 47.0 with 2, 46.0 with 4, 44.9 with 6, 45.0 with 12); a window's mostly two or three (26 calls alike to 1 %
+  // with 4, 6 and 8, but 128 sequences 144.1 us with 4 and 145.6 with 8).
+  constexpr int kAhead = kView == View::kTail ? 8 : 4;
   __shared__ float2 s_ml[kSlices][G];
   __shared__ float s_o[kSlices][G][D];
   const int hkv = p.num_kv_heads;
