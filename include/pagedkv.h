@@ -425,11 +425,13 @@ pkv_status pkv_window_decode_workspace_size(int32_t num_seqs, int32_t num_q_head
  * (Calls of more than 320 sequences are not split, and need none.)
  *
  * Table entries of blocks that no row of the sequence's chunk sees are not read, and tokens that no row of the
- * chunk sees do not matter, whatever they hold.  num_query_tokens is the number of rows of q and out (0: a no-op); a sequence whose
- * chunk reaches outside them sets PKV_DEVERR_CONTEXT_LEN_TOO_LONG and is skipped, and so is one that starts before the end of
- * an earlier sequence's chunk (of its 320, counted from the first).  A token that some rows see has to be
+ * chunk sees do not matter, whatever they hold.  num_query_tokens is the number of rows of q and out (0: a no-op); a
+ * sequence whose chunk reaches outside them sets PKV_DEVERR_CONTEXT_LEN_TOO_LONG and is skipped, and so is one that starts
+ * before the end of an earlier sequence's chunk (of its 320, counted from the first).  A token that some rows see has to be
  * finite: rows of the same 128-row tile that do not see it weight it with 0, and 0 times infinity is no number.  (A CTA
- * reads the blocks that its own rows see.)
+ * reads the blocks that its own rows see.)  The weights are rounded to bf16 against the running maximum, as in
+ * pkv_paged_prefill_attention, so the last bits of a row depend on the steps and splits
+ * that its keys fall into, which go by the whole call.
  */
 pkv_status pkv_paged_window_prefill_attention(const void* q, const void* k_cache, const void* v_cache,
                                               const int32_t* block_tables, int32_t max_blocks_per_seq,

@@ -663,7 +663,8 @@ __device__ __forceinline__ int pieces_of(const DecodeViewParams& p, long long to
 
 // Tail view: where piece w of a stream of `total` items begins.  CTAs start in their order, as SMs become free of the
 // prefix kernel, so the pieces get smaller, from 1.6 to 0.4 of their mean: the CTAs that start last are soon done (24 calls,
-// as for the tail's shape, 46.2 us in the geometric mean; from 1.5 46.3, from 1.7 46.2, all alike 47.9).  With a mean of 6 items no piece is empty.
+// as for the tail's shape, 46.2 us in the geometric mean; from 1.5 46.3, from 1.7 46.2, all alike 47.9).  With a mean of 6
+// items no piece is empty.
 __device__ __forceinline__ long long shrinking_bound(int w, long long total, int pieces) {
   if (w >= pieces) return total;
   const float x = static_cast<float>(w) / static_cast<float>(pieces);

@@ -9,8 +9,8 @@
 
 namespace pkv {
 cudaError_t prefix_cluster_ctas(int head_dim, int group, int num_seqs, int num_kv_heads, int visible_blocks, int* ctas) {
-  // What the three kernels take depends on lengths that only the device knows: 10 us at least, 14 to 15 where a warp here
-  // has 8 blocks (which takes 12), and less than here where it has 16 (16 sequences of 8 kv heads behind 2048 tokens: 15.2
+  // What the three kernels take depends on lengths that only the device knows: 10 us at least, 13 to 14 where a warp here
+  // has 8 blocks (which takes 12), and less than here where it has 16 (16 sequences of 8 kv heads behind 2048 tokens: 14.3
   // and 18.7 us).
   return dispatch_cluster<View::kTail>(head_dim, group, [&](auto form) {
     return decltype(form)::ctas(num_seqs, num_kv_heads, visible_blocks, 13.2f, false, ctas);

@@ -15,9 +15,9 @@ constexpr int kPlanRows = 256;  // query rows of a unit (a tile pair)
 // bytes a microsecond that an SM streams of a tail, beside the prefix and when all SMs stream; and microseconds that a
 // tail which outlasts the prefix takes to get going.  Chosen so that the splits they lead to are near the best of all
 // splits, measured over 24 calls (16 to 128 sequences, one to six groups, prefixes of 200 to 16384 tokens, 1 to 8 kv heads):
-// 46.2 us in the geometric mean (44.4 since the join fetches eight states ahead), against 47.0 with (4, 1.85, 1, 3.8e4, 3.6e4, 2), the choice for steps with weights in one
-// part, 46.4 with (4, 2.6, 1.4, 4.1e4, 3.9e4, 2), 46.3 with (5, 2.6, 1.4, 4.4e4, 4.2e4, 2) and 47.3, with one call half as
-// slow again, with (4, 2.45, 1.4, 3.8e4, 3.6e4, 2).
+// 46.2 us in the geometric mean (44.4 since the join fetches eight states ahead), against 47.0 with (4, 1.85, 1, 3.8e4,
+// 3.6e4, 2), the choice for steps with weights in one part, 46.4 with (4, 2.6, 1.4, 4.1e4, 3.9e4, 2), 46.3 with (5, 2.6,
+// 1.4, 4.4e4, 4.2e4, 2) and 47.3, with one call half as slow again, with (4, 2.45, 1.4, 3.8e4, 3.6e4, 2).
 constexpr float kSharedCtaUs = 4.f, kSharedStepUs = 2.45f, kSharedOneTileStepUs = 1.4f;
 constexpr float kTailEarlyRate = 4.4e4f, kTailLateRate = 4.2e4f, kTailLateUs = 2.f;
 
