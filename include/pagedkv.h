@@ -493,6 +493,81 @@ pkv_status pkv_prefix_decode_workspace_size(int32_t num_seqs, int32_t num_q_head
                                             size_t* bytes);
 
 /*
+ * The cache in 8 bits.  A row (one token's K or V of one kv head, head_dim values) is held as e4m3 codes and one exponent
+ * byte e, and stands for code * 2^(e - 127):
+ *
+ *   k_cache, v_cache  device, e4m3 [num_blocks][num_kv_heads][16][head_dim]
+ *   kv_scales         device, uint8 [num_blocks][num_kv_heads][2][16]: the exponents of a block's K rows, then of its V rows
+ *
+ * With a the row's largest finite magnitude, e - 127 is the least integer s >= -127 with a <= 448 * 2^s (-127 if a is 0),
+ * and the codes are x * 2^-s rounded to nearest even; infinities and NaN become NaN.  The type keeps four significant bits
+ * and a power of two takes none of them, so that codes and values are exact in any arithmetic.  16-byte alignment, streams
+ * and errors are those of the bf16 calls.  Exponents of 248 and above, which no append writes, give unspecified results.
+ *
+ * pkv_kv_append_fp8: pkv_kv_append into such a cache.  Rows t of k and v start t * (stride) elements behind the first and
+ * hold [num_kv_heads][head_dim] contiguously; a stride is a multiple of 8 (rows may be slices of a projection's output).
+ */
+pkv_status pkv_kv_append_fp8(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int64_t* slot_mapping,
+                             int64_t num_tokens, int32_t num_kv_heads, int32_t head_dim, void* k_cache, void* v_cache,
+                             void* kv_scales, int64_t num_blocks, int32_t block_size, pkv_stream_t stream);
+/* pkv_rope_append into such a cache: the rotated k, rounded to bf16, and v are quantised as they are written. */
+pkv_status pkv_rope_append_fp8(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                               int64_t v_stride, const int64_t* positions, int32_t num_axes, int64_t axis_stride,
+                               const uint8_t* freq_axes, const float* cos_sin, int64_t max_position,
+                               const int64_t* slot_mapping, int64_t num_tokens, int32_t num_q_heads,
+                               int32_t num_kv_heads, int32_t head_dim, void* q_out, int64_t q_out_stride, void* k_cache,
+                               void* v_cache, void* kv_scales, int64_t num_blocks, int32_t block_size,
+                               pkv_stream_t stream);
+/*
+ * Cached rows read back as bf16: for every i in [0, num_tokens) with slot_mapping[i] >= 0, the rows of that slot go to
+ * k[i][:][:] and v[i][:][:] (strides as for the append, at least num_kv_heads * head_dim; k and v must not overlap).  Exact:
+ * bf16 holds every value, but that one of 2^128 (stored for magnitudes above 3.29e38) is infinity and those below 2^-133 are
+ * rounded.  A negative slot leaves its rows as they are; a slot may come several times.  Device-side: a slot >= 16 *
+ * num_blocks sets PKV_DEVERR_SLOT_OUT_OF_RANGE and its rows are left as they are.
+ */
+pkv_status pkv_kv_gather_fp8(const void* k_cache, const void* v_cache, const void* kv_scales, int64_t num_blocks,
+                             int32_t block_size, const int64_t* slot_mapping, int64_t num_tokens, int32_t num_kv_heads,
+                             int32_t head_dim, void* k, int64_t k_stride, void* v, int64_t v_stride,
+                             pkv_stream_t stream);
+/* pkv_copy_blocks of such a cache: codes and exponents. */
+pkv_status pkv_copy_blocks_fp8(void* k_cache, void* v_cache, void* kv_scales, const int64_t* src_dst, int32_t num_pairs,
+                               int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks, pkv_stream_t stream);
+/*
+ * pkv_paged_decode_attention over such a cache (q and out bf16).  num_blocks * num_kv_heads * 16 must be below 2^31 and
+ * num_seqs at most 65535.  A token that a sequence does not see does not matter, whatever its row and exponent hold.
+ *
+ *   workspace   device, 16-byte aligned, at least pkv_fp8_decode_workspace_size bytes (may be NULL if that is 0); scratch,
+ *               as for pkv_paged_decode_attention
+ */
+pkv_status pkv_paged_fp8_decode_attention(const void* q, const void* k_cache, const void* v_cache, const void* kv_scales,
+                                          const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                          const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
+                                          int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks,
+                                          int32_t block_size, float scale, void* out, void* workspace,
+                                          size_t workspace_bytes, pkv_stream_t stream);
+/* Its workspace on the current device.  What is enough for num_seqs sequences and max_blocks_per_seq is enough for fewer. */
+pkv_status pkv_fp8_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                         int32_t max_blocks_per_seq, size_t* bytes);
+/*
+ * pkv_paged_prefill_attention over such a cache (q and out bf16), scale > 0: prompt chunks, and the few rows a sequence of
+ * drafted tokens.  num_query_tokens is the number of rows of q and out (0: a no-op); a sequence whose chunk reaches outside
+ * them, or is longer than its context, sets PKV_DEVERR_CONTEXT_LEN_TOO_LONG and is skipped; rows past max_query_len of a
+ * chunk are not written, and set it too.  num_blocks * num_kv_heads * 16 must be below 2^31.  A token that some rows of a
+ * sequence's chunk see has to be finite, or the rows of the chunk that do not see it are unspecified.
+ */
+pkv_status pkv_paged_fp8_prefill_attention(const void* q, const void* k_cache, const void* v_cache, const void* kv_scales,
+                                           const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                           const int32_t* context_lens, const int32_t* query_start,
+                                           int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs,
+                                           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                           int64_t num_blocks, int32_t block_size, float scale, void* out,
+                                           void* workspace, size_t workspace_bytes, pkv_stream_t stream);
+/* Its workspace on the current device, for these sizes. */
+pkv_status pkv_fp8_prefill_workspace_size(int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs,
+                                          int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                          int32_t max_blocks_per_seq, size_t* bytes);
+
+/*
  * Copy whole KV blocks inside the pool: the copy half of copy-on-write for
  * blocks shared between sequences.  The pages let requests share a prompt's
  * KV blocks ("v0版本介绍", section "为什么需要推理框架") and plan a prefix

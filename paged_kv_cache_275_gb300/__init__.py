@@ -14,7 +14,9 @@ from ._capi import (BLOCK_SIZE, DEVERR_BLOCK_ID_OUT_OF_RANGE, DEVERR_COPY_OUT_OF
                     selftest_wait_timeout, workspace_size, MAX_POSITION_AXES, paged_prefix_decode_attention,
                     paged_window_decode_attention, paged_window_prefill_attention, prefix_decode_workspace_size,
                     rope_append, rope_freq_axes, window_decode_workspace_size, window_prefill_default_splits,
-                    window_prefill_splits, window_prefill_workspace_size)
+                    window_prefill_splits, window_prefill_workspace_size, copy_blocks_fp8, fp8_decode_workspace_size,
+                    fp8_prefill_workspace_size, kv_append_fp8, kv_gather_fp8, paged_fp8_decode_attention,
+                    paged_fp8_prefill_attention, rope_append_fp8)
 
 __all__ = [
     "BLOCK_SIZE", "MAX_SEQS", "EXPORTS", "LIB_PATH", "PagedKVError", "PHASE_ALL", "PHASE_MERGE", "PHASE_PARTITION",
@@ -29,4 +31,6 @@ __all__ = [
     "window_decode_workspace_size", "paged_window_prefill_attention", "window_prefill_default_splits",
     "window_prefill_splits", "window_prefill_workspace_size",
     "paged_prefix_decode_attention", "prefix_decode_workspace_size",
+    "kv_append_fp8", "rope_append_fp8", "kv_gather_fp8", "copy_blocks_fp8", "paged_fp8_decode_attention",
+    "paged_fp8_prefill_attention", "fp8_decode_workspace_size", "fp8_prefill_workspace_size",
 ]

@@ -63,6 +63,14 @@ EXPORTS = (
     "pkv_window_prefill_workspace_size",
     "pkv_paged_prefix_decode_attention",
     "pkv_prefix_decode_workspace_size",
+    "pkv_kv_append_fp8",
+    "pkv_rope_append_fp8",
+    "pkv_kv_gather_fp8",
+    "pkv_copy_blocks_fp8",
+    "pkv_paged_fp8_decode_attention",
+    "pkv_fp8_decode_workspace_size",
+    "pkv_paged_fp8_prefill_attention",
+    "pkv_fp8_prefill_workspace_size",
     "pkv_bm_create",
     "pkv_bm_destroy",
     "pkv_bm_num_free",
@@ -133,6 +141,16 @@ def load(path: Path | str | None = None) -> ctypes.CDLL:
         lib.pkv_paged_prefix_decode_attention.argtypes = [V, V, V, V, I32, V, V, V, I32, I32, I32, I32, I32, I64, I32,
                                                           F32, V, V, SZ, V]
         lib.pkv_prefix_decode_workspace_size.argtypes = [I32] * 6 + [ctypes.POINTER(SZ)]
+        lib.pkv_kv_append_fp8.argtypes = [V, I64, V, I64, V, I64, I32, I32, V, V, V, I64, I32, V]
+        lib.pkv_rope_append_fp8.argtypes = [V, I64, V, I64, V, I64, V, I32, I64, ctypes.c_char_p, V, I64, V, I64, I32, I32,
+                                            I32, V, I64, V, V, V, I64, I32, V]
+        lib.pkv_kv_gather_fp8.argtypes = [V, V, V, I64, I32, V, I64, I32, I32, V, I64, V, I64, V]
+        lib.pkv_copy_blocks_fp8.argtypes = [V, V, V, V, I32, I32, I32, I64, V]
+        lib.pkv_paged_fp8_decode_attention.argtypes = [V, V, V, V, V, I32, V, I32, I32, I32, I32, I64, I32, F32, V, V, SZ, V]
+        lib.pkv_fp8_decode_workspace_size.argtypes = [I32] * 5 + [ctypes.POINTER(SZ)]
+        lib.pkv_paged_fp8_prefill_attention.argtypes = [V, V, V, V, V, I32, V, V, I64, I32, I32, I32, I32, I32, I64, I32, F32,
+                                                        V, V, SZ, V]
+        lib.pkv_fp8_prefill_workspace_size.argtypes = [I64] + [I32] * 6 + [ctypes.POINTER(SZ)]
         lib.pkv_bm_create.argtypes = [I64, V, ctypes.POINTER(V)]
         lib.pkv_bm_destroy.argtypes = [V]
         lib.pkv_bm_num_free.argtypes = [V, ctypes.POINTER(I64)]
@@ -155,7 +173,10 @@ def load(path: Path | str | None = None) -> ctypes.CDLL:
                      "pkv_window_decode_workspace_size", "pkv_paged_window_prefill_attention",
                      "pkv_window_prefill_default_splits", "pkv_window_prefill_splits",
                      "pkv_window_prefill_workspace_size", "pkv_paged_prefix_decode_attention",
-                     "pkv_prefix_decode_workspace_size"):
+                     "pkv_prefix_decode_workspace_size", "pkv_kv_append_fp8", "pkv_rope_append_fp8",
+                     "pkv_kv_gather_fp8", "pkv_copy_blocks_fp8", "pkv_paged_fp8_decode_attention",
+                     "pkv_fp8_decode_workspace_size", "pkv_paged_fp8_prefill_attention",
+                     "pkv_fp8_prefill_workspace_size"):
             getattr(lib, name).restype = ctypes.c_int
         lib.pkv_last_error_message.argtypes = []
         lib.pkv_last_error_message.restype = ctypes.c_char_p
@@ -616,3 +637,77 @@ def paged_prefix_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cach
     """
     return (_binding or _native()).prefix_decode(q, k_cache, v_cache, block_tables, context_lens, group_start,
                                                  prefix_lens, scale, out, workspace, stream)
+
+
+# ----------------------------------------------------------------------------
+# The cache in 8 bits
+# ----------------------------------------------------------------------------
+# k_cache, v_cache: float8_e4m3fn [NB, Hkv, 16, D]; kv_scales: uint8 [NB, Hkv, 2, 16], the exponents of a block's K rows and
+# then of its V rows.  A row stands for codes * 2^(exponent - 127); include/pagedkv.h has the rule that picks the exponent.
+def kv_append_fp8(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                  v_cache: torch.Tensor, kv_scales: torch.Tensor, *, stream: torch.cuda.Stream | None = None) -> None:
+    """kv_append into an 8-bit cache: k/v [N, Hkv, D] bf16 are quantised as they are written (in place).
+
+    k and v may be slices of wider rows, as of one projection's output: only a token's own [Hkv, D] has to be contiguous.
+    """
+    (_binding or _native()).kv_append_fp8(k, v, slot_mapping, k_cache, v_cache, kv_scales, stream)
+
+
+def rope_append_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                    slot_mapping: torch.Tensor, cos_sin: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    kv_scales: torch.Tensor, q_out: torch.Tensor, *, freq_axes=None,
+                    stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """rope_append into an 8-bit cache: the rotated k, rounded to bf16, and v are quantised as they are written.
+
+    Arguments as for ``rope_append``.  Returns ``q_out``, which may be ``q``.
+    """
+    return (_binding or _native()).rope_append_fp8(q, k, v, positions, slot_mapping, cos_sin, k_cache, v_cache, kv_scales,
+                                                   q_out, freq_axes, stream)
+
+
+def kv_gather_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, kv_scales: torch.Tensor, slot_mapping: torch.Tensor,
+                  k: torch.Tensor, v: torch.Tensor, *, stream: torch.cuda.Stream | None = None) -> None:
+    """Read the rows at slot_mapping [N] int64 back into k and v [N, Hkv, D] bf16; negative slots leave theirs alone."""
+    (_binding or _native()).kv_gather_fp8(k_cache, v_cache, kv_scales, slot_mapping, k, v, stream)
+
+
+def copy_blocks_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, kv_scales: torch.Tensor, src_dst: torch.Tensor, *,
+                    stream: torch.cuda.Stream | None = None) -> None:
+    """copy_blocks of an 8-bit cache: codes and exponents, for every row (src, dst) of src_dst [n, 2] int64."""
+    (_binding or _native()).copy_blocks_fp8(k_cache, v_cache, kv_scales, src_dst, stream)
+
+
+def fp8_decode_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                              max_blocks_per_seq: int) -> int:
+    """Bytes of the workspace of a decode call over an 8-bit cache on the current device."""
+    return _query(ctypes.c_size_t, load().pkv_fp8_decode_workspace_size, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                  max_blocks_per_seq)
+
+
+def fp8_prefill_workspace_size(num_query_tokens: int, max_query_len: int, num_seqs: int, num_q_heads: int,
+                               num_kv_heads: int, head_dim: int, max_blocks_per_seq: int) -> int:
+    """Bytes of the workspace of a chunk attention call over an 8-bit cache on the current device."""
+    return _query(ctypes.c_size_t, load().pkv_fp8_prefill_workspace_size, num_query_tokens, max_query_len, num_seqs,
+                  num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq)
+
+
+def paged_fp8_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, kv_scales: torch.Tensor,
+                               block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float, out: torch.Tensor, *,
+                               workspace: torch.Tensor | None = None,
+                               stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """paged_decode_attention over an 8-bit cache; q and out [B, Hq, D] are bf16.  Returns ``out``."""
+    return (_binding or _native()).fp8_decode(q, k_cache, v_cache, kv_scales, block_tables, context_lens, scale, out,
+                                              workspace, stream)
+
+
+def paged_fp8_prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, kv_scales: torch.Tensor,
+                                block_tables: torch.Tensor, context_lens: torch.Tensor, query_start: torch.Tensor,
+                                max_query_len: int, scale: float, out: torch.Tensor, *,
+                                workspace: torch.Tensor | None = None,
+                                stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """paged_prefill_attention over an 8-bit cache: prompt chunks, or the few rows a sequence of drafted tokens.
+
+    q and out [T, Hq, D] are bf16; max_query_len is at least every chunk's length.  Returns ``out``.
+    """
+    return (_binding or _native()).fp8_prefill(q, k_cache, v_cache, kv_scales, block_tables, context_lens, query_start,
+                                               max_query_len, scale, out, workspace, stream)

@@ -37,6 +37,7 @@ std::string type_name(at::ScalarType t) {
     case at::kInt: return "torch.int32";
     case at::kLong: return "torch.int64";
     case at::kByte: return "torch.uint8";
+    case at::kFloat8_e4m3fn: return "torch.float8_e4m3fn";
     default: return c10::toString(t);
   }
 }
@@ -236,56 +237,172 @@ int64_t token_stride(const at::Tensor& t, const char* name, int64_t tokens, int6
   return tokens > 1 ? t.stride(0) : heads * head_dim;
 }
 
+// An 8-bit cache: its codes and exponents.
+struct Fp8Cache {
+  void *k, *v, *scales;
+  int64_t blocks, heads, rows, head_dim;
+  Fp8Cache(PyObject* k_, PyObject* v_, PyObject* scales_, int& dev) {
+    const at::Tensor& kc = contiguous(k_, "k_cache", at::kFloat8_e4m3fn, 4, dev);
+    const at::Tensor& vc = contiguous(v_, "v_cache", at::kFloat8_e4m3fn, 4, dev);
+    const at::Tensor& sc = contiguous(scales_, "kv_scales", at::kByte, 4, dev);
+    if (vc.sizes() != kc.sizes()) raise(PyExc_ValueError, "k_cache and v_cache shapes differ");
+    if (sc.size(0) != kc.size(0) || sc.size(1) != kc.size(1) || sc.size(2) != 2 || sc.size(3) != kc.size(2))
+      raise(PyExc_ValueError, "kv_scales must be " + shape_of({kc.size(0), kc.size(1), 2, kc.size(2)}) + ", got " +
+                                  shape_of(sc.sizes()));
+    k = kc.data_ptr();
+    v = vc.data_ptr();
+    scales = sc.data_ptr();
+    blocks = kc.size(0);
+    heads = kc.size(1);
+    rows = kc.size(2);
+    head_dim = kc.size(3);
+  }
+};
+
+// The position axis of each frequency as bytes, held while it lives; null with one axis.
+struct FreqAxes {
+  PyObject* held = nullptr;
+  const uint8_t* data = nullptr;
+  FreqAxes(PyObject* given, int64_t axes, int64_t head_dim) {
+    if (axes <= 1) return;
+    if (given == Py_None) raise(PyExc_ValueError, "positions of several axes need freq_axes");
+    held = PyBytes_FromObject(given);
+    if (!held) throw Raised{};
+    if (PyBytes_GET_SIZE(held) != head_dim / 2) {
+      const std::string got = std::to_string(PyBytes_GET_SIZE(held));
+      Py_DECREF(held);  // (a constructor that throws has no destructor to do it)
+      raise(PyExc_ValueError,
+            "freq_axes must hold head_dim / 2 = " + std::to_string(head_dim / 2) + " axes (got " + got + ")");
+    }
+    data = reinterpret_cast<const uint8_t*>(PyBytes_AS_STRING(held));
+  }
+  FreqAxes(const FreqAxes&) = delete;
+  ~FreqAxes() { Py_XDECREF(held); }
+};
+
+const at::Tensor& positions_of(PyObject* o, int64_t n, int dev) {
+  const at::Tensor& pos = tensor(o, "positions");
+  if (pos.scalar_type() != at::kLong || !pos.is_cuda() || pos.get_device() != dev || pos.dim() < 1 || pos.dim() > 2 ||
+      pos.size(-1) != n || (n > 1 && pos.stride(-1) != 1))
+    raise(PyExc_ValueError, "positions must be int64 [" + std::to_string(n) + "] or [axes, " + std::to_string(n) +
+                                "] on cuda:" + std::to_string(dev) + ", with contiguous rows");
+  return pos;
+}
+
+// rope_append: a = q, k, v, positions, slot_mapping, cos_sin, k_cache, v_cache, q_out, freq_axes, stream;
+// rope_append_fp8 has kv_scales behind the caches.
+template <bool kFp8>
 PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t) {
   return guarded([&]() -> PyObject* {
+    constexpr int kOut = kFp8 ? 9 : 8;
     int dev = -1;
-    const at::Tensor& kc = contiguous(a[6], "k_cache", at::kBFloat16, 4, dev);
-    const at::Tensor& vc = contiguous(a[7], "v_cache", at::kBFloat16, 4, dev);
+    void *kc, *vc, *scales = nullptr;
+    int64_t blocks, hkv, rows, d;
+    if constexpr (kFp8) {
+      const Fp8Cache cache(a[6], a[7], a[8], dev);
+      kc = cache.k, vc = cache.v, scales = cache.scales;
+      blocks = cache.blocks, hkv = cache.heads, rows = cache.rows, d = cache.head_dim;
+    } else {
+      const at::Tensor& k = contiguous(a[6], "k_cache", at::kBFloat16, 4, dev);
+      const at::Tensor& v = contiguous(a[7], "v_cache", at::kBFloat16, 4, dev);
+      if (v.sizes() != k.sizes()) raise(PyExc_ValueError, "k_cache and v_cache shapes differ");
+      kc = k.data_ptr(), vc = v.data_ptr();
+      blocks = k.size(0), hkv = k.size(1), rows = k.size(2), d = k.size(3);
+    }
     const at::Tensor& slots = contiguous(a[4], "slot_mapping", at::kLong, 1, dev);
     const at::Tensor& table = contiguous(a[5], "cos_sin", at::kFloat, 2, dev);
     const at::Tensor& q = on_device(a[0], "q", at::kBFloat16, 3, dev);
     const at::Tensor& k = on_device(a[1], "k", at::kBFloat16, 3, dev);
     const at::Tensor& v = on_device(a[2], "v", at::kBFloat16, 3, dev);
-    const at::Tensor& out = on_device(a[8], "q_out", at::kBFloat16, 3, dev);
-    const int64_t n = slots.size(0), hkv = kc.size(1), d = kc.size(3), hq = q.size(1);
-    if (vc.sizes() != kc.sizes()) raise(PyExc_ValueError, "k_cache and v_cache shapes differ");
+    const at::Tensor& out = on_device(a[kOut], "q_out", at::kBFloat16, 3, dev);
+    const int64_t n = slots.size(0), hq = q.size(1);
     if (table.size(1) != d) raise(PyExc_ValueError, "cos_sin must be [max_position, head_dim]");
     const int64_t qs = token_stride(q, "q", n, hq, d), ks = token_stride(k, "k", n, hkv, d);
     const int64_t vs = token_stride(v, "v", n, hkv, d), os = token_stride(out, "q_out", n, hq, d);
-    const at::Tensor& pos = tensor(a[3], "positions");
-    if (pos.scalar_type() != at::kLong || !pos.is_cuda() || pos.get_device() != dev || pos.dim() < 1 || pos.dim() > 2 ||
-        pos.size(-1) != n || (n > 1 && pos.stride(-1) != 1))
-      raise(PyExc_ValueError, "positions must be int64 [" + std::to_string(n) + "] or [axes, " + std::to_string(n) +
-                                  "] on cuda:" + std::to_string(dev) + ", with contiguous rows");
+    const at::Tensor& pos = positions_of(a[3], n, dev);
     const int64_t axes = pos.dim() == 1 ? 1 : pos.size(0), axis_stride = pos.dim() == 1 ? 0 : pos.stride(0);
-    PyObject* held = nullptr;  // the axes as bytes
-    struct Release {
-      PyObject*& o;
-      ~Release() { Py_XDECREF(o); }
-    } release{held};
-    const uint8_t* axis_of = nullptr;
-    if (axes > 1) {
-      if (a[9] == Py_None) raise(PyExc_ValueError, "positions of several axes need freq_axes");
-      held = PyBytes_FromObject(a[9]);
-      if (!held) throw Raised{};
-      if (PyBytes_GET_SIZE(held) != d / 2)
-        raise(PyExc_ValueError, "freq_axes must hold head_dim / 2 = " + std::to_string(d / 2) + " axes (got " +
-                                    std::to_string(PyBytes_GET_SIZE(held)) + ")");
-      axis_of = reinterpret_cast<const uint8_t*>(PyBytes_AS_STRING(held));
-    }
-    const pkv_stream_t stream = stream_of(a[10], dev);
+    const FreqAxes freq(a[kOut + 1], axes, d);
+    const pkv_stream_t stream = stream_of(a[kOut + 2], dev);
     const int32_t num_axes = extent(axes, "positions"), num_q = extent(hq, "q"), num_kv = extent(hkv, "k_cache");
-    const int32_t head_dim = extent(d, "head_dim"), block = extent(kc.size(2), "block size");
+    const int32_t head_dim = extent(d, "head_dim"), block = extent(rows, "block size");
     const OnDevice guard(dev);
     run([&] {
-      return pkv_rope_append(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-                             static_cast<const int64_t*>(pos.data_ptr()), num_axes, axis_stride, axis_of,
-                             static_cast<const float*>(table.data_ptr()), table.size(0),
-                             static_cast<const int64_t*>(slots.data_ptr()), n, num_q, num_kv, head_dim, out.data_ptr(),
-                             os, kc.data_ptr(), vc.data_ptr(), kc.size(0), block, stream);
+      const int64_t* at_pos = static_cast<const int64_t*>(pos.data_ptr());
+      const int64_t* at_slot = static_cast<const int64_t*>(slots.data_ptr());
+      const float* angles = static_cast<const float*>(table.data_ptr());
+      if constexpr (kFp8)
+        return pkv_rope_append_fp8(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, at_pos, num_axes, axis_stride,
+                                   freq.data, angles, table.size(0), at_slot, n, num_q, num_kv, head_dim, out.data_ptr(),
+                                   os, kc, vc, scales, blocks, block, stream);
+      else
+        return pkv_rope_append(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, at_pos, num_axes, axis_stride,
+                               freq.data, angles, table.size(0), at_slot, n, num_q, num_kv, head_dim, out.data_ptr(), os,
+                               kc, vc, blocks, block, stream);
     });
-    Py_INCREF(a[8]);
-    return a[8];
+    Py_INCREF(a[kOut]);
+    return a[kOut];
+  });
+}
+
+// kv_append_fp8(k, v, slot_mapping, k_cache, v_cache, kv_scales, stream)
+PyObject* kv_append_fp8(PyObject*, PyObject* const* a, Py_ssize_t) {
+  return guarded([&]() -> PyObject* {
+    int dev = -1;
+    const Fp8Cache cache(a[3], a[4], a[5], dev);
+    const at::Tensor& slots = contiguous(a[2], "slot_mapping", at::kLong, 1, dev);
+    const at::Tensor& k = on_device(a[0], "k", at::kBFloat16, 3, dev);
+    const at::Tensor& v = on_device(a[1], "v", at::kBFloat16, 3, dev);
+    const int64_t n = slots.size(0);
+    const int64_t ks = token_stride(k, "k", n, cache.heads, cache.head_dim), vs = token_stride(v, "v", n, cache.heads, cache.head_dim);
+    const int32_t heads = extent(cache.heads, "k_cache"), d = extent(cache.head_dim, "head_dim"), block = extent(cache.rows, "block size");
+    const pkv_stream_t stream = stream_of(a[6], dev);
+    const OnDevice guard(dev);
+    run([&] {
+      return pkv_kv_append_fp8(k.data_ptr(), ks, v.data_ptr(), vs, static_cast<const int64_t*>(slots.data_ptr()), n, heads, d,
+                               cache.k, cache.v, cache.scales, cache.blocks, block, stream);
+    });
+    Py_RETURN_NONE;
+  });
+}
+
+// kv_gather_fp8(k_cache, v_cache, kv_scales, slot_mapping, k, v, stream)
+PyObject* kv_gather_fp8(PyObject*, PyObject* const* a, Py_ssize_t) {
+  return guarded([&]() -> PyObject* {
+    int dev = -1;
+    const Fp8Cache cache(a[0], a[1], a[2], dev);
+    const at::Tensor& slots = contiguous(a[3], "slot_mapping", at::kLong, 1, dev);
+    const at::Tensor& k = on_device(a[4], "k", at::kBFloat16, 3, dev);
+    const at::Tensor& v = on_device(a[5], "v", at::kBFloat16, 3, dev);
+    const int64_t n = slots.size(0);
+    const int64_t ks = token_stride(k, "k", n, cache.heads, cache.head_dim), vs = token_stride(v, "v", n, cache.heads, cache.head_dim);
+    const int32_t heads = extent(cache.heads, "k_cache"), d = extent(cache.head_dim, "head_dim"), block = extent(cache.rows, "block size");
+    const pkv_stream_t stream = stream_of(a[6], dev);
+    const OnDevice guard(dev);
+    run([&] {
+      return pkv_kv_gather_fp8(cache.k, cache.v, cache.scales, cache.blocks, block,
+                               static_cast<const int64_t*>(slots.data_ptr()), n, heads, d, k.data_ptr(), ks, v.data_ptr(), vs,
+                               stream);
+    });
+    Py_RETURN_NONE;
+  });
+}
+
+// copy_blocks_fp8(k_cache, v_cache, kv_scales, src_dst, stream)
+PyObject* copy_blocks_fp8(PyObject*, PyObject* const* a, Py_ssize_t) {
+  return guarded([&]() -> PyObject* {
+    int dev = -1;
+    const Fp8Cache cache(a[0], a[1], a[2], dev);
+    const at::Tensor& pairs = contiguous(a[3], "src_dst", at::kLong, 2, dev);
+    if (pairs.size(1) != 2) raise(PyExc_ValueError, "src_dst must be [n, 2]");
+    if (cache.rows != PKV_BLOCK_SIZE) raise(PyExc_ValueError, "blocks must hold " + std::to_string(PKV_BLOCK_SIZE) + " tokens");
+    const int32_t n = extent(pairs.size(0), "src_dst"), heads = extent(cache.heads, "k_cache"), d = extent(cache.head_dim, "head_dim");
+    const pkv_stream_t stream = stream_of(a[4], dev);
+    const OnDevice guard(dev);
+    run([&] {
+      return pkv_copy_blocks_fp8(cache.k, cache.v, cache.scales, static_cast<const int64_t*>(pairs.data_ptr()), n, heads, d,
+                                 cache.blocks, stream);
+    });
+    Py_RETURN_NONE;
   });
 }
 
@@ -297,10 +414,11 @@ struct Attention {
   void* out;
   int32_t rows, hq, hkv, d, width, batch, block;
   int64_t blocks;
-  Attention(PyObject* q_, PyObject* kc_, PyObject* vc_, PyObject* table_, PyObject* lens_, PyObject* out_) {
+  Attention(PyObject* q_, PyObject* kc_, PyObject* vc_, PyObject* table_, PyObject* lens_, PyObject* out_,
+            at::ScalarType cache = at::kBFloat16) {
     const at::Tensor& tq = contiguous(q_, "q", at::kBFloat16, 3, dev);
-    const at::Tensor& tk = contiguous(kc_, "k_cache", at::kBFloat16, 4, dev);
-    const at::Tensor& tv = contiguous(vc_, "v_cache", at::kBFloat16, 4, dev);
+    const at::Tensor& tk = contiguous(kc_, "k_cache", cache, 4, dev);
+    const at::Tensor& tv = contiguous(vc_, "v_cache", cache, 4, dev);
     const at::Tensor& tt = contiguous(table_, "block_tables", at::kInt, 2, dev);
     const at::Tensor& tl = contiguous(lens_, "context_lens", at::kInt, 1, dev);
     const at::Tensor& to = contiguous(out_, "out", at::kBFloat16, 3, dev);
@@ -416,6 +534,61 @@ PyObject* prefix_decode(PyObject*, PyObject* const* a, Py_ssize_t) {
   });
 }
 
+// fp8_decode(q, k_cache, v_cache, kv_scales, block_tables, context_lens, scale, out, workspace, stream)
+PyObject* fp8_decode(PyObject*, PyObject* const* a, Py_ssize_t) {
+  return guarded([&]() -> PyObject* {
+    Attention t(a[0], a[1], a[2], a[4], a[5], a[7], at::kFloat8_e4m3fn);
+    t.one_row_a_sequence();
+    const Fp8Cache cache(a[1], a[2], a[3], t.dev);
+    const double scale = PyFloat_AsDouble(a[6]);
+    if (PyErr_Occurred()) throw Raised{};
+    if (t.rows > 0) {
+      const pkv_stream_t stream = stream_of(a[9], t.dev);
+      const OnDevice guard(t.dev);
+      size_t need = 0;
+      check(pkv_fp8_decode_workspace_size(t.rows, t.hq, t.hkv, t.d, t.width, &need));
+      Workspace ws;
+      if (need > 0) ws.take(a[8], t.dev, stream, need);
+      run([&] {
+        return pkv_paged_fp8_decode_attention(t.q, t.kc, t.vc, cache.scales, t.table, t.width, t.lens, t.rows, t.hq, t.hkv,
+                                              t.d, t.blocks, t.block, static_cast<float>(scale), t.out, ws.data, ws.bytes,
+                                              stream);
+      });
+    }
+    Py_INCREF(a[7]);
+    return a[7];
+  });
+}
+
+// fp8_prefill(q, k_cache, v_cache, kv_scales, block_tables, context_lens, query_start, max_query_len, scale, out, workspace,
+// stream)
+PyObject* fp8_prefill(PyObject*, PyObject* const* a, Py_ssize_t) {
+  return guarded([&]() -> PyObject* {
+    Attention t(a[0], a[1], a[2], a[4], a[5], a[9], at::kFloat8_e4m3fn);
+    const Fp8Cache cache(a[1], a[2], a[3], t.dev);
+    const at::Tensor& start = contiguous(a[6], "query_start", at::kInt, 1, t.dev);
+    if (start.size(0) != static_cast<int64_t>(t.batch) + 1)
+      raise(PyExc_ValueError, "query_start must hold " + std::to_string(static_cast<int64_t>(t.batch) + 1) + " rows' starts");
+    const int32_t most = int32(a[7], "max_query_len");
+    const double scale = PyFloat_AsDouble(a[8]);
+    if (PyErr_Occurred()) throw Raised{};
+    const pkv_stream_t stream = stream_of(a[11], t.dev);
+    const OnDevice guard(t.dev);
+    size_t need = 0;
+    check(pkv_fp8_prefill_workspace_size(t.rows, most, t.batch, t.hq, t.hkv, t.d, t.width, &need));
+    Workspace ws;
+    if (need > 0) ws.take(a[10], t.dev, stream, need);
+    run([&] {
+      return pkv_paged_fp8_prefill_attention(t.q, t.kc, t.vc, cache.scales, t.table, t.width, t.lens,
+                                             static_cast<const int32_t*>(start.data_ptr()), t.rows, most, t.batch, t.hq,
+                                             t.hkv, t.d, t.blocks, t.block, static_cast<float>(scale), t.out, ws.data,
+                                             ws.bytes, stream);
+    });
+    Py_INCREF(a[9]);
+    return a[9];
+  });
+}
+
 // register(check): the Python side's helper.
 PyObject* register_helpers(PyObject*, PyObject* const* a, Py_ssize_t) {
   Py_INCREF(a[0]);
@@ -441,9 +614,12 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef g_methods[] = {
-    method<1, register_helpers>("register"), method<11, rope_append>("rope_append"),
+    method<1, register_helpers>("register"), method<11, rope_append<false>>("rope_append"),
     method<12, window_decode>("window_decode"), method<14, window_prefill>("window_prefill"),
-    method<11, prefix_decode>("prefix_decode"), {nullptr, nullptr, 0, nullptr},
+    method<11, prefix_decode>("prefix_decode"), method<12, rope_append<true>>("rope_append_fp8"),
+    method<7, kv_append_fp8>("kv_append_fp8"), method<7, kv_gather_fp8>("kv_gather_fp8"),
+    method<5, copy_blocks_fp8>("copy_blocks_fp8"), method<10, fp8_decode>("fp8_decode"),
+    method<12, fp8_prefill>("fp8_prefill"), {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -16,6 +16,7 @@
 #include "pagedkv.h"
 #include "copy_blocks.h"
 #include "decode_views.h"
+#include "fp8_cache.h"
 #include "paged_prefill.h"
 #include "pkv_internal.h"
 #include "rope_append.h"
@@ -1009,6 +1010,298 @@ pkv_status pkv_paged_prefix_decode_attention(const void* q, const void* k_cache,
   if ((e = pkv::launch_tail_partition(p, head_dim, group, s)) != cudaSuccess) return cuda_fail(e, "tail partition launch");
   if ((e = pkv::launch_prefix_join(p, head_dim, group, s)) != cudaSuccess) return cuda_fail(e, "prefix join launch");
   g_launches.fetch_add(3);
+  return ok();
+}
+
+namespace {
+// What the append, the way back and the copies of an 8-bit cache have in common.
+pkv_status check_fp8_rows(int64_t num_tokens, int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks,
+                          int32_t block_size) {
+  if (num_tokens < 0) return fail(PKV_ERR_INVALID_ARGUMENT, "num_tokens must be >= 0 (got %lld)", (long long)num_tokens);
+  if (num_tokens > (int64_t{1} << 32)) return fail(PKV_ERR_UNSUPPORTED, "num_tokens %lld too large", (long long)num_tokens);
+  if (num_kv_heads <= 0 || num_kv_heads > (1 << 20))
+    return fail(PKV_ERR_INVALID_ARGUMENT, "num_kv_heads must be in [1, 2^20] (got %d)", num_kv_heads);
+  if (head_dim != 64 && head_dim != 128)
+    return fail(PKV_ERR_UNSUPPORTED, "head_dim %d not built (64 or 128)", head_dim);
+  if (block_size != PKV_BLOCK_SIZE)
+    return fail(PKV_ERR_UNSUPPORTED, "block_size must be %d (got %d)", PKV_BLOCK_SIZE, block_size);
+  if (num_blocks <= 0 || num_blocks > (int64_t{1} << 40))
+    return fail(PKV_ERR_INVALID_ARGUMENT, "num_blocks out of range (got %lld)", (long long)num_blocks);
+  return PKV_OK;
+}
+pkv_status check_stride(const char* name, int64_t stride, int64_t least) {
+  if (stride >= least && stride % 8 == 0 && stride <= (int64_t{1} << 40)) return PKV_OK;
+  return fail(PKV_ERR_INVALID_ARGUMENT, "%s must be a multiple of 8 elements and at least %lld (got %lld)", name,
+              (long long)least, (long long)stride);
+}
+
+pkv_status append_fp8_impl(pkv::Fp8AppendParams& p, int32_t head_dim, pkv_stream_t stream) {
+  if (p.num_tokens == 0) return ok();
+  if (!p.k || !p.v || !p.slot_mapping || !p.k_cache || !p.v_cache || !p.kv_scales)
+    return fail(PKV_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (!aligned16(p.k) || !aligned16(p.v) || !aligned16(p.k_cache) || !aligned16(p.v_cache) || !aligned16(p.kv_scales) ||
+      (reinterpret_cast<uintptr_t>(p.slot_mapping) & 7u))
+    return fail(PKV_ERR_INVALID_ARGUMENT, "k, v, the caches and kv_scales must be 16-byte aligned, slot_mapping 8-byte");
+  int sms = 0;
+  if (pkv_status st = device_state(&p.err, &sms); st != PKV_OK) return st;
+  const cudaError_t e = pkv::launch_append_fp8(p, head_dim, sms, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "append_fp8 launch");
+  g_launches.fetch_add(1);
+  return ok();
+}
+
+// The checks of both attention calls; *nothing: there is no row to compute.
+pkv_status check_fp8_attention(const pkv::Fp8AttentionParams& p, int32_t head_dim, int32_t block_size, void* workspace) {
+  if (pkv_status st = check_shapes(p.num_seqs, p.num_seqs, p.num_q_heads, p.num_kv_heads, head_dim, p.max_blocks_per_seq);
+      st != PKV_OK)
+    return st;
+  if (p.num_seqs > 65535) return fail(PKV_ERR_UNSUPPORTED, "num_seqs %d exceeds 65535", p.num_seqs);
+  if (block_size != PKV_BLOCK_SIZE)
+    return fail(PKV_ERR_UNSUPPORTED, "block_size must be %d (got %d)", PKV_BLOCK_SIZE, block_size);
+  if (p.num_blocks <= 0 || p.num_blocks > (int64_t{1} << 40) ||
+      p.num_blocks * p.num_kv_heads * PKV_BLOCK_SIZE >= (int64_t{1} << 31))
+    return fail(PKV_ERR_UNSUPPORTED, "num_blocks * num_kv_heads * 16 must be in (0, 2^31) (got %lld blocks)",
+                (long long)p.num_blocks);
+  if (!std::isfinite(p.scale)) return fail(PKV_ERR_INVALID_ARGUMENT, "scale must be finite");
+  if (p.num_seqs == 0 || p.query_rows == 0 || p.max_query_len == 0) return PKV_OK;
+  if (!p.q || !p.k_cache || !p.v_cache || !p.kv_scales || !p.block_tables || !p.context_lens || !p.out)
+    return fail(PKV_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (!aligned16(p.q) || !aligned16(p.k_cache) || !aligned16(p.v_cache) || !aligned16(p.kv_scales) || !aligned16(p.out) ||
+      !aligned16(workspace) ||
+      ((reinterpret_cast<uintptr_t>(p.block_tables) | reinterpret_cast<uintptr_t>(p.context_lens) |
+        reinterpret_cast<uintptr_t>(p.query_start)) &
+       3u))
+    return fail(PKV_ERR_INVALID_ARGUMENT, "q, caches, kv_scales, out and workspace must be 16-byte aligned");
+  return PKV_OK;
+}
+}  // namespace
+
+pkv_status pkv_kv_append_fp8(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int64_t* slot_mapping,
+                             int64_t num_tokens, int32_t num_kv_heads, int32_t head_dim, void* k_cache, void* v_cache,
+                             void* kv_scales, int64_t num_blocks, int32_t block_size, pkv_stream_t stream) {
+  if (pkv_status st = check_fp8_rows(num_tokens, num_kv_heads, head_dim, num_blocks, block_size); st != PKV_OK) return st;
+  if (pkv_status st = check_stride("k_stride", k_stride, 0); st != PKV_OK) return st;
+  if (pkv_status st = check_stride("v_stride", v_stride, 0); st != PKV_OK) return st;
+  pkv::Fp8AppendParams p{};
+  p.k = k;
+  p.v = v;
+  p.k_stride = k_stride / 8;
+  p.v_stride = v_stride / 8;
+  p.slot_mapping = slot_mapping;
+  p.k_cache = static_cast<uint8_t*>(k_cache);
+  p.v_cache = static_cast<uint8_t*>(v_cache);
+  p.kv_scales = static_cast<uint8_t*>(kv_scales);
+  p.num_tokens = num_tokens;
+  p.num_slots = num_blocks * PKV_BLOCK_SIZE;
+  p.num_kv_heads = num_kv_heads;
+  return append_fp8_impl(p, head_dim, stream);
+}
+
+pkv_status pkv_rope_append_fp8(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                               int64_t v_stride, const int64_t* positions, int32_t num_axes, int64_t axis_stride,
+                               const uint8_t* freq_axes, const float* cos_sin, int64_t max_position,
+                               const int64_t* slot_mapping, int64_t num_tokens, int32_t num_q_heads,
+                               int32_t num_kv_heads, int32_t head_dim, void* q_out, int64_t q_out_stride, void* k_cache,
+                               void* v_cache, void* kv_scales, int64_t num_blocks, int32_t block_size,
+                               pkv_stream_t stream) {
+  if (pkv_status st = check_fp8_rows(num_tokens, num_kv_heads, head_dim, num_blocks, block_size); st != PKV_OK) return st;
+  if (num_q_heads <= 0 || num_q_heads > (1 << 20))
+    return fail(PKV_ERR_INVALID_ARGUMENT, "num_q_heads must be in [1, 2^20] (got %d)", num_q_heads);
+  if (num_axes < 1 || num_axes > pkv::kFp8MaxAxes)
+    return fail(PKV_ERR_INVALID_ARGUMENT, "num_axes must be in [1, %d] (got %d)", pkv::kFp8MaxAxes, num_axes);
+  if (max_position <= 0)
+    return fail(PKV_ERR_INVALID_ARGUMENT, "max_position must be positive (got %lld)", (long long)max_position);
+  if (num_axes > 1) {
+    if (axis_stride < 0) return fail(PKV_ERR_INVALID_ARGUMENT, "axis_stride must be >= 0 (got %lld)", (long long)axis_stride);
+    if (!freq_axes) return fail(PKV_ERR_INVALID_ARGUMENT, "freq_axes is null with %d axes", num_axes);
+    for (int i = 0; i < head_dim / 2; ++i)
+      if (freq_axes[i] >= num_axes)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "freq_axes[%d] = %d, with %d axes", i, freq_axes[i], num_axes);
+  }
+  if (pkv_status st = check_stride("q_stride", q_stride, 0); st != PKV_OK) return st;
+  if (pkv_status st = check_stride("k_stride", k_stride, 0); st != PKV_OK) return st;
+  if (pkv_status st = check_stride("v_stride", v_stride, 0); st != PKV_OK) return st;
+  if (pkv_status st = check_stride("q_out_stride", q_out_stride, static_cast<int64_t>(num_q_heads) * head_dim); st != PKV_OK)
+    return st;
+  if (num_tokens == 0) return ok();
+  if (!q || !q_out || !positions || !cos_sin) return fail(PKV_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(cos_sin) || (reinterpret_cast<uintptr_t>(positions) & 7u))
+    return fail(PKV_ERR_INVALID_ARGUMENT, "q, q_out and cos_sin must be 16-byte aligned, positions 8-byte");
+  pkv::Fp8AppendParams p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_out = q_out;
+  p.q_stride = q_stride / 8;
+  p.k_stride = k_stride / 8;
+  p.v_stride = v_stride / 8;
+  p.q_out_stride = q_out_stride / 8;
+  p.positions = positions;
+  p.axis_stride = axis_stride;
+  p.cos_sin = cos_sin;
+  p.max_position = max_position;
+  p.slot_mapping = slot_mapping;
+  p.k_cache = static_cast<uint8_t*>(k_cache);
+  p.v_cache = static_cast<uint8_t*>(v_cache);
+  p.kv_scales = static_cast<uint8_t*>(kv_scales);
+  p.num_tokens = num_tokens;
+  p.num_slots = num_blocks * PKV_BLOCK_SIZE;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.num_axes = num_axes;
+  if (num_axes > 1) memcpy(p.freq_axis, freq_axes, head_dim / 2);
+  return append_fp8_impl(p, head_dim, stream);
+}
+
+pkv_status pkv_kv_gather_fp8(const void* k_cache, const void* v_cache, const void* kv_scales, int64_t num_blocks,
+                             int32_t block_size, const int64_t* slot_mapping, int64_t num_tokens, int32_t num_kv_heads,
+                             int32_t head_dim, void* k, int64_t k_stride, void* v, int64_t v_stride,
+                             pkv_stream_t stream) {
+  if (pkv_status st = check_fp8_rows(num_tokens, num_kv_heads, head_dim, num_blocks, block_size); st != PKV_OK) return st;
+  const int64_t row = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (pkv_status st = check_stride("k_stride", k_stride, row); st != PKV_OK) return st;
+  if (pkv_status st = check_stride("v_stride", v_stride, row); st != PKV_OK) return st;
+  if (num_tokens == 0) return ok();
+  if (!k_cache || !v_cache || !kv_scales || !slot_mapping || !k || !v)
+    return fail(PKV_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(kv_scales) ||
+      (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+    return fail(PKV_ERR_INVALID_ARGUMENT, "k, v, the caches and kv_scales must be 16-byte aligned, slot_mapping 8-byte");
+  pkv::Fp8GatherParams p{};
+  int sms = 0;
+  if (pkv_status st = device_state(&p.err, &sms); st != PKV_OK) return st;
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.kv_scales = static_cast<const uint8_t*>(kv_scales);
+  p.slot_mapping = slot_mapping;
+  p.k = k;
+  p.v = v;
+  p.k_stride = k_stride / 8;
+  p.v_stride = v_stride / 8;
+  p.num_tokens = num_tokens;
+  p.num_slots = num_blocks * PKV_BLOCK_SIZE;
+  p.num_kv_heads = num_kv_heads;
+  const cudaError_t e = pkv::launch_gather_fp8(p, head_dim, sms, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_gather_fp8 launch");
+  g_launches.fetch_add(1);
+  return ok();
+}
+
+pkv_status pkv_copy_blocks_fp8(void* k_cache, void* v_cache, void* kv_scales, const int64_t* src_dst, int32_t num_pairs,
+                               int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks, pkv_stream_t stream) {
+  if (num_pairs < 0) return fail(PKV_ERR_INVALID_ARGUMENT, "num_pairs must be >= 0 (got %d)", num_pairs);
+  if (num_pairs > (1 << 30)) return fail(PKV_ERR_UNSUPPORTED, "num_pairs %d too large", num_pairs);
+  if (pkv_status st = check_fp8_rows(0, num_kv_heads, head_dim, num_blocks, PKV_BLOCK_SIZE); st != PKV_OK) return st;
+  if (num_pairs == 0) return ok();
+  if (!k_cache || !v_cache || !kv_scales || !src_dst) return fail(PKV_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(kv_scales) || (reinterpret_cast<uintptr_t>(src_dst) & 7u))
+    return fail(PKV_ERR_INVALID_ARGUMENT, "caches and kv_scales must be 16-byte aligned, src_dst 8-byte aligned");
+  pkv::Fp8CopyParams p{};
+  if (pkv_status st = device_state(&p.err, nullptr); st != PKV_OK) return st;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.kv_scales = kv_scales;
+  p.src_dst = src_dst;
+  p.num_blocks = num_blocks;
+  p.cache_chunks = static_cast<int64_t>(num_kv_heads) * head_dim;  // 16 rows of head_dim bytes a head
+  p.scale_chunks = static_cast<int64_t>(num_kv_heads) * 2;
+  const cudaError_t e = pkv::launch_copy_blocks_fp8(p, num_pairs, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "copy_blocks_fp8 launch");
+  g_launches.fetch_add(1);
+  return ok();
+}
+
+pkv_status pkv_fp8_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                         int32_t max_blocks_per_seq, size_t* bytes) {
+  if (!bytes) return fail(PKV_ERR_INVALID_ARGUMENT, "bytes is null");
+  if (pkv_status st = check_shapes(num_seqs, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq); st != PKV_OK)
+    return st;
+  *bytes = 0;
+  return ok();
+}
+
+pkv_status pkv_fp8_prefill_workspace_size(int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs,
+                                          int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                          int32_t max_blocks_per_seq, size_t* bytes) {
+  if (!bytes) return fail(PKV_ERR_INVALID_ARGUMENT, "bytes is null");
+  if (num_query_tokens < 0 || max_query_len < 0)
+    return fail(PKV_ERR_INVALID_ARGUMENT, "num_query_tokens and max_query_len must be >= 0");
+  if (pkv_status st = check_shapes(num_seqs, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq); st != PKV_OK)
+    return st;
+  *bytes = 0;
+  return ok();
+}
+
+pkv_status pkv_paged_fp8_decode_attention(const void* q, const void* k_cache, const void* v_cache, const void* kv_scales,
+                                          const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                          const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
+                                          int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks,
+                                          int32_t block_size, float scale, void* out, void* workspace,
+                                          size_t workspace_bytes, pkv_stream_t stream) {
+  pkv::Fp8AttentionParams p{};
+  p.q = q;
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.kv_scales = static_cast<const uint8_t*>(kv_scales);
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.out = out;
+  p.num_blocks = num_blocks;
+  p.query_rows = num_seqs;
+  p.num_seqs = num_seqs;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.max_query_len = 1;
+  p.scale = scale;
+  if (pkv_status st = check_fp8_attention(p, head_dim, block_size, workspace); st != PKV_OK) return st;
+  if (num_seqs == 0) return ok();
+  if (pkv_status st = device_state(&p.err, nullptr); st != PKV_OK) return st;
+  const cudaError_t e = pkv::launch_attention_fp8(p, head_dim, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "fp8 decode launch");
+  g_launches.fetch_add(1);
+  return ok();
+}
+
+pkv_status pkv_paged_fp8_prefill_attention(const void* q, const void* k_cache, const void* v_cache, const void* kv_scales,
+                                           const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                           const int32_t* context_lens, const int32_t* query_start,
+                                           int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs,
+                                           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                           int64_t num_blocks, int32_t block_size, float scale, void* out,
+                                           void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+  if (num_query_tokens < 0)
+    return fail(PKV_ERR_INVALID_ARGUMENT, "num_query_tokens must be >= 0 (got %lld)", (long long)num_query_tokens);
+  if (max_query_len < 0) return fail(PKV_ERR_INVALID_ARGUMENT, "max_query_len must be >= 0 (got %d)", max_query_len);
+  if (!(scale > 0.f)) return fail(PKV_ERR_INVALID_ARGUMENT, "scale must be positive");
+  pkv::Fp8AttentionParams p{};
+  p.q = q;
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.kv_scales = static_cast<const uint8_t*>(kv_scales);
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.query_start = query_start;
+  p.out = out;
+  p.num_blocks = num_blocks;
+  p.query_rows = num_query_tokens;
+  p.num_seqs = num_seqs;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.max_query_len = max_query_len;
+  p.scale = scale;
+  if (pkv_status st = check_fp8_attention(p, head_dim, block_size, workspace); st != PKV_OK) return st;
+  // A CTA takes two 128-row tiles of 128 / G chunk tokens each; its sequence's tiles are one grid dimension.
+  const int32_t cta_tokens = pkv::prefill_cta_tokens(num_q_heads / num_kv_heads);
+  if ((static_cast<int64_t>(max_query_len) + cta_tokens - 1) / cta_tokens > 65535)
+    return fail(PKV_ERR_UNSUPPORTED, "max_query_len %d exceeds 65535 CTAs of %d chunk tokens", max_query_len, cta_tokens);
+  if (num_seqs == 0 || num_query_tokens == 0 || max_query_len == 0) return ok();
+  if (!query_start) return fail(PKV_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (pkv_status st = device_state(&p.err, nullptr); st != PKV_OK) return st;
+  const cudaError_t e = pkv::launch_attention_fp8(p, head_dim, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "fp8 prefill launch");
+  g_launches.fetch_add(1);
   return ok();
 }
 

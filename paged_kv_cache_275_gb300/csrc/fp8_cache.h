@@ -1,0 +1,90 @@
+// Internal interface of the kernels over an 8-bit cache, used by capi.cu.
+//
+// The format: a row of one kv head (head_dim values of one token's K or V) is held as e4m3 codes and one exponent byte e
+// and stands for code * 2^(e - 127).  Codes: [num_blocks][num_kv_heads][16][head_dim]; exponents:
+// [num_blocks][num_kv_heads][2][16], those of the block's K rows and then those of its V rows.
+#pragma once
+
+#include "pkv_internal.h"
+
+namespace pkv {
+
+constexpr int kFp8MaxAxes = 4;
+
+// Quantising append, with the rotation of q and k before it if cos_sin is given (fp8_cache.cu).
+struct Fp8AppendParams {
+  const void* q;  // rows of [heads][head_dim] bf16, `stride` 16-byte chunks apart
+  const void* k;
+  const void* v;
+  void* q_out;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  const int64_t* positions;  // [num_axes][num_tokens], axes axis_stride apart
+  int64_t axis_stride;
+  const float* cos_sin;  // fp32 [max_position][head_dim], or null: no rotation, and no q
+  int64_t max_position;
+  const int64_t* slot_mapping;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  uint8_t* kv_scales;
+  unsigned* err;
+  int64_t num_tokens;
+  int64_t num_slots;  // 16 * num_blocks
+  int num_q_heads;    // 0 without rotation
+  int num_kv_heads;
+  int num_axes;
+  int parts;  // warps that share a token's rows
+  uint8_t freq_axis[64];  // position axis of each of the head_dim / 2 frequencies
+};
+
+// Rows read back as bf16, by slot.
+struct Fp8GatherParams {
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const uint8_t* kv_scales;
+  const int64_t* slot_mapping;
+  void* k;  // rows of [num_kv_heads][head_dim] bf16, `stride` 16-byte chunks apart
+  void* v;
+  int64_t k_stride, v_stride;
+  unsigned* err;
+  int64_t num_tokens;
+  int64_t num_slots;
+  int num_kv_heads;
+};
+
+struct Fp8CopyParams {
+  void* k_cache;
+  void* v_cache;
+  void* kv_scales;
+  const int64_t* src_dst;  // [num_pairs][2]
+  unsigned* err;
+  int64_t num_blocks;
+  int64_t cache_chunks;  // 16-byte chunks of a block's codes of K (or V), all kv heads
+  int64_t scale_chunks;  // and of its exponents
+};
+
+struct Fp8AttentionParams {
+  const void* q;  // bf16 [query_rows][num_q_heads][head_dim]
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const uint8_t* kv_scales;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* query_start;  // [num_seqs + 1], or null: row b is sequence b's one query token
+  void* out;                   // bf16, as q
+  unsigned* err;
+  int64_t num_blocks;
+  int64_t query_rows;
+  int num_seqs;
+  int num_q_heads;
+  int num_kv_heads;
+  int max_blocks_per_seq;
+  int max_query_len;
+  float scale;
+};
+
+cudaError_t launch_append_fp8(const Fp8AppendParams& p, int head_dim, int num_sms, cudaStream_t stream);
+cudaError_t launch_gather_fp8(const Fp8GatherParams& p, int head_dim, int num_sms, cudaStream_t stream);
+cudaError_t launch_copy_blocks_fp8(const Fp8CopyParams& p, int num_pairs, cudaStream_t stream);
+cudaError_t launch_attention_fp8(const Fp8AttentionParams& p, int head_dim, cudaStream_t stream);
+
+}  // namespace pkv
