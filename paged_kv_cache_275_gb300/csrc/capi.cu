@@ -1211,12 +1211,61 @@ pkv_status pkv_copy_blocks_fp8(void* k_cache, void* v_cache, void* kv_scales, co
   return ok();
 }
 
+namespace {
+// Least units of a piece of the few-row kernel's stream.
+constexpr int32_t kFp8PieceUnits = 2;
+
+pkv_status few_rows_fp8(pkv::Fp8AttentionParams p, int32_t head_dim, void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+  int sms = 0;
+  if (pkv_status st = device_state(&p.err, &sms); st != PKV_OK) return st;
+  const int rows = p.max_query_len * (p.num_q_heads / p.num_kv_heads);
+  const pkv::Fp8FewPlan all(p.num_seqs, p.num_kv_heads, head_dim, p.max_blocks_per_seq, rows, kFp8PieceUnits, sms);
+  if (!workspace || workspace_bytes < all.bytes)
+    return fail(PKV_ERR_INVALID_ARGUMENT, "workspace too small: %zu bytes given, %zu needed", workspace ? workspace_bytes : size_t{0},
+                all.bytes);
+  p.qscale = p.scale * 1.4426950408889634f;
+  p.min_piece_units = kFp8PieceUnits;
+  p.state_rows = rows;
+  // A large batch runs in slices, in order on the same stream and workspace.
+  const size_t q_row = static_cast<size_t>(p.num_q_heads) * head_dim * 2;
+  const int32_t num_seqs = p.num_seqs;
+  for (int32_t s0 = 0; s0 < num_seqs; s0 += pkv::kFp8LaunchSeqs) {
+    pkv::Fp8AttentionParams s = p;
+    s.num_seqs = num_seqs - s0 < pkv::kFp8LaunchSeqs ? num_seqs - s0 : pkv::kFp8LaunchSeqs;
+    s.block_tables += static_cast<size_t>(s0) * p.max_blocks_per_seq;
+    s.context_lens += s0;
+    if (s.query_start) {
+      s.query_start += s0;
+    } else {
+      s.q = static_cast<const unsigned char*>(p.q) + s0 * q_row;
+      s.out = static_cast<unsigned char*>(p.out) + s0 * q_row;
+    }
+    const pkv::Fp8FewPlan plan(s.num_seqs, p.num_kv_heads, head_dim, p.max_blocks_per_seq, rows, kFp8PieceUnits, sms);
+    s.unit_heads = plan.unit_heads;
+    s.num_pieces = plan.num_pieces;
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    s.ws_records = reinterpret_cast<int*>(ws);
+    s.ws_ml = reinterpret_cast<float2*>(ws + plan.ml);
+    s.ws_states = reinterpret_cast<float*>(ws + plan.states);
+    const cudaError_t e = pkv::launch_few_rows_fp8(s, head_dim, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "fp8 attention launch");
+    g_launches.fetch_add(2);
+  }
+  return ok();
+}
+}  // namespace
+
 pkv_status pkv_fp8_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                          int32_t max_blocks_per_seq, size_t* bytes) {
   if (!bytes) return fail(PKV_ERR_INVALID_ARGUMENT, "bytes is null");
   if (pkv_status st = check_shapes(num_seqs, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq); st != PKV_OK)
     return st;
-  *bytes = 0;
+  int sms = 0;
+  if (pkv_status st = device_state(nullptr, &sms); st != PKV_OK) return st;
+  *bytes = num_seqs == 0 ? 0
+                         : pkv::Fp8FewPlan(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, num_q_heads / num_kv_heads,
+                                           kFp8PieceUnits, sms)
+                               .bytes;
   return ok();
 }
 
@@ -1229,6 +1278,12 @@ pkv_status pkv_fp8_prefill_workspace_size(int64_t num_query_tokens, int32_t max_
   if (pkv_status st = check_shapes(num_seqs, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq); st != PKV_OK)
     return st;
   *bytes = 0;
+  if (num_seqs == 0 || num_query_tokens == 0 || max_query_len == 0) return ok();
+  int sms = 0;
+  if (pkv_status st = device_state(nullptr, &sms); st != PKV_OK) return st;
+  const int64_t rows = static_cast<int64_t>(max_query_len) * (num_q_heads / num_kv_heads);
+  if (rows <= pkv::kFp8MostRows)
+    *bytes = pkv::Fp8FewPlan(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, static_cast<int>(rows), kFp8PieceUnits, sms).bytes;
   return ok();
 }
 
@@ -1256,11 +1311,7 @@ pkv_status pkv_paged_fp8_decode_attention(const void* q, const void* k_cache, co
   p.scale = scale;
   if (pkv_status st = check_fp8_attention(p, head_dim, block_size, workspace); st != PKV_OK) return st;
   if (num_seqs == 0) return ok();
-  if (pkv_status st = device_state(&p.err, nullptr); st != PKV_OK) return st;
-  const cudaError_t e = pkv::launch_attention_fp8(p, head_dim, reinterpret_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "fp8 decode launch");
-  g_launches.fetch_add(1);
-  return ok();
+  return few_rows_fp8(p, head_dim, workspace, workspace_bytes, stream);
 }
 
 pkv_status pkv_paged_fp8_prefill_attention(const void* q, const void* k_cache, const void* v_cache, const void* kv_scales,
@@ -1298,6 +1349,8 @@ pkv_status pkv_paged_fp8_prefill_attention(const void* q, const void* k_cache, c
     return fail(PKV_ERR_UNSUPPORTED, "max_query_len %d exceeds 65535 CTAs of %d chunk tokens", max_query_len, cta_tokens);
   if (num_seqs == 0 || num_query_tokens == 0 || max_query_len == 0) return ok();
   if (!query_start) return fail(PKV_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (static_cast<int64_t>(max_query_len) * (num_q_heads / num_kv_heads) <= pkv::kFp8MostRows)
+    return few_rows_fp8(p, head_dim, workspace, workspace_bytes, stream);
   if (pkv_status st = device_state(&p.err, nullptr); st != PKV_OK) return st;
   const cudaError_t e = pkv::launch_attention_fp8(p, head_dim, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "fp8 prefill launch");

@@ -1,0 +1,64 @@
+// Decode and chunks of a few tokens over the 8-bit cache (fp8_decode.cuh): instances and launches.
+#include "fp8_decode.cuh"
+
+namespace pkv {
+namespace {
+
+// The cache's codes as rows of head_dim bytes, a box the rows of a unit's heads of one block.  As wide as a row, the swizzle
+// spreads a chunk of eight rows over all banks.
+cudaError_t code_map(CUtensorMap* map, const void* cache, int64_t rows, int head_dim, int box_rows) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(head_dim)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(head_dim), static_cast<cuuint32_t>(box_rows)};
+  return encode_code_map(map, cache, 2, dims, strides, box,
+                         head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+template <int D, int NC>
+cudaError_t launch(const Fp8AttentionParams& p, cudaStream_t stream) {
+  constexpr int kMost = Few<D, NC>::smem(kFp8LaunchSeqs);
+  static_assert(Few<D, NC>::kCtas * (kMost + 1024 + 256) <= 228 * 1024, "shared memory of an SM's CTAs");
+  static std::mutex mu;
+  static uint64_t ready = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!(dev < 64 && ((ready >> dev) & 1u))) {
+      e = cudaFuncSetAttribute(&few_rows_fp8_kernel<D, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+      if (e != cudaSuccess) return e;
+      e = cudaFuncSetAttribute(&few_rows_fp8_kernel<D, NC>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+      if (e != cudaSuccess) return e;
+      if (dev < 64) ready |= uint64_t{1} << dev;
+    }
+  }
+  CUtensorMap mk, mv;
+  const int64_t rows = p.num_blocks * p.num_kv_heads * kBlockTokens;
+  if ((e = code_map(&mk, p.k_cache, rows, D, p.unit_heads * kBlockTokens)) != cudaSuccess) return e;
+  if ((e = code_map(&mv, p.v_cache, rows, D, p.unit_heads * kBlockTokens)) != cudaSuccess) return e;
+  e = launch_pdl(few_rows_fp8_kernel<D, NC>, dim3(p.num_pieces), dim3(kThreads), Few<D, NC>::smem(p.num_seqs), stream, p, mk, mv);
+  if (e != cudaSuccess) return e;
+  const unsigned pairs = static_cast<unsigned>(p.num_seqs) * p.num_kv_heads;
+  const unsigned cols = p.state_rows;
+  // Few pairs have many states each.
+  if (pairs * cols <= 1216) return launch_pdl(join_fp8_kernel<D, 8>, dim3(pairs, cols), dim3(256), 0, stream, p);
+  return launch_pdl(join_fp8_kernel<D, 1>, dim3(pairs, (cols + 3) / 4), dim3(128), 0, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_few_rows_fp8(const Fp8AttentionParams& p, int head_dim, cudaStream_t stream) {
+  const int nc = fp8_columns(p.state_rows);
+  switch (head_dim * 8 + nc) {
+    case 64 * 8 + 1: return launch<64, 1>(p, stream);
+    case 64 * 8 + 2: return launch<64, 2>(p, stream);
+    case 64 * 8 + 4: return launch<64, 4>(p, stream);
+    case 128 * 8 + 1: return launch<128, 1>(p, stream);
+    case 128 * 8 + 2: return launch<128, 2>(p, stream);
+    case 128 * 8 + 4: return launch<128, 4>(p, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace pkv

@@ -1,0 +1,731 @@
+// Attention of few query rows a sequence over the 8-bit cache: decode (one query token), and chunks of a few tokens.
+//
+//   out[row][h] = softmax_j(scale <q[row][h], K_j>) V_j  over the tokens j that the row sees,
+//   K_j = 2^(ke_j) kc_j,  V_j = 2^(ve_j) vc_j   (codes kc, vc in e4m3; one exponent a row and kv head)
+//
+// Bound by HBM: a token's K and V of a kv head are 2 D + 2 bytes, read once, and feed 4 D flop a query row.
+//
+// Products.  The rows of a (sequence, kv head), G heads of up to a few tokens, are the columns of two small products on the
+// warp-level tensor cores, a block of 16 tokens at a time:
+//   S^T [16 tokens x columns] = Kc q^T,   O^T [D x columns] += Vc^T W^T,
+// in fp16 with 32-bit sums: fp16 holds every e4m3 code exactly, and q too (bf16, eight significant bits) once a row is
+// brought to a largest value of 2^14 by a power of two, down to 2^-28 of it; smaller values lose bits that a score does not
+// show.  The exponents stay outside of the products: a score is S 2^(ke) scale, and a weight takes V's exponent with it,
+//   w_j = 2^((s_j - m) + ve_j - r),   O = 2^r sum_j w_j vc_j,   l = sum_j 2^(s_j - m),
+// with running references (base 2) m of s and r of (s - m) + ve, raised when some value passes them by 2^8, so that w is at
+// most 2^15 and the largest of a row is 2^7 or more: fp16's 11 bits hold for weights down to 2^-21 of the largest, and those
+// below 2^-32 of it vanish.  (m comes off first: next to a large score an exponent would lose its bits.)
+//
+// Work.  The batch's blocks form one stream of units: eight (block, kv head) tiles that lie next to one another, all eight
+// heads of a block, or two blocks of four heads and so on (32 KB of K and V at D = 128).  The stream is cut into equal
+// contiguous pieces, one a CTA, so that every CTA moves the same bytes whatever the lengths.  One warp fills a ring of units:
+// a block's heads are neighbours in the cache, so a unit takes one or a few large tensor copies (swizzled, so that ldmatrix
+// reads without bank conflicts).  Each of eight warps takes its tile of every unit.  A (sequence, heads) pair cut by a piece's
+// border leaves partial states (m, l, O) that a second kernel joins.
+//
+// Every wait is bounded: one that runs out sets PKV_DEVERR_PIPELINE_TIMEOUT, and its warp goes on without computing.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <mutex>
+
+#include "fp8_cache.h"
+#include "fp8_format.cuh"
+#include "fp8_maps.h"
+
+namespace pkv {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kUnitTiles = 8;  // (block, kv head) tiles of a unit, one a warp
+constexpr int kProducer = kUnitTiles;
+constexpr int kThreads = 32 * (kUnitTiles + 1);
+constexpr float kNone = -3.0e38f;  // the reference of a row that has seen no token
+constexpr float kSlack = 8.f;
+constexpr float kWeightShift = 7.f;  // the largest weight is brought to 2^7 .. 2^15
+constexpr unsigned long long kWaitNs = 2000000000ull;
+
+template <int D, int NC>
+struct Few {
+  static constexpr int kCols = 8 * NC;
+  static constexpr int kTile = kBlockTokens * D;           // bytes of one tile of K (or V)
+  static constexpr int kOperand = kUnitTiles * kTile;      // K (or V) of a unit
+  static constexpr int kScales = kUnitTiles * 2 * kBlockTokens;
+  static constexpr int kCtas = NC == 1 ? 2 : 1;            // per SM
+  static constexpr int kStages = (D == 128 ? 3 : 6) * 2 / kCtas;
+  static constexpr int kOffV = kOperand;
+  static constexpr int kStage = 2 * kOperand;
+  static constexpr int kOffScales = kStages * kStage;
+  static constexpr int kOffExchange = kOffScales + kStages * kScales;
+  static constexpr int kExchange = kUnitTiles / 2 * 32 * 64;  // 16 values a lane of four warps
+  static constexpr int kOffMl = kOffExchange + kExchange;
+  static constexpr int kMl = kUnitTiles / 2 * kCols * 8;
+  static constexpr int kOffBar = kOffMl + kMl;
+  static constexpr int kOffSeq = kOffBar + 16 * kStages;  // units before each sequence, [num_seqs + 1]
+  static constexpr int smem(int num_seqs) { return kOffSeq + (num_seqs + 1) * 4 + 1024; }  // 1024 to align the ring
+};
+
+// ---------------------------------------------------------------------------
+// PTX
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t saddr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void bar_init(uint32_t b, uint32_t n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(b), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t b) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(b) : "memory");
+}
+__device__ __forceinline__ void bar_expect_tx(uint32_t b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(b), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(b), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Bounded wait of a whole warp; false if the phase did not complete in time.
+__device__ __forceinline__ bool bar_wait(uint32_t b, uint32_t parity) {
+  bool ok = bar_try(b, parity);
+  if (!ok) {
+    const unsigned long long t0 = now_ns();
+    for (uint32_t it = 1; !ok && it < (1u << 30); ++it) {
+      ok = bar_try(b, parity);
+      if ((it & 63u) == 0 && now_ns() - t0 > kWaitNs) break;
+    }
+  }
+  return __all_sync(kAll, ok);
+}
+__device__ __forceinline__ void tensor_load(uint32_t dst, const CUtensorMap* map, int row, uint32_t b) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(b)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t b) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(b)
+               : "memory");
+}
+__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// ---------------------------------------------------------------------------
+// A sequence's rows and tokens
+// ---------------------------------------------------------------------------
+struct Rows {
+  int first;   // row of q and out
+  int count;   // query tokens computed; 0: none, or the sequence is skipped
+  int tokens;  // cached tokens that the last of them sees; row i sees tokens - count + i + 1
+  unsigned wrong;  // error bits
+};
+__device__ __forceinline__ Rows rows_of(const Fp8AttentionParams& p, int b) {
+  const int cap = p.max_blocks_per_seq * kBlockTokens;
+  const int len = __ldg(p.context_lens + b);
+  if (!p.query_start) {
+    if (len < 0) return {b, 1, 0, kErrLenNegative};
+    if (len > cap) return {b, 1, cap, kErrLenTooLong};
+    return {b, 1, len, 0u};
+  }
+  const int q0 = __ldg(p.query_start + b), q1 = __ldg(p.query_start + b + 1);
+  const int64_t chunk = static_cast<int64_t>(q1) - q0;
+  if (chunk < 0 || len < chunk || len > cap || q0 < 0 || q1 > p.query_rows) return {0, 0, 0, kErrLenTooLong};
+  const int count = min(static_cast<int>(chunk), p.max_query_len);
+  return {q0, count, len - static_cast<int>(chunk) + count, count < chunk ? kErrLenTooLong : 0u};
+}
+
+// Where of the stream a thread is: sequence, group of heads, unit of the sequence's.
+struct Walk {
+  int b, heads, unit, units;
+};
+
+// Pieces that a stream of `total` units is cut into.
+__device__ __forceinline__ int pieces_of(const Fp8AttentionParams& p, int total) {
+  const int most = (total + p.min_piece_units - 1) / p.min_piece_units;
+  return min(most, p.num_pieces);
+}
+
+template <int D, int NC>
+__global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
+    few_rows_fp8_kernel(const Fp8AttentionParams p, const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_v) {
+  using T = Few<D, NC>;
+  constexpr int kSteps = D / 16;  // 16-byte chunks of a row of codes: 16 dims, the depth of a product
+  constexpr int kStages = T::kStages;
+  extern __shared__ unsigned char raw[];
+  unsigned char* smem = raw + (-saddr(raw) & 1023u);
+  const uint32_t base = saddr(smem);
+  int* s_units = reinterpret_cast<int*>(smem + T::kOffSeq);
+  __shared__ int s_sum[kThreads / 32 + 1];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hc = p.unit_heads, nb = kUnitTiles / hc;  // heads and blocks of a unit
+  const int head_groups = p.num_kv_heads / hc;
+  const uint32_t full = base + T::kOffBar, empty = full + 8 * kStages;
+  pdl_trigger();
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      bar_init(full + 8 * s, 1);
+      bar_init(empty + 8 * s, kUnitTiles);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_units[0] = 0;
+  }
+  pdl_wait();
+
+  // Units before each sequence.
+  int running = 0;
+  for (int first = 0; first < p.num_seqs; first += kThreads) {
+    const int b = first + tid;
+    int units = 0;
+    if (b < p.num_seqs) {
+      const Rows r = rows_of(p, b);
+      if (r.wrong && blockIdx.x == 0) atomicOr(p.err, r.wrong);
+      units = r.count > 0 ? ((r.tokens + kBlockTokens - 1) / kBlockTokens + nb - 1) / nb : 0;
+    }
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(kAll, units, off);
+      if (lane >= off) units += y;
+    }
+    if (lane == 31) s_sum[warp] = units;
+    __syncthreads();
+    int before = running;
+    for (int w = 0; w < warp; ++w) before += s_sum[w];
+    if (b < p.num_seqs) s_units[b + 1] = before + units;
+    for (int w = 0; w < kThreads / 32; ++w) running += s_sum[w];
+    __syncthreads();
+  }
+  const int total = running * head_groups;
+  const int pieces = pieces_of(p, total);
+  const int piece = blockIdx.x;
+  if (piece >= pieces) return;
+  const int n0 = static_cast<int>(static_cast<int64_t>(piece) * total / pieces);
+  const int n1 = static_cast<int>(static_cast<int64_t>(piece + 1) * total / pieces);
+  Walk at;
+  {
+    int lo = 0, hi = p.num_seqs - 1;  // the sequence of unit n0: the last with units before it at or below
+    const int n = n0 / head_groups;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_units[mid] <= n) lo = mid;
+      else hi = mid - 1;
+    }
+    at.b = lo;
+    at.units = s_units[lo + 1] - s_units[lo];
+    const int rest = n0 - s_units[lo] * head_groups;
+    at.heads = rest / at.units;
+    at.unit = rest - at.heads * at.units;
+  }
+  auto advance = [&] {
+    if (++at.unit < at.units) return;
+    at.unit = 0;
+    if (++at.heads < head_groups) return;
+    at.heads = 0;
+    do {
+      ++at.b;
+      at.units = s_units[at.b + 1] - s_units[at.b];
+    } while (at.units == 0);
+  };
+
+  if (warp == kProducer) {
+    // ---------------- copies (whole warp) ----------------
+    int window = -1, ids = 0, next_ids = 0;  // 32 block ids of the sequence, one a lane, and the 32 behind them
+    int seq = -1, heads = -1, blocks = 0, issued = 0;
+    const int32_t* table = nullptr;
+    bool ok = true;
+    auto fetch = [&](int w) -> int {
+      const int col = 32 * w + lane;
+      if (col >= blocks) return 0;
+      const int id = __ldg(table + col);
+      if (id < 0 || id >= p.num_blocks) {
+        atomicOr(p.err, kErrBlockId);
+        return 0;
+      }
+      return id;
+    };
+    for (int n = n0; n < n1; ++n) {
+      if (at.b != seq || at.heads != heads) {
+        const Rows r = rows_of(p, at.b);
+        blocks = (r.tokens + kBlockTokens - 1) / kBlockTokens;
+        table = p.block_tables + static_cast<int64_t>(at.b) * p.max_blocks_per_seq;
+        seq = at.b;
+        heads = at.heads;
+        window = -1;
+        // Its queries are on their way to L2 while its first unit is.
+        const int group = p.num_q_heads / p.num_kv_heads;
+        for (int i = lane; i < r.count; i += 32)
+          l2_prefetch(static_cast<const __nv_bfloat16*>(p.q) +
+                          (static_cast<int64_t>(r.first + i) * p.num_q_heads + heads * hc * group) * D,
+                      hc * group * D * 2);
+      }
+      const int first = at.unit * nb, count = min(nb, blocks - first), w = first / 32;
+      if (w != window) {
+        ids = window >= 0 && w == window + 1 ? next_ids : fetch(w);
+        next_ids = fetch(w + 1);
+        window = w;
+      }
+      const int id = __shfl_sync(kAll, ids, (first & 31) + min(lane, nb - 1));
+      const int k = n - n0, stage = k % kStages;
+      if (k >= kStages && !bar_wait(empty + 8 * stage, (k / kStages - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) bar_expect_tx(full + 8 * stage, static_cast<uint32_t>(count * hc * (2 * T::kTile + 2 * kBlockTokens)));
+      __syncwarp();
+      if (lane < count) {
+        const int tile = id * p.num_kv_heads + heads * hc;
+        const uint32_t dst = base + stage * T::kStage + lane * hc * T::kTile;
+        tensor_load(dst, &map_k, tile * kBlockTokens, full + 8 * stage);
+        tensor_load(dst + T::kOffV, &map_v, tile * kBlockTokens, full + 8 * stage);
+        bulk_load(base + T::kOffScales + stage * T::kScales + lane * hc * 2 * kBlockTokens,
+                  p.kv_scales + static_cast<int64_t>(tile) * 2 * kBlockTokens, hc * 2 * kBlockTokens, full + 8 * stage);
+      }
+      issued = k + 1;
+      if (n + 1 < n1) advance();
+    }
+    if (!ok) {  // what is still on its way lands before the CTA exits
+      if (lane == 0) atomicOr(p.err, kErrTimeout);
+      for (int k = issued > kStages ? issued - kStages : 0; k < issued; ++k)
+        bar_wait(full + 8 * (k % kStages), (k / kStages) & 1);
+    }
+    return;
+  }
+
+  // ---------------- products (a tile of every unit a warp) ----------------
+  const int g = lane >> 2, t = lane & 3;      // fragments: row g and columns 2t, 2t + 1 of an accumulator
+  const int head_of = warp & (hc - 1), block_of = warp / hc;  // (hc is a power of two)
+  const int group = p.num_q_heads / p.num_kv_heads, group_bits = 31 - __clz(group);
+  uint32_t q[NC][kSteps][2];                  // B fragments of the rows
+  float q_scale[NC][2];                       // of columns 2t, 2t + 1: what takes a product to a score
+  int limit[NC][2];                           // tokens that they see
+  float m[NC][2], r[NC][2], l[NC][2];
+  float o[kSteps][NC][4];
+  // ldmatrix: lane i gives the address of row i % 8 of matrix i / 8; matrices 0, 1: tokens 0..7 and 8..15 of a chunk,
+  // 2, 3: of the next chunk.
+  const int ld_row = (lane & 7) + ((lane >> 3) & 1) * 8, ld_chunk = lane >> 4;
+  const int ld_swizzle = D == 128 ? (ld_row & 7) : ((ld_row >> 1) & 3);
+  uint32_t ld_at[kSteps / 2];
+#pragma unroll
+  for (int c = 0; c < kSteps / 2; ++c) ld_at[c] = ld_row * D + ((2 * c + ld_chunk) ^ ld_swizzle) * 16;
+  Rows rows{};
+  int tokens = 0, first_limit = 0;
+  bool started = false, failed = false, first_pair = true;
+
+  for (int n = n0; n < n1; ++n) {
+    if (n == n0 || at.unit == 0) {  // a new pair of sequence and heads
+      rows = rows_of(p, at.b);
+      tokens = rows.tokens;
+      first_limit = tokens - rows.count + 1;
+      started = at.unit == 0;
+      const int kvh = at.heads * hc + head_of;
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc) {
+        const int col = nc * 8 + g, i = col >> group_bits;
+        uint2 x[kSteps];
+        float top = 0.f;
+#pragma unroll
+        for (int c = 0; c < kSteps; ++c) {
+          x[c] = make_uint2(0u, 0u);
+          if (i < rows.count)
+            x[c] = __ldg(reinterpret_cast<const uint2*>(
+                static_cast<const __nv_bfloat16*>(p.q) +
+                (static_cast<int64_t>(rows.first + i) * p.num_q_heads + kvh * group + (col & (group - 1))) * D + 16 * c + 4 * t));
+        }
+#pragma unroll
+        for (int c = 0; c < kSteps; ++c) {
+          top = fmaxf(fmaxf(top, fabsf(__uint_as_float(x[c].x << 16))), fabsf(__uint_as_float(x[c].x & 0xffff0000u)));
+          top = fmaxf(fmaxf(top, fabsf(__uint_as_float(x[c].y << 16))), fabsf(__uint_as_float(x[c].y & 0xffff0000u)));
+        }
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+        // To a largest value in [2^14, 2^15): by 2^up.
+        const int up = min(14 + 127 - static_cast<int>(__float_as_uint(top) >> 23), 100);
+        const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+#pragma unroll
+        for (int c = 0; c < kSteps; ++c) {
+          q[nc][c][0] = pack_f16(__uint_as_float(x[c].x << 16) * by, __uint_as_float(x[c].x & 0xffff0000u) * by);
+          q[nc][c][1] = pack_f16(__uint_as_float(x[c].y << 16) * by, __uint_as_float(x[c].y & 0xffff0000u) * by);
+        }
+        const float back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23) * p.qscale;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          q_scale[nc][k] = __shfl_sync(kAll, back, (2 * t + k) * 4);
+          limit[nc][k] = first_limit + ((nc * 8 + 2 * t + k) >> group_bits);
+          m[nc][k] = r[nc][k] = kNone;
+          l[nc][k] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < kSteps; ++c)
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[c][nc][k] = 0.f;
+    }
+    const int k_of = n - n0, stage = k_of % kStages;
+    if (!failed && !bar_wait(full + 8 * stage, (k_of / kStages) & 1)) {
+      failed = true;
+      if (lane == 0) atomicOr(p.err, kErrTimeout);
+    }
+    const int token0 = (at.unit * nb + block_of) * kBlockTokens;
+    if (!failed && token0 < tokens) {
+      const uint32_t sk = base + stage * T::kStage + warp * T::kTile, sv = sk + T::kOffV;
+      const unsigned char* sc = smem + T::kOffScales + stage * T::kScales + warp * 2 * kBlockTokens;
+      // S^T = Kc q^T.  Chunk c of a row: its 16 codes are the product's depth, in the order 4t, 4t + 1, 4t + 2, 4t + 3 of a
+      // lane's four, as q's fragments are.
+      float s[NC][4], s2[NC][4];
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[nc][k] = s2[nc][k] = 0.f;
+#pragma unroll
+      for (int c = 0; c < kSteps / 2; ++c) {
+        uint32_t x[4];
+        ldsm_x4(sk + ld_at[c], x);
+        uint32_t a[4][2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          a[k][0] = fp8_halves(static_cast<uint16_t>(x[k]));
+          a[k][1] = fp8_halves(static_cast<uint16_t>(x[k] >> 16));
+        }
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc) {
+          mma_f16(s[nc], a[0][0], a[1][0], a[0][1], a[1][1], q[nc][2 * c][0], q[nc][2 * c][1]);
+          mma_f16(s2[nc], a[2][0], a[3][0], a[2][1], a[3][1], q[nc][2 * c + 1][0], q[nc][2 * c + 1][1]);
+        }
+      }
+      const float k_lo = fp8_scale(sc[g]), k_hi = fp8_scale(sc[g + 8]);
+      const float v_lo = static_cast<float>(static_cast<int>(sc[16 + g]) - 127);
+      const float v_hi = static_cast<float>(static_cast<int>(sc[24 + g]) - 127);
+      const bool masked = token0 + kBlockTokens > first_limit;
+      bool raise = false;
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[nc][k] = (s[nc][k] + s2[nc][k]) * q_scale[nc][k & 1] * (k < 2 ? k_lo : k_hi);
+        if (masked) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (token0 + g + (k < 2 ? 0 : 8) >= limit[nc][k & 1]) s[nc][k] = -INFINITY;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float d = s[nc][k] - m[nc][k & 1];
+          raise |= d > kSlack || d + (k < 2 ? v_lo : v_hi) > r[nc][k & 1] + kSlack;
+        }
+      }
+      if (__any_sync(kAll, raise)) {  // seldom but for a pair's first block
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float top = fmaxf(s[nc][k], s[nc][k + 2]);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+            top = fmaxf(top, m[nc][k]);
+            const float by = m[nc][k] - top;
+            m[nc][k] = top;
+            l[nc][k] *= ex2(by);
+            float top_w = fmaxf(s[nc][k] - top + v_lo, s[nc][k + 2] - top + v_hi);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) top_w = fmaxf(top_w, __shfl_xor_sync(kAll, top_w, off));
+            const float was = r[nc][k] + by;  // against the new m
+            r[nc][k] = fmaxf(top_w, was);
+            const float alpha = ex2(was - r[nc][k]);
+#pragma unroll
+            for (int c = 0; c < kSteps; ++c) {
+              o[c][nc][k] *= alpha;
+              o[c][nc][k + 2] *= alpha;
+            }
+          }
+      }
+      uint32_t w[NC][2];  // B fragments of the weights
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc) {
+        float wt[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float d = s[nc][k] - m[nc][k & 1];
+          l[nc][k & 1] += ex2(d);
+          wt[k] = ex2(d + (k < 2 ? v_lo : v_hi) - r[nc][k & 1] + kWeightShift);
+        }
+        w[nc][0] = transpose8(pack_f16(wt[0], wt[1]));
+        w[nc][1] = transpose8(pack_f16(wt[2], wt[3]));
+      }
+      // Rows that nobody sees must not reach the product (0 times no number).
+      uint32_t keep_lo = kAll, keep_hi = kAll;  // of tokens 2t, 2t + 1 and of 2t + 8, 2t + 9
+      if (masked) {
+        const int left = tokens - token0 - 2 * t;
+        keep_lo = left > 1 ? kAll : left > 0 ? 0xffffu : 0u;
+        keep_hi = left > 9 ? kAll : left > 8 ? 0xffffu : 0u;
+      }
+      // O^T += Vc^T W^T.  A lane's four codes of a chunk: tokens 2t and 2t + 1, dims 2g and 2g + 1; dims 2g are rows g of
+      // the product, dims 2g + 1 rows g + 8.
+#pragma unroll
+      for (int c = 0; c < kSteps / 2; ++c) {
+        uint32_t x[4];
+        ldsm_x4_t(sv + ld_at[c], x);
+        if (masked) {
+          x[0] &= keep_lo;
+          x[1] &= keep_hi;
+          x[2] &= keep_lo;
+          x[3] &= keep_hi;
+        }
+        uint32_t a[4][2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t y = __byte_perm(x[k], 0, 0x3120);
+          a[k][0] = fp8_halves(static_cast<uint16_t>(y));
+          a[k][1] = fp8_halves(static_cast<uint16_t>(y >> 16));
+        }
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc) {
+          mma_f16(o[2 * c][nc], a[0][0], a[0][1], a[1][0], a[1][1], w[nc][0], w[nc][1]);
+          mma_f16(o[2 * c + 1][nc], a[2][0], a[2][1], a[3][0], a[3][1], w[nc][0], w[nc][1]);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) bar_arrive(empty + 8 * stage);
+
+    const bool ended = at.unit == at.units - 1;
+    if (ended || n + 1 == n1) {
+      // The pair's end here: O against m, l summed over the lanes that share a column.
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) l[nc][k] += __shfl_xor_sync(kAll, l[nc][k], off);
+          const float f = m[nc][k] == kNone ? 0.f : ex2(r[nc][k] - kWeightShift);
+#pragma unroll
+          for (int c = 0; c < kSteps; ++c) {
+            o[c][nc][k] *= f;
+            o[c][nc][k + 2] *= f;
+          }
+        }
+      // The warps of a head join their states, half of them handing theirs to the other half at a time.
+      float4* exchange = reinterpret_cast<float4*>(smem + T::kOffExchange);
+      float2* s_ml = reinterpret_cast<float2*>(smem + T::kOffMl);
+      for (int half = nb / 2; half > 0; half >>= 1) {
+        const bool gives = block_of >= half && block_of < 2 * half, takes = block_of < half;
+        const int place = (block_of & (half - 1)) * hc + head_of;
+        float mine[NC][2], other[NC][2];
+        if (gives && g == 0)
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) s_ml[place * T::kCols + nc * 8 + 2 * t + k] = make_float2(m[nc][k], l[nc][k]);
+#pragma unroll
+        for (int part = 0; part < kSteps * NC / 4; ++part) {
+          if (gives)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float(&v)[4] = o[(4 * part + x) / NC][(4 * part + x) % NC];
+              exchange[(place * 4 + x) * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
+            }
+          asm volatile("bar.sync 1, %0;" ::"n"(32 * kUnitTiles) : "memory");
+          if (takes) {
+            if (part == 0)
+#pragma unroll
+              for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const float2 y = s_ml[place * T::kCols + nc * 8 + 2 * t + k];
+                  const float top = fmaxf(m[nc][k], y.x);
+                  mine[nc][k] = ex2(m[nc][k] - top);
+                  other[nc][k] = ex2(y.x - top);
+                  l[nc][k] = l[nc][k] * mine[nc][k] + y.y * other[nc][k];
+                  m[nc][k] = top;
+                }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              constexpr int kN = NC;
+              const int nc = (4 * part + x) % kN;
+              float(&v)[4] = o[(4 * part + x) / kN][nc];
+              const float4 y = exchange[(place * 4 + x) * 32 + lane];
+              v[0] = v[0] * mine[nc][0] + y.x * other[nc][0];
+              v[1] = v[1] * mine[nc][1] + y.y * other[nc][1];
+              v[2] = v[2] * mine[nc][0] + y.z * other[nc][0];
+              v[3] = v[3] * mine[nc][1] + y.w * other[nc][1];
+            }
+          }
+          asm volatile("bar.sync 1, %0;" ::"n"(32 * kUnitTiles) : "memory");
+        }
+      }
+      const bool whole = started && ended;
+      const int slot = first_pair ? 0 : 1;
+      if (warp == 0 && lane == 0) {
+        int* record = p.ws_records + 2 * (static_cast<int64_t>(at.b) * head_groups + at.heads);
+        if (started) record[0] = piece * 2 + slot;
+        if (ended) record[1] = piece;
+      }
+      if (block_of == 0 && !failed) {
+        const int kvh = at.heads * hc + head_of;
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int col = nc * 8 + 2 * t + k, i = col >> group_bits;
+            if (i >= rows.count) continue;
+            if (whole) {
+              const float inv = 1.f / l[nc][k];
+              __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
+                                   (static_cast<int64_t>(rows.first + i) * p.num_q_heads + kvh * group + (col & (group - 1))) * D;
+#pragma unroll
+              for (int c = 0; c < kSteps; ++c)
+                *reinterpret_cast<uint32_t*>(dst + 16 * c + 2 * g) = pack_bf16(o[c][nc][k] * inv, o[c][nc][k + 2] * inv);
+            } else {
+              const int64_t state = (static_cast<int64_t>(piece * 2 + slot) * hc + head_of) * p.state_rows + col;
+              float* dst = p.ws_states + state * D;
+#pragma unroll
+              for (int c = 0; c < kSteps; ++c)
+                *reinterpret_cast<float2*>(dst + 16 * c + 2 * g) = make_float2(o[c][nc][k], o[c][nc][k + 2]);
+              if (g == 0) p.ws_ml[state] = make_float2(m[nc][k], l[nc][k]);
+            }
+          }
+      }
+      first_pair = false;
+    }
+    if (n + 1 < n1) advance();
+  }
+}
+
+// Joins the states of every pair that a piece's border cuts: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s; zeros for a
+// sequence without tokens.  A CTA per (sequence, kv head), a warp per row and slice of its states; a warp fetches kAhead
+// states before it joins any.
+template <int D, int kSlices>
+__global__ void __launch_bounds__(kSlices == 1 ? 128 : kSlices * 32) join_fp8_kernel(const Fp8AttentionParams p) {
+  constexpr int kPer = D / 32, kAhead = 8;
+  constexpr int kRows = kSlices == 1 ? 4 : 1;  // rows of a CTA at a time
+  __shared__ float2 s_ml[kSlices];
+  __shared__ float s_o[kSlices][D];
+  const int b = blockIdx.x / p.num_kv_heads, kvh = blockIdx.x - b * p.num_kv_heads;
+  const int warp = threadIdx.x >> 5, slice = kSlices == 1 ? 0 : warp, lane = threadIdx.x & 31;
+  const int hc = p.unit_heads, group = p.num_q_heads / p.num_kv_heads;
+  pdl_trigger();
+  pdl_wait();
+  const Rows rows = rows_of(p, b);
+  const int2 record = *reinterpret_cast<const int2*>(
+      p.ws_records + 2 * (static_cast<int64_t>(b) * (p.num_kv_heads / hc) + kvh / hc));
+  if (rows.count == 0) return;
+  const int first = record.x >> 1;
+  int states = rows.tokens > 0 ? record.y - first + 1 : 0;
+  if (rows.tokens > 0 && (first < 0 || states < 1 || record.y >= p.num_pieces)) return;  // (a piece timed out)
+  if (states == 1) return;  // whole in one piece, which wrote it
+  for (int col = blockIdx.y * kRows + (kRows > 1 ? warp : 0); col < rows.count * group; col += gridDim.y * kRows) {
+    float top = kNone, l = 0.f, acc[kPer];
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
+    for (int u0 = slice; u0 < states; u0 += kSlices * kAhead) {
+      float2 ml[kAhead];
+      float a[kAhead][kPer];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int u = u0 + k * kSlices;
+        ml[k] = make_float2(kNone, 0.f);
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) a[k][x] = 0.f;
+        if (u >= states) continue;
+        const int64_t state =
+            (static_cast<int64_t>((first + u) * 2 + (u == 0 ? record.x & 1 : 0)) * hc + kvh % hc) * p.state_rows + col;
+        ml[k] = p.ws_ml[state];
+        const float* src = p.ws_states + state * D + lane * kPer;
+        if constexpr (kPer == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          a[k][0] = v.x; a[k][1] = v.y; a[k][2] = v.z; a[k][3] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          a[k][0] = v.x; a[k][1] = v.y;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const float mn = fmaxf(top, ml[k].x);
+        const float alpha = ex2(top - mn), beta = ex2(ml[k].x - mn);
+        l = l * alpha + ml[k].y * beta;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) acc[x] = acc[x] * alpha + a[k][x] * beta;
+        top = mn;
+      }
+    }
+    if constexpr (kSlices > 1) {
+      __syncthreads();  // the column before has been read
+      if (lane == 0) s_ml[slice] = make_float2(top, l);
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) s_o[slice][lane * kPer + x] = acc[x];
+      __syncthreads();
+      if (slice > 0) continue;
+#pragma unroll
+      for (int k = 1; k < kSlices; ++k) {
+        const float2 y = s_ml[k];
+        const float mn = fmaxf(top, y.x);
+        const float alpha = ex2(top - mn), beta = ex2(y.x - mn);
+        l = l * alpha + y.y * beta;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) acc[x] = acc[x] * alpha + s_o[k][lane * kPer + x] * beta;
+        top = mn;
+      }
+    }
+    const float inv = states > 0 ? 1.f / l : 0.f;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
+                         (static_cast<int64_t>(rows.first + col / group) * p.num_q_heads + kvh * group + col % group) * D + lane * kPer;
+#pragma unroll
+    for (int x = 0; x < kPer; x += 2)
+      *reinterpret_cast<uint32_t*>(dst + x) = pack_bf16(acc[x] * inv, acc[x + 1] * inv);
+  }
+}
+
+}  // namespace
+}  // namespace pkv
