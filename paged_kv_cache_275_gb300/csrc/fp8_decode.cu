@@ -53,9 +53,11 @@ cudaError_t launch_few_rows_fp8(const Fp8AttentionParams& p, int head_dim, cudaS
   switch (head_dim * 8 + nc) {
     case 64 * 8 + 1: return launch<64, 1>(p, stream);
     case 64 * 8 + 2: return launch<64, 2>(p, stream);
+    case 64 * 8 + 3: return launch<64, 3>(p, stream);
     case 64 * 8 + 4: return launch<64, 4>(p, stream);
     case 128 * 8 + 1: return launch<128, 1>(p, stream);
     case 128 * 8 + 2: return launch<128, 2>(p, stream);
+    case 128 * 8 + 3: return launch<128, 3>(p, stream);
     case 128 * 8 + 4: return launch<128, 4>(p, stream);
     default: return cudaErrorInvalidValue;
   }

@@ -18,10 +18,12 @@
 //
 // Work.  The batch's blocks form one stream of units: eight (block, kv head) tiles that lie next to one another, all eight
 // heads of a block, or two blocks of four heads and so on (32 KB of K and V at D = 128).  The stream is cut into equal
-// contiguous pieces, one a CTA, so that every CTA moves the same bytes whatever the lengths.  One warp fills a ring of units:
-// a block's heads are neighbours in the cache, so a unit takes one or a few large tensor copies (swizzled, so that ldmatrix
-// reads without bank conflicts).  Each of eight warps takes its tile of every unit.  A (sequence, heads) pair cut by a piece's
-// border leaves partial states (m, l, O) that a second kernel joins.
+// contiguous pieces, one a CTA, so that every CTA moves the same bytes whatever the lengths.  Units arrive in a ring: a
+// block's heads are neighbours in the cache, so a unit takes one or a few large tensor copies (swizzled, so that ldmatrix
+// reads without bank conflicts).  Each of the CTA's eight warps takes its tile of every unit, and they send for the units in
+// turns, a warp every eighth, with its block ids looked up eight units ahead.  (A warp that only copies would cost the others
+// a quarter of their registers.)  A (sequence, heads) pair cut by a piece's border leaves partial states (m, l, O) that a
+// second kernel joins.
 //
 // Every wait is bounded: one that runs out sets PKV_DEVERR_PIPELINE_TIMEOUT, and its warp goes on without computing.
 #pragma once
@@ -43,8 +45,7 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kUnitTiles = 8;  // (block, kv head) tiles of a unit, one a warp
-constexpr int kProducer = kUnitTiles;
-constexpr int kThreads = 32 * (kUnitTiles + 1);
+constexpr int kThreads = 32 * kUnitTiles;
 constexpr float kNone = -3.0e38f;  // the reference of a row that has seen no token
 constexpr float kSlack = 8.f;
 constexpr float kWeightShift = 7.f;  // the largest weight is brought to 2^7 .. 2^15
@@ -62,12 +63,12 @@ struct Few {
   static constexpr int kStage = 2 * kOperand;
   static constexpr int kOffScales = kStages * kStage;
   static constexpr int kOffExchange = kOffScales + kStages * kScales;
-  static constexpr int kExchange = kUnitTiles / 2 * 32 * 64;  // 16 values a lane of four warps
+  static constexpr int kExchange = kUnitTiles / 2 * 32 * 32;  // 8 values a lane of four warps
   static constexpr int kOffMl = kOffExchange + kExchange;
   static constexpr int kMl = kUnitTiles / 2 * kCols * 8;
   static constexpr int kOffBar = kOffMl + kMl;
-  static constexpr int kOffSeq = kOffBar + 16 * kStages;  // units before each sequence, [num_seqs + 1]
-  static constexpr int smem(int num_seqs) { return kOffSeq + (num_seqs + 1) * 4 + 1024; }  // 1024 to align the ring
+  static constexpr int kOffSeq = kOffBar + 16 * kStages;  // units before each sequence, [num_seqs + 1]; tokens, [num_seqs]
+  static constexpr int smem(int num_seqs) { return kOffSeq + (2 * num_seqs + 1) * 4 + 1024; }  // 1024 to align the ring
 };
 
 // ---------------------------------------------------------------------------
@@ -207,7 +208,8 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
   unsigned char* smem = raw + (-saddr(raw) & 1023u);
   const uint32_t base = saddr(smem);
   int* s_units = reinterpret_cast<int*>(smem + T::kOffSeq);
-  __shared__ int s_sum[kThreads / 32 + 1];
+  int* s_tokens = s_units + p.num_seqs + 1;
+  __shared__ int s_sum[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hc = p.unit_heads, nb = kUnitTiles / hc;  // heads and blocks of a unit
   const int head_groups = p.num_kv_heads / hc;
@@ -231,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
     if (b < p.num_seqs) {
       const Rows r = rows_of(p, b);
       if (r.wrong && blockIdx.x == 0) atomicOr(p.err, r.wrong);
+      s_tokens[b] = r.tokens;
       units = r.count > 0 ? ((r.tokens + kBlockTokens - 1) / kBlockTokens + nb - 1) / nb : 0;
     }
 #pragma unroll
@@ -252,394 +255,388 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
   if (piece >= pieces) return;
   const int n0 = static_cast<int>(static_cast<int64_t>(piece) * total / pieces);
   const int n1 = static_cast<int>(static_cast<int64_t>(piece + 1) * total / pieces);
-  Walk at;
-  {
-    int lo = 0, hi = p.num_seqs - 1;  // the sequence of unit n0: the last with units before it at or below
-    const int n = n0 / head_groups;
+  // Unit n of the stream (there is one).
+  auto walk_to = [&](int n) {
+    int lo = 0, hi = p.num_seqs - 1;  // its sequence: the last with units before it at or below
+    const int of_group = n / head_groups;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (s_units[mid] <= n) lo = mid;
+      if (s_units[mid] <= of_group) lo = mid;
       else hi = mid - 1;
     }
-    at.b = lo;
-    at.units = s_units[lo + 1] - s_units[lo];
-    const int rest = n0 - s_units[lo] * head_groups;
-    at.heads = rest / at.units;
-    at.unit = rest - at.heads * at.units;
-  }
-  auto advance = [&] {
-    if (++at.unit < at.units) return;
-    at.unit = 0;
-    if (++at.heads < head_groups) return;
-    at.heads = 0;
-    do {
-      ++at.b;
-      at.units = s_units[at.b + 1] - s_units[at.b];
-    } while (at.units == 0);
+    Walk x;
+    x.b = lo;
+    x.units = s_units[lo + 1] - s_units[lo];
+    const int rest = n - s_units[lo] * head_groups;
+    x.heads = rest / x.units;
+    x.unit = rest - x.heads * x.units;
+    return x;
+  };
+  // On to the pair that unit x.unit, past its own pair's end, lies in (there is one).
+  auto carry = [&](Walk& x) {
+    while (x.unit >= x.units) {
+      x.unit -= x.units;
+      if (++x.heads < head_groups) continue;
+      x.heads = 0;
+      do {
+        ++x.b;
+        x.units = s_units[x.b + 1] - s_units[x.b];
+      } while (x.units == 0);
+    }
   };
 
-  if (warp == kProducer) {
-    // ---------------- copies (whole warp) ----------------
-    int window = -1, ids = 0, next_ids = 0;  // 32 block ids of the sequence, one a lane, and the 32 behind them
-    int seq = -1, heads = -1, blocks = 0, issued = 0;
-    const int32_t* table = nullptr;
-    bool ok = true;
-    auto fetch = [&](int w) -> int {
-      const int col = 32 * w + lane;
-      if (col >= blocks) return 0;
-      const int id = __ldg(table + col);
-      if (id < 0 || id >= p.num_blocks) {
+  // ---------------- copies ----------------
+  // The unit that this warp sends for next: its number in the piece, and a lane's block id of it.
+  int ahead = warp, ahead_id = 0, ahead_blocks = 0;
+  Walk far{};
+  auto look_up = [&] {
+    const int first = far.unit * nb;
+    ahead_blocks = min(nb, (s_tokens[far.b] + kBlockTokens - 1) / kBlockTokens - first);
+    if (lane < ahead_blocks) ahead_id = __ldg(p.block_tables + static_cast<int64_t>(far.b) * p.max_blocks_per_seq + first + lane);
+  };
+  auto send = [&] {
+    const int stage = ahead % kStages;
+    const uint32_t bar = full + 8 * stage;
+    if (lane == 0) bar_expect_tx(bar, static_cast<uint32_t>(ahead_blocks * hc * (2 * T::kTile + 2 * kBlockTokens)));
+    __syncwarp();
+    if (lane < ahead_blocks) {
+      if (ahead_id < 0 || ahead_id >= p.num_blocks) {
         atomicOr(p.err, kErrBlockId);
-        return 0;
+        ahead_id = 0;
       }
-      return id;
-    };
-    for (int n = n0; n < n1; ++n) {
-      if (at.b != seq || at.heads != heads) {
-        const Rows r = rows_of(p, at.b);
-        blocks = (r.tokens + kBlockTokens - 1) / kBlockTokens;
-        table = p.block_tables + static_cast<int64_t>(at.b) * p.max_blocks_per_seq;
-        seq = at.b;
-        heads = at.heads;
-        window = -1;
-        // Its queries are on their way to L2 while its first unit is.
-        const int group = p.num_q_heads / p.num_kv_heads;
-        for (int i = lane; i < r.count; i += 32)
-          l2_prefetch(static_cast<const __nv_bfloat16*>(p.q) +
-                          (static_cast<int64_t>(r.first + i) * p.num_q_heads + heads * hc * group) * D,
-                      hc * group * D * 2);
-      }
-      const int first = at.unit * nb, count = min(nb, blocks - first), w = first / 32;
-      if (w != window) {
-        ids = window >= 0 && w == window + 1 ? next_ids : fetch(w);
-        next_ids = fetch(w + 1);
-        window = w;
-      }
-      const int id = __shfl_sync(kAll, ids, (first & 31) + min(lane, nb - 1));
-      const int k = n - n0, stage = k % kStages;
-      if (k >= kStages && !bar_wait(empty + 8 * stage, (k / kStages - 1) & 1)) {
-        ok = false;
-        break;
-      }
-      if (lane == 0) bar_expect_tx(full + 8 * stage, static_cast<uint32_t>(count * hc * (2 * T::kTile + 2 * kBlockTokens)));
-      __syncwarp();
-      if (lane < count) {
-        const int tile = id * p.num_kv_heads + heads * hc;
-        const uint32_t dst = base + stage * T::kStage + lane * hc * T::kTile;
-        tensor_load(dst, &map_k, tile * kBlockTokens, full + 8 * stage);
-        tensor_load(dst + T::kOffV, &map_v, tile * kBlockTokens, full + 8 * stage);
-        bulk_load(base + T::kOffScales + stage * T::kScales + lane * hc * 2 * kBlockTokens,
-                  p.kv_scales + static_cast<int64_t>(tile) * 2 * kBlockTokens, hc * 2 * kBlockTokens, full + 8 * stage);
-      }
-      issued = k + 1;
-      if (n + 1 < n1) advance();
+      const int tile = ahead_id * p.num_kv_heads + far.heads * hc;
+      const uint32_t dst = base + stage * T::kStage + lane * hc * T::kTile;
+      tensor_load(dst, &map_k, tile * kBlockTokens, bar);
+      tensor_load(dst + T::kOffV, &map_v, tile * kBlockTokens, bar);
+      bulk_load(base + T::kOffScales + stage * T::kScales + lane * hc * 2 * kBlockTokens,
+                p.kv_scales + static_cast<int64_t>(tile) * 2 * kBlockTokens, hc * 2 * kBlockTokens, bar);
     }
-    if (!ok) {  // what is still on its way lands before the CTA exits
-      if (lane == 0) atomicOr(p.err, kErrTimeout);
-      for (int k = issued > kStages ? issued - kStages : 0; k < issued; ++k)
-        bar_wait(full + 8 * (k % kStages), (k / kStages) & 1);
+    if (far.unit == 0 || ahead == 0) {  // a pair's queries are on their way to L2 while its first unit is
+      const Rows r = rows_of(p, far.b);
+      const int heads = hc * (p.num_q_heads / p.num_kv_heads);
+      for (int i = lane; i < r.count; i += 32)
+        l2_prefetch(static_cast<const __nv_bfloat16*>(p.q) +
+                        (static_cast<int64_t>(r.first + i) * p.num_q_heads + far.heads * heads) * D,
+                    heads * D * 2);
     }
-    return;
+    ahead += kUnitTiles;
+    if (ahead < n1 - n0) {
+      far.unit += kUnitTiles;
+      carry(far);
+      look_up();
+    }
+  };
+  if (n0 + warp < n1) {
+    far = walk_to(n0 + warp);
+    look_up();
+    while (ahead < kStages && ahead < n1 - n0) send();
   }
+  Walk at = walk_to(n0);
 
   // ---------------- products (a tile of every unit a warp) ----------------
   const int g = lane >> 2, t = lane & 3;      // fragments: row g and columns 2t, 2t + 1 of an accumulator
   const int head_of = warp & (hc - 1), block_of = warp / hc;  // (hc is a power of two)
   const int group = p.num_q_heads / p.num_kv_heads, group_bits = 31 - __clz(group);
-  uint32_t q[NC][kSteps][2];                  // B fragments of the rows
-  float q_scale[NC][2];                       // of columns 2t, 2t + 1: what takes a product to a score
-  int limit[NC][2];                           // tokens that they see
-  float m[NC][2], r[NC][2], l[NC][2];
-  float o[kSteps][NC][4];
   // ldmatrix: lane i gives the address of row i % 8 of matrix i / 8; matrices 0, 1: tokens 0..7 and 8..15 of a chunk,
-  // 2, 3: of the next chunk.
-  const int ld_row = (lane & 7) + ((lane >> 3) & 1) * 8, ld_chunk = lane >> 4;
-  const int ld_swizzle = D == 128 ? (ld_row & 7) : ((ld_row >> 1) & 3);
-  uint32_t ld_at[kSteps / 2];
-#pragma unroll
-  for (int c = 0; c < kSteps / 2; ++c) ld_at[c] = ld_row * D + ((2 * c + ld_chunk) ^ ld_swizzle) * 16;
-  Rows rows{};
-  int tokens = 0, first_limit = 0;
-  bool started = false, failed = false, first_pair = true;
+  // 2, 3: of the next chunk.  Two chunks on are 32 bytes on, through the swizzle an exclusive or.
+  const int ld_row = (lane & 7) + ((lane >> 3) & 1) * 8;
+  const uint32_t ld_at = base + warp * T::kTile + ld_row * D +
+                         (((lane >> 4) ^ (D == 128 ? (ld_row & 7) : ((ld_row >> 1) & 3))) << 4);
+  bool failed = false;
+  int stage = 0;
+  uint32_t use = 0;  // parity of the stage's next copy
 
-  for (int n = n0; n < n1; ++n) {
-    if (n == n0 || at.unit == 0) {  // a new pair of sequence and heads
-      rows = rows_of(p, at.b);
-      tokens = rows.tokens;
-      first_limit = tokens - rows.count + 1;
-      started = at.unit == 0;
-      const int kvh = at.heads * hc + head_of;
+  // The piece's pairs of sequence and heads.
+  for (int n = n0; n < n1;) {
+    const Rows rows = rows_of(p, at.b);
+    const int kvh = at.heads * hc + head_of;
+    const int first_limit = rows.tokens - rows.count + 1;  // tokens that the first row sees
+    const int count = min(at.units - at.unit, n1 - n);      // units of the pair here
+    const bool started = at.unit == 0, ended = at.unit + count == at.units;
+    uint32_t q[NC][kSteps][2];  // B fragments of the rows
+    float q_scale[NC][2];       // of columns 2t, 2t + 1: what takes a product to a score
+    float m[NC][2], r[NC][2], l[NC][2];
+    float o[kSteps][NC][4];
 #pragma unroll
-      for (int nc = 0; nc < NC; ++nc) {
-        const int col = nc * 8 + g, i = col >> group_bits;
-        uint2 x[kSteps];
-        float top = 0.f;
+    for (int nc = 0; nc < NC; ++nc) {
+      const int col = nc * 8 + g, i = col >> group_bits;
+      float top = 0.f;
 #pragma unroll
-        for (int c = 0; c < kSteps; ++c) {
-          x[c] = make_uint2(0u, 0u);
-          if (i < rows.count)
-            x[c] = __ldg(reinterpret_cast<const uint2*>(
-                static_cast<const __nv_bfloat16*>(p.q) +
-                (static_cast<int64_t>(rows.first + i) * p.num_q_heads + kvh * group + (col & (group - 1))) * D + 16 * c + 4 * t));
-        }
-#pragma unroll
-        for (int c = 0; c < kSteps; ++c) {
-          top = fmaxf(fmaxf(top, fabsf(__uint_as_float(x[c].x << 16))), fabsf(__uint_as_float(x[c].x & 0xffff0000u)));
-          top = fmaxf(fmaxf(top, fabsf(__uint_as_float(x[c].y << 16))), fabsf(__uint_as_float(x[c].y & 0xffff0000u)));
-        }
-        top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
-        // To a largest value in [2^14, 2^15): by 2^up.
-        const int up = min(14 + 127 - static_cast<int>(__float_as_uint(top) >> 23), 100);
-        const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-#pragma unroll
-        for (int c = 0; c < kSteps; ++c) {
-          q[nc][c][0] = pack_f16(__uint_as_float(x[c].x << 16) * by, __uint_as_float(x[c].x & 0xffff0000u) * by);
-          q[nc][c][1] = pack_f16(__uint_as_float(x[c].y << 16) * by, __uint_as_float(x[c].y & 0xffff0000u) * by);
-        }
-        const float back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23) * p.qscale;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          q_scale[nc][k] = __shfl_sync(kAll, back, (2 * t + k) * 4);
-          limit[nc][k] = first_limit + ((nc * 8 + 2 * t + k) >> group_bits);
-          m[nc][k] = r[nc][k] = kNone;
-          l[nc][k] = 0.f;
-        }
+      for (int c = 0; c < kSteps; ++c) {
+        uint2 x = make_uint2(0u, 0u);
+        if (i < rows.count)
+          x = __ldg(reinterpret_cast<const uint2*>(
+              static_cast<const __nv_bfloat16*>(p.q) +
+              (static_cast<int64_t>(rows.first + i) * p.num_q_heads + kvh * group + (col & (group - 1))) * D + 16 * c + 4 * t));
+        q[nc][c][0] = x.x;
+        q[nc][c][1] = x.y;
       }
 #pragma unroll
       for (int c = 0; c < kSteps; ++c)
 #pragma unroll
-        for (int nc = 0; nc < NC; ++nc)
+        for (int k = 0; k < 2; ++k)
+          top = fmaxf(fmaxf(top, fabsf(__uint_as_float(q[nc][c][k] << 16))), fabsf(__uint_as_float(q[nc][c][k] & 0xffff0000u)));
+      top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+      // To a largest value in [2^14, 2^15): by 2^up.
+      const int up = min(14 + 127 - static_cast<int>(__float_as_uint(top) >> 23), 100);
+      const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o[c][nc][k] = 0.f;
+      for (int c = 0; c < kSteps; ++c)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          q[nc][c][k] = pack_f16(__uint_as_float(q[nc][c][k] << 16) * by, __uint_as_float(q[nc][c][k] & 0xffff0000u) * by);
+      const float back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23) * p.qscale;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        q_scale[nc][k] = __shfl_sync(kAll, back, (2 * t + k) * 4);
+        m[nc][k] = r[nc][k] = kNone;
+        l[nc][k] = 0.f;
+      }
     }
-    const int k_of = n - n0, stage = k_of % kStages;
-    if (!failed && !bar_wait(full + 8 * stage, (k_of / kStages) & 1)) {
-      failed = true;
-      if (lane == 0) atomicOr(p.err, kErrTimeout);
-    }
-    const int token0 = (at.unit * nb + block_of) * kBlockTokens;
-    if (!failed && token0 < tokens) {
-      const uint32_t sk = base + stage * T::kStage + warp * T::kTile, sv = sk + T::kOffV;
-      const unsigned char* sc = smem + T::kOffScales + stage * T::kScales + warp * 2 * kBlockTokens;
-      // S^T = Kc q^T.  Chunk c of a row: its 16 codes are the product's depth, in the order 4t, 4t + 1, 4t + 2, 4t + 3 of a
-      // lane's four, as q's fragments are.
-      float s[NC][4], s2[NC][4];
+#pragma unroll
+    for (int c = 0; c < kSteps; ++c)
 #pragma unroll
       for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s[nc][k] = s2[nc][k] = 0.f;
-#pragma unroll
-      for (int c = 0; c < kSteps / 2; ++c) {
-        uint32_t x[4];
-        ldsm_x4(sk + ld_at[c], x);
-        uint32_t a[4][2];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          a[k][0] = fp8_halves(static_cast<uint16_t>(x[k]));
-          a[k][1] = fp8_halves(static_cast<uint16_t>(x[k] >> 16));
-        }
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc) {
-          mma_f16(s[nc], a[0][0], a[1][0], a[0][1], a[1][1], q[nc][2 * c][0], q[nc][2 * c][1]);
-          mma_f16(s2[nc], a[2][0], a[3][0], a[2][1], a[3][1], q[nc][2 * c + 1][0], q[nc][2 * c + 1][1]);
-        }
+        for (int k = 0; k < 4; ++k) o[c][nc][k] = 0.f;
+
+    int token0 = (at.unit * nb + block_of) * kBlockTokens;  // this warp's block
+    for (int u = 0; u < count; ++u, token0 += nb * kBlockTokens) {
+      if (!failed && !bar_wait(full + 8 * stage, use)) {
+        failed = true;
+        if (lane == 0) atomicOr(p.err, kErrTimeout);
       }
-      const float k_lo = fp8_scale(sc[g]), k_hi = fp8_scale(sc[g + 8]);
-      const float v_lo = static_cast<float>(static_cast<int>(sc[16 + g]) - 127);
-      const float v_hi = static_cast<float>(static_cast<int>(sc[24 + g]) - 127);
-      const bool masked = token0 + kBlockTokens > first_limit;
-      bool raise = false;
-#pragma unroll
-      for (int nc = 0; nc < NC; ++nc) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s[nc][k] = (s[nc][k] + s2[nc][k]) * q_scale[nc][k & 1] * (k < 2 ? k_lo : k_hi);
-        if (masked) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (token0 + g + (k < 2 ? 0 : 8) >= limit[nc][k & 1]) s[nc][k] = -INFINITY;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float d = s[nc][k] - m[nc][k & 1];
-          raise |= d > kSlack || d + (k < 2 ? v_lo : v_hi) > r[nc][k & 1] + kSlack;
-        }
-      }
-      if (__any_sync(kAll, raise)) {  // seldom but for a pair's first block
+      if (!failed && token0 < rows.tokens) {
+        const uint32_t sk = ld_at + stage * T::kStage;
+        const unsigned char* sc = smem + T::kOffScales + stage * T::kScales + warp * 2 * kBlockTokens;
+        // S^T = Kc q^T.  Chunk c of a row: its 16 codes are the product's depth, in the order 4t, 4t + 1, 4t + 2, 4t + 3 of
+        // a lane's four, as q's fragments are.
+        float s[NC][4], s2[NC][4];
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float top = fmaxf(s[nc][k], s[nc][k + 2]);
+          for (int k = 0; k < 4; ++k) s[nc][k] = s2[nc][k] = 0.f;
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
-            top = fmaxf(top, m[nc][k]);
-            const float by = m[nc][k] - top;
-            m[nc][k] = top;
-            l[nc][k] *= ex2(by);
-            float top_w = fmaxf(s[nc][k] - top + v_lo, s[nc][k + 2] - top + v_hi);
+        for (int c = 0; c < kSteps / 2; ++c) {
+          uint32_t x[4], a[4][2];
+          ldsm_x4(sk ^ (32u * c), x);
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) top_w = fmaxf(top_w, __shfl_xor_sync(kAll, top_w, off));
-            const float was = r[nc][k] + by;  // against the new m
-            r[nc][k] = fmaxf(top_w, was);
-            const float alpha = ex2(was - r[nc][k]);
-#pragma unroll
-            for (int c = 0; c < kSteps; ++c) {
-              o[c][nc][k] *= alpha;
-              o[c][nc][k + 2] *= alpha;
-            }
+          for (int k = 0; k < 4; ++k) {
+            a[k][0] = fp8_halves(static_cast<uint16_t>(x[k]));
+            a[k][1] = fp8_halves(static_cast<uint16_t>(x[k] >> 16));
           }
-      }
-      uint32_t w[NC][2];  // B fragments of the weights
 #pragma unroll
-      for (int nc = 0; nc < NC; ++nc) {
-        float wt[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float d = s[nc][k] - m[nc][k & 1];
-          l[nc][k & 1] += ex2(d);
-          wt[k] = ex2(d + (k < 2 ? v_lo : v_hi) - r[nc][k & 1] + kWeightShift);
+          for (int nc = 0; nc < NC; ++nc) {
+            mma_f16(s[nc], a[0][0], a[1][0], a[0][1], a[1][1], q[nc][2 * c][0], q[nc][2 * c][1]);
+            mma_f16(s2[nc], a[2][0], a[3][0], a[2][1], a[3][1], q[nc][2 * c + 1][0], q[nc][2 * c + 1][1]);
+          }
         }
-        w[nc][0] = transpose8(pack_f16(wt[0], wt[1]));
-        w[nc][1] = transpose8(pack_f16(wt[2], wt[3]));
-      }
-      // Rows that nobody sees must not reach the product (0 times no number).
-      uint32_t keep_lo = kAll, keep_hi = kAll;  // of tokens 2t, 2t + 1 and of 2t + 8, 2t + 9
-      if (masked) {
-        const int left = tokens - token0 - 2 * t;
-        keep_lo = left > 1 ? kAll : left > 0 ? 0xffffu : 0u;
-        keep_hi = left > 9 ? kAll : left > 8 ? 0xffffu : 0u;
-      }
-      // O^T += Vc^T W^T.  A lane's four codes of a chunk: tokens 2t and 2t + 1, dims 2g and 2g + 1; dims 2g are rows g of
-      // the product, dims 2g + 1 rows g + 8.
-#pragma unroll
-      for (int c = 0; c < kSteps / 2; ++c) {
-        uint32_t x[4];
-        ldsm_x4_t(sv + ld_at[c], x);
-        if (masked) {
-          x[0] &= keep_lo;
-          x[1] &= keep_hi;
-          x[2] &= keep_lo;
-          x[3] &= keep_hi;
-        }
-        uint32_t a[4][2];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t y = __byte_perm(x[k], 0, 0x3120);
-          a[k][0] = fp8_halves(static_cast<uint16_t>(y));
-          a[k][1] = fp8_halves(static_cast<uint16_t>(y >> 16));
-        }
+        const float k_lo = fp8_scale(sc[g]), k_hi = fp8_scale(sc[g + 8]);
+        const float v_lo = static_cast<float>(static_cast<int>(sc[16 + g]) - 127);
+        const float v_hi = static_cast<float>(static_cast<int>(sc[24 + g]) - 127);
+        const bool masked = token0 + kBlockTokens > first_limit;
+        bool raise = false;
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc) {
-          mma_f16(o[2 * c][nc], a[0][0], a[0][1], a[1][0], a[1][1], w[nc][0], w[nc][1]);
-          mma_f16(o[2 * c + 1][nc], a[2][0], a[2][1], a[3][0], a[3][1], w[nc][0], w[nc][1]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[nc][k] = (s[nc][k] + s2[nc][k]) * q_scale[nc][k & 1] * (k < 2 ? k_lo : k_hi);
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (token0 + g + (k < 2 ? 0 : 8) >= first_limit + ((nc * 8 + 2 * t + (k & 1)) >> group_bits)) s[nc][k] = -INFINITY;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float d = s[nc][k] - m[nc][k & 1];
+            raise |= d > kSlack || d + (k < 2 ? v_lo : v_hi) > r[nc][k & 1] + kSlack;
+          }
+        }
+        if (__any_sync(kAll, raise)) {  // seldom but for a pair's first block
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float top = fmaxf(s[nc][k], s[nc][k + 2]);
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+              top = fmaxf(top, m[nc][k]);
+              const float by = m[nc][k] - top;
+              m[nc][k] = top;
+              l[nc][k] *= ex2(by);
+              float top_w = fmaxf(s[nc][k] - top + v_lo, s[nc][k + 2] - top + v_hi);
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1) top_w = fmaxf(top_w, __shfl_xor_sync(kAll, top_w, off));
+              const float was = r[nc][k] + by;  // against the new m
+              r[nc][k] = fmaxf(top_w, was);
+              const float alpha = ex2(was - r[nc][k]);
+#pragma unroll
+              for (int c = 0; c < kSteps; ++c) {
+                o[c][nc][k] *= alpha;
+                o[c][nc][k + 2] *= alpha;
+              }
+            }
+        }
+        uint32_t w[NC][2];  // B fragments of the weights
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc) {
+          float wt[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float d = s[nc][k] - m[nc][k & 1];
+            l[nc][k & 1] += ex2(d);
+            wt[k] = ex2(d + (k < 2 ? v_lo : v_hi) - r[nc][k & 1] + kWeightShift);
+          }
+          w[nc][0] = transpose8(pack_f16(wt[0], wt[1]));
+          w[nc][1] = transpose8(pack_f16(wt[2], wt[3]));
+        }
+        // Rows that nobody sees must not reach the product (0 times no number).
+        uint32_t keep_lo = kAll, keep_hi = kAll;  // of tokens 2t, 2t + 1 and of 2t + 8, 2t + 9
+        if (masked) {
+          const int left = rows.tokens - token0 - 2 * t;
+          keep_lo = left > 1 ? kAll : left > 0 ? 0xffffu : 0u;
+          keep_hi = left > 9 ? kAll : left > 8 ? 0xffffu : 0u;
+        }
+        // O^T += Vc^T W^T.  A lane's four codes of a chunk: tokens 2t and 2t + 1, dims 2g and 2g + 1; dims 2g are rows g of
+        // the product, dims 2g + 1 rows g + 8.
+#pragma unroll
+        for (int c = 0; c < kSteps / 2; ++c) {
+          uint32_t x[4], a[4][2];
+          ldsm_x4_t((sk ^ (32u * c)) + T::kOffV, x);
+          if (masked) {
+            x[0] &= keep_lo;
+            x[1] &= keep_hi;
+            x[2] &= keep_lo;
+            x[3] &= keep_hi;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t y = __byte_perm(x[k], 0, 0x3120);
+            a[k][0] = fp8_halves(static_cast<uint16_t>(y));
+            a[k][1] = fp8_halves(static_cast<uint16_t>(y >> 16));
+          }
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc) {
+            mma_f16(o[2 * c][nc], a[0][0], a[0][1], a[1][0], a[1][1], w[nc][0], w[nc][1]);
+            mma_f16(o[2 * c + 1][nc], a[2][0], a[2][1], a[3][0], a[3][1], w[nc][0], w[nc][1]);
+          }
         }
       }
+      __syncwarp();
+      if (lane == 0) bar_arrive(empty + 8 * stage);
+      const int k = n - n0 + u;
+      if (k + kStages == ahead && ahead < n1 - n0) {  // this warp's turn, when all have done with the stage
+        if (!failed && !bar_wait(empty + 8 * stage, use)) {
+          failed = true;
+          if (lane == 0) atomicOr(p.err, kErrTimeout);
+        }
+        if (!failed) send();
+      }
+      if (++stage == kStages) {
+        stage = 0;
+        use ^= 1;
+      }
     }
-    __syncwarp();
-    if (lane == 0) bar_arrive(empty + 8 * stage);
 
-    const bool ended = at.unit == at.units - 1;
-    if (ended || n + 1 == n1) {
-      // The pair's end here: O against m, l summed over the lanes that share a column.
+    // The pair's end here: O against m, l summed over the lanes that share a column.
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l[nc][k] += __shfl_xor_sync(kAll, l[nc][k], off);
+        const float f = m[nc][k] == kNone ? 0.f : ex2(r[nc][k] - kWeightShift);
+#pragma unroll
+        for (int c = 0; c < kSteps; ++c) {
+          o[c][nc][k] *= f;
+          o[c][nc][k + 2] *= f;
+        }
+      }
+    // The warps of a head join their states, half of them handing theirs to the other half at a time.
+    float4* exchange = reinterpret_cast<float4*>(smem + T::kOffExchange);
+    float2* s_ml = reinterpret_cast<float2*>(smem + T::kOffMl);
+    for (int half = nb / 2; half > 0; half >>= 1) {
+      const bool gives = block_of >= half && block_of < 2 * half, takes = block_of < half;
+      const int place = (block_of & (half - 1)) * hc + head_of;
+      float mine[NC][2], other[NC][2];
+      if (gives && g == 0)
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) s_ml[place * T::kCols + nc * 8 + 2 * t + k] = make_float2(m[nc][k], l[nc][k]);
+#pragma unroll
+      for (int part = 0; part < kSteps * NC / 2; ++part) {
+        if (gives)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float(&v)[4] = o[(2 * part + x) / NC][(2 * part + x) % NC];
+            exchange[(place * 2 + x) * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
+          }
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kUnitTiles) : "memory");
+        if (takes) {
+          if (part == 0)
+#pragma unroll
+            for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const float2 y = s_ml[place * T::kCols + nc * 8 + 2 * t + k];
+                const float top = fmaxf(m[nc][k], y.x);
+                mine[nc][k] = ex2(m[nc][k] - top);
+                other[nc][k] = ex2(y.x - top);
+                l[nc][k] = l[nc][k] * mine[nc][k] + y.y * other[nc][k];
+                m[nc][k] = top;
+              }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int nc = (2 * part + x) % NC;
+            float(&v)[4] = o[(2 * part + x) / NC][nc];
+            const float4 y = exchange[(place * 2 + x) * 32 + lane];
+            v[0] = v[0] * mine[nc][0] + y.x * other[nc][0];
+            v[1] = v[1] * mine[nc][1] + y.y * other[nc][1];
+            v[2] = v[2] * mine[nc][0] + y.z * other[nc][0];
+            v[3] = v[3] * mine[nc][1] + y.w * other[nc][1];
+          }
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kUnitTiles) : "memory");
+      }
+    }
+    const int slot = n == n0 ? 0 : 1;
+    if (warp == 0 && lane == 0) {
+      int* record = p.ws_records + 2 * (static_cast<int64_t>(at.b) * head_groups + at.heads);
+      if (started) record[0] = piece * 2 + slot;
+      if (ended) record[1] = piece;
+    }
+    if (block_of == 0 && !failed) {
 #pragma unroll
       for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
+          const int col = nc * 8 + 2 * t + k, i = col >> group_bits;
+          if (i >= rows.count) continue;
+          if (started && ended) {
+            const float inv = 1.f / l[nc][k];
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
+                                 (static_cast<int64_t>(rows.first + i) * p.num_q_heads + kvh * group + (col & (group - 1))) * D;
 #pragma unroll
-          for (int off = 4; off < 32; off <<= 1) l[nc][k] += __shfl_xor_sync(kAll, l[nc][k], off);
-          const float f = m[nc][k] == kNone ? 0.f : ex2(r[nc][k] - kWeightShift);
+            for (int c = 0; c < kSteps; ++c)
+              *reinterpret_cast<uint32_t*>(dst + 16 * c + 2 * g) = pack_bf16(o[c][nc][k] * inv, o[c][nc][k + 2] * inv);
+          } else {
+            const int64_t state = (static_cast<int64_t>(piece * 2 + slot) * hc + head_of) * p.state_rows + col;
+            float* dst = p.ws_states + state * D;
 #pragma unroll
-          for (int c = 0; c < kSteps; ++c) {
-            o[c][nc][k] *= f;
-            o[c][nc][k + 2] *= f;
+            for (int c = 0; c < kSteps; ++c)
+              *reinterpret_cast<float2*>(dst + 16 * c + 2 * g) = make_float2(o[c][nc][k], o[c][nc][k + 2]);
+            if (g == 0) p.ws_ml[state] = make_float2(m[nc][k], l[nc][k]);
           }
         }
-      // The warps of a head join their states, half of them handing theirs to the other half at a time.
-      float4* exchange = reinterpret_cast<float4*>(smem + T::kOffExchange);
-      float2* s_ml = reinterpret_cast<float2*>(smem + T::kOffMl);
-      for (int half = nb / 2; half > 0; half >>= 1) {
-        const bool gives = block_of >= half && block_of < 2 * half, takes = block_of < half;
-        const int place = (block_of & (half - 1)) * hc + head_of;
-        float mine[NC][2], other[NC][2];
-        if (gives && g == 0)
-#pragma unroll
-          for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) s_ml[place * T::kCols + nc * 8 + 2 * t + k] = make_float2(m[nc][k], l[nc][k]);
-#pragma unroll
-        for (int part = 0; part < kSteps * NC / 4; ++part) {
-          if (gives)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float(&v)[4] = o[(4 * part + x) / NC][(4 * part + x) % NC];
-              exchange[(place * 4 + x) * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
-            }
-          asm volatile("bar.sync 1, %0;" ::"n"(32 * kUnitTiles) : "memory");
-          if (takes) {
-            if (part == 0)
-#pragma unroll
-              for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const float2 y = s_ml[place * T::kCols + nc * 8 + 2 * t + k];
-                  const float top = fmaxf(m[nc][k], y.x);
-                  mine[nc][k] = ex2(m[nc][k] - top);
-                  other[nc][k] = ex2(y.x - top);
-                  l[nc][k] = l[nc][k] * mine[nc][k] + y.y * other[nc][k];
-                  m[nc][k] = top;
-                }
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              constexpr int kN = NC;
-              const int nc = (4 * part + x) % kN;
-              float(&v)[4] = o[(4 * part + x) / kN][nc];
-              const float4 y = exchange[(place * 4 + x) * 32 + lane];
-              v[0] = v[0] * mine[nc][0] + y.x * other[nc][0];
-              v[1] = v[1] * mine[nc][1] + y.y * other[nc][1];
-              v[2] = v[2] * mine[nc][0] + y.z * other[nc][0];
-              v[3] = v[3] * mine[nc][1] + y.w * other[nc][1];
-            }
-          }
-          asm volatile("bar.sync 1, %0;" ::"n"(32 * kUnitTiles) : "memory");
-        }
-      }
-      const bool whole = started && ended;
-      const int slot = first_pair ? 0 : 1;
-      if (warp == 0 && lane == 0) {
-        int* record = p.ws_records + 2 * (static_cast<int64_t>(at.b) * head_groups + at.heads);
-        if (started) record[0] = piece * 2 + slot;
-        if (ended) record[1] = piece;
-      }
-      if (block_of == 0 && !failed) {
-        const int kvh = at.heads * hc + head_of;
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int col = nc * 8 + 2 * t + k, i = col >> group_bits;
-            if (i >= rows.count) continue;
-            if (whole) {
-              const float inv = 1.f / l[nc][k];
-              __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
-                                   (static_cast<int64_t>(rows.first + i) * p.num_q_heads + kvh * group + (col & (group - 1))) * D;
-#pragma unroll
-              for (int c = 0; c < kSteps; ++c)
-                *reinterpret_cast<uint32_t*>(dst + 16 * c + 2 * g) = pack_bf16(o[c][nc][k] * inv, o[c][nc][k + 2] * inv);
-            } else {
-              const int64_t state = (static_cast<int64_t>(piece * 2 + slot) * hc + head_of) * p.state_rows + col;
-              float* dst = p.ws_states + state * D;
-#pragma unroll
-              for (int c = 0; c < kSteps; ++c)
-                *reinterpret_cast<float2*>(dst + 16 * c + 2 * g) = make_float2(o[c][nc][k], o[c][nc][k + 2]);
-              if (g == 0) p.ws_ml[state] = make_float2(m[nc][k], l[nc][k]);
-            }
-          }
-      }
-      first_pair = false;
     }
-    if (n + 1 < n1) advance();
+    n += count;
+    at.unit += count;
+    if (n < n1) carry(at);
   }
+  if (failed)  // what this warp sent for lands before the CTA exits
+    for (int k = ahead - kUnitTiles; k >= 0 && k >= ahead - kUnitTiles - kStages; k -= kUnitTiles)
+      bar_wait(full + 8 * (k % kStages), (k / kStages) & 1);
 }
 
 // Joins the states of every pair that a piece's border cuts: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s; zeros for a
