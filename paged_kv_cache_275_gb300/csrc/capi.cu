@@ -1269,6 +1269,23 @@ pkv_status pkv_fp8_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, 
   return ok();
 }
 
+namespace {
+// CTAs that a tile pair's keys are split over: as many as leave every CTA an SM, at least two steps of 128 keys each (by the
+// longest context that the tables can hold).
+int32_t fp8_prefill_splits(int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs, int32_t num_q_heads,
+                           int32_t num_kv_heads, int32_t max_blocks_per_seq, int sms) {
+  const int64_t cta = pkv::prefill_cta_tokens(num_q_heads / num_kv_heads);
+  const int64_t grid = num_seqs * ((max_query_len + cta - 1) / cta), rows = num_query_tokens / cta + num_seqs;
+  const int64_t units = (grid < rows ? grid : rows) * num_kv_heads;
+  int64_t n = units > 0 ? sms / units : 1;
+  const int64_t most = (static_cast<int64_t>(max_blocks_per_seq) + 15) / 16;
+  if (n > most) n = most;
+  if (n > kMaxPrefillSplits) n = kMaxPrefillSplits;
+  if (num_seqs > 0 && n > 65535 / num_seqs) n = 65535 / num_seqs;
+  return static_cast<int32_t>(n < 1 ? 1 : n);
+}
+}  // namespace
+
 pkv_status pkv_fp8_prefill_workspace_size(int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs,
                                           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                           int32_t max_blocks_per_seq, size_t* bytes) {
@@ -1284,6 +1301,10 @@ pkv_status pkv_fp8_prefill_workspace_size(int64_t num_query_tokens, int32_t max_
   const int64_t rows = static_cast<int64_t>(max_query_len) * (num_q_heads / num_kv_heads);
   if (rows <= pkv::kFp8MostRows)
     *bytes = pkv::Fp8FewPlan(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, static_cast<int>(rows), kFp8PieceUnits, sms).bytes;
+  else
+    *bytes = pkv::prefill_workspace_bytes(
+        num_seqs, max_query_len, num_q_heads, num_kv_heads, head_dim,
+        fp8_prefill_splits(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq, sms));
   return ok();
 }
 
@@ -1351,10 +1372,17 @@ pkv_status pkv_paged_fp8_prefill_attention(const void* q, const void* k_cache, c
   if (!query_start) return fail(PKV_ERR_INVALID_ARGUMENT, "null pointer argument");
   if (static_cast<int64_t>(max_query_len) * (num_q_heads / num_kv_heads) <= pkv::kFp8MostRows)
     return few_rows_fp8(p, head_dim, workspace, workspace_bytes, stream);
-  if (pkv_status st = device_state(&p.err, nullptr); st != PKV_OK) return st;
-  const cudaError_t e = pkv::launch_attention_fp8(p, head_dim, reinterpret_cast<cudaStream_t>(stream));
+  int sms = 0;
+  if (pkv_status st = device_state(&p.err, &sms); st != PKV_OK) return st;
+  const int32_t splits =
+      fp8_prefill_splits(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq, sms);
+  const size_t need = pkv::prefill_workspace_bytes(num_seqs, max_query_len, num_q_heads, num_kv_heads, head_dim, splits);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(PKV_ERR_INVALID_ARGUMENT, "workspace too small: %zu bytes given, %zu needed", workspace ? workspace_bytes : size_t{0},
+                need);
+  const cudaError_t e = pkv::launch_prefill_fp8(p, head_dim, splits, static_cast<float*>(workspace), reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "fp8 prefill launch");
-  g_launches.fetch_add(1);
+  g_launches.fetch_add(splits > 1 ? 2 : 1);
   return ok();
 }
 

@@ -120,6 +120,7 @@ cudaError_t launch_append_fp8(const Fp8AppendParams& p, int head_dim, int num_sm
 cudaError_t launch_gather_fp8(const Fp8GatherParams& p, int head_dim, int num_sms, cudaStream_t stream);
 cudaError_t launch_copy_blocks_fp8(const Fp8CopyParams& p, int num_pairs, cudaStream_t stream);
 cudaError_t launch_few_rows_fp8(const Fp8AttentionParams& p, int head_dim, cudaStream_t stream);
-cudaError_t launch_attention_fp8(const Fp8AttentionParams& p, int head_dim, cudaStream_t stream);
+// Chunks on the 5th-generation tensor cores (fp8_prefill.cu); ws: prefill_workspace_bytes of num_splits > 1.
+cudaError_t launch_prefill_fp8(const Fp8AttentionParams& p, int head_dim, int num_splits, float* ws, cudaStream_t stream);
 
 }  // namespace pkv

@@ -4,14 +4,13 @@
 namespace pkv {
 namespace {
 
-// The cache's codes as rows of head_dim bytes, a box the rows of a unit's heads of one block.  As wide as a row, the swizzle
-// spreads a chunk of eight rows over all banks.
-cudaError_t code_map(CUtensorMap* map, const void* cache, int64_t rows, int head_dim, int box_rows) {
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(head_dim)};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(head_dim), static_cast<cuuint32_t>(box_rows)};
-  return encode_code_map(map, cache, 2, dims, strides, box,
-                         head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+// The cache's codes as rows of 128 bytes (a token of 128 dims, or two of 64), a box the rows of a unit's heads of one block,
+// swizzled.  (With boxes of 64-byte rows, 64 dims are copied at 5.0 TB/s, so XXX.)
+cudaError_t code_map(CUtensorMap* map, const void* cache, int64_t bytes, int box_bytes) {
+  const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(bytes / 128)};
+  const cuuint64_t strides[1] = {128};
+  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_bytes / 128)};
+  return encode_code_map(map, cache, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int D, int NC>
@@ -34,9 +33,9 @@ cudaError_t launch(const Fp8AttentionParams& p, cudaStream_t stream) {
     }
   }
   CUtensorMap mk, mv;
-  const int64_t rows = p.num_blocks * p.num_kv_heads * kBlockTokens;
-  if ((e = code_map(&mk, p.k_cache, rows, D, p.unit_heads * kBlockTokens)) != cudaSuccess) return e;
-  if ((e = code_map(&mv, p.v_cache, rows, D, p.unit_heads * kBlockTokens)) != cudaSuccess) return e;
+  const int64_t bytes = p.num_blocks * p.num_kv_heads * Few<D, NC>::kTile;
+  if ((e = code_map(&mk, p.k_cache, bytes, p.unit_heads * Few<D, NC>::kTile)) != cudaSuccess) return e;
+  if ((e = code_map(&mv, p.v_cache, bytes, p.unit_heads * Few<D, NC>::kTile)) != cudaSuccess) return e;
   e = launch_pdl(few_rows_fp8_kernel<D, NC>, dim3(p.num_pieces), dim3(kThreads), Few<D, NC>::smem(p.num_seqs), stream, p, mk, mv);
   if (e != cudaSuccess) return e;
   const unsigned pairs = static_cast<unsigned>(p.num_seqs) * p.num_kv_heads;

@@ -306,8 +306,8 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
       }
       const int tile = ahead_id * p.num_kv_heads + far.heads * hc;
       const uint32_t dst = base + stage * T::kStage + lane * hc * T::kTile;
-      tensor_load(dst, &map_k, tile * kBlockTokens, bar);
-      tensor_load(dst + T::kOffV, &map_v, tile * kBlockTokens, bar);
+      tensor_load(dst, &map_k, tile * (T::kTile / 128), bar);
+      tensor_load(dst + T::kOffV, &map_v, tile * (T::kTile / 128), bar);
       bulk_load(base + T::kOffScales + stage * T::kScales + lane * hc * 2 * kBlockTokens,
                 p.kv_scales + static_cast<int64_t>(tile) * 2 * kBlockTokens, hc * 2 * kBlockTokens, bar);
     }
@@ -338,10 +338,11 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
   const int head_of = warp & (hc - 1), block_of = warp / hc;  // (hc is a power of two)
   const int group = p.num_q_heads / p.num_kv_heads, group_bits = 31 - __clz(group);
   // ldmatrix: lane i gives the address of row i % 8 of matrix i / 8; matrices 0, 1: tokens 0..7 and 8..15 of a chunk,
-  // 2, 3: of the next chunk.  Two chunks on are 32 bytes on, through the swizzle an exclusive or.
+  // 2, 3: of the next chunk.  A tile is lines of 128 bytes, swizzled: chunk c of line y lies at c ^ (y % 8) (two tokens of 64
+  // dims share a line).  Two chunks on are 32 bytes on, through the swizzle an exclusive or.
   const int ld_row = (lane & 7) + ((lane >> 3) & 1) * 8;
-  const uint32_t ld_at = base + warp * T::kTile + ld_row * D +
-                         (((lane >> 4) ^ (D == 128 ? (ld_row & 7) : ((ld_row >> 1) & 3))) << 4);
+  const int ld_line = ld_row * D / 128, ld_chunk = (D == 128 ? 0 : (ld_row & 1) * 4) + (lane >> 4);
+  const uint32_t ld_at = base + warp * T::kTile + ld_line * 128 + ((ld_chunk ^ (ld_line & 7)) << 4);
   bool failed = false;
   int stage = 0;
   uint32_t use = 0;  // parity of the stage's next copy
