@@ -6,13 +6,14 @@
 // two is a bf16 value exactly.  So the cache's rows become bf16 on their way into shared memory, and everything behind that,
 // and every result's bits, are those of the bf16 kernel over the values that the cache stands for.
 //
-// Roles (12 warps, one CTA an SM, two 128-row query tiles):
-//   * warps 9-11: each fills every third tile of the K/V ring.  A lane loads 16 codes at a time, 8 KB a warp ahead of what it
-//     converts (two codes to fp16, to fp32, times the row's scale, to bf16, all exact), and stores them where the products
-//     read them (128-byte swizzle).  Rows past the last key become zeros.
+// Roles (16 warps, one CTA an SM, two 128-row query tiles):
+//   * warps 9-15: convert.  A tile of the K/V ring is four units of 32 rows, and the units go to the warps in turns.  A lane
+//     takes 16 codes at a time (to fp16, to fp32, times the row's scale, to bf16, all exact), stores them where the products
+//     read them (128-byte swizzle) and requests those of the same place of its next unit.  Rows past the last key become
+//     zeros.
 //   * warp 8: issues the products, as there; it owns the tensor memory.
 //   * warps 0-7: softmax and epilogue, a row a thread, as there.
-// Ten warps or twelve, a thread has 168 registers; so the converters cost the softmax none.
+// The softmax warps take 168 registers a thread and leave the others 88: 256 (168 + 88) is the block's 512 * 128.
 #include "paged_prefill_kernel.cuh"
 
 #include "fp8_cache.h"
@@ -22,9 +23,12 @@ namespace pkv {
 namespace {
 
 constexpr int kIssuer = 4 * kTiles;
-constexpr int kConverters = 3;
+constexpr int kConverters = 7;
 constexpr int kFp8Threads = 32 * (kIssuer + 1 + kConverters);
-static_assert(kRing >= kConverters, "a converter's next tile may not wait for one it has yet to fill");
+constexpr int kUnitRows = 32, kUnits = kKeys / kUnitRows;  // a converter's unit, and units of a tile
+static_assert(kRing * kUnits >= kConverters, "a converter's next unit may not wait for a tile that it has yet to fill");
+constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
+static_assert(kFp8Threads == 512 && 256 * (kSoftmaxRegs + kOtherRegs) == 512 * 128, "the block's registers");
 
 struct Fp8PrefillParams : PrefillParams {
   const uint8_t* kv_scales;
@@ -129,7 +133,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
   }
   if (tid == 0) {
     for (int s = 0; s < kRing; ++s) {
-      bar_init(r_full + 8 * s, 1);
+      bar_init(r_full + 8 * s, kUnits);
       bar_init(r_empty + 8 * s, 1);
     }
     for (int t = 0; t < kTiles; ++t) {
@@ -155,21 +159,22 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
   bool failed = false;
 
   if (warp > kIssuer) {
-    // ---------------- converters: ring tiles first, first + 3, ... (tile n = 2 j is K of step j, n = 2 j + 1 its V) ----------
-    constexpr int kChunks = D / 16;                    // 16-code chunks of a row
-    constexpr int kLoads = kKeys * kChunks / 32;       // of a tile a lane
-    constexpr int kHalf = kLoads / 2;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    // ---------------- converters (tile n = 2 j is K of step j, n = 2 j + 1 its V; unit u is rows of tile u / 4) ------------
+    constexpr int kChunks = D / 16;                   // 16-code chunks of a row
+    constexpr int kLoads = kUnitRows * kChunks / 32;  // of a unit a lane
     constexpr int kPages = kKeys / kBlockTokens;
     // A load instruction covers 32 / kChunks whole rows; eight consecutive lanes hold four chunks of two of them, whose
     // swizzled bf16 places are in different banks.
     const int my_row = D == 128 ? (lane >> 2) & 3 : lane >> 2, my_chunk = D == 128 ? (lane & 3) + ((lane >> 4) << 2) : lane & 3;
     const int npages = (kv_end + kBlockTokens - 1) / kBlockTokens;
     const int32_t* table = p.block_tables + static_cast<size_t>(b) * p.max_blocks_per_seq;
-    const int tiles = 2 * nsteps;
-    // What a lane knows of a tile: the block of page lane / 4 (-1: none), and four exponents, those of rows 4 lane .. + 3.
-    auto block_of = [&](int n) -> int {
-      const int page = (j0 + (n >> 1)) * kPages + (lane >> 2);
-      if (n >= tiles || page >= npages) return -1;
+    const int units = 2 * nsteps * kUnits;
+    // What a lane knows of a unit: the block of its page lane / 4 % 2 (-1: none), and four exponents, those of its rows
+    // 4 (lane % 8) .. + 3.
+    auto block_of = [&](int u) -> int {
+      const int n = u / kUnits, page = (j0 + (n >> 1)) * kPages + (u % kUnits) * 2 + ((lane >> 2) & 1);
+      if (u >= units || page >= npages) return -1;
       int id = __ldg(table + page);
       if (id < 0 || id >= p.num_blocks) {
         atomicOr(p.err, kErrBlockId);
@@ -177,29 +182,40 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       }
       return id;
     };
-    auto exponents_of = [&](int n, int id) -> uint32_t {
+    auto exponents_of = [&](int u, int id) -> uint32_t {
       if (id < 0) return 0x7f7f7f7fu;
-      return __ldg(reinterpret_cast<const uint32_t*>(
-          p.kv_scales + (static_cast<int64_t>(id) * p.num_kv_heads + kvh) * 2 * kBlockTokens + (n & 1) * kBlockTokens + 4 * (lane & 3)));
+      return __ldg(reinterpret_cast<const uint32_t*>(p.kv_scales + (static_cast<int64_t>(id) * p.num_kv_heads + kvh) * 2 * kBlockTokens +
+                                                     (u / kUnits & 1) * kBlockTokens + 4 * (lane & 3)));
     };
-    auto load_half = [&](int n, int id, int half, uint4 (&x)[kHalf]) {
-      const uint8_t* cache = static_cast<const uint8_t*>((n & 1) ? p.v_cache : p.k_cache);
+    // Chunk i of unit u: row i * 32 / kChunks + my_row of it.
+    auto load = [&](int u, int id, int i) -> uint4 {
+      const int row = i * (32 / kChunks) + my_row;
+      const int of = __shfl_sync(0xffffffffu, id, (row >> 4) * 4);
+      if (of < 0) return make_uint4(0u, 0u, 0u, 0u);
+      const uint8_t* cache = static_cast<const uint8_t*>((u / kUnits & 1) ? p.v_cache : p.k_cache);
+      return load_codes(cache + ((static_cast<int64_t>(of) * p.num_kv_heads + kvh) * kBlockTokens + (row & 15)) * D + my_chunk * 16);
+    };
+    int u = warp - kIssuer - 1;
+    int id = block_of(u), next_id = block_of(u + kConverters);
+    uint32_t exponents = exponents_of(u, id);
+    uint4 x[kLoads];
 #pragma unroll
-      for (int i = 0; i < kHalf; ++i) {
-        const int row = (half * kHalf + i) * (32 / kChunks) + my_row;
-        const int of = __shfl_sync(0xffffffffu, id, (row >> 4) * 4);
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (of >= 0)
-          x[i] = load_codes(cache + ((static_cast<int64_t>(of) * p.num_kv_heads + kvh) * kBlockTokens + (row & 15)) * D + my_chunk * 16);
+    for (int i = 0; i < kLoads; ++i) x[i] = load(u, id, i);
+    for (; u < units; u += kConverters) {
+      const int n = u / kUnits, slot = n % kRing;
+      const int after = block_of(u + 2 * kConverters);
+      const uint32_t next_exponents = exponents_of(u + kConverters, next_id);
+      if (n >= kRing && !__all_sync(0xffffffffu, bar_wait(r_empty + 8 * slot, (n / kRing + 1) & 1))) {
+        failed = true;
+        break;
       }
-    };
-    auto store_half = [&](int n, uint32_t exponents, int half, const uint4 (&x)[kHalf]) {
-      unsigned char* tile_at = smem + T::kOffKV + (n % kRing) * T::kTile;
-      const int left = kv_end - (j0 + (n >> 1)) * kKeys;  // the tile's rows that hold keys
+      const int row_of_unit = (u % kUnits) * kUnitRows;
+      unsigned char* tile_at = smem + T::kOffKV + slot * T::kTile;
+      const int left = kv_end - (j0 + (n >> 1)) * kKeys - row_of_unit;  // the unit's rows that hold keys
 #pragma unroll
-      for (int i = 0; i < kHalf; ++i) {
-        const int row0 = (half * kHalf + i) * (32 / kChunks), row = row0 + my_row;
-        const uint32_t four = __shfl_sync(0xffffffffu, exponents, (row0 + my_row) >> 2);
+      for (int i = 0; i < kLoads; ++i) {
+        const int row = i * (32 / kChunks) + my_row;
+        const uint32_t four = __shfl_sync(0xffffffffu, exponents, row >> 2);
         const float f = fp8_scale((four >> 8 * (row & 3)) & 0xffu);
         const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
         uint32_t r[8];
@@ -208,39 +224,26 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
           const float2 v = __fmul2_rn(fp8_floats(static_cast<uint16_t>(w[k / 2] >> 16 * (k & 1))), make_float2(f, f));
           r[k] = pack_bf16(v.x, v.y);
         }
-        if (row >= left)
+        x[i] = load(u + kConverters, next_id, i);
+        if (left < kUnitRows && row >= left)
 #pragma unroll
           for (int k = 0; k < 8; ++k) r[k] = 0u;
         const int c = 2 * my_chunk;
-        *reinterpret_cast<uint4*>(tile_at + kv_off<D>(row, c / 8, c % 8)) = make_uint4(r[0], r[1], r[2], r[3]);
-        *reinterpret_cast<uint4*>(tile_at + kv_off<D>(row, c / 8, c % 8 + 1)) = make_uint4(r[4], r[5], r[6], r[7]);
+        unsigned char* dst = tile_at + kv_off<D>(row_of_unit + row, c / 8, c % 8);
+        *reinterpret_cast<uint4*>(dst) = make_uint4(r[0], r[1], r[2], r[3]);
+        *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(reinterpret_cast<uintptr_t>(dst) ^ 16)) =
+            make_uint4(r[4], r[5], r[6], r[7]);
       }
-    };
-    int n = warp - kIssuer - 1;
-    int id = block_of(n), next_id = block_of(n + kConverters);
-    uint32_t exponents = exponents_of(n, id);
-    uint4 x[kHalf], y[kHalf];
-    if (n < tiles) load_half(n, id, 0, x);
-    for (; n < tiles; n += kConverters) {
-      load_half(n, id, 1, y);
-      if (n >= kRing && !__all_sync(0xffffffffu, bar_wait(r_empty + 8 * (n % kRing), (n / kRing + 1) & 1))) {
-        failed = true;
-        break;
-      }
-      store_half(n, exponents, 0, x);
-      const int after = block_of(n + 2 * kConverters);
-      const uint32_t next_exponents = exponents_of(n + kConverters, next_id);
-      if (n + kConverters < tiles) load_half(n + kConverters, next_id, 0, x);
-      store_half(n, exponents, 1, y);
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) bar_arrive(r_full + 8 * (n % kRing));
+      if (lane == 0) bar_arrive(r_full + 8 * slot);
       id = next_id;
       next_id = after;
       exponents = next_exponents;
     }
     if (failed && lane == 0) atomicOr(p.err, kErrTimeout);
   } else if (warp == kIssuer) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     // ---------------- MMA issuer: S of both tiles for step 0, then per step and tile P V and S of the next ----------------
     constexpr uint32_t kIdS = idesc_bf16(kKeys, false);
     constexpr uint32_t kIdPV = idesc_bf16(D, true);
@@ -303,9 +306,11 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       bar_poll(mma_drained, 0);
     }
     __syncwarp();
-  } else if ((warp >> 2) < n_tiles) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---------------- softmax / epilogue (thread = row of tile warp / 4) ----------------
     const int t = warp >> 2;
+    if (t < n_tiles) {
     const int r = tid & (kRows - 1);
     constexpr int kChunks = D / 8;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -454,6 +459,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       }
     }
     if (failed && lane == 0) atomicOr(p.err, kErrTimeout);
+    }
   }
 
   tc_before_sync();
