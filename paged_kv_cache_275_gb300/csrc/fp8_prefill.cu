@@ -164,16 +164,16 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     constexpr int kChunks = D / 16;                   // 16-code chunks of a row
     constexpr int kLoads = kUnitRows * kChunks / 32;  // of a unit a lane
     constexpr int kPages = kKeys / kBlockTokens;
-    // A load instruction covers 32 / kChunks whole rows; eight consecutive lanes hold four chunks of two of them, whose
-    // swizzled bf16 places are in different banks.
+    constexpr int kLoadRows = 32 / kChunks;           // rows of a load instruction
+    // Eight consecutive lanes hold four chunks of two rows, whose swizzled bf16 places are in different banks.
     const int my_row = D == 128 ? (lane >> 2) & 3 : lane >> 2, my_chunk = D == 128 ? (lane & 3) + ((lane >> 4) << 2) : lane & 3;
     const int npages = (kv_end + kBlockTokens - 1) / kBlockTokens;
     const int32_t* table = p.block_tables + static_cast<size_t>(b) * p.max_blocks_per_seq;
     const int units = 2 * nsteps * kUnits;
-    // What a lane knows of a unit: the block of its page lane / 4 % 2 (-1: none), and four exponents, those of its rows
+    // A unit is two blocks.  What a lane knows of one: the id of block lane / 4 % 2 (-1: none), and the exponents of rows
     // 4 (lane % 8) .. + 3.
     auto block_of = [&](int u) -> int {
-      const int n = u / kUnits, page = (j0 + (n >> 1)) * kPages + (u % kUnits) * 2 + ((lane >> 2) & 1);
+      const int page = (j0 + u / (2 * kUnits)) * kPages + (u % kUnits) * 2 + ((lane >> 2) & 1);
       if (u >= units || page >= npages) return -1;
       int id = __ldg(table + page);
       if (id < 0 || id >= p.num_blocks) {
@@ -187,36 +187,53 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       return __ldg(reinterpret_cast<const uint32_t*>(p.kv_scales + (static_cast<int64_t>(id) * p.num_kv_heads + kvh) * 2 * kBlockTokens +
                                                      (u / kUnits & 1) * kBlockTokens + 4 * (lane & 3)));
     };
-    // Chunk i of unit u: row i * 32 / kChunks + my_row of it.
-    auto load = [&](int u, int id, int i) -> uint4 {
-      const int row = i * (32 / kChunks) + my_row;
-      const int of = __shfl_sync(0xffffffffu, id, (row >> 4) * 4);
-      if (of < 0) return make_uint4(0u, 0u, 0u, 0u);
-      const uint8_t* cache = static_cast<const uint8_t*>((u / kUnits & 1) ? p.v_cache : p.k_cache);
-      return load_codes(cache + ((static_cast<int64_t>(of) * p.num_kv_heads + kvh) * kBlockTokens + (row & 15)) * D + my_chunk * 16);
+    // Where a lane's codes of each of the unit's blocks are; null: there is none.
+    auto codes_of = [&](int u, int id, int block) -> const uint8_t* {
+      const int of = __shfl_sync(0xffffffffu, id, 4 * block);
+      if (of < 0) return nullptr;
+      return static_cast<const uint8_t*>((u / kUnits & 1) ? p.v_cache : p.k_cache) +
+             ((static_cast<int64_t>(of) * p.num_kv_heads + kvh) * kBlockTokens + my_row) * D + my_chunk * 16;
     };
+    constexpr int kHalf = kLoads / 2;  // loads of a block
+    auto load = [&](const uint8_t* from, int i) -> uint4 {
+      return from ? load_codes(from + (i % kHalf) * kLoadRows * D) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    // Chunk i's bf16 places: row 16 (i / kHalf) + (i % kHalf) kLoadRows + my_row, so that of its place in the swizzle only
+    // bit 2 of the row goes by i, and only with 128 dims.
+    const uint32_t even = kv_off<D>(my_row, 2 * my_chunk / 8, 2 * my_chunk % 8);
+    const uint32_t odd = D == 128 ? kv_off<D>(my_row + 4, 2 * my_chunk / 8, 2 * my_chunk % 8) : 0u;
+    auto place = [&](int i) -> uint32_t {
+      const uint32_t at = (i / kHalf) * T::kPageBytes;
+      if (D == 128) return at + ((i >> 1) & 1) * T::kGroupBytes + (i & 1 ? odd : even);
+      return at + (i & 1) * T::kGroupBytes + even;
+    };
+    const uint32_t pick = 0x0444u | (lane >> 2 & 3) << 12;  // a row's exponent, byte my_row % 4, to the top byte
+
     int u = warp - kIssuer - 1;
     int id = block_of(u), next_id = block_of(u + kConverters);
     uint32_t exponents = exponents_of(u, id);
     uint4 x[kLoads];
+    {
+      const uint8_t *first = codes_of(u, id, 0), *second = codes_of(u, id, 1);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) x[i] = load(u, id, i);
+      for (int i = 0; i < kLoads; ++i) x[i] = load(i < kHalf ? first : second, i);
+    }
     for (; u < units; u += kConverters) {
       const int n = u / kUnits, slot = n % kRing;
       const int after = block_of(u + 2 * kConverters);
       const uint32_t next_exponents = exponents_of(u + kConverters, next_id);
+      const uint8_t *first = codes_of(u + kConverters, next_id, 0), *second = codes_of(u + kConverters, next_id, 1);
       if (n >= kRing && !__all_sync(0xffffffffu, bar_wait(r_empty + 8 * slot, (n / kRing + 1) & 1))) {
         failed = true;
         break;
       }
-      const int row_of_unit = (u % kUnits) * kUnitRows;
-      unsigned char* tile_at = smem + T::kOffKV + slot * T::kTile;
-      const int left = kv_end - (j0 + (n >> 1)) * kKeys - row_of_unit;  // the unit's rows that hold keys
+      unsigned char* unit_at = smem + T::kOffKV + slot * T::kTile + (u % kUnits) * 2 * T::kPageBytes;
+      const int left = kv_end - (j0 + (n >> 1)) * kKeys - (u % kUnits) * kUnitRows;  // the unit's rows that hold keys
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int row = i * (32 / kChunks) + my_row;
-        const uint32_t four = __shfl_sync(0xffffffffu, exponents, row >> 2);
-        const float f = fp8_scale((four >> 8 * (row & 3)) & 0xffu);
+        const uint32_t four = __shfl_sync(0xffffffffu, exponents, (i * kLoadRows + my_row) >> 2);
+        // 2^(e - 127), as fp8_scale.
+        const float f = __uint_as_float(max(__byte_perm(four, 0, pick) >> 1, 0x00400000u));
         const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
         uint32_t r[8];
 #pragma unroll
@@ -224,15 +241,12 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
           const float2 v = __fmul2_rn(fp8_floats(static_cast<uint16_t>(w[k / 2] >> 16 * (k & 1))), make_float2(f, f));
           r[k] = pack_bf16(v.x, v.y);
         }
-        x[i] = load(u + kConverters, next_id, i);
-        if (left < kUnitRows && row >= left)
+        x[i] = load(i < kHalf ? first : second, i);
+        if (left < kUnitRows && i * kLoadRows + my_row >= left)
 #pragma unroll
           for (int k = 0; k < 8; ++k) r[k] = 0u;
-        const int c = 2 * my_chunk;
-        unsigned char* dst = tile_at + kv_off<D>(row_of_unit + row, c / 8, c % 8);
-        *reinterpret_cast<uint4*>(dst) = make_uint4(r[0], r[1], r[2], r[3]);
-        *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(reinterpret_cast<uintptr_t>(dst) ^ 16)) =
-            make_uint4(r[4], r[5], r[6], r[7]);
+        *reinterpret_cast<uint4*>(unit_at + place(i)) = make_uint4(r[0], r[1], r[2], r[3]);
+        *reinterpret_cast<uint4*>(unit_at + (place(i) ^ 16)) = make_uint4(r[4], r[5], r[6], r[7]);
       }
       fence_async_smem();
       __syncwarp();
