@@ -1215,17 +1215,43 @@ namespace {
 // Least units of a piece of the few-row kernel's stream.
 constexpr int32_t kFp8PieceUnits = 2;
 
+// Its workspace, and the CTAs a pair if it needs none.
+pkv_status few_rows_need(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int32_t max_blocks_per_seq, int rows,
+                         int* cluster, size_t* need) {
+  *cluster = 0;
+  *need = 0;
+  if (num_seqs == 0) return PKV_OK;
+  if (num_seqs <= pkv::kFp8LaunchSeqs) {
+    const cudaError_t e = pkv::fp8_cluster_ctas(head_dim, rows, num_seqs, num_kv_heads, max_blocks_per_seq, cluster);
+    if (e != cudaSuccess) return cuda_fail(e, "cluster occupancy query");
+    if (*cluster) return PKV_OK;
+  }
+  int sms = 0;
+  if (pkv_status st = device_state(nullptr, &sms); st != PKV_OK) return st;
+  *need = pkv::Fp8FewPlan(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, rows, kFp8PieceUnits, sms).bytes;
+  return PKV_OK;
+}
+
 pkv_status few_rows_fp8(pkv::Fp8AttentionParams p, int32_t head_dim, void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
   int sms = 0;
   if (pkv_status st = device_state(&p.err, &sms); st != PKV_OK) return st;
   const int rows = p.max_query_len * (p.num_q_heads / p.num_kv_heads);
-  const pkv::Fp8FewPlan all(p.num_seqs, p.num_kv_heads, head_dim, p.max_blocks_per_seq, rows, kFp8PieceUnits, sms);
-  if (!workspace || workspace_bytes < all.bytes)
+  size_t need = 0;
+  if (pkv_status st = few_rows_need(p.num_seqs, p.num_kv_heads, head_dim, p.max_blocks_per_seq, rows, &p.cluster_ctas, &need);
+      st != PKV_OK)
+    return st;
+  if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(PKV_ERR_INVALID_ARGUMENT, "workspace too small: %zu bytes given, %zu needed", workspace ? workspace_bytes : size_t{0},
-                all.bytes);
+                need);
   p.qscale = p.scale * 1.4426950408889634f;
   p.min_piece_units = kFp8PieceUnits;
   p.state_rows = rows;
+  if (p.cluster_ctas) {
+    const cudaError_t e = pkv::launch_few_rows_fp8(p, head_dim, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "fp8 attention launch");
+    g_launches.fetch_add(1);
+    return ok();
+  }
   // A large batch runs in slices, in order on the same stream and workspace.
   const size_t q_row = static_cast<size_t>(p.num_q_heads) * head_dim * 2;
   const int32_t num_seqs = p.num_seqs;
@@ -1260,12 +1286,12 @@ pkv_status pkv_fp8_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, 
   if (!bytes) return fail(PKV_ERR_INVALID_ARGUMENT, "bytes is null");
   if (pkv_status st = check_shapes(num_seqs, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq); st != PKV_OK)
     return st;
-  int sms = 0;
-  if (pkv_status st = device_state(nullptr, &sms); st != PKV_OK) return st;
-  *bytes = num_seqs == 0 ? 0
-                         : pkv::Fp8FewPlan(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, num_q_heads / num_kv_heads,
-                                           kFp8PieceUnits, sms)
-                               .bytes;
+  int cluster = 0;
+  size_t need = 0;
+  if (pkv_status st = few_rows_need(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, num_q_heads / num_kv_heads, &cluster, &need);
+      st != PKV_OK)
+    return st;
+  *bytes = need;
   return ok();
 }
 
@@ -1299,12 +1325,18 @@ pkv_status pkv_fp8_prefill_workspace_size(int64_t num_query_tokens, int32_t max_
   int sms = 0;
   if (pkv_status st = device_state(nullptr, &sms); st != PKV_OK) return st;
   const int64_t rows = static_cast<int64_t>(max_query_len) * (num_q_heads / num_kv_heads);
-  if (rows <= pkv::kFp8MostRows)
-    *bytes = pkv::Fp8FewPlan(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, static_cast<int>(rows), kFp8PieceUnits, sms).bytes;
-  else
-    *bytes = pkv::prefill_workspace_bytes(
+  int cluster = 0;
+  size_t need = 0;
+  if (rows <= pkv::kFp8MostRows) {
+    if (pkv_status st = few_rows_need(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, static_cast<int>(rows), &cluster, &need);
+        st != PKV_OK)
+      return st;
+  } else {
+    need = pkv::prefill_workspace_bytes(
         num_seqs, max_query_len, num_q_heads, num_kv_heads, head_dim,
         fp8_prefill_splits(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq, sms));
+  }
+  *bytes = need;
   return ok();
 }
 

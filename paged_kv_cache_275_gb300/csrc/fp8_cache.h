@@ -82,6 +82,7 @@ struct Fp8AttentionParams {
   float scale;
   // Few rows a sequence (fp8_decode.cuh), up to kFp8LaunchSeqs sequences a launch.
   float qscale;         // scale * log2(e): scores are kept in base-2 units
+  int cluster_ctas;     // CTAs a (sequence, kv head), joined through their shared memory; 0: the stream form, all below
   int unit_heads;       // kv heads of a unit: 8, 4, 2 or 1
   int num_pieces;       // most pieces that the stream of units is cut into
   int min_piece_units;  // least units of a piece, while there are so many
@@ -103,7 +104,7 @@ struct Fp8FewPlan {
     const int seqs = num_seqs < kFp8LaunchSeqs ? num_seqs : kFp8LaunchSeqs;
     unit_heads = 8;
     while (num_kv_heads % unit_heads) unit_heads /= 2;
-    const int blocks = 8 / unit_heads;
+    const int blocks = (head_dim == 128 ? 8 : 16) / unit_heads;
     const int64_t units = static_cast<int64_t>(seqs) * (num_kv_heads / unit_heads) * ((max_blocks_per_seq + blocks - 1) / blocks);
     const int64_t most = (units + min_piece_units - 1) / min_piece_units;
     const int64_t ctas = static_cast<int64_t>(sms) * (fp8_columns(state_rows) == 1 ? 2 : 1);
@@ -119,6 +120,8 @@ struct Fp8FewPlan {
 cudaError_t launch_append_fp8(const Fp8AppendParams& p, int head_dim, int num_sms, cudaStream_t stream);
 cudaError_t launch_gather_fp8(const Fp8GatherParams& p, int head_dim, int num_sms, cudaStream_t stream);
 cudaError_t launch_copy_blocks_fp8(const Fp8CopyParams& p, int num_pairs, cudaStream_t stream);
+// CTAs a pair of a call of few pairs, which needs no workspace; 0: the call takes the stream form.
+cudaError_t fp8_cluster_ctas(int head_dim, int rows, int num_seqs, int num_kv_heads, int max_blocks_per_seq, int* ctas);
 cudaError_t launch_few_rows_fp8(const Fp8AttentionParams& p, int head_dim, cudaStream_t stream);
 // Chunks on the 5th-generation tensor cores (fp8_prefill.cu); ws: prefill_workspace_bytes of num_splits > 1.
 cudaError_t launch_prefill_fp8(const Fp8AttentionParams& p, int head_dim, int num_splits, float* ws, cudaStream_t stream);

@@ -4,6 +4,13 @@
 namespace pkv {
 namespace {
 
+// Which form a call takes: clusters if all of its pairs' run at once and they are expected to be done before the stream
+// form, by what each takes more of: a cluster CTA's units one after the other, or the second launch and the pass over the
+// lengths, and the bytes over the whole GPU.
+constexpr float kClusterUnitUs = 0.5f;
+constexpr float kStreamUs = 5.f;
+constexpr float kStreamBytesPerUs = 6.5e6f;
+
 // The cache's codes as rows of 128 bytes (a token of 128 dims, or two of 64), a box the rows of a unit's heads of one block,
 // swizzled.  (With boxes of 64-byte rows, 64 dims are copied at 5.0 TB/s, so XXX.)
 cudaError_t code_map(CUtensorMap* map, const void* cache, int64_t bytes, int box_bytes) {
@@ -14,52 +21,123 @@ cudaError_t code_map(CUtensorMap* map, const void* cache, int64_t bytes, int box
 }
 
 template <int D, int NC>
-cudaError_t launch(const Fp8AttentionParams& p, cudaStream_t stream) {
-  constexpr int kMost = Few<D, NC>::smem(kFp8LaunchSeqs);
+struct Instance {
+  static constexpr int kMost = Few<D, NC>::smem(kFp8LaunchSeqs);
+  static constexpr int kClusterSmem = Few<D, NC>::smem(0);
   static_assert(Few<D, NC>::kCtas * (kMost + 1024 + 256) <= 228 * 1024, "shared memory of an SM's CTAs");
-  static std::mutex mu;
-  static uint64_t ready = 0;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (!(dev < 64 && ((ready >> dev) & 1u))) {
-      e = cudaFuncSetAttribute(&few_rows_fp8_kernel<D, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-      if (e != cudaSuccess) return e;
-      e = cudaFuncSetAttribute(&few_rows_fp8_kernel<D, NC>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-      if (e != cudaSuccess) return e;
-      if (dev < 64) ready |= uint64_t{1} << dev;
-    }
+  static_assert(Few<D, NC>::kCols * (D * 4 + 8) <= Few<D, NC>::kOffScales, "a cluster CTA's state lies in the ring");
+  static constexpr auto kStream = &few_rows_fp8_kernel<D, NC, false>;
+  static constexpr auto kCluster = &few_rows_fp8_kernel<D, NC, true>;
+
+  static cudaError_t maps(const Fp8AttentionParams& p, int heads, CUtensorMap* mk, CUtensorMap* mv) {
+    const int64_t bytes = p.num_blocks * p.num_kv_heads * Few<D, NC>::kTile;
+    const cudaError_t e = code_map(mk, p.k_cache, bytes, heads * Few<D, NC>::kTile);
+    return e != cudaSuccess ? e : code_map(mv, p.v_cache, bytes, heads * Few<D, NC>::kTile);
   }
-  CUtensorMap mk, mv;
-  const int64_t bytes = p.num_blocks * p.num_kv_heads * Few<D, NC>::kTile;
-  if ((e = code_map(&mk, p.k_cache, bytes, p.unit_heads * Few<D, NC>::kTile)) != cudaSuccess) return e;
-  if ((e = code_map(&mv, p.v_cache, bytes, p.unit_heads * Few<D, NC>::kTile)) != cudaSuccess) return e;
-  e = launch_pdl(few_rows_fp8_kernel<D, NC>, dim3(p.num_pieces), dim3(kThreads), Few<D, NC>::smem(p.num_seqs), stream, p, mk, mv);
-  if (e != cudaSuccess) return e;
-  const unsigned pairs = static_cast<unsigned>(p.num_seqs) * p.num_kv_heads;
-  const unsigned cols = p.state_rows;
-  // Few pairs have many states each.
-  if (pairs * cols <= 1216) return launch_pdl(join_fp8_kernel<D, 8>, dim3(pairs, cols), dim3(256), 0, stream, p);
-  return launch_pdl(join_fp8_kernel<D, 1>, dim3(pairs, (cols + 3) / 4), dim3(128), 0, stream, p);
+
+  static cudaLaunchConfig_t cluster_config(unsigned pairs, int ctas, cudaStream_t stream, cudaLaunchAttribute (&attr)[2]) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(pairs * static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kClusterSmem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cfg;
+  }
+
+  // Clusters of 1, 2, 4 and 8 CTAs that the current device holds at once; both kernels' shared memory is set on the way.
+  static cudaError_t prepare(const int** counts) {
+    static std::mutex mu;
+    static int known[64][4];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (known[dev][0] == 0) {
+      if ((e = cudaFuncSetAttribute(kStream, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost)) != cudaSuccess) return e;
+      if ((e = cudaFuncSetAttribute(kStream, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess) return e;
+      if ((e = cudaFuncSetAttribute(kCluster, cudaFuncAttributeMaxDynamicSharedMemorySize, kClusterSmem)) != cudaSuccess) return e;
+      if ((e = cudaFuncSetAttribute(kCluster, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess) return e;
+      for (int k = 3; k >= 0; --k) {
+        cudaLaunchAttribute attr[2];
+        cudaLaunchConfig_t cfg = cluster_config(1, 1 << k, nullptr, attr);
+        cfg.numAttrs = 1;
+        if ((e = cudaOccupancyMaxActiveClusters(&known[dev][k], kCluster, &cfg)) != cudaSuccess) {
+          known[dev][0] = 0;
+          return e;
+        }
+      }
+    }
+    *counts = known[dev];
+    return cudaSuccess;
+  }
+
+  static cudaError_t cluster_ctas(int num_seqs, int num_kv_heads, int max_blocks_per_seq, int* ctas) {
+    const int* counts = nullptr;
+    const cudaError_t e = prepare(&counts);
+    if (e != cudaSuccess) return e;
+    const int64_t pairs = static_cast<int64_t>(num_seqs) * num_kv_heads;
+    const int units = (max_blocks_per_seq + Few<D, NC>::kUnitTiles - 1) / Few<D, NC>::kUnitTiles;
+    int k = 0;
+    while (k < 3 && (1 << k) < units && pairs <= counts[k + 1]) ++k;
+    const float mine = kClusterUnitUs * ((units + (1 << k) - 1) >> k);
+    const float other = kStreamUs + static_cast<float>(pairs) * units * (2.f * Few<D, NC>::kOperand) / kStreamBytesPerUs;
+    *ctas = pairs <= counts[k] && mine <= other ? 1 << k : 0;
+    return cudaSuccess;
+  }
+
+  static cudaError_t launch(const Fp8AttentionParams& p, cudaStream_t stream) {
+    const int* counts = nullptr;
+    cudaError_t e = prepare(&counts);
+    if (e != cudaSuccess) return e;
+    CUtensorMap mk, mv;
+    if ((e = maps(p, p.cluster_ctas ? 1 : p.unit_heads, &mk, &mv)) != cudaSuccess) return e;
+    const unsigned pairs = static_cast<unsigned>(p.num_seqs) * p.num_kv_heads;
+    if (p.cluster_ctas) {
+      cudaLaunchAttribute attr[2];
+      const cudaLaunchConfig_t cfg = cluster_config(pairs, p.cluster_ctas, stream, attr);
+      return cudaLaunchKernelEx(&cfg, kCluster, p, mk, mv);
+    }
+    e = launch_pdl(kStream, dim3(p.num_pieces), dim3(kThreads), Few<D, NC>::smem(p.num_seqs), stream, p, mk, mv);
+    if (e != cudaSuccess) return e;
+    const unsigned cols = p.state_rows;
+    // Few pairs have many states each.
+    if (pairs * cols <= 1216) return launch_pdl(join_fp8_kernel<D, 8>, dim3(pairs, cols), dim3(256), 0, stream, p);
+    return launch_pdl(join_fp8_kernel<D, 1>, dim3(pairs, (cols + 3) / 4), dim3(128), 0, stream, p);
+  }
+};
+
+template <typename F>
+cudaError_t dispatch(int head_dim, int rows, F&& f) {
+  switch (head_dim * 8 + fp8_columns(rows)) {
+    case 64 * 8 + 1: return f(Instance<64, 1>{});
+    case 64 * 8 + 2: return f(Instance<64, 2>{});
+    case 64 * 8 + 3: return f(Instance<64, 3>{});
+    case 64 * 8 + 4: return f(Instance<64, 4>{});
+    case 128 * 8 + 1: return f(Instance<128, 1>{});
+    case 128 * 8 + 2: return f(Instance<128, 2>{});
+    case 128 * 8 + 3: return f(Instance<128, 3>{});
+    case 128 * 8 + 4: return f(Instance<128, 4>{});
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_few_rows_fp8(const Fp8AttentionParams& p, int head_dim, cudaStream_t stream) {
-  const int nc = fp8_columns(p.state_rows);
-  switch (head_dim * 8 + nc) {
-    case 64 * 8 + 1: return launch<64, 1>(p, stream);
-    case 64 * 8 + 2: return launch<64, 2>(p, stream);
-    case 64 * 8 + 3: return launch<64, 3>(p, stream);
-    case 64 * 8 + 4: return launch<64, 4>(p, stream);
-    case 128 * 8 + 1: return launch<128, 1>(p, stream);
-    case 128 * 8 + 2: return launch<128, 2>(p, stream);
-    case 128 * 8 + 3: return launch<128, 3>(p, stream);
-    case 128 * 8 + 4: return launch<128, 4>(p, stream);
-    default: return cudaErrorInvalidValue;
-  }
+  return dispatch(head_dim, p.state_rows, [&](auto instance) { return instance.launch(p, stream); });
+}
+
+cudaError_t fp8_cluster_ctas(int head_dim, int rows, int num_seqs, int num_kv_heads, int max_blocks_per_seq, int* ctas) {
+  return dispatch(head_dim, rows,
+                  [&](auto instance) { return instance.cluster_ctas(num_seqs, num_kv_heads, max_blocks_per_seq, ctas); });
 }
 
 }  // namespace pkv

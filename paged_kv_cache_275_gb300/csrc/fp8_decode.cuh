@@ -16,14 +16,18 @@
 // most 2^15 and the largest of a row is 2^7 or more: fp16's 11 bits hold for weights down to 2^-21 of the largest, and those
 // below 2^-32 of it vanish.  (m comes off first: next to a large score an exponent would lose its bits.)
 //
-// Work.  The batch's blocks form one stream of units: eight (block, kv head) tiles that lie next to one another, all eight
-// heads of a block, or two blocks of four heads and so on (32 KB of K and V at D = 128).  The stream is cut into equal
+// Work.  The batch's blocks form one stream of units of 32 KB of K and V, eight (block, kv head) tiles of 128 dims or sixteen
+// of 64: all eight heads of a block (of two), or two (four) blocks of four heads, and so on.  The stream is cut into equal
 // contiguous pieces, one a CTA, so that every CTA moves the same bytes whatever the lengths.  Units arrive in a ring: a
 // block's heads are neighbours in the cache, so a unit takes one or a few large tensor copies (swizzled, so that ldmatrix
 // reads without bank conflicts).  Each of the CTA's eight warps takes its tile of every unit, and they send for the units in
 // turns, a warp every eighth, with its block ids looked up eight units ahead.  (A warp that only copies would cost the others
 // a quarter of their registers.)  A (sequence, heads) pair cut by a piece's border leaves partial states (m, l, O) that a
 // second kernel joins.
+//
+// Few pairs.  A call of few (sequence, kv head) pairs takes a thread-block cluster a pair instead: its units, of one head, are
+// dealt to the cluster's CTAs, whose states are joined through distributed shared memory.  One launch, no workspace, and no
+// pass over the batch's lengths.
 //
 // Every wait is bounded: one that runs out sets PKV_DEVERR_PIPELINE_TIMEOUT, and its warp goes on without computing.
 #pragma once
@@ -44,8 +48,9 @@ namespace pkv {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kUnitTiles = 8;  // (block, kv head) tiles of a unit, one a warp
-constexpr int kThreads = 32 * kUnitTiles;
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMostCluster = 8;
 constexpr float kNone = -3.0e38f;  // the reference of a row that has seen no token
 constexpr float kSlack = 8.f;
 constexpr float kWeightShift = 7.f;  // the largest weight is brought to 2^7 .. 2^15
@@ -55,17 +60,19 @@ template <int D, int NC>
 struct Few {
   static constexpr int kCols = 8 * NC;
   static constexpr int kTile = kBlockTokens * D;           // bytes of one tile of K (or V)
+  static constexpr int kTurns = 128 / D;                   // tiles of a unit that a warp takes, one after the other
+  static constexpr int kUnitTiles = kWarps * kTurns;       // (block, kv head) tiles of a unit
   static constexpr int kOperand = kUnitTiles * kTile;      // K (or V) of a unit
   static constexpr int kScales = kUnitTiles * 2 * kBlockTokens;
   static constexpr int kCtas = NC == 1 ? 2 : 1;            // per SM
-  static constexpr int kStages = (D == 128 ? 3 : 6) * 2 / kCtas;
+  static constexpr int kStages = 6 / kCtas;
   static constexpr int kOffV = kOperand;
   static constexpr int kStage = 2 * kOperand;
   static constexpr int kOffScales = kStages * kStage;
   static constexpr int kOffExchange = kOffScales + kStages * kScales;
-  static constexpr int kExchange = kUnitTiles / 2 * 32 * 32;  // 8 values a lane of four warps
+  static constexpr int kExchange = kWarps / 2 * 32 * 32;  // 8 values a lane of four warps
   static constexpr int kOffMl = kOffExchange + kExchange;
-  static constexpr int kMl = kUnitTiles / 2 * kCols * 8;
+  static constexpr int kMl = kWarps / 2 * kCols * 8;
   static constexpr int kOffBar = kOffMl + kMl;
   static constexpr int kOffSeq = kOffBar + 16 * kStages;  // units before each sequence, [num_seqs + 1]; tokens, [num_seqs]
   static constexpr int smem(int num_seqs) { return kOffSeq + (2 * num_seqs + 1) * 4 + 1024; }  // 1024 to align the ring
@@ -153,6 +160,35 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address of the same shared-memory location in CTA `rank` of the cluster, and loads from there.
+__device__ __forceinline__ uint32_t remote(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 remote_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 remote_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -197,7 +233,7 @@ __device__ __forceinline__ int pieces_of(const Fp8AttentionParams& p, int total)
   return min(most, p.num_pieces);
 }
 
-template <int D, int NC>
+template <int D, int NC, bool kCluster>
 __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
     few_rows_fp8_kernel(const Fp8AttentionParams p, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v) {
@@ -211,52 +247,75 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
   int* s_tokens = s_units + p.num_seqs + 1;
   __shared__ int s_sum[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int hc = p.unit_heads, nb = kUnitTiles / hc;  // heads and blocks of a unit
+  const int hc = kCluster ? 1 : p.unit_heads, nb = T::kUnitTiles / hc;  // heads and blocks of a unit
   const int head_groups = p.num_kv_heads / hc;
   const uint32_t full = base + T::kOffBar, empty = full + 8 * kStages;
   pdl_trigger();
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       bar_init(full + 8 * s, 1);
-      bar_init(empty + 8 * s, kUnitTiles);
+      bar_init(empty + 8 * s, kWarps);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    s_units[0] = 0;
   }
   pdl_wait();
 
-  // Units before each sequence.
-  int running = 0;
-  for (int first = 0; first < p.num_seqs; first += kThreads) {
-    const int b = first + tid;
-    int units = 0;
-    if (b < p.num_seqs) {
-      const Rows r = rows_of(p, b);
-      if (r.wrong && blockIdx.x == 0) atomicOr(p.err, r.wrong);
-      s_tokens[b] = r.tokens;
-      units = r.count > 0 ? ((r.tokens + kBlockTokens - 1) / kBlockTokens + nb - 1) / nb : 0;
-    }
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(kAll, units, off);
-      if (lane >= off) units += y;
-    }
-    if (lane == 31) s_sum[warp] = units;
-    __syncthreads();
-    int before = running;
-    for (int w = 0; w < warp; ++w) before += s_sum[w];
-    if (b < p.num_seqs) s_units[b + 1] = before + units;
-    for (int w = 0; w < kThreads / 32; ++w) running += s_sum[w];
-    __syncthreads();
-  }
-  const int total = running * head_groups;
-  const int pieces = pieces_of(p, total);
   const int piece = blockIdx.x;
-  if (piece >= pieces) return;
-  const int n0 = static_cast<int>(static_cast<int64_t>(piece) * total / pieces);
-  const int n1 = static_cast<int>(static_cast<int64_t>(piece + 1) * total / pieces);
+  int n0, n1;     // this CTA's units: of the stream, or of the cluster's pair
+  Rows pair{};    // a cluster's rows
+  Walk start{};   // unit n0
+  if constexpr (kCluster) {
+    const uint32_t size = cluster_size(), rank = cluster_rank();
+    const int at = static_cast<int>(blockIdx.x / size);
+    start.b = at / head_groups;
+    start.heads = at - start.b * head_groups;
+    pair = rows_of(p, start.b);
+    if (pair.wrong && rank == 0 && start.heads == 0 && tid == 0) atomicOr(p.err, pair.wrong);
+    if (pair.count == 0) return;  // (the whole cluster)
+    start.units = ((pair.tokens + kBlockTokens - 1) / kBlockTokens + nb - 1) / nb;
+    n0 = static_cast<int>(static_cast<int64_t>(rank) * start.units / size);
+    n1 = static_cast<int>(static_cast<int64_t>(rank + 1) * start.units / size);
+    start.unit = n0;
+    __syncthreads();
+  } else {
+    // Units before each sequence.
+    if (tid == 0) s_units[0] = 0;
+    int running = 0;
+    for (int first = 0; first < p.num_seqs; first += kThreads) {
+      const int b = first + tid;
+      int units = 0;
+      if (b < p.num_seqs) {
+        const Rows r = rows_of(p, b);
+        if (r.wrong && blockIdx.x == 0) atomicOr(p.err, r.wrong);
+        s_tokens[b] = r.tokens;
+        units = r.count > 0 ? ((r.tokens + kBlockTokens - 1) / kBlockTokens + nb - 1) / nb : 0;
+      }
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(kAll, units, off);
+        if (lane >= off) units += y;
+      }
+      if (lane == 31) s_sum[warp] = units;
+      __syncthreads();
+      int before = running;
+      for (int w = 0; w < warp; ++w) before += s_sum[w];
+      if (b < p.num_seqs) s_units[b + 1] = before + units;
+      for (int w = 0; w < kThreads / 32; ++w) running += s_sum[w];
+      __syncthreads();
+    }
+    const int total = running * head_groups;
+    const int pieces = pieces_of(p, total);
+    if (piece >= pieces) return;
+    n0 = static_cast<int>(static_cast<int64_t>(piece) * total / pieces);
+    n1 = static_cast<int>(static_cast<int64_t>(piece + 1) * total / pieces);
+  }
   // Unit n of the stream (there is one).
   auto walk_to = [&](int n) {
+    Walk x = start;
+    if constexpr (kCluster) {
+      x.unit = n;
+      return x;
+    }
     int lo = 0, hi = p.num_seqs - 1;  // its sequence: the last with units before it at or below
     const int of_group = n / head_groups;
     while (lo < hi) {
@@ -264,7 +323,6 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
       if (s_units[mid] <= of_group) lo = mid;
       else hi = mid - 1;
     }
-    Walk x;
     x.b = lo;
     x.units = s_units[lo + 1] - s_units[lo];
     const int rest = n - s_units[lo] * head_groups;
@@ -274,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
   };
   // On to the pair that unit x.unit, past its own pair's end, lies in (there is one).
   auto carry = [&](Walk& x) {
-    while (x.unit >= x.units) {
+    while (!kCluster && x.unit >= x.units) {
       x.unit -= x.units;
       if (++x.heads < head_groups) continue;
       x.heads = 0;
@@ -291,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
   Walk far{};
   auto look_up = [&] {
     const int first = far.unit * nb;
-    ahead_blocks = min(nb, (s_tokens[far.b] + kBlockTokens - 1) / kBlockTokens - first);
+    ahead_blocks = min(nb, ((kCluster ? pair.tokens : s_tokens[far.b]) + kBlockTokens - 1) / kBlockTokens - first);
     if (lane < ahead_blocks) ahead_id = __ldg(p.block_tables + static_cast<int64_t>(far.b) * p.max_blocks_per_seq + first + lane);
   };
   auto send = [&] {
@@ -319,9 +377,9 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
                         (static_cast<int64_t>(r.first + i) * p.num_q_heads + far.heads * heads) * D,
                     heads * D * 2);
     }
-    ahead += kUnitTiles;
+    ahead += kWarps;
     if (ahead < n1 - n0) {
-      far.unit += kUnitTiles;
+      far.unit += kWarps;
       carry(far);
       look_up();
     }
@@ -333,23 +391,23 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
   }
   Walk at = walk_to(n0);
 
-  // ---------------- products (a tile of every unit a warp) ----------------
+  // ---------------- products (a tile of every unit a warp, or kTurns) ----------------
   const int g = lane >> 2, t = lane & 3;      // fragments: row g and columns 2t, 2t + 1 of an accumulator
-  const int head_of = warp & (hc - 1), block_of = warp / hc;  // (hc is a power of two)
+  const int head_of = warp & (hc - 1), place_of = warp / hc;  // (hc is a power of two); of a unit's blocks place_of kTurns ..
   const int group = p.num_q_heads / p.num_kv_heads, group_bits = 31 - __clz(group);
   // ldmatrix: lane i gives the address of row i % 8 of matrix i / 8; matrices 0, 1: tokens 0..7 and 8..15 of a chunk,
   // 2, 3: of the next chunk.  A tile is lines of 128 bytes, swizzled: chunk c of line y lies at c ^ (y % 8) (two tokens of 64
   // dims share a line).  Two chunks on are 32 bytes on, through the swizzle an exclusive or.
   const int ld_row = (lane & 7) + ((lane >> 3) & 1) * 8;
   const int ld_line = ld_row * D / 128, ld_chunk = (D == 128 ? 0 : (ld_row & 1) * 4) + (lane >> 4);
-  const uint32_t ld_at = base + warp * T::kTile + ld_line * 128 + ((ld_chunk ^ (ld_line & 7)) << 4);
+  const uint32_t ld_at = base + (place_of * T::kTurns * hc + head_of) * T::kTile + ld_line * 128 + ((ld_chunk ^ (ld_line & 7)) << 4);
   bool failed = false;
   int stage = 0;
   uint32_t use = 0;  // parity of the stage's next copy
 
-  // The piece's pairs of sequence and heads.
-  for (int n = n0; n < n1;) {
-    const Rows rows = rows_of(p, at.b);
+  // The piece's pairs of sequence and heads; a cluster's one, of which a CTA may have no unit.
+  for (int n = n0; kCluster || n < n1;) {
+    const Rows rows = kCluster ? pair : rows_of(p, at.b);
     const int kvh = at.heads * hc + head_of;
     const int first_limit = rows.tokens - rows.count + 1;  // tokens that the first row sees
     const int count = min(at.units - at.unit, n1 - n);      // units of the pair here
@@ -402,15 +460,19 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[c][nc][k] = 0.f;
 
-    int token0 = (at.unit * nb + block_of) * kBlockTokens;  // this warp's block
-    for (int u = 0; u < count; ++u, token0 += nb * kBlockTokens) {
+    int first_token = (at.unit * nb + place_of * T::kTurns) * kBlockTokens;  // of this warp's blocks
+    for (int u = 0; u < count; ++u, first_token += nb * kBlockTokens) {
       if (!failed && !bar_wait(full + 8 * stage, use)) {
         failed = true;
         if (lane == 0) atomicOr(p.err, kErrTimeout);
       }
-      if (!failed && token0 < rows.tokens) {
-        const uint32_t sk = ld_at + stage * T::kStage;
-        const unsigned char* sc = smem + T::kOffScales + stage * T::kScales + warp * 2 * kBlockTokens;
+#pragma unroll
+      for (int turn = 0; turn < T::kTurns; ++turn) {
+        const int token0 = first_token + turn * kBlockTokens;
+        if (failed || token0 >= rows.tokens) continue;
+        const uint32_t sk = ld_at + stage * T::kStage + turn * hc * T::kTile;
+        const unsigned char* sc = smem + T::kOffScales + stage * T::kScales +
+                                  ((place_of * T::kTurns + turn) * hc + head_of) * 2 * kBlockTokens;
         // S^T = Kc q^T.  Chunk c of a row: its 16 codes are the product's depth, in the order 4t, 4t + 1, 4t + 2, 4t + 3 of
         // a lane's four, as q's fragments are.
         float s[NC][4], s2[NC][4];
@@ -556,9 +618,9 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
     // The warps of a head join their states, half of them handing theirs to the other half at a time.
     float4* exchange = reinterpret_cast<float4*>(smem + T::kOffExchange);
     float2* s_ml = reinterpret_cast<float2*>(smem + T::kOffMl);
-    for (int half = nb / 2; half > 0; half >>= 1) {
-      const bool gives = block_of >= half && block_of < 2 * half, takes = block_of < half;
-      const int place = (block_of & (half - 1)) * hc + head_of;
+    for (int half = kWarps / hc / 2; half > 0; half >>= 1) {
+      const bool gives = place_of >= half && place_of < 2 * half, takes = place_of < half;
+      const int place = (place_of & (half - 1)) * hc + head_of;
       float mine[NC][2], other[NC][2];
       if (gives && g == 0)
 #pragma unroll
@@ -573,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
             const float(&v)[4] = o[(2 * part + x) / NC][(2 * part + x) % NC];
             exchange[(place * 2 + x) * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
           }
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * kUnitTiles) : "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
         if (takes) {
           if (part == 0)
 #pragma unroll
@@ -598,45 +660,99 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
             v[3] = v[3] * mine[nc][1] + y.w * other[nc][1];
           }
         }
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * kUnitTiles) : "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
       }
     }
-    const int slot = n == n0 ? 0 : 1;
-    if (warp == 0 && lane == 0) {
-      int* record = p.ws_records + 2 * (static_cast<int64_t>(at.b) * head_groups + at.heads);
-      if (started) record[0] = piece * 2 + slot;
-      if (ended) record[1] = piece;
-    }
-    if (block_of == 0 && !failed) {
+    if constexpr (!kCluster) {
+      const int slot = n == n0 ? 0 : 1;
+      if (warp == 0 && lane == 0) {
+        int* record = p.ws_records + 2 * (static_cast<int64_t>(at.b) * head_groups + at.heads);
+        if (started) record[0] = piece * 2 + slot;
+        if (ended) record[1] = piece;
+      }
+      if (place_of == 0 && !failed) {
 #pragma unroll
-      for (int nc = 0; nc < NC; ++nc)
+        for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int col = nc * 8 + 2 * t + k, i = col >> group_bits;
-          if (i >= rows.count) continue;
-          if (started && ended) {
-            const float inv = 1.f / l[nc][k];
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
-                                 (static_cast<int64_t>(rows.first + i) * p.num_q_heads + kvh * group + (col & (group - 1))) * D;
+          for (int k = 0; k < 2; ++k) {
+            const int col = nc * 8 + 2 * t + k, i = col >> group_bits;
+            if (i >= rows.count) continue;
+            if (started && ended) {
+              const float inv = 1.f / l[nc][k];
+              __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
+                                   (static_cast<int64_t>(rows.first + i) * p.num_q_heads + kvh * group + (col & (group - 1))) * D;
 #pragma unroll
-            for (int c = 0; c < kSteps; ++c)
-              *reinterpret_cast<uint32_t*>(dst + 16 * c + 2 * g) = pack_bf16(o[c][nc][k] * inv, o[c][nc][k + 2] * inv);
-          } else {
-            const int64_t state = (static_cast<int64_t>(piece * 2 + slot) * hc + head_of) * p.state_rows + col;
-            float* dst = p.ws_states + state * D;
+              for (int c = 0; c < kSteps; ++c)
+                *reinterpret_cast<uint32_t*>(dst + 16 * c + 2 * g) = pack_bf16(o[c][nc][k] * inv, o[c][nc][k + 2] * inv);
+            } else {
+              const int64_t state = (static_cast<int64_t>(piece * 2 + slot) * hc + head_of) * p.state_rows + col;
+              float* dst = p.ws_states + state * D;
 #pragma unroll
-            for (int c = 0; c < kSteps; ++c)
-              *reinterpret_cast<float2*>(dst + 16 * c + 2 * g) = make_float2(o[c][nc][k], o[c][nc][k + 2]);
-            if (g == 0) p.ws_ml[state] = make_float2(m[nc][k], l[nc][k]);
+              for (int c = 0; c < kSteps; ++c)
+                *reinterpret_cast<float2*>(dst + 16 * c + 2 * g) = make_float2(o[c][nc][k], o[c][nc][k + 2]);
+              if (g == 0) p.ws_ml[state] = make_float2(m[nc][k], l[nc][k]);
+            }
           }
+      }
+      n += count;
+      at.unit += count;
+      if (n < n1) carry(at);
+    } else {
+      // The CTA's state, in the ring (done with, by all warps: they have joined); then every CTA of the cluster forms its
+      // share of the outputs from all states.
+      float* s_o = reinterpret_cast<float*>(smem);
+      float2* s_state = reinterpret_cast<float2*>(smem + T::kCols * D * 4);
+      if (warp == 0) {
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int col = nc * 8 + 2 * t + k;
+#pragma unroll
+            for (int c = 0; c < kSteps; ++c)
+              *reinterpret_cast<float2*>(s_o + col * D + 16 * c + 2 * g) = make_float2(o[c][nc][k], o[c][nc][k + 2]);
+            if (g == 0) s_state[col] = make_float2(m[nc][k], l[nc][k]);
+          }
+      }
+      cluster_sync();
+      const int size = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+      for (int x = rank + size * tid; x < rows.count * group * (D / 4); x += size * kThreads) {
+        const int col = x / (D / 4), dim = x % (D / 4) * 4;
+        float2 ml[kMostCluster];
+        float4 v[kMostCluster];
+        float top = kNone;
+#pragma unroll
+        for (int y = 0; y < kMostCluster; ++y) {
+          ml[y] = make_float2(kNone, 0.f);
+          v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (y >= size) continue;
+          ml[y] = remote_f2(remote(saddr(s_state + col), y));
+          v[y] = remote_f4(remote(saddr(s_o + col * D + dim), y));
         }
+#pragma unroll
+        for (int y = 0; y < kMostCluster; ++y) top = fmaxf(top, ml[y].x);
+        float sum = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int y = 0; y < kMostCluster; ++y) {
+          const float by = ex2(ml[y].x - top);
+          sum += ml[y].y * by;
+          a.x += v[y].x * by;
+          a.y += v[y].y * by;
+          a.z += v[y].z * by;
+          a.w += v[y].w * by;
+        }
+        const float inv = rows.tokens > 0 ? 1.f / sum : 0.f;  // no token: zeros
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
+                             (static_cast<int64_t>(rows.first + (col >> group_bits)) * p.num_q_heads + kvh * group + (col & (group - 1))) * D + dim;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+      }
+      cluster_sync();  // no CTA leaves while another reads its state
+      break;
     }
-    n += count;
-    at.unit += count;
-    if (n < n1) carry(at);
   }
   if (failed)  // what this warp sent for lands before the CTA exits
-    for (int k = ahead - kUnitTiles; k >= 0 && k >= ahead - kUnitTiles - kStages; k -= kUnitTiles)
+    for (int k = ahead - kWarps; k >= 0 && k >= ahead - kWarps - kStages; k -= kWarps)
       bar_wait(full + 8 * (k % kStages), (k / kStages) & 1);
 }
 

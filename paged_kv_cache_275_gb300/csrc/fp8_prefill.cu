@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     const uint32_t pick = 0x0444u | (lane >> 2 & 3) << 12;  // a row's exponent, byte my_row % 4, to the top byte
 
     int u = warp - kIssuer - 1;
-    int id = block_of(u), next_id = block_of(u + kConverters);
+    int id = block_of(u), next_id = block_of(u + kConverters), second_id = block_of(u + 2 * kConverters);
     uint32_t exponents = exponents_of(u, id);
     uint4 x[kLoads];
     {
@@ -220,7 +220,12 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     }
     for (; u < units; u += kConverters) {
       const int n = u / kUnits, slot = n % kRing;
-      const int after = block_of(u + 2 * kConverters);
+      const int third_id = block_of(u + 3 * kConverters);
+      // The unit behind the next is on its way to L2 (28 KB in registers on their way from HBM would be too few).
+      if ((lane & ~4) == 0 && second_id >= 0)
+        l2_prefetch(static_cast<const uint8_t*>((u + 2 * kConverters) / kUnits & 1 ? p.v_cache : p.k_cache) +
+                        (static_cast<int64_t>(second_id) * p.num_kv_heads + kvh) * kBlockTokens * D,
+                    kBlockTokens * D);
       const uint32_t next_exponents = exponents_of(u + kConverters, next_id);
       const uint8_t *first = codes_of(u + kConverters, next_id, 0), *second = codes_of(u + kConverters, next_id, 1);
       if (n >= kRing && !__all_sync(0xffffffffu, bar_wait(r_empty + 8 * slot, (n / kRing + 1) & 1))) {
@@ -252,7 +257,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       __syncwarp();
       if (lane == 0) bar_arrive(r_full + 8 * slot);
       id = next_id;
-      next_id = after;
+      next_id = second_id;
+      second_id = third_id;
       exponents = next_exponents;
     }
     if (failed && lane == 0) atomicOr(p.err, kErrTimeout);
@@ -336,9 +342,16 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     fence_async_smem();
     bar_arrive(q_ready + 8 * t);
     const int limit = row_ok ? prefix + i + 1 : 0;
+    // A warp without rows of the chunk leaves its part of P as it is: a row of O takes only its own row of P.
+    // (In a loop of its own: as a branch of the loop below it costs that a sixth of its speed.)
+    const bool idle = i0 + t * kTokens + (warp & 3) * 32 / G >= C;
+    for (int j = 0; idle && j < nsteps && !failed; ++j) {
+      if (!__all_sync(0xffffffffu, bar_wait(s_full + 8 * t, j & 1))) failed = true;
+      else bar_arrive(p_full + 8 * t);
+    }
     const bool sees = kSplit ? limit > j0 * kKeys : row_ok;  // (a split's range may start behind the row's last key)
     float m_used = -INFINITY, l = 0.f;
-    for (int j = 0; j < nsteps && !failed; ++j) {
+    for (int j = idle ? nsteps : 0; j < nsteps && !failed; ++j) {
       if (!__all_sync(0xffffffffu, bar_wait(s_full + 8 * t, j & 1))) {
         failed = true;
         break;
