@@ -30,7 +30,7 @@ LIB = PKG / "libpagedkv.so"
 BINDING = PKG / "_binding.so"
 SOURCES = ["capi.cu", "kv_append.cu", "rope_append.cu", "paged_decode.cu", "window_decode.cu", "prefix_decode.cu",
            "static_workspace.cu", "copy_blocks.cu", "block_manager.cpp", "paged_prefill.cu", "window_prefill.cu",
-           "shared_prefix.cu", "fp8_cache.cu", "fp8_decode.cu", "fp8_maps.cu",
+           "shared_prefix.cu", "fp8_cache.cu", "fp8_decode.cu",
            "fp8_prefill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

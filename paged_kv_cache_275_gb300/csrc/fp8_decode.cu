@@ -11,29 +11,14 @@ constexpr float kClusterUnitUs = 0.5f;
 constexpr float kStreamUs = 5.f;
 constexpr float kStreamBytesPerUs = 6.5e6f;
 
-// The cache's codes as rows of 128 bytes (a token of 128 dims, or two of 64), a box the rows of a unit's heads of one block,
-// swizzled.  (With boxes of 64-byte rows, 64 dims are copied at 5.0 TB/s, so XXX.)
-cudaError_t code_map(CUtensorMap* map, const void* cache, int64_t bytes, int box_bytes) {
-  const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(bytes / 128)};
-  const cuuint64_t strides[1] = {128};
-  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_bytes / 128)};
-  return encode_code_map(map, cache, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
 template <int D, int NC>
 struct Instance {
   static constexpr int kMost = Few<D, NC>::smem(kFp8LaunchSeqs);
   static constexpr int kClusterSmem = Few<D, NC>::smem(0);
   static_assert(Few<D, NC>::kCtas * (kMost + 1024 + 256) <= 228 * 1024, "shared memory of an SM's CTAs");
-  static_assert(Few<D, NC>::kCols * (D * 4 + 8) <= Few<D, NC>::kOffScales, "a cluster CTA's state lies in the ring");
+  static_assert(Few<D, NC>::kCols * (D * 4 + 8) <= Few<D, NC>::kOffScales, "a cluster CTA's state lies in the rings");
   static constexpr auto kStream = &few_rows_fp8_kernel<D, NC, false>;
   static constexpr auto kCluster = &few_rows_fp8_kernel<D, NC, true>;
-
-  static cudaError_t maps(const Fp8AttentionParams& p, int heads, CUtensorMap* mk, CUtensorMap* mv) {
-    const int64_t bytes = p.num_blocks * p.num_kv_heads * Few<D, NC>::kTile;
-    const cudaError_t e = code_map(mk, p.k_cache, bytes, heads * Few<D, NC>::kTile);
-    return e != cudaSuccess ? e : code_map(mv, p.v_cache, bytes, heads * Few<D, NC>::kTile);
-  }
 
   static cudaLaunchConfig_t cluster_config(unsigned pairs, int ctas, cudaStream_t stream, cudaLaunchAttribute (&attr)[2]) {
     cudaLaunchConfig_t cfg = {};
@@ -88,7 +73,7 @@ struct Instance {
     int k = 0;
     while (k < 3 && (1 << k) < units && pairs <= counts[k + 1]) ++k;
     const float mine = kClusterUnitUs * ((units + (1 << k) - 1) >> k);
-    const float other = kStreamUs + static_cast<float>(pairs) * units * (2.f * Few<D, NC>::kOperand) / kStreamBytesPerUs;
+    const float other = kStreamUs + static_cast<float>(pairs) * units * (2.f * Few<D, NC>::kUnitTiles * Few<D, NC>::kTile) / kStreamBytesPerUs;
     *ctas = pairs <= counts[k] && mine <= other ? 1 << k : 0;
     return cudaSuccess;
   }
@@ -97,15 +82,13 @@ struct Instance {
     const int* counts = nullptr;
     cudaError_t e = prepare(&counts);
     if (e != cudaSuccess) return e;
-    CUtensorMap mk, mv;
-    if ((e = maps(p, p.cluster_ctas ? 1 : p.unit_heads, &mk, &mv)) != cudaSuccess) return e;
     const unsigned pairs = static_cast<unsigned>(p.num_seqs) * p.num_kv_heads;
     if (p.cluster_ctas) {
       cudaLaunchAttribute attr[2];
       const cudaLaunchConfig_t cfg = cluster_config(pairs, p.cluster_ctas, stream, attr);
-      return cudaLaunchKernelEx(&cfg, kCluster, p, mk, mv);
+      return cudaLaunchKernelEx(&cfg, kCluster, p);
     }
-    e = launch_pdl(kStream, dim3(p.num_pieces), dim3(kThreads), Few<D, NC>::smem(p.num_seqs), stream, p, mk, mv);
+    e = launch_pdl(kStream, dim3(p.num_pieces), dim3(kThreads), Few<D, NC>::smem(p.num_seqs), stream, p);
     if (e != cudaSuccess) return e;
     const unsigned cols = p.state_rows;
     // Few pairs have many states each.

@@ -18,21 +18,19 @@
 //
 // Work.  The batch's blocks form one stream of units of 32 KB of K and V, eight (block, kv head) tiles of 128 dims or sixteen
 // of 64: all eight heads of a block (of two), or two (four) blocks of four heads, and so on.  The stream is cut into equal
-// contiguous pieces, one a CTA, so that every CTA moves the same bytes whatever the lengths.  Units arrive in a ring: a
-// block's heads are neighbours in the cache, so a unit takes one or a few large tensor copies (swizzled, so that ldmatrix
-// reads without bank conflicts).  Each of the CTA's eight warps takes its tile of every unit, and they send for the units in
-// turns, a warp every eighth, with its block ids looked up eight units ahead.  (A warp that only copies would cost the others
-// a quarter of their registers.)  A (sequence, heads) pair cut by a piece's border leaves partial states (m, l, O) that a
-// second kernel joins.
+// contiguous pieces, one a CTA, so that every CTA moves the same bytes whatever the lengths.  Each of a CTA's eight warps takes
+// its tile of every unit, which are neighbours in memory, through a ring of its own: the lanes copy it in 16-byte pieces
+// (cp.async), placed so that ldmatrix reads without bank conflicts.  So no warp waits for another, but where the warps of a
+// head join their states at a pair's end.  (By tensor copies, as large as a unit for eight heads, a CTA has to wait for all its
+// warps at every unit, and a unit of one head is 24 copies, whose number bounds an SM: 128 sequences of 2048 tokens of one head
+// took 28.7 us so, XX like this; of eight heads XX and XX.)  A (sequence, heads) pair cut by a piece's border leaves partial
+// states (m, l, O) that a second kernel joins.
 //
 // Few pairs.  A call of few (sequence, kv head) pairs takes a thread-block cluster a pair instead: its units, of one head, are
 // dealt to the cluster's CTAs, whose states are joined through distributed shared memory.  One launch, no workspace, and no
 // pass over the batch's lengths.
-//
-// Every wait is bounded: one that runs out sets PKV_DEVERR_PIPELINE_TIMEOUT, and its warp goes on without computing.
 #pragma once
 
-#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -42,7 +40,6 @@
 
 #include "fp8_cache.h"
 #include "fp8_format.cuh"
-#include "fp8_maps.h"
 
 namespace pkv {
 namespace {
@@ -54,7 +51,6 @@ constexpr int kMostCluster = 8;
 constexpr float kNone = -3.0e38f;  // the reference of a row that has seen no token
 constexpr float kSlack = 8.f;
 constexpr float kWeightShift = 7.f;  // the largest weight is brought to 2^7 .. 2^15
-constexpr unsigned long long kWaitNs = 2000000000ull;
 
 template <int D, int NC>
 struct Few {
@@ -62,71 +58,31 @@ struct Few {
   static constexpr int kTile = kBlockTokens * D;           // bytes of one tile of K (or V)
   static constexpr int kTurns = 128 / D;                   // tiles of a unit that a warp takes, one after the other
   static constexpr int kUnitTiles = kWarps * kTurns;       // (block, kv head) tiles of a unit
-  static constexpr int kOperand = kUnitTiles * kTile;      // K (or V) of a unit
-  static constexpr int kScales = kUnitTiles * 2 * kBlockTokens;
   static constexpr int kCtas = NC == 1 ? 2 : 1;            // per SM
-  static constexpr int kStages = 6 / kCtas;
-  static constexpr int kOffV = kOperand;
-  static constexpr int kStage = 2 * kOperand;
-  static constexpr int kOffScales = kStages * kStage;
-  static constexpr int kOffExchange = kOffScales + kStages * kScales;
+  static constexpr int kStages = 6 * kTurns / kCtas;       // tiles of a warp's ring
+  static constexpr int kStage = 2 * kTile;                 // K, V
+  static constexpr int kScales = 2 * kBlockTokens;         // the exponents of both
+  static constexpr int kOffScales = kWarps * kStages * kStage;
+  static constexpr int kOffExchange = kOffScales + kWarps * kStages * kScales;
   static constexpr int kExchange = kWarps / 2 * 32 * 32;  // 8 values a lane of four warps
   static constexpr int kOffMl = kOffExchange + kExchange;
   static constexpr int kMl = kWarps / 2 * kCols * 8;
-  static constexpr int kOffBar = kOffMl + kMl;
-  static constexpr int kOffSeq = kOffBar + 16 * kStages;  // units before each sequence, [num_seqs + 1]; tokens, [num_seqs]
-  static constexpr int smem(int num_seqs) { return kOffSeq + (2 * num_seqs + 1) * 4 + 1024; }  // 1024 to align the ring
+  static constexpr int kOffSeq = kOffMl + kMl;  // units before each sequence, [num_seqs + 1]; tokens, [num_seqs]
+  static constexpr int smem(int num_seqs) { return kOffSeq + (2 * num_seqs + 1) * 4; }
 };
 
 // ---------------------------------------------------------------------------
 // PTX
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t saddr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-__device__ __forceinline__ void bar_init(uint32_t b, uint32_t n) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(b), "r"(n) : "memory");
+// 16 bytes global -> shared, past L1.
+__device__ __forceinline__ void copy_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void bar_arrive(uint32_t b) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(b) : "memory");
-}
-__device__ __forceinline__ void bar_expect_tx(uint32_t b, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(b), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ bool bar_try(uint32_t b, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(b), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ unsigned long long now_ns() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-// Bounded wait of a whole warp; false if the phase did not complete in time.
-__device__ __forceinline__ bool bar_wait(uint32_t b, uint32_t parity) {
-  bool ok = bar_try(b, parity);
-  if (!ok) {
-    const unsigned long long t0 = now_ns();
-    for (uint32_t it = 1; !ok && it < (1u << 30); ++it) {
-      ok = bar_try(b, parity);
-      if ((it & 63u) == 0 && now_ns() - t0 > kWaitNs) break;
-    }
-  }
-  return __all_sync(kAll, ok);
-}
-__device__ __forceinline__ void tensor_load(uint32_t dst, const CUtensorMap* map, int row, uint32_t b) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(b)
-      : "memory");
-}
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t b) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(b)
-               : "memory");
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {  // all groups but the last kLeft have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 __device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
@@ -235,13 +191,10 @@ __device__ __forceinline__ int pieces_of(const Fp8AttentionParams& p, int total)
 
 template <int D, int NC, bool kCluster>
 __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
-    few_rows_fp8_kernel(const Fp8AttentionParams p, const __grid_constant__ CUtensorMap map_k,
-                        const __grid_constant__ CUtensorMap map_v) {
+    few_rows_fp8_kernel(const Fp8AttentionParams p) {
   using T = Few<D, NC>;
   constexpr int kSteps = D / 16;  // 16-byte chunks of a row of codes: 16 dims, the depth of a product
-  constexpr int kStages = T::kStages;
-  extern __shared__ unsigned char raw[];
-  unsigned char* smem = raw + (-saddr(raw) & 1023u);
+  extern __shared__ __align__(128) unsigned char smem[];
   const uint32_t base = saddr(smem);
   int* s_units = reinterpret_cast<int*>(smem + T::kOffSeq);
   int* s_tokens = s_units + p.num_seqs + 1;
@@ -249,15 +202,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hc = kCluster ? 1 : p.unit_heads, nb = T::kUnitTiles / hc;  // heads and blocks of a unit
   const int head_groups = p.num_kv_heads / hc;
-  const uint32_t full = base + T::kOffBar, empty = full + 8 * kStages;
   pdl_trigger();
-  if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      bar_init(full + 8 * s, 1);
-      bar_init(empty + 8 * s, kWarps);
-    }
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
   pdl_wait();
 
   const int piece = blockIdx.x;
@@ -276,7 +221,6 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
     n0 = static_cast<int>(static_cast<int64_t>(rank) * start.units / size);
     n1 = static_cast<int>(static_cast<int64_t>(rank + 1) * start.units / size);
     start.unit = n0;
-    __syncthreads();
   } else {
     // Units before each sequence.
     if (tid == 0) s_units[0] = 0;
@@ -343,67 +287,97 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
     }
   };
 
-  // ---------------- copies ----------------
-  // The unit that this warp sends for next: its number in the piece, and a lane's block id of it.
-  int ahead = warp, ahead_id = 0, ahead_blocks = 0;
-  Walk far{};
-  auto look_up = [&] {
-    const int first = far.unit * nb;
-    ahead_blocks = min(nb, ((kCluster ? pair.tokens : s_tokens[far.b]) + kBlockTokens - 1) / kBlockTokens - first);
-    if (lane < ahead_blocks) ahead_id = __ldg(p.block_tables + static_cast<int64_t>(far.b) * p.max_blocks_per_seq + first + lane);
+  const int head_of = warp & (hc - 1), place_of = warp / hc;  // (hc is a power of two); of a unit's blocks place_of kTurns ..
+
+  // ---------------- copies: the piece's tiles of this warp, kStages of them ahead ----------------
+  // Block ids come in windows of 32 tiles of a pair, one a lane; the window behind the current one is on its way.
+  constexpr int kWindow = 32 / T::kTurns;  // units
+  struct Window {
+    Walk x;   // its first unit
+    int n;    // that one's number in the stream
   };
-  auto send = [&] {
-    const int stage = ahead % kStages;
-    const uint32_t bar = full + 8 * stage;
-    if (lane == 0) bar_expect_tx(bar, static_cast<uint32_t>(ahead_blocks * hc * (2 * T::kTile + 2 * kBlockTokens)));
-    __syncwarp();
-    if (lane < ahead_blocks) {
-      if (ahead_id < 0 || ahead_id >= p.num_blocks) {
-        atomicOr(p.err, kErrBlockId);
-        ahead_id = 0;
+  auto ids_of = [&](const Window& w) -> int {  // -1: no tile
+    const int unit = w.x.unit + lane / T::kTurns, block = unit * nb + place_of * T::kTurns + lane % T::kTurns;
+    if (w.n >= n1 || unit >= w.x.units || block * kBlockTokens >= (kCluster ? pair.tokens : s_tokens[w.x.b])) return -1;
+    const int id = __ldg(p.block_tables + static_cast<int64_t>(w.x.b) * p.max_blocks_per_seq + block);
+    if (id >= 0 && id < p.num_blocks) return id;
+    atomicOr(p.err, kErrBlockId);
+    return 0;
+  };
+  auto tiles_of = [&](const Window& w) -> int { return min(kWindow, min(w.x.units - w.x.unit, n1 - w.n)) * T::kTurns; };
+  auto behind = [&](Window w) {
+    const int units = min(kWindow, w.x.units - w.x.unit);
+    w.n += units;
+    if (w.n < n1) {
+      w.x.unit += units;
+      carry(w.x);
+      if (warp == 0 && w.x.unit == 0) {  // a pair's queries are on their way to L2 early
+        const Rows r = rows_of(p, w.x.b);
+        const int heads = hc * (p.num_q_heads / p.num_kv_heads);
+        for (int i = lane; i < r.count; i += 32)
+          l2_prefetch(static_cast<const __nv_bfloat16*>(p.q) +
+                          (static_cast<int64_t>(r.first + i) * p.num_q_heads + w.x.heads * heads) * D,
+                      heads * D * 2);
       }
-      const int tile = ahead_id * p.num_kv_heads + far.heads * hc;
-      const uint32_t dst = base + stage * T::kStage + lane * hc * T::kTile;
-      tensor_load(dst, &map_k, tile * (T::kTile / 128), bar);
-      tensor_load(dst + T::kOffV, &map_v, tile * (T::kTile / 128), bar);
-      bulk_load(base + T::kOffScales + stage * T::kScales + lane * hc * 2 * kBlockTokens,
-                p.kv_scales + static_cast<int64_t>(tile) * 2 * kBlockTokens, hc * 2 * kBlockTokens, bar);
     }
-    if (far.unit == 0 || ahead == 0) {  // a pair's queries are on their way to L2 while its first unit is
-      const Rows r = rows_of(p, far.b);
-      const int heads = hc * (p.num_q_heads / p.num_kv_heads);
-      for (int i = lane; i < r.count; i += 32)
-        l2_prefetch(static_cast<const __nv_bfloat16*>(p.q) +
-                        (static_cast<int64_t>(r.first + i) * p.num_q_heads + far.heads * heads) * D,
-                    heads * D * 2);
-    }
-    ahead += kWarps;
-    if (ahead < n1 - n0) {
-      far.unit += kWarps;
-      carry(far);
-      look_up();
-    }
+    return w;
   };
-  if (n0 + warp < n1) {
-    far = walk_to(n0 + warp);
-    look_up();
-    while (ahead < kStages && ahead < n1 - n0) send();
+  Window window{}, next{};
+  int ids = -1, next_ids = -1, sent = 0, tiles = 0;  // of the window: tiles sent for, and all
+  int to = 0;                                        // ring place of the next tile
+  // A lane's 16-byte pieces of a tile: line i 4 + lane / 8 of 128 bytes, chunk lane % 8 of it, swizzled by the line.
+  const uint32_t ring = base + warp * T::kStages * T::kStage, scales = base + T::kOffScales + warp * T::kStages * T::kScales;
+  const uint32_t copy_even = (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4), copy_odd = copy_even ^ 64;
+  auto send = [&] {
+    if (tiles > 0) {
+      const int id = __shfl_sync(kAll, ids, sent);
+      if (id >= 0) {
+        const int64_t tile = static_cast<int64_t>(id) * p.num_kv_heads + window.x.heads * hc + head_of;
+        const uint8_t *k = p.k_cache + tile * T::kTile + lane * 16, *v = p.v_cache + tile * T::kTile + lane * 16;
+        const uint32_t dst = ring + to * T::kStage;
+#pragma unroll
+        for (int i = 0; i < T::kTile / 512; ++i) {
+          copy_16(dst + i * 512 + (i & 1 ? copy_odd : copy_even), k + i * 512);
+          copy_16(dst + T::kTile + i * 512 + (i & 1 ? copy_odd : copy_even), v + i * 512);
+        }
+        if (lane < 2) copy_16(scales + to * T::kScales + lane * 16, p.kv_scales + tile * 2 * kBlockTokens + lane * 16);
+      }
+      if (++sent == tiles) {
+        window = next;
+        ids = next_ids;
+        sent = 0;
+        tiles = window.n < n1 ? tiles_of(window) : 0;
+        if (tiles > 0) {
+          next = behind(window);
+          next_ids = ids_of(next);
+        }
+      }
+    }
+    copies_commit();  // (a group a call, whether or not there was a tile)
+    if (++to == T::kStages) to = 0;
+  };
+  Walk at = start;
+  if (n0 < n1) {
+    at = walk_to(n0);
+    window = {at, n0};
+    ids = ids_of(window);
+    tiles = tiles_of(window);
+    next = behind(window);
+    next_ids = ids_of(next);
   }
-  Walk at = walk_to(n0);
+#pragma unroll 1
+  for (int k = 0; k < T::kStages; ++k) send();
 
   // ---------------- products (a tile of every unit a warp, or kTurns) ----------------
   const int g = lane >> 2, t = lane & 3;      // fragments: row g and columns 2t, 2t + 1 of an accumulator
-  const int head_of = warp & (hc - 1), place_of = warp / hc;  // (hc is a power of two); of a unit's blocks place_of kTurns ..
   const int group = p.num_q_heads / p.num_kv_heads, group_bits = 31 - __clz(group);
   // ldmatrix: lane i gives the address of row i % 8 of matrix i / 8; matrices 0, 1: tokens 0..7 and 8..15 of a chunk,
   // 2, 3: of the next chunk.  A tile is lines of 128 bytes, swizzled: chunk c of line y lies at c ^ (y % 8) (two tokens of 64
   // dims share a line).  Two chunks on are 32 bytes on, through the swizzle an exclusive or.
   const int ld_row = (lane & 7) + ((lane >> 3) & 1) * 8;
   const int ld_line = ld_row * D / 128, ld_chunk = (D == 128 ? 0 : (ld_row & 1) * 4) + (lane >> 4);
-  const uint32_t ld_at = base + (place_of * T::kTurns * hc + head_of) * T::kTile + ld_line * 128 + ((ld_chunk ^ (ld_line & 7)) << 4);
-  bool failed = false;
+  const uint32_t ld_at = ring + ld_line * 128 + ((ld_chunk ^ (ld_line & 7)) << 4);
   int stage = 0;
-  uint32_t use = 0;  // parity of the stage's next copy
 
   // The piece's pairs of sequence and heads; a cluster's one, of which a CTA may have no unit.
   for (int n = n0; kCluster || n < n1;) {
@@ -462,17 +436,14 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
 
     int first_token = (at.unit * nb + place_of * T::kTurns) * kBlockTokens;  // of this warp's blocks
     for (int u = 0; u < count; ++u, first_token += nb * kBlockTokens) {
-      if (!failed && !bar_wait(full + 8 * stage, use)) {
-        failed = true;
-        if (lane == 0) atomicOr(p.err, kErrTimeout);
-      }
 #pragma unroll
       for (int turn = 0; turn < T::kTurns; ++turn) {
         const int token0 = first_token + turn * kBlockTokens;
-        if (failed || token0 >= rows.tokens) continue;
-        const uint32_t sk = ld_at + stage * T::kStage + turn * hc * T::kTile;
-        const unsigned char* sc = smem + T::kOffScales + stage * T::kScales +
-                                  ((place_of * T::kTurns + turn) * hc + head_of) * 2 * kBlockTokens;
+        copies_wait<T::kStages - 1>();
+        __syncwarp();
+        if (token0 < rows.tokens) {
+        const uint32_t sk = ld_at + stage * T::kStage;
+        const unsigned char* sc = smem + T::kOffScales + (warp * T::kStages + stage) * T::kScales;
         // S^T = Kc q^T.  Chunk c of a row: its 16 codes are the product's depth, in the order 4t, 4t + 1, 4t + 2, 4t + 3 of
         // a lane's four, as q's fragments are.
         float s[NC][4], s2[NC][4];
@@ -565,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
 #pragma unroll
         for (int c = 0; c < kSteps / 2; ++c) {
           uint32_t x[4], a[4][2];
-          ldsm_x4_t((sk ^ (32u * c)) + T::kOffV, x);
+          ldsm_x4_t((sk ^ (32u * c)) + T::kTile, x);
           if (masked) {
             x[0] &= keep_lo;
             x[1] &= keep_hi;
@@ -585,19 +556,9 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) bar_arrive(empty + 8 * stage);
-      const int k = n - n0 + u;
-      if (k + kStages == ahead && ahead < n1 - n0) {  // this warp's turn, when all have done with the stage
-        if (!failed && !bar_wait(empty + 8 * stage, use)) {
-          failed = true;
-          if (lane == 0) atomicOr(p.err, kErrTimeout);
-        }
-        if (!failed) send();
-      }
-      if (++stage == kStages) {
-        stage = 0;
-        use ^= 1;
+        __syncwarp();  // the tile has been read
+        send();
+        if (++stage == T::kStages) stage = 0;
       }
     }
 
@@ -670,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
         if (started) record[0] = piece * 2 + slot;
         if (ended) record[1] = piece;
       }
-      if (place_of == 0 && !failed) {
+      if (place_of == 0) {
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
@@ -698,8 +659,10 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
       at.unit += count;
       if (n < n1) carry(at);
     } else {
-      // The CTA's state, in the ring (done with, by all warps: they have joined); then every CTA of the cluster forms its
-      // share of the outputs from all states.
+      copies_wait<0>();
+      __syncthreads();
+      // The CTA's state, in the rings (done with); then every CTA of the cluster forms its share of the outputs from all
+      // states.
       float* s_o = reinterpret_cast<float*>(smem);
       float2* s_state = reinterpret_cast<float2*>(smem + T::kCols * D * 4);
       if (warp == 0) {
@@ -751,9 +714,6 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
       break;
     }
   }
-  if (failed)  // what this warp sent for lands before the CTA exits
-    for (int k = ahead - kWarps; k >= 0 && k >= ahead - kWarps - kStages; k -= kWarps)
-      bar_wait(full + 8 * (k % kStages), (k / kStages) & 1);
 }
 
 // Joins the states of every pair that a piece's border cuts: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s; zeros for a
