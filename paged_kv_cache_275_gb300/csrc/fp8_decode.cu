@@ -92,7 +92,7 @@ struct Instance {
     if (e != cudaSuccess) return e;
     const unsigned cols = p.state_rows;
     // Few pairs have many states each.
-    if (pairs * cols <= 1216) return launch_pdl(join_fp8_kernel<D, 8>, dim3(pairs, cols), dim3(256), 0, stream, p);
+    if (pairs * cols <= 1216) return launch_pdl(join_fp8_kernel<D, 16>, dim3(pairs, cols), dim3(512), 0, stream, p);
     return launch_pdl(join_fp8_kernel<D, 1>, dim3(pairs, (cols + 3) / 4), dim3(128), 0, stream, p);
   }
 };

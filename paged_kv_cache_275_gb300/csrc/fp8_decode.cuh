@@ -27,8 +27,8 @@
 // states (m, l, O) that a second kernel joins.
 //
 // Few pairs.  A call of few (sequence, kv head) pairs takes a thread-block cluster a pair instead: its units, of one head, are
-// dealt to the cluster's CTAs, whose states are joined through distributed shared memory.  One launch, no workspace, and no
-// pass over the batch's lengths.
+// dealt to the cluster's CTAs in turns (so that their block ids can be asked for along with the length), whose states are
+// joined through distributed shared memory.  One launch, no workspace, and no pass over the batch's lengths.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -66,7 +66,7 @@ struct Few {
   static constexpr int kOffExchange = kOffScales + kWarps * kStages * kScales;
   static constexpr int kExchange = kWarps / 2 * 32 * 32;  // 8 values a lane of four warps
   static constexpr int kOffMl = kOffExchange + kExchange;
-  static constexpr int kMl = kWarps / 2 * kCols * 8;
+  static constexpr int kMl = (kWarps + 1) * kCols * 8;  // a cluster CTA's: of every warp, and joined
   static constexpr int kOffSeq = kOffMl + kMl;  // units before each sequence, [num_seqs + 1]; tokens, [num_seqs]
   static constexpr int smem(int num_seqs) { return kOffSeq + (2 * num_seqs + 1) * 4; }
 };
@@ -193,6 +193,7 @@ template <int D, int NC, bool kCluster>
 __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
     few_rows_fp8_kernel(const Fp8AttentionParams p) {
   using T = Few<D, NC>;
+  constexpr int kTurns = T::kTurns;
   constexpr int kSteps = D / 16;  // 16-byte chunks of a row of codes: 16 dims, the depth of a product
   extern __shared__ __align__(128) unsigned char smem[];
   const uint32_t base = saddr(smem);
@@ -205,22 +206,19 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
   pdl_trigger();
   pdl_wait();
 
+  const int head_of = warp & (hc - 1), place_of = warp / hc;  // (hc is a power of two); of a unit's blocks place_of kTurns ..
+
+  // This CTA's units are numbers n0 .. n1 - 1 of the stream; of a cluster's pair, its rank and every stride-th from there on.
   const int piece = blockIdx.x;
-  int n0, n1;     // this CTA's units: of the stream, or of the cluster's pair
-  Rows pair{};    // a cluster's rows
-  Walk start{};   // unit n0
+  int n0 = 0, n1 = 0, stride = 1;
+  Rows pair{};
+  Walk at{};  // unit n0
   if constexpr (kCluster) {
-    const uint32_t size = cluster_size(), rank = cluster_rank();
-    const int at = static_cast<int>(blockIdx.x / size);
-    start.b = at / head_groups;
-    start.heads = at - start.b * head_groups;
-    pair = rows_of(p, start.b);
-    if (pair.wrong && rank == 0 && start.heads == 0 && tid == 0) atomicOr(p.err, pair.wrong);
-    if (pair.count == 0) return;  // (the whole cluster)
-    start.units = ((pair.tokens + kBlockTokens - 1) / kBlockTokens + nb - 1) / nb;
-    n0 = static_cast<int>(static_cast<int64_t>(rank) * start.units / size);
-    n1 = static_cast<int>(static_cast<int64_t>(rank + 1) * start.units / size);
-    start.unit = n0;
+    stride = static_cast<int>(cluster_size());
+    const int number = static_cast<int>(blockIdx.x) / stride;
+    at.b = number / head_groups;
+    at.heads = number - at.b * head_groups;
+    at.unit = static_cast<int>(cluster_rank());
   } else {
     // Units before each sequence.
     if (tid == 0) s_units[0] = 0;
@@ -252,28 +250,18 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
     if (piece >= pieces) return;
     n0 = static_cast<int>(static_cast<int64_t>(piece) * total / pieces);
     n1 = static_cast<int>(static_cast<int64_t>(piece + 1) * total / pieces);
-  }
-  // Unit n of the stream (there is one).
-  auto walk_to = [&](int n) {
-    Walk x = start;
-    if constexpr (kCluster) {
-      x.unit = n;
-      return x;
-    }
-    int lo = 0, hi = p.num_seqs - 1;  // its sequence: the last with units before it at or below
-    const int of_group = n / head_groups;
+    int lo = 0, hi = p.num_seqs - 1;  // unit n0's sequence: the last with units before it at or below
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (s_units[mid] <= of_group) lo = mid;
+      if (s_units[mid] <= n0 / head_groups) lo = mid;
       else hi = mid - 1;
     }
-    x.b = lo;
-    x.units = s_units[lo + 1] - s_units[lo];
-    const int rest = n - s_units[lo] * head_groups;
-    x.heads = rest / x.units;
-    x.unit = rest - x.heads * x.units;
-    return x;
-  };
+    at.b = lo;
+    at.units = s_units[lo + 1] - s_units[lo];
+    const int rest = n0 - s_units[lo] * head_groups;
+    at.heads = rest / at.units;
+    at.unit = rest - at.heads * at.units;
+  }
   // On to the pair that unit x.unit, past its own pair's end, lies in (there is one).
   auto carry = [&](Walk& x) {
     while (!kCluster && x.unit >= x.units) {
@@ -287,31 +275,54 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
     }
   };
 
-  const int head_of = warp & (hc - 1), place_of = warp / hc;  // (hc is a power of two); of a unit's blocks place_of kTurns ..
-
   // ---------------- copies: the piece's tiles of this warp, kStages of them ahead ----------------
   // Block ids come in windows of 32 tiles of a pair, one a lane; the window behind the current one is on its way.
-  constexpr int kWindow = 32 / T::kTurns;  // units
+  constexpr int kWindow = 32 / kTurns;  // units
   struct Window {
-    Walk x;   // its first unit
-    int n;    // that one's number in the stream
+    Walk x;  // its first unit
+    int n;   // that one's number in the stream
   };
-  auto ids_of = [&](const Window& w) -> int {  // -1: no tile
-    const int unit = w.x.unit + lane / T::kTurns, block = unit * nb + place_of * T::kTurns + lane % T::kTurns;
-    if (w.n >= n1 || unit >= w.x.units || block * kBlockTokens >= (kCluster ? pair.tokens : s_tokens[w.x.b])) return -1;
-    const int id = __ldg(p.block_tables + static_cast<int64_t>(w.x.b) * p.max_blocks_per_seq + block);
+  auto block_at = [&](const Window& w) -> int {  // of this lane's tile
+    return (w.x.unit + lane / kTurns * stride) * nb + place_of * kTurns + lane % kTurns;
+  };
+  auto id_at = [&](const Window& w, int block) -> int {
+    return __ldg(p.block_tables + static_cast<int64_t>(w.x.b) * p.max_blocks_per_seq + block);
+  };
+  auto checked = [&](int id) -> int {
     if (id >= 0 && id < p.num_blocks) return id;
     atomicOr(p.err, kErrBlockId);
     return 0;
   };
-  auto tiles_of = [&](const Window& w) -> int { return min(kWindow, min(w.x.units - w.x.unit, n1 - w.n)) * T::kTurns; };
+  Window window{at, n0}, next{};
+  int ids = -1, next_ids = -1;  // -1: no tile
+  int asked = 0;
+  if constexpr (kCluster) {  // the first window's ids are asked for before the length is known
+    const int block = block_at(window);
+    if (block < p.max_blocks_per_seq) asked = id_at(window, block);
+    pair = rows_of(p, at.b);
+    if (pair.wrong && at.unit == 0 && at.heads == 0 && tid == 0) atomicOr(p.err, pair.wrong);
+    if (pair.count == 0) return;  // (the whole cluster)
+    at.units = ((pair.tokens + kBlockTokens - 1) / kBlockTokens + nb - 1) / nb;
+    window.x.units = at.units;
+    n1 = at.unit < at.units ? (at.units - at.unit + stride - 1) / stride : 0;
+    if (n1 > 0 && block * kBlockTokens < pair.tokens) ids = checked(asked);
+  }
+  auto ids_of = [&](const Window& w) -> int {
+    const int block = block_at(w);
+    const bool in_pair = kCluster || w.x.unit + lane / kTurns < w.x.units;
+    if (w.n >= n1 || !in_pair || block * kBlockTokens >= (kCluster ? pair.tokens : s_tokens[w.x.b])) return -1;
+    return checked(id_at(w, block));
+  };
+  auto units_of = [&](const Window& w) -> int {  // up to the pair's end and the piece's
+    return max(0, min(kWindow, min(kCluster ? kWindow : w.x.units - w.x.unit, n1 - w.n)));
+  };
   auto behind = [&](Window w) {
-    const int units = min(kWindow, w.x.units - w.x.unit);
+    const int units = kCluster ? kWindow : min(kWindow, w.x.units - w.x.unit);
     w.n += units;
     if (w.n < n1) {
-      w.x.unit += units;
+      w.x.unit += units * stride;
       carry(w.x);
-      if (warp == 0 && w.x.unit == 0) {  // a pair's queries are on their way to L2 early
+      if (!kCluster && warp == 0 && w.x.unit == 0) {  // a pair's queries are on their way to L2 early
         const Rows r = rows_of(p, w.x.b);
         const int heads = hc * (p.num_q_heads / p.num_kv_heads);
         for (int i = lane; i < r.count; i += 32)
@@ -322,9 +333,14 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
     }
     return w;
   };
-  Window window{}, next{};
-  int ids = -1, next_ids = -1, sent = 0, tiles = 0;  // of the window: tiles sent for, and all
-  int to = 0;                                        // ring place of the next tile
+  auto tiles_of = [&](const Window& w) -> int { return units_of(w) * kTurns; };
+  if (!kCluster && n0 < n1) ids = ids_of(window);
+  int sent = 0, tiles = tiles_of(window);  // of the window: tiles sent for, and all
+  if (tiles > 0) {
+    next = behind(window);
+    next_ids = ids_of(next);
+  }
+  int to = 0;  // ring place of the next tile
   // A lane's 16-byte pieces of a tile: line i 4 + lane / 8 of 128 bytes, chunk lane % 8 of it, swizzled by the line.
   const uint32_t ring = base + warp * T::kStages * T::kStage, scales = base + T::kOffScales + warp * T::kStages * T::kScales;
   const uint32_t copy_even = (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4), copy_odd = copy_even ^ 64;
@@ -346,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
         window = next;
         ids = next_ids;
         sent = 0;
-        tiles = window.n < n1 ? tiles_of(window) : 0;
+        tiles = tiles_of(window);
         if (tiles > 0) {
           next = behind(window);
           next_ids = ids_of(next);
@@ -356,15 +372,6 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
     copies_commit();  // (a group a call, whether or not there was a tile)
     if (++to == T::kStages) to = 0;
   };
-  Walk at = start;
-  if (n0 < n1) {
-    at = walk_to(n0);
-    window = {at, n0};
-    ids = ids_of(window);
-    tiles = tiles_of(window);
-    next = behind(window);
-    next_ids = ids_of(next);
-  }
 #pragma unroll 1
   for (int k = 0; k < T::kStages; ++k) send();
 
@@ -380,12 +387,11 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
   int stage = 0;
 
   // The piece's pairs of sequence and heads; a cluster's one, of which a CTA may have no unit.
-  for (int n = n0; kCluster || n < n1;) {
+  for (int n = kCluster ? 0 : n0; kCluster || n < n1;) {
     const Rows rows = kCluster ? pair : rows_of(p, at.b);
     const int kvh = at.heads * hc + head_of;
     const int first_limit = rows.tokens - rows.count + 1;  // tokens that the first row sees
-    const int count = min(at.units - at.unit, n1 - n);      // units of the pair here
-    const bool started = at.unit == 0, ended = at.unit + count == at.units;
+    const int count = kCluster ? n1 : min(at.units - at.unit, n1 - n);  // units of the pair here
     uint32_t q[NC][kSteps][2];  // B fragments of the rows
     float q_scale[NC][2];       // of columns 2t, 2t + 1: what takes a product to a score
     float m[NC][2], r[NC][2], l[NC][2];
@@ -434,16 +440,34 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[c][nc][k] = 0.f;
 
-    int first_token = (at.unit * nb + place_of * T::kTurns) * kBlockTokens;  // of this warp's blocks
-    for (int u = 0; u < count; ++u, first_token += nb * kBlockTokens) {
+    int first_token = (at.unit * nb + place_of * kTurns) * kBlockTokens;  // of this warp's blocks
+    for (int u = 0; u < count; ++u, first_token += stride * nb * kBlockTokens) {
 #pragma unroll
-      for (int turn = 0; turn < T::kTurns; ++turn) {
+      for (int turn = 0; turn < kTurns; ++turn) {
         const int token0 = first_token + turn * kBlockTokens;
         copies_wait<T::kStages - 1>();
         __syncwarp();
-        if (token0 < rows.tokens) {
         const uint32_t sk = ld_at + stage * T::kStage;
         const unsigned char* sc = smem + T::kOffScales + (warp * T::kStages + stage) * T::kScales;
+        if (++stage == T::kStages) stage = 0;
+        if (token0 >= rows.tokens) {
+          send();
+          continue;
+        }
+        // With few tiles a warp it is their latency that counts: V's codes, too, are taken into registers first, and the tile's
+        // place is free for the next copies.  With many it is registers (V's codes first: 128 sequences 107 -> 110 us, drafts
+        // of up to five tokens 106 -> 128; one sequence 10.2 -> 8.9).
+        constexpr bool kEarly = kCluster;
+        const float k_lo = fp8_scale(sc[g]), k_hi = fp8_scale(sc[g + 8]);
+        const float v_lo = static_cast<float>(static_cast<int>(sc[16 + g]) - 127);
+        const float v_hi = static_cast<float>(static_cast<int>(sc[24 + g]) - 127);
+        uint32_t kx[kSteps / 2][4], vx[kSteps / 2][4];
+        if constexpr (kEarly) {
+#pragma unroll
+          for (int c = 0; c < kSteps / 2; ++c) ldsm_x4(sk ^ (32u * c), kx[c]);
+#pragma unroll
+          for (int c = 0; c < kSteps / 2; ++c) ldsm_x4_t((sk ^ (32u * c)) + T::kTile, vx[c]);
+        }
         // S^T = Kc q^T.  Chunk c of a row: its 16 codes are the product's depth, in the order 4t, 4t + 1, 4t + 2, 4t + 3 of
         // a lane's four, as q's fragments are.
         float s[NC][4], s2[NC][4];
@@ -453,12 +477,12 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
           for (int k = 0; k < 4; ++k) s[nc][k] = s2[nc][k] = 0.f;
 #pragma unroll
         for (int c = 0; c < kSteps / 2; ++c) {
-          uint32_t x[4], a[4][2];
-          ldsm_x4(sk ^ (32u * c), x);
+          uint32_t a[4][2];
+          if constexpr (!kEarly) ldsm_x4(sk ^ (32u * c), kx[c]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            a[k][0] = fp8_halves(static_cast<uint16_t>(x[k]));
-            a[k][1] = fp8_halves(static_cast<uint16_t>(x[k] >> 16));
+            a[k][0] = fp8_halves(static_cast<uint16_t>(kx[c][k]));
+            a[k][1] = fp8_halves(static_cast<uint16_t>(kx[c][k] >> 16));
           }
 #pragma unroll
           for (int nc = 0; nc < NC; ++nc) {
@@ -466,15 +490,17 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
             mma_f16(s2[nc], a[2][0], a[3][0], a[2][1], a[3][1], q[nc][2 * c + 1][0], q[nc][2 * c + 1][1]);
           }
         }
-        const float k_lo = fp8_scale(sc[g]), k_hi = fp8_scale(sc[g + 8]);
-        const float v_lo = static_cast<float>(static_cast<int>(sc[16 + g]) - 127);
-        const float v_hi = static_cast<float>(static_cast<int>(sc[24 + g]) - 127);
+        if constexpr (kEarly) {
+          __syncwarp();  // the tile has been read
+          send();
+        }
         const bool masked = token0 + kBlockTokens > first_limit;
         bool raise = false;
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) s[nc][k] = (s[nc][k] + s2[nc][k]) * q_scale[nc][k & 1] * (k < 2 ? k_lo : k_hi);
+          for (int k = 0; k < 4; ++k)
+            s[nc][k] = (s[nc][k] + s2[nc][k]) * (q_scale[nc][k & 1] * (k < 2 ? k_lo : k_hi));
           if (masked) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -519,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
           for (int k = 0; k < 4; ++k) {
             const float d = s[nc][k] - m[nc][k & 1];
             l[nc][k & 1] += ex2(d);
-            wt[k] = ex2(d + (k < 2 ? v_lo : v_hi) - r[nc][k & 1] + kWeightShift);
+            wt[k] = ex2(d + ((k < 2 ? v_lo : v_hi) - r[nc][k & 1] + kWeightShift));
           }
           w[nc][0] = transpose8(pack_f16(wt[0], wt[1]));
           w[nc][1] = transpose8(pack_f16(wt[2], wt[3]));
@@ -535,17 +561,11 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
         // the product, dims 2g + 1 rows g + 8.
 #pragma unroll
         for (int c = 0; c < kSteps / 2; ++c) {
-          uint32_t x[4], a[4][2];
-          ldsm_x4_t((sk ^ (32u * c)) + T::kTile, x);
-          if (masked) {
-            x[0] &= keep_lo;
-            x[1] &= keep_hi;
-            x[2] &= keep_lo;
-            x[3] &= keep_hi;
-          }
+          uint32_t a[4][2];
+          if constexpr (!kEarly) ldsm_x4_t((sk ^ (32u * c)) + T::kTile, vx[c]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint32_t y = __byte_perm(x[k], 0, 0x3120);
+            const uint32_t y = __byte_perm(masked ? vx[c][k] & (k & 1 ? keep_hi : keep_lo) : vx[c][k], 0, 0x3120);
             a[k][0] = fp8_halves(static_cast<uint16_t>(y));
             a[k][1] = fp8_halves(static_cast<uint16_t>(y >> 16));
           }
@@ -555,10 +575,10 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
             mma_f16(o[2 * c + 1][nc], a[2][0], a[2][1], a[3][0], a[3][1], w[nc][0], w[nc][1]);
           }
         }
-      }
-        __syncwarp();  // the tile has been read
-        send();
-        if (++stage == T::kStages) stage = 0;
+        if constexpr (!kEarly) {
+          __syncwarp();
+          send();
+        }
       }
     }
 
@@ -576,56 +596,57 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
           o[c][nc][k + 2] *= f;
         }
       }
-    // The warps of a head join their states, half of them handing theirs to the other half at a time.
-    float4* exchange = reinterpret_cast<float4*>(smem + T::kOffExchange);
-    float2* s_ml = reinterpret_cast<float2*>(smem + T::kOffMl);
-    for (int half = kWarps / hc / 2; half > 0; half >>= 1) {
-      const bool gives = place_of >= half && place_of < 2 * half, takes = place_of < half;
-      const int place = (place_of & (half - 1)) * hc + head_of;
-      float mine[NC][2], other[NC][2];
-      if (gives && g == 0)
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) s_ml[place * T::kCols + nc * 8 + 2 * t + k] = make_float2(m[nc][k], l[nc][k]);
-#pragma unroll
-      for (int part = 0; part < kSteps * NC / 2; ++part) {
-        if (gives)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float(&v)[4] = o[(2 * part + x) / NC][(2 * part + x) % NC];
-            exchange[(place * 2 + x) * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
-          }
-        asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
-        if (takes) {
-          if (part == 0)
-#pragma unroll
-            for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const float2 y = s_ml[place * T::kCols + nc * 8 + 2 * t + k];
-                const float top = fmaxf(m[nc][k], y.x);
-                mine[nc][k] = ex2(m[nc][k] - top);
-                other[nc][k] = ex2(y.x - top);
-                l[nc][k] = l[nc][k] * mine[nc][k] + y.y * other[nc][k];
-                m[nc][k] = top;
-              }
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int nc = (2 * part + x) % NC;
-            float(&v)[4] = o[(2 * part + x) / NC][nc];
-            const float4 y = exchange[(place * 2 + x) * 32 + lane];
-            v[0] = v[0] * mine[nc][0] + y.x * other[nc][0];
-            v[1] = v[1] * mine[nc][1] + y.y * other[nc][1];
-            v[2] = v[2] * mine[nc][0] + y.z * other[nc][0];
-            v[3] = v[3] * mine[nc][1] + y.w * other[nc][1];
-          }
-        }
-        asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
-      }
-    }
     if constexpr (!kCluster) {
-      const int slot = n == n0 ? 0 : 1;
+      // The warps of a head join their states, half of them handing theirs to the other half at a time.
+      float4* exchange = reinterpret_cast<float4*>(smem + T::kOffExchange);
+      float2* s_ml = reinterpret_cast<float2*>(smem + T::kOffMl);
+      for (int half = kWarps / hc / 2; half > 0; half >>= 1) {
+        const bool gives = place_of >= half && place_of < 2 * half, takes = place_of < half;
+        const int place = (place_of & (half - 1)) * hc + head_of;
+        float mine[NC][2], other[NC][2];
+        if (gives && g == 0)
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) s_ml[place * T::kCols + nc * 8 + 2 * t + k] = make_float2(m[nc][k], l[nc][k]);
+#pragma unroll
+        for (int part = 0; part < kSteps * NC / 2; ++part) {
+          if (gives)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float(&v)[4] = o[(2 * part + x) / NC][(2 * part + x) % NC];
+              exchange[(place * 2 + x) * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
+            }
+          asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+          if (takes) {
+            if (part == 0)
+#pragma unroll
+              for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const float2 y = s_ml[place * T::kCols + nc * 8 + 2 * t + k];
+                  const float top = fmaxf(m[nc][k], y.x);
+                  mine[nc][k] = ex2(m[nc][k] - top);
+                  other[nc][k] = ex2(y.x - top);
+                  l[nc][k] = l[nc][k] * mine[nc][k] + y.y * other[nc][k];
+                  m[nc][k] = top;
+                }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int nc = (2 * part + x) % NC;
+              float(&v)[4] = o[(2 * part + x) / NC][nc];
+              const float4 y = exchange[(place * 2 + x) * 32 + lane];
+              v[0] = v[0] * mine[nc][0] + y.x * other[nc][0];
+              v[1] = v[1] * mine[nc][1] + y.y * other[nc][1];
+              v[2] = v[2] * mine[nc][0] + y.z * other[nc][0];
+              v[3] = v[3] * mine[nc][1] + y.w * other[nc][1];
+            }
+          }
+          asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+        }
+      }
+      const bool started = at.unit == 0, ended = at.unit + count == at.units;
+      const int slot = n == n0 ? 0 : 1;  // of the piece's states
       if (warp == 0 && lane == 0) {
         int* record = p.ws_records + 2 * (static_cast<int64_t>(at.b) * head_groups + at.heads);
         if (started) record[0] = piece * 2 + slot;
@@ -659,28 +680,52 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
       at.unit += count;
       if (n < n1) carry(at);
     } else {
+      // The warps' states, each in its own ring (done with), joined to the CTA's.
+      static_assert(T::kCols * D * 4 <= T::kStages * T::kStage, "a warp's state fits its ring");
       copies_wait<0>();
-      __syncthreads();
-      // The CTA's state, in the rings (done with); then every CTA of the cluster forms its share of the outputs from all
-      // states.
       float* s_o = reinterpret_cast<float*>(smem);
-      float2* s_state = reinterpret_cast<float2*>(smem + T::kCols * D * 4);
-      if (warp == 0) {
+      constexpr int kRing = T::kStages * T::kStage / 4;  // floats
+      float2* s_ml = reinterpret_cast<float2*>(smem + T::kOffMl);
+      float2* s_joined = s_ml + kWarps * T::kCols;
 #pragma unroll
-        for (int nc = 0; nc < NC; ++nc)
+      for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int col = nc * 8 + 2 * t + k;
+        for (int k = 0; k < 2; ++k) {
+          const int col = nc * 8 + 2 * t + k;
+          if (col >> group_bits >= rows.count) continue;
 #pragma unroll
-            for (int c = 0; c < kSteps; ++c)
-              *reinterpret_cast<float2*>(s_o + col * D + 16 * c + 2 * g) = make_float2(o[c][nc][k], o[c][nc][k + 2]);
-            if (g == 0) s_state[col] = make_float2(m[nc][k], l[nc][k]);
-          }
+          for (int c = 0; c < kSteps; ++c)
+            *reinterpret_cast<float2*>(s_o + warp * kRing + col * D + 16 * c + 2 * g) = make_float2(o[c][nc][k], o[c][nc][k + 2]);
+          if (g == 0) s_ml[warp * T::kCols + col] = make_float2(m[nc][k], l[nc][k]);
+        }
+      __syncthreads();
+      constexpr int kQuads = D / 4;
+      const int cols = rows.count * group;
+      for (int x = tid; x < cols * kQuads; x += kThreads) {
+        const int dim = x % kQuads * 4, col = x / kQuads;
+        float top = kNone, sum = 0.f;
+#pragma unroll
+        for (int y = 0; y < kWarps; ++y) top = fmaxf(top, s_ml[y * T::kCols + col].x);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int y = 0; y < kWarps; ++y) {
+          const float2 ml = s_ml[y * T::kCols + col];
+          const float by = ex2(ml.x - top);
+          const float4 v = *reinterpret_cast<const float4*>(s_o + y * kRing + col * D + dim);
+          sum += ml.y * by;
+          a.x += v.x * by;
+          a.y += v.y * by;
+          a.z += v.z * by;
+          a.w += v.w * by;
+        }
+        *reinterpret_cast<float4*>(s_o + col * D + dim) = a;  // in place of the first warp's, which only this thread reads
+        if (dim == 0) s_joined[col] = make_float2(top, sum);
       }
+      // Then every CTA of the cluster forms its share of the outputs from the CTAs' states.
       cluster_sync();
-      const int size = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
-      for (int x = rank + size * tid; x < rows.count * group * (D / 4); x += size * kThreads) {
-        const int col = x / (D / 4), dim = x % (D / 4) * 4;
+      const int rank = static_cast<int>(cluster_rank());
+      for (int x = rank + stride * tid; x < cols * kQuads; x += stride * kThreads) {
+        const int col = x / kQuads, dim = x % kQuads * 4;
         float2 ml[kMostCluster];
         float4 v[kMostCluster];
         float top = kNone;
@@ -688,8 +733,8 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
         for (int y = 0; y < kMostCluster; ++y) {
           ml[y] = make_float2(kNone, 0.f);
           v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (y >= size) continue;
-          ml[y] = remote_f2(remote(saddr(s_state + col), y));
+          if (y >= stride) continue;
+          ml[y] = remote_f2(remote(saddr(s_joined + col), y));
           v[y] = remote_f4(remote(saddr(s_o + col * D + dim), y));
         }
 #pragma unroll
@@ -721,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
 // states before it joins any.
 template <int D, int kSlices>
 __global__ void __launch_bounds__(kSlices == 1 ? 128 : kSlices * 32) join_fp8_kernel(const Fp8AttentionParams p) {
-  constexpr int kPer = D / 32, kAhead = 8;
+  constexpr int kPer = D / 32, kAhead = kSlices == 1 ? 8 : 10;
   constexpr int kRows = kSlices == 1 ? 4 : 1;  // rows of a CTA at a time
   __shared__ float2 s_ml[kSlices];
   __shared__ float s_o[kSlices][D];
