@@ -76,17 +76,20 @@ __device__ __forceinline__ uint2 quantise(const uint4& a, float inverse, bool od
 constexpr int kAppendThreads = 128;
 constexpr int kAppendCtas = 16;  // per SM at most; beyond that a warp takes several tokens
 
-// A lane owns the 16-byte chunks c and c + D / 16 of a row, the rotation's two halves, so D / 16 lanes cover a row and a warp
-// 4 (D = 128) or 8 rows at a time.  A warp takes a token, or a part of its rows.
+// A lane owns two 16-byte chunks of a row, so that D / 16 lanes cover it and a warp takes 4 (D = 128) or 8 rows at a time:
+// the chunks c and c + D / 16, the rotation's two halves, or without rotation 2 c and 2 c + 1, whose codes are 16 bytes.
+// A warp takes a token, or a part of its rows, and has kAhead rows a lane in flight, the first while it looks up the slot.
 template <int D, bool kRotary>
 __global__ void __launch_bounds__(kAppendThreads) append_fp8_kernel(const Fp8AppendParams p) {
   pdl_trigger();
   pdl_wait();
+  constexpr int kAhead = kRotary ? 2 : 4;
   constexpr int kLanes = D / 16;  // lanes of a row
   constexpr int kRowsAtOnce = 32 / kLanes;
   constexpr int kChunks = D / 8;  // 16-byte chunks of a bf16 row
   const int lane = threadIdx.x & 31;
   const int c = lane % kLanes, sub = lane / kLanes;
+  const int chunk_a = kRotary ? c : 2 * c, chunk_b = kRotary ? c + kLanes : 2 * c + 1;
   const int rows = p.num_q_heads + 2 * p.num_kv_heads;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kAppendThreads / 32);
   const int64_t items = p.num_tokens * p.parts;
@@ -94,6 +97,23 @@ __global__ void __launch_bounds__(kAppendThreads) append_fp8_kernel(const Fp8App
        item += warps) {
     const int64_t t = item / p.parts;
     const int part = static_cast<int>(item - t * p.parts);
+    const int step = p.parts * kRowsAtOnce;
+    uint4 a[kAhead], b[kAhead];
+    auto fetch = [&](int r0) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int r = r0 + k * step + sub;
+        a[k] = b[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (r >= rows) continue;
+        const int kr = r - p.num_q_heads, vr = kr - p.num_kv_heads;
+        const uint4* src = kr < 0 ? static_cast<const uint4*>(p.q) + t * p.q_stride + r * kChunks
+                           : vr < 0 ? static_cast<const uint4*>(p.k) + t * p.k_stride + kr * kChunks
+                                    : static_cast<const uint4*>(p.v) + t * p.v_stride + vr * kChunks;
+        a[k] = load_once(src + chunk_a);
+        b[k] = load_once(src + chunk_b);
+      }
+    };
+    fetch(part * kRowsAtOnce);
     const int64_t slot = p.slot_mapping[t];
     if (slot < 0) continue;  // padding
     const bool stored = slot < p.num_slots;
@@ -126,76 +146,96 @@ __global__ void __launch_bounds__(kAppendThreads) append_fp8_kernel(const Fp8App
     const int64_t block_head = (slot / kBlockTokens) * p.num_kv_heads;
     const int offset = static_cast<int>(slot % kBlockTokens);
     // The whole warp goes through the rows together (the row's lanes exchange their maxima).
-    for (int r0 = part * kRowsAtOnce; r0 < rows; r0 += p.parts * kRowsAtOnce) {
-      const int r = r0 + sub;
-      const int kr = r - p.num_q_heads, vr = kr - p.num_kv_heads;
-      uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-      if (r < rows) {
-        const uint4* src = kr < 0 ? static_cast<const uint4*>(p.q) + t * p.q_stride + r * kChunks
-                           : vr < 0 ? static_cast<const uint4*>(p.k) + t * p.k_stride + kr * kChunks
-                                    : static_cast<const uint4*>(p.v) + t * p.v_stride + vr * kChunks;
-        a = load_once(src + c);
-        b = load_once(src + c + kLanes);
-        if (kRotary && vr < 0) rotate(a, b, cs, sn);
+    for (int r0 = part * kRowsAtOnce; r0 < rows; r0 += kAhead * step) {
+      if (r0 != part * kRowsAtOnce) fetch(r0);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int r = r0 + k * step + sub;
+        const int kr = r - p.num_q_heads, vr = kr - p.num_kv_heads;
+        if (kRotary && vr < 0) rotate(a[k], b[k], cs, sn);
+        uint32_t top = top_bits(a[k], b[k]);
+        const bool odd = __any_sync(kFull, top >= 0x7f80u);  // some value of the warp's rows is not finite
+        if (odd) top = top_finite_bits(a[k], b[k]);
+#pragma unroll
+        for (int off = 1; off < kLanes; off <<= 1) top = max(top, __shfl_xor_sync(kFull, top, off));
+        if (r >= rows) continue;
         if (kRotary && kr < 0) {
           uint4* dst = static_cast<uint4*>(p.q_out) + t * p.q_out_stride + static_cast<int64_t>(r) * kChunks;
-          dst[c] = a;
-          dst[c + kLanes] = b;
+          dst[chunk_a] = a[k];
+          dst[chunk_b] = b[k];
         }
+        if (kr < 0 || !stored) continue;
+        const uint32_t e = fp8_exponent(top);
+        const float inverse = fp8_inverse(e);
+        const int64_t tile = block_head + (vr < 0 ? kr : vr);
+        uint8_t* dst = (vr < 0 ? p.k_cache : p.v_cache) + (tile * kBlockTokens + offset) * D;
+        const uint2 x = quantise(a[k], inverse, odd), y = quantise(b[k], inverse, odd);
+        if constexpr (kRotary) {
+          *reinterpret_cast<uint2*>(dst + 8 * chunk_a) = x;
+          *reinterpret_cast<uint2*>(dst + 8 * chunk_b) = y;
+        } else {
+          *reinterpret_cast<uint4*>(dst + 8 * chunk_a) = make_uint4(x.x, x.y, y.x, y.y);
+        }
+        if (c == 0) p.kv_scales[(tile * 2 + (vr < 0 ? 0 : 1)) * kBlockTokens + offset] = static_cast<uint8_t>(e);
       }
-      uint32_t top = top_bits(a, b);
-      const bool odd = __any_sync(kFull, top >= 0x7f80u);  // some value of the warp's rows is not finite
-      if (odd) top = top_finite_bits(a, b);
-#pragma unroll
-      for (int off = 1; off < kLanes; off <<= 1) top = max(top, __shfl_xor_sync(kFull, top, off));
-      if (r >= rows || kr < 0 || !stored) continue;
-      const uint32_t e = fp8_exponent(top);
-      const float inverse = fp8_inverse(e);
-      const int64_t tile = block_head + (vr < 0 ? kr : vr);
-      uint8_t* dst = (vr < 0 ? p.k_cache : p.v_cache) + (tile * kBlockTokens + offset) * D;
-      *reinterpret_cast<uint2*>(dst + 8 * c) = quantise(a, inverse, odd);
-      *reinterpret_cast<uint2*>(dst + D / 2 + 8 * c) = quantise(b, inverse, odd);
-      if (c == 0) p.kv_scales[(tile * 2 + (vr < 0 ? 0 : 1)) * kBlockTokens + offset] = static_cast<uint8_t>(e);
     }
   }
 }
 
-// A thread reads 16 codes of a row of K and of V and writes 16 bf16 values of each.
+// A thread reads 8 codes of a row of K and of V, of kGatherTokens tokens at once, and writes 8 bf16 values of each: so the
+// loads and the stores of a warp are whole rows.
+constexpr int kGatherTokens = 4;
 template <int D>
 __global__ void __launch_bounds__(256) gather_fp8_kernel(const Fp8GatherParams p) {
   pdl_trigger();
   pdl_wait();
-  constexpr int kLanes = D / 16;
-  const int per_token = p.num_kv_heads * kLanes;
+  constexpr int kChunks = D / 8;
+  const int per_token = p.num_kv_heads * kChunks;
   const int64_t total = p.num_tokens * per_token;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t idx = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; idx < total; idx += stride) {
-    const int64_t token = idx / per_token;
-    const int rem = static_cast<int>(idx - token * per_token);
-    const int64_t slot = __ldg(p.slot_mapping + token);
-    if (slot < 0) continue;  // padding
-    if (slot >= p.num_slots) {
-      atomicOr(p.err, kErrSlot);
-      continue;
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; first < total; first += kGatherTokens * stride) {
+    int64_t token[kGatherTokens], slot[kGatherTokens];
+    int rem[kGatherTokens];
+#pragma unroll
+    for (int k = 0; k < kGatherTokens; ++k) {
+      const int64_t idx = first + k * stride;
+      token[k] = idx / per_token;
+      rem[k] = static_cast<int>(idx - token[k] * per_token);
+      slot[k] = idx < total ? __ldg(p.slot_mapping + token[k]) : -1;
     }
-    const int head = rem / kLanes, c = rem - head * kLanes;
-    const int64_t tile = (slot / kBlockTokens) * p.num_kv_heads + head;
-    const int offset = static_cast<int>(slot % kBlockTokens);
+    uint2 codes[kGatherTokens][2];
+    uint8_t e[kGatherTokens][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 codes = load_once(reinterpret_cast<const uint4*>((i ? p.v_cache : p.k_cache) +
-                                                                   (tile * kBlockTokens + offset) * D) + c);
-      const float s = fp8_scale(p.kv_scales[(tile * 2 + i) * kBlockTokens + offset]);
-      const uint32_t* w = &codes.x;
-      uint32_t r[8];
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const float2 f = fp8_floats(static_cast<uint16_t>(w[x / 2] >> 16 * (x & 1)));
-        r[x] = narrow(f.x * s, f.y * s);
+    for (int k = 0; k < kGatherTokens; ++k) {
+      if (slot[k] >= p.num_slots) {
+        atomicOr(p.err, kErrSlot);
+        slot[k] = -1;
       }
-      uint4* dst = static_cast<uint4*>(i ? p.v : p.k) + token * (i ? p.v_stride : p.k_stride) + head * (D / 8) + 2 * c;
-      dst[0] = make_uint4(r[0], r[1], r[2], r[3]);
-      dst[1] = make_uint4(r[4], r[5], r[6], r[7]);
+      if (slot[k] < 0) continue;  // padding
+      const int64_t tile = (slot[k] / kBlockTokens) * p.num_kv_heads + rem[k] / kChunks;
+      const int offset = static_cast<int>(slot[k] % kBlockTokens);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint8_t* src = (i ? p.v_cache : p.k_cache) + (tile * kBlockTokens + offset) * D + rem[k] % kChunks * 8;
+        asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(codes[k][i].x), "=r"(codes[k][i].y) : "l"(src) : "memory");
+        e[k][i] = p.kv_scales[(tile * 2 + i) * kBlockTokens + offset];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kGatherTokens; ++k) {
+      if (slot[k] < 0) continue;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float s = fp8_scale(e[k][i]);
+        const uint32_t w[2] = {codes[k][i].x, codes[k][i].y};
+        uint32_t r[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float2 f = fp8_floats(static_cast<uint16_t>(w[x / 2] >> 16 * (x & 1)));
+          r[x] = narrow(f.x * s, f.y * s);
+        }
+        static_cast<uint4*>(i ? p.v : p.k)[token[k] * (i ? p.v_stride : p.k_stride) + rem[k]] = make_uint4(r[0], r[1], r[2], r[3]);
+      }
     }
   }
 }
@@ -254,7 +294,7 @@ cudaError_t launch_append_fp8(const Fp8AppendParams& p, int head_dim, int num_sm
 }
 
 cudaError_t launch_gather_fp8(const Fp8GatherParams& p, int head_dim, int num_sms, cudaStream_t stream) {
-  const int64_t total = p.num_tokens * p.num_kv_heads * (head_dim / 16);
+  const int64_t total = p.num_tokens * p.num_kv_heads * (head_dim / 8);
   int64_t blocks = (total + 255) / 256;
   const int64_t cap = static_cast<int64_t>(num_sms) * 8;
   if (blocks > cap) blocks = cap;

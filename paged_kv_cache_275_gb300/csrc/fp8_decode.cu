@@ -4,12 +4,16 @@
 namespace pkv {
 namespace {
 
-// Which form a call takes: clusters if all of its pairs' run at once and they are expected to be done before the stream
-// form, by what each takes more of: a cluster CTA's units one after the other, or the second launch and the pass over the
-// lengths, and the bytes over the whole GPU.
-constexpr float kClusterUnitUs = 0.5f;
-constexpr float kStreamUs = 5.f;
-constexpr float kStreamBytesPerUs = 6.5e6f;
+// Which form a call takes: clusters if those of all its pairs run at once and are expected to be done before the stream form.
+// Microseconds a call, measured (32 q and 8 kv heads of 128 dims, sequences of half a length to all of it; stream, clusters):
+//   1 x 128 8.4, 5.0; 1 x 8192 13.9, 13.4; 1 x 32768 23, 38; 8 x 2048 15.7, 9.9; 8 x 8192 29, 25; 32 x 2048 30, 25; 32 x 8192
+//   76, 81; of one kv head 16 x 8192 15.8, 14.0 and 16 x 32768 29, 38.
+// A cluster's units come one after the other; the stream form has a second launch and a pass over the lengths; and either takes
+// the bytes' time, of a batch whose tables are filled to three quarters.
+constexpr float kClusterUs = 4.6f, kStreamUs = 10.5f;
+constexpr float kBytesPerUs = 7.0e6f, kFilled = 0.75f;
+template <int D, int NC>
+constexpr float kClusterUnitUs = (D == 128 ? 1.05f : 1.4f) + 0.4f * (NC - 1);
 
 template <int D, int NC>
 struct Instance {
@@ -72,8 +76,10 @@ struct Instance {
     const int units = (max_blocks_per_seq + Few<D, NC>::kUnitTiles - 1) / Few<D, NC>::kUnitTiles;
     int k = 0;
     while (k < 3 && (1 << k) < units && pairs <= counts[k + 1]) ++k;
-    const float mine = kClusterUnitUs * ((units + (1 << k) - 1) >> k);
-    const float other = kStreamUs + static_cast<float>(pairs) * units * (2.f * Few<D, NC>::kUnitTiles * Few<D, NC>::kTile) / kStreamBytesPerUs;
+    const float bytes_us =
+        kFilled / kBytesPerUs * static_cast<float>(pairs) * units * (2.f * Few<D, NC>::kUnitTiles * Few<D, NC>::kTile);
+    const float units_us = kClusterUnitUs<D, NC> * ((units + (1 << k) - 1) >> k);
+    const float mine = kClusterUs + (units_us > bytes_us ? units_us : bytes_us), other = kStreamUs + bytes_us;
     *ctas = pairs <= counts[k] && mine <= other ? 1 << k : 0;
     return cudaSuccess;
   }
@@ -91,8 +97,10 @@ struct Instance {
     e = launch_pdl(kStream, dim3(p.num_pieces), dim3(kThreads), Few<D, NC>::smem(p.num_seqs), stream, p);
     if (e != cudaSuccess) return e;
     const unsigned cols = p.state_rows;
-    // Few pairs have many states each.
-    if (pairs * cols <= 1216) return launch_pdl(join_fp8_kernel<D, 16>, dim3(pairs, cols), dim3(512), 0, stream, p);
+    // A pair has about as many states as pieces come to it.  Up to twice the eight that a warp fetches at once it takes them
+    // alone.
+    if (p.num_pieces > 16 * p.num_seqs * (p.num_kv_heads / p.unit_heads))
+      return launch_pdl(join_fp8_kernel<D, 16>, dim3(pairs, cols), dim3(512), 0, stream, p);
     return launch_pdl(join_fp8_kernel<D, 1>, dim3(pairs, (cols + 3) / 4), dim3(128), 0, stream, p);
   }
 };

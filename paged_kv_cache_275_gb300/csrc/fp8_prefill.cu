@@ -498,62 +498,78 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
 }
 
 // Merge of a split call: for every row, over the splits whose m is finite, M = max m_s and out = sum_s 2^(m_s - M) O_s /
-// sum_s 2^(m_s - M) l_s.  A warp takes a (chunk token, q head) row at a time, lane s the (m, l) of split s.
+// sum_s 2^(m_s - M) l_s.  A warp takes kMergeRows (chunk token, q head) rows at a time, lane s the (m, l) of split s.  It is
+// latency that counts: the first kFirst splits' O are requested before their (m, l) say which of them saw a key.
+constexpr int kMergeRows = 2;
 template <int D>
 __global__ void __launch_bounds__(256) merge_fp8_kernel(const Fp8PrefillParams p) {
-  constexpr int kCols = D / 32, kAhead = 8;
+  constexpr int kCols = D / 32, kFirst = 8;
   const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   pdl_wait();
   const int q0 = p.query_start[b], q1 = p.query_start[b + 1], len = p.context_lens[b];
   const int64_t chunk = static_cast<int64_t>(q1) - q0;
-  if (chunk < 0 || len < chunk || len > p.max_blocks_per_seq * kBlockTokens || q0 < 0 || q1 > p.query_rows) return;
-  const int rows = min(static_cast<int>(chunk), p.max_query_len) * p.num_q_heads;
   const size_t stride = static_cast<size_t>(p.num_seqs) * p.ws_rows * p.num_q_heads;  // rows of a split
   const float2* ml = reinterpret_cast<const float2*>(p.ws + static_cast<size_t>(p.num_splits) * stride * D);
-  for (int row = blockIdx.x * 8 + warp; row < rows; row += gridDim.x * 8) {
-    const size_t r0 = static_cast<size_t>(b) * p.ws_rows * p.num_q_heads + row;
-    float2 s = make_float2(-INFINITY, 0.f);
-    if (lane < p.num_splits) s = ml[lane * stride + r0];
-    float mx = s.x;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    const float w = s.x == -INFINITY ? 0.f : exp2f(s.x - mx);
-    float den = w * s.y;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
-    const float inv = den != 0.f ? 1.f / den : 0.f;
-    float acc[kCols];
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
-    for (int s0 = 0; s0 < p.num_splits; s0 += kAhead) {
-      float v[kAhead][kCols], ws[kAhead];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        ws[k] = __shfl_sync(0xffffffffu, w, (s0 + k) & 31);
-        if (s0 + k >= p.num_splits) ws[k] = 0.f;
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) v[k][c] = 0.f;
-        if (ws[k] != 0.f) {  // (a split that saw no key wrote no O)
-          const float* o = p.ws + ((s0 + k) * stride + r0) * D + lane * kCols;
-          if constexpr (kCols == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(o);
-            v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
-          } else {
-            const float2 x = *reinterpret_cast<const float2*>(o);
-            v[k][0] = x.x; v[k][1] = x.y;
-          }
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) acc[c] += ws[k] * v[k][c];
+  if (chunk < 0 || len < chunk || len > p.max_blocks_per_seq * kBlockTokens || q0 < 0 || q1 > p.query_rows) return;
+  const int rows = min(static_cast<int>(chunk), p.max_query_len) * p.num_q_heads;
+  auto load = [&](const float* o, float (&v)[kCols]) {
+    if constexpr (kCols == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(o);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(o);
+      v[0] = x.x; v[1] = x.y;
     }
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) +
-                                                (static_cast<size_t>(q0) * p.num_q_heads + row) * D + lane * kCols);
+  };
+  for (int row0 = (blockIdx.x * 8 + warp) * kMergeRows; row0 < rows; row0 += gridDim.x * 8 * kMergeRows) {
+    const size_t r0 = static_cast<size_t>(b) * p.ws_rows * p.num_q_heads + row0;
+    float2 s[kMergeRows];
+    float v[kMergeRows][kFirst][kCols];
 #pragma unroll
-    for (int c = 0; c < kCols; c += 2) dst[c / 2] = pack_bf16(acc[c] * inv, acc[c + 1] * inv);
+    for (int k = 0; k < kMergeRows; ++k) {
+      s[k] = make_float2(-INFINITY, 0.f);
+      if (row0 + k < rows && lane < p.num_splits) s[k] = ml[lane * stride + r0 + k];
+    }
+#pragma unroll
+    for (int k = 0; k < kMergeRows; ++k)
+#pragma unroll
+      for (int f = 0; f < kFirst; ++f)
+        if (row0 + k < rows && f < p.num_splits) load(p.ws + (f * stride + r0 + k) * D + lane * kCols, v[k][f]);
+#pragma unroll
+    for (int k = 0; k < kMergeRows; ++k) {
+      if (row0 + k >= rows) break;
+      float mx = s[k].x;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      const float w = s[k].x == -INFINITY ? 0.f : exp2f(s[k].x - mx);
+      float den = w * s[k].y;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
+      const float inv = den != 0.f ? 1.f / den : 0.f;
+      float acc[kCols];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
+#pragma unroll
+      for (int f = 0; f < kFirst; ++f) {
+        const float wf = __shfl_sync(0xffffffffu, w, f);
+        if (wf == 0.f) continue;  // no such split, or one that saw no key and wrote no O
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) acc[c] += wf * v[k][f][c];
+      }
+      for (int f = kFirst; f < p.num_splits; ++f) {
+        const float wf = __shfl_sync(0xffffffffu, w, f);
+        if (wf == 0.f) continue;
+        float o[kCols];
+        load(p.ws + (f * stride + r0 + k) * D + lane * kCols, o);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) acc[c] += wf * o[c];
+      }
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) +
+                                                  (static_cast<size_t>(q0) * p.num_q_heads + row0 + k) * D + lane * kCols);
+#pragma unroll
+      for (int c = 0; c < kCols; c += 2) dst[c / 2] = pack_bf16(acc[c] * inv, acc[c + 1] * inv);
+    }
   }
 }
 
@@ -581,7 +597,7 @@ cudaError_t launch_fp8(Fp8PrefillParams p, cudaStream_t stream) {
   const dim3 grid(p.num_kv_heads, tiles, p.num_seqs * (kSplit ? p.num_splits : 1));
   e = launch_pdl(prefill_fp8_kernel<D, G, kSplit>, grid, dim3(kFp8Threads), Pf<D>::kSmem, stream, p, mo);
   if (!kSplit || e != cudaSuccess) return e;
-  const int64_t blocks = (static_cast<int64_t>(p.max_query_len) * p.num_q_heads + 7) / 8;
+  const int64_t blocks = (static_cast<int64_t>(p.max_query_len) * p.num_q_heads + 8 * kMergeRows - 1) / (8 * kMergeRows);
   return launch_pdl(merge_fp8_kernel<D>, dim3(static_cast<unsigned>(blocks < 65535 ? blocks : 65535), p.num_seqs), dim3(256), 0,
                     stream, p);
 }
