@@ -48,9 +48,10 @@ __device__ __forceinline__ uint32_t top_bits(const uint4& a, const uint4& b) {
   for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i / 4][i % 4] & 0x7fff7fffu);
   return max(top & 0xffffu, top >> 16);
 }
-__device__ __noinline__ uint32_t top_finite_bits(const uint4& a, const uint4& b) {
+__device__ __forceinline__ uint32_t top_finite_bits(const uint4& a, const uint4& b) {
   const uint32_t* w[2] = {&a.x, &b.x};
   uint32_t top = 0;
+#pragma unroll
   for (int i = 0; i < 16; ++i) {
     const uint32_t x = (w[i / 8][i / 2 % 4] >> 16 * (i & 1)) & 0x7fffu;
     if (x < 0x7f80u) top = max(top, x);
@@ -74,7 +75,7 @@ __device__ __forceinline__ uint2 quantise(const uint4& a, float inverse, bool od
 }
 
 constexpr int kAppendThreads = 128;
-constexpr int kAppendCtas = 16;  // per SM at most; beyond that a warp takes several tokens
+constexpr int kAppendCtas = 64;  // per SM at most; beyond that a warp takes several tokens
 
 // A lane owns two 16-byte chunks of a row, so that D / 16 lanes cover it and a warp takes 4 (D = 128) or 8 rows at a time:
 // the chunks c and c + D / 16, the rotation's two halves, or without rotation 2 c and 2 c + 1, whose codes are 16 bytes.
@@ -83,7 +84,7 @@ template <int D, bool kRotary>
 __global__ void __launch_bounds__(kAppendThreads) append_fp8_kernel(const Fp8AppendParams p) {
   pdl_trigger();
   pdl_wait();
-  constexpr int kAhead = kRotary ? 2 : 4;
+  constexpr int kAhead = 2;
   constexpr int kLanes = D / 16;  // lanes of a row
   constexpr int kRowsAtOnce = 32 / kLanes;
   constexpr int kChunks = D / 8;  // 16-byte chunks of a bf16 row
@@ -184,21 +185,24 @@ __global__ void __launch_bounds__(kAppendThreads) append_fp8_kernel(const Fp8App
 
 // A thread reads 8 codes of a row of K and of V, of kGatherTokens tokens at once, and writes 8 bf16 values of each: so the
 // loads and the stores of a warp are whole rows.
-constexpr int kGatherTokens = 4;
+constexpr int kGatherThreads = 256;
+constexpr int kGatherTokens = 2;
+constexpr int kGatherCtas = 64;  // per SM at most
 template <int D>
-__global__ void __launch_bounds__(256) gather_fp8_kernel(const Fp8GatherParams p) {
+__global__ void __launch_bounds__(kGatherThreads) gather_fp8_kernel(const Fp8GatherParams p) {
   pdl_trigger();
   pdl_wait();
   constexpr int kChunks = D / 8;
   const int per_token = p.num_kv_heads * kChunks;
   const int64_t total = p.num_tokens * per_token;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; first < total; first += kGatherTokens * stride) {
+  // A CTA's are neighbours, so that blocks are read whole.
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kGatherThreads * kGatherTokens;
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kGatherThreads * kGatherTokens + threadIdx.x; first < total; first += stride) {
     int64_t token[kGatherTokens], slot[kGatherTokens];
     int rem[kGatherTokens];
 #pragma unroll
     for (int k = 0; k < kGatherTokens; ++k) {
-      const int64_t idx = first + k * stride;
+      const int64_t idx = first + k * kGatherThreads;
       token[k] = idx / per_token;
       rem[k] = static_cast<int>(idx - token[k] * per_token);
       slot[k] = idx < total ? __ldg(p.slot_mapping + token[k]) : -1;
@@ -295,11 +299,12 @@ cudaError_t launch_append_fp8(const Fp8AppendParams& p, int head_dim, int num_sm
 
 cudaError_t launch_gather_fp8(const Fp8GatherParams& p, int head_dim, int num_sms, cudaStream_t stream) {
   const int64_t total = p.num_tokens * p.num_kv_heads * (head_dim / 8);
-  int64_t blocks = (total + 255) / 256;
-  const int64_t cap = static_cast<int64_t>(num_sms) * 8;
+  constexpr int kPerCta = kGatherThreads * kGatherTokens;
+  int64_t blocks = (total + kPerCta - 1) / kPerCta;
+  const int64_t cap = static_cast<int64_t>(num_sms) * kGatherCtas;
   if (blocks > cap) blocks = cap;
   return launch_pdl(head_dim == 128 ? gather_fp8_kernel<128> : gather_fp8_kernel<64>, dim3(static_cast<unsigned>(blocks)),
-                    dim3(256), 0, stream, p);
+                    dim3(kGatherThreads), 0, stream, p);
 }
 
 cudaError_t launch_copy_blocks_fp8(const Fp8CopyParams& p, int num_pairs, cudaStream_t stream) {

@@ -93,7 +93,7 @@ struct Fp8AttentionParams {
 };
 
 constexpr int kFp8LaunchSeqs = 1024;
-constexpr int kFp8MostRows = 32;
+constexpr int kFp8MostRows = 24;
 // Blocks of eight columns that hold so many rows; 0: too many.
 inline int fp8_columns(int rows) { return rows <= kFp8MostRows ? (rows + 7) / 8 : 0; }
 // Its workspace and how its work is cut.

@@ -111,11 +111,9 @@ cudaError_t dispatch(int head_dim, int rows, F&& f) {
     case 64 * 8 + 1: return f(Instance<64, 1>{});
     case 64 * 8 + 2: return f(Instance<64, 2>{});
     case 64 * 8 + 3: return f(Instance<64, 3>{});
-    case 64 * 8 + 4: return f(Instance<64, 4>{});
     case 128 * 8 + 1: return f(Instance<128, 1>{});
     case 128 * 8 + 2: return f(Instance<128, 2>{});
     case 128 * 8 + 3: return f(Instance<128, 3>{});
-    case 128 * 8 + 4: return f(Instance<128, 4>{});
     default: return cudaErrorInvalidValue;
   }
 }
