@@ -1212,9 +1212,6 @@ pkv_status pkv_copy_blocks_fp8(void* k_cache, void* v_cache, void* kv_scales, co
 }
 
 namespace {
-// Least units of a piece of the few-row kernel's stream.
-constexpr int32_t kFp8PieceUnits = 2;
-
 // Its workspace, and the CTAs a pair if it needs none.
 pkv_status few_rows_need(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int32_t max_blocks_per_seq, int rows,
                          int* cluster, size_t* need) {
@@ -1228,7 +1225,7 @@ pkv_status few_rows_need(int32_t num_seqs, int32_t num_kv_heads, int32_t head_di
   }
   int sms = 0;
   if (pkv_status st = device_state(nullptr, &sms); st != PKV_OK) return st;
-  *need = pkv::Fp8FewPlan(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, rows, kFp8PieceUnits, sms).bytes;
+  *need = pkv::Fp8FewPlan(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, rows, sms).bytes;
   return PKV_OK;
 }
 
@@ -1244,7 +1241,6 @@ pkv_status few_rows_fp8(pkv::Fp8AttentionParams p, int32_t head_dim, void* works
     return fail(PKV_ERR_INVALID_ARGUMENT, "workspace too small: %zu bytes given, %zu needed", workspace ? workspace_bytes : size_t{0},
                 need);
   p.qscale = p.scale * 1.4426950408889634f;
-  p.min_piece_units = kFp8PieceUnits;
   p.state_rows = rows;
   if (p.cluster_ctas) {
     const cudaError_t e = pkv::launch_few_rows_fp8(p, head_dim, reinterpret_cast<cudaStream_t>(stream));
@@ -1266,7 +1262,7 @@ pkv_status few_rows_fp8(pkv::Fp8AttentionParams p, int32_t head_dim, void* works
       s.q = static_cast<const unsigned char*>(p.q) + s0 * q_row;
       s.out = static_cast<unsigned char*>(p.out) + s0 * q_row;
     }
-    const pkv::Fp8FewPlan plan(s.num_seqs, p.num_kv_heads, head_dim, p.max_blocks_per_seq, rows, kFp8PieceUnits, sms);
+    const pkv::Fp8FewPlan plan(s.num_seqs, p.num_kv_heads, head_dim, p.max_blocks_per_seq, rows, sms);
     s.unit_heads = plan.unit_heads;
     s.num_pieces = plan.num_pieces;
     unsigned char* ws = static_cast<unsigned char*>(workspace);

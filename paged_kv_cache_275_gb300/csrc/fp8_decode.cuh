@@ -183,12 +183,6 @@ struct Walk {
   int b, heads, unit, units;
 };
 
-// Pieces that a stream of `total` units is cut into.
-__device__ __forceinline__ int pieces_of(const Fp8AttentionParams& p, int total) {
-  const int most = (total + p.min_piece_units - 1) / p.min_piece_units;
-  return min(most, p.num_pieces);
-}
-
 template <int D, int NC, bool kCluster>
 __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
     few_rows_fp8_kernel(const Fp8AttentionParams p) {
@@ -246,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
       __syncthreads();
     }
     const int total = running * head_groups;
-    const int pieces = pieces_of(p, total);
+    const int pieces = min(total, p.num_pieces);
     if (piece >= pieces) return;
     n0 = static_cast<int>(static_cast<int64_t>(piece) * total / pieces);
     n1 = static_cast<int>(static_cast<int64_t>(piece + 1) * total / pieces);
