@@ -533,8 +533,8 @@ pkv_status pkv_kv_gather_fp8(const void* k_cache, const void* v_cache, const voi
 pkv_status pkv_copy_blocks_fp8(void* k_cache, void* v_cache, void* kv_scales, const int64_t* src_dst, int32_t num_pairs,
                                int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks, pkv_stream_t stream);
 /*
- * pkv_paged_decode_attention over such a cache (q and out bf16).  num_blocks * num_kv_heads * 16 must be below 2^31 and
- * num_seqs at most 65535.  A token that a sequence does not see does not matter, whatever its row and exponent hold.
+ * pkv_paged_decode_attention over such a cache (q and out bf16).  num_blocks * num_kv_heads * 16 must be below 2^31,
+ * max_blocks_per_seq at most 2^26 and num_seqs at most 65535.  A token that a sequence does not see does not matter, whatever its row and exponent hold.
  *
  *   workspace   device, 16-byte aligned, at least pkv_fp8_decode_workspace_size bytes (may be NULL if that is 0); scratch,
  *               as for pkv_paged_decode_attention
@@ -545,15 +545,16 @@ pkv_status pkv_paged_fp8_decode_attention(const void* q, const void* k_cache, co
                                           int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks,
                                           int32_t block_size, float scale, void* out, void* workspace,
                                           size_t workspace_bytes, pkv_stream_t stream);
-/* Its workspace on the current device.  What is enough for num_seqs sequences and max_blocks_per_seq is enough for fewer. */
+/* Enough workspace on the current device for calls of up to num_seqs sequences and max_blocks_per_seq. */
 pkv_status pkv_fp8_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                          int32_t max_blocks_per_seq, size_t* bytes);
 /*
  * pkv_paged_prefill_attention over such a cache (q and out bf16), scale > 0: prompt chunks, and the few rows a sequence of
  * drafted tokens.  num_query_tokens is the number of rows of q and out (0: a no-op); a sequence whose chunk reaches outside
  * them, or is longer than its context, sets PKV_DEVERR_CONTEXT_LEN_TOO_LONG and is skipped; rows past max_query_len of a
- * chunk are not written, and set it too.  num_blocks * num_kv_heads * 16 must be below 2^31.  A token that some rows of a
- * sequence's chunk see has to be finite, or the rows of the chunk that do not see it are unspecified.
+ * chunk are not written, and set it too.  num_blocks * num_kv_heads * 16 must be below 2^31, max_blocks_per_seq at most 2^26
+ * and num_seqs at most 65535.  A token that some rows of a sequence's chunk see has to be finite, or the rows of the chunk that
+ * do not see it are unspecified.
  */
 pkv_status pkv_paged_fp8_prefill_attention(const void* q, const void* k_cache, const void* v_cache, const void* kv_scales,
                                            const int32_t* block_tables, int32_t max_blocks_per_seq,

@@ -1050,10 +1050,18 @@ pkv_status append_fp8_impl(pkv::Fp8AppendParams& p, int32_t head_dim, pkv_stream
   return ok();
 }
 
-// The checks of both attention calls; *nothing: there is no row to compute.
+// The checks of both attention calls.
+pkv_status check_fp8_shapes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                            int32_t max_blocks_per_seq) {
+  if (pkv_status st = check_shapes(num_seqs, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq); st != PKV_OK)
+    return st;
+  if (max_blocks_per_seq > pkv::kFp8MostBlocks)
+    return fail(PKV_ERR_UNSUPPORTED, "max_blocks_per_seq %d exceeds %d", max_blocks_per_seq, pkv::kFp8MostBlocks);
+  return PKV_OK;
+}
+
 pkv_status check_fp8_attention(const pkv::Fp8AttentionParams& p, int32_t head_dim, int32_t block_size, void* workspace) {
-  if (pkv_status st = check_shapes(p.num_seqs, p.num_seqs, p.num_q_heads, p.num_kv_heads, head_dim, p.max_blocks_per_seq);
-      st != PKV_OK)
+  if (pkv_status st = check_fp8_shapes(p.num_seqs, p.num_q_heads, p.num_kv_heads, head_dim, p.max_blocks_per_seq); st != PKV_OK)
     return st;
   if (p.num_seqs > 65535) return fail(PKV_ERR_UNSUPPORTED, "num_seqs %d exceeds 65535", p.num_seqs);
   if (block_size != PKV_BLOCK_SIZE)
@@ -1212,20 +1220,21 @@ pkv_status pkv_copy_blocks_fp8(void* k_cache, void* v_cache, void* kv_scales, co
 }
 
 namespace {
-// Its workspace, and the CTAs a pair if it needs none.
+// The few-row kernel's CTAs a pair (0: the stream form), its workspace, and what is enough for smaller batches and narrower
+// tables as well.
 pkv_status few_rows_need(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int32_t max_blocks_per_seq, int rows,
-                         int* cluster, size_t* need) {
+                         int* cluster, size_t* need, size_t* enough) {
+  bool fewer = true;
   *cluster = 0;
-  *need = 0;
+  *need = *enough = 0;
   if (num_seqs == 0) return PKV_OK;
-  if (num_seqs <= pkv::kFp8LaunchSeqs) {
-    const cudaError_t e = pkv::fp8_cluster_ctas(head_dim, rows, num_seqs, num_kv_heads, max_blocks_per_seq, cluster);
-    if (e != cudaSuccess) return cuda_fail(e, "cluster occupancy query");
-    if (*cluster) return PKV_OK;
-  }
+  const cudaError_t e = pkv::fp8_cluster_ctas(head_dim, rows, num_seqs, num_kv_heads, max_blocks_per_seq, cluster, &fewer);
+  if (e != cudaSuccess) return cuda_fail(e, "cluster occupancy query");
+  if (*cluster && fewer) return PKV_OK;
   int sms = 0;
   if (pkv_status st = device_state(nullptr, &sms); st != PKV_OK) return st;
-  *need = pkv::Fp8FewPlan(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, rows, sms).bytes;
+  *enough = pkv::Fp8FewPlan(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, rows, sms).bytes;
+  if (!*cluster) *need = *enough;
   return PKV_OK;
 }
 
@@ -1233,8 +1242,9 @@ pkv_status few_rows_fp8(pkv::Fp8AttentionParams p, int32_t head_dim, void* works
   int sms = 0;
   if (pkv_status st = device_state(&p.err, &sms); st != PKV_OK) return st;
   const int rows = p.max_query_len * (p.num_q_heads / p.num_kv_heads);
-  size_t need = 0;
-  if (pkv_status st = few_rows_need(p.num_seqs, p.num_kv_heads, head_dim, p.max_blocks_per_seq, rows, &p.cluster_ctas, &need);
+  size_t need = 0, enough = 0;
+  if (pkv_status st =
+          few_rows_need(p.num_seqs, p.num_kv_heads, head_dim, p.max_blocks_per_seq, rows, &p.cluster_ctas, &need, &enough);
       st != PKV_OK)
     return st;
   if (need > 0 && (!workspace || workspace_bytes < need))
@@ -1280,14 +1290,14 @@ pkv_status few_rows_fp8(pkv::Fp8AttentionParams p, int32_t head_dim, void* works
 pkv_status pkv_fp8_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                          int32_t max_blocks_per_seq, size_t* bytes) {
   if (!bytes) return fail(PKV_ERR_INVALID_ARGUMENT, "bytes is null");
-  if (pkv_status st = check_shapes(num_seqs, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq); st != PKV_OK)
-    return st;
+  if (pkv_status st = check_fp8_shapes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq); st != PKV_OK) return st;
   int cluster = 0;
-  size_t need = 0;
-  if (pkv_status st = few_rows_need(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, num_q_heads / num_kv_heads, &cluster, &need);
+  size_t need = 0, enough = 0;
+  if (pkv_status st = few_rows_need(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, num_q_heads / num_kv_heads, &cluster,
+                                    &need, &enough);
       st != PKV_OK)
     return st;
-  *bytes = need;
+  *bytes = enough;
   return ok();
 }
 
@@ -1314,17 +1324,17 @@ pkv_status pkv_fp8_prefill_workspace_size(int64_t num_query_tokens, int32_t max_
   if (!bytes) return fail(PKV_ERR_INVALID_ARGUMENT, "bytes is null");
   if (num_query_tokens < 0 || max_query_len < 0)
     return fail(PKV_ERR_INVALID_ARGUMENT, "num_query_tokens and max_query_len must be >= 0");
-  if (pkv_status st = check_shapes(num_seqs, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq); st != PKV_OK)
-    return st;
+  if (pkv_status st = check_fp8_shapes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq); st != PKV_OK) return st;
   *bytes = 0;
   if (num_seqs == 0 || num_query_tokens == 0 || max_query_len == 0) return ok();
   int sms = 0;
   if (pkv_status st = device_state(nullptr, &sms); st != PKV_OK) return st;
   const int64_t rows = static_cast<int64_t>(max_query_len) * (num_q_heads / num_kv_heads);
   int cluster = 0;
-  size_t need = 0;
+  size_t need = 0, enough = 0;
   if (rows <= pkv::kFp8MostRows) {
-    if (pkv_status st = few_rows_need(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, static_cast<int>(rows), &cluster, &need);
+    if (pkv_status st = few_rows_need(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, static_cast<int>(rows), &cluster,
+                                      &need, &enough);
         st != PKV_OK)
       return st;
   } else {

@@ -92,7 +92,11 @@ struct Fp8AttentionParams {
 };
 
 constexpr int kFp8LaunchSeqs = 1024;
+// Above this the chunk kernel is faster (sequences of 512..8192 tokens, 64 of them: 24 rows 110 us here, 176 there; 32 rows 253
+// and 165), although it pads them to 128.
 constexpr int kFp8MostRows = 24;
+// Tables up to here keep every position, past the last unit's end too, below 2^31.
+constexpr int kFp8MostBlocks = 1 << 26;
 // Blocks of eight columns that hold so many rows; 0: too many.
 inline int fp8_columns(int rows) { return rows <= kFp8MostRows ? (rows + 7) / 8 : 0; }
 // Its workspace and how its work is cut.
@@ -118,8 +122,10 @@ struct Fp8FewPlan {
 cudaError_t launch_append_fp8(const Fp8AppendParams& p, int head_dim, int num_sms, cudaStream_t stream);
 cudaError_t launch_gather_fp8(const Fp8GatherParams& p, int head_dim, int num_sms, cudaStream_t stream);
 cudaError_t launch_copy_blocks_fp8(const Fp8CopyParams& p, int num_pairs, cudaStream_t stream);
-// CTAs a pair of a call of few pairs, which needs no workspace; 0: the call takes the stream form.
-cudaError_t fp8_cluster_ctas(int head_dim, int rows, int num_seqs, int num_kv_heads, int max_blocks_per_seq, int* ctas);
+// CTAs a pair of a call of few pairs, which needs no workspace; 0: the call takes the stream form.  *fewer: whether the calls of
+// every smaller batch and narrower table need none either.
+cudaError_t fp8_cluster_ctas(int head_dim, int rows, int num_seqs, int num_kv_heads, int max_blocks_per_seq, int* ctas,
+                             bool* fewer);
 cudaError_t launch_few_rows_fp8(const Fp8AttentionParams& p, int head_dim, cudaStream_t stream);
 // Chunks on the 5th-generation tensor cores (fp8_prefill.cu); ws: prefill_workspace_bytes of num_splits > 1.
 cudaError_t launch_prefill_fp8(const Fp8AttentionParams& p, int head_dim, int num_splits, float* ws, cudaStream_t stream);

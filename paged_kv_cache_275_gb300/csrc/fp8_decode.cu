@@ -68,19 +68,32 @@ struct Instance {
     return cudaSuccess;
   }
 
-  static cudaError_t cluster_ctas(int num_seqs, int num_kv_heads, int max_blocks_per_seq, int* ctas) {
-    const int* counts = nullptr;
-    const cudaError_t e = prepare(&counts);
-    if (e != cudaSuccess) return e;
-    const int64_t pairs = static_cast<int64_t>(num_seqs) * num_kv_heads;
+  static int choose(const int* counts, int64_t pairs, int max_blocks_per_seq) {
     const int units = (max_blocks_per_seq + Few<D, NC>::kUnitTiles - 1) / Few<D, NC>::kUnitTiles;
     int k = 0;
     while (k < 3 && (1 << k) < units && pairs <= counts[k + 1]) ++k;
+    if (pairs > counts[k]) return 0;
     const float bytes_us =
         kFilled / kBytesPerUs * static_cast<float>(pairs) * units * (2.f * Few<D, NC>::kUnitTiles * Few<D, NC>::kTile);
-    const float units_us = kClusterUnitUs<D, NC> * ((units + (1 << k) - 1) >> k);
-    const float mine = kClusterUs + (units_us > bytes_us ? units_us : bytes_us), other = kStreamUs + bytes_us;
-    *ctas = pairs <= counts[k] && mine <= other ? 1 << k : 0;
+    const float units_us = kClusterUnitUs<D, NC> * static_cast<float>(units) / (1 << k);
+    return kClusterUs + (units_us > bytes_us ? units_us : bytes_us) <= kStreamUs + bytes_us ? 1 << k : 0;
+  }
+
+  // CTAs a pair of a call; *fewer: whether every smaller batch, and narrower table, takes clusters too.  With as many CTAs a
+  // pair the smallest batch is the first not to (the stream form has fewest bytes then), so one batch for each number of CTAs
+  // is looked at; a table that is not too wide for a batch leaves none narrower that is, for a cluster's time over the stream
+  // form's is linear in the units.
+  static cudaError_t cluster_ctas(int num_seqs, int num_kv_heads, int max_blocks_per_seq, int* ctas, bool* fewer) {
+    const int* counts = nullptr;
+    const cudaError_t e = prepare(&counts);
+    if (e != cudaSuccess) return e;
+    auto takes = [&](int64_t seqs) { return choose(counts, seqs * num_kv_heads, max_blocks_per_seq); };
+    *ctas = takes(num_seqs);
+    *fewer = *ctas != 0 && takes(1) != 0;
+    for (int k = 1; k <= 3; ++k) {
+      const int64_t first = counts[k] / num_kv_heads + 1;  // the smallest batch whose pairs get no more than 2^(k - 1)
+      if (first < num_seqs) *fewer = *fewer && takes(first) != 0;
+    }
     return cudaSuccess;
   }
 
@@ -124,9 +137,11 @@ cudaError_t launch_few_rows_fp8(const Fp8AttentionParams& p, int head_dim, cudaS
   return dispatch(head_dim, p.state_rows, [&](auto instance) { return instance.launch(p, stream); });
 }
 
-cudaError_t fp8_cluster_ctas(int head_dim, int rows, int num_seqs, int num_kv_heads, int max_blocks_per_seq, int* ctas) {
-  return dispatch(head_dim, rows,
-                  [&](auto instance) { return instance.cluster_ctas(num_seqs, num_kv_heads, max_blocks_per_seq, ctas); });
+cudaError_t fp8_cluster_ctas(int head_dim, int rows, int num_seqs, int num_kv_heads, int max_blocks_per_seq, int* ctas,
+                             bool* fewer) {
+  return dispatch(head_dim, rows, [&](auto instance) {
+    return instance.cluster_ctas(num_seqs, num_kv_heads, max_blocks_per_seq, ctas, fewer);
+  });
 }
 
 }  // namespace pkv

@@ -165,3 +165,12 @@ def test_quantise_at_the_borders():
     # The least subnormal code, and half of it.
     assert quantise(bf(448.0, 2.0**-9, 2.0**-10, 1.5 * 2.0**-9))[0][0, 1:].tolist() == [2.0**-9, 0.0, 2.0**-8]
     assert values(torch.tensor([[1.0]]).to(FP8), torch.tensor([130], dtype=torch.uint8))[0, 0] == 8.0
+
+
+@pytest.mark.parametrize("function", [decode, prefill])
+def test_tables_of_more_than_2_26_blocks_are_refused(lib, function):
+    kw = dict(B=1, hq=1, hkv=1)
+    assert function(lib, W=(1 << 26) + 1, **kw) == 2 and "max_blocks_per_seq" in msg(lib)
+    n = ctypes.c_size_t(0)
+    assert lib.pkv_fp8_decode_workspace_size(1, 1, 1, 128, (1 << 26) + 1, ctypes.byref(n)) == 2
+    assert lib.pkv_fp8_prefill_workspace_size(4, 4, 1, 1, 1, 128, (1 << 26) + 1, ctypes.byref(n)) == 2

@@ -188,6 +188,44 @@ def test_a_given_workspace_and_one_that_is_too_small():
             run(pages.lens, 8, 2, 128, pages=pages, q=q, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
 
 
+SEQS = [1, 2, 3, 4, 5, 8, 9, 12, 16, 18, 19, 20, 24, 36, 37, 38, 40, 64, 75, 76, 77, 100, 151, 152, 153, 200, 303, 304, 305, 600,
+        1023, 1024, 1025, 4000]
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(1, 1, 128), (8, 1, 128), (2, 2, 64), (32, 8, 128), (64, 8, 64), (12, 3, 128)])
+def test_workspace_sizes_do_not_fall(hq, hkv, d):
+    sizes = [[pkv.fp8_decode_workspace_size(n, hq, hkv, d, width) for n in SEQS]
+             for width in (1, 8, 9, 60, 100, 300, 410, 500, 512, 521, 600, 700, 1000, 1024, 2000, 2048, 4000, 20000)]
+    assert (np.diff(sizes, axis=0) >= 0).all() and (np.diff(sizes, axis=1) >= 0).all()
+    assert sizes[0][0] == 0 and sizes[-1][0] > 0  # (both forms)
+
+
+@pytest.mark.parametrize("hkv", [1, 8])
+def test_one_workspace_for_all_batches(hkv):
+    """Lengths that a few sequences take in the stream and more in clusters: every batch with the largest one's workspace."""
+    lens = [6000, 9000]
+    pages = Fp8Pages(lens, hkv, 128, hkv, width=1500)
+    q = pages.randn(8, hkv, 128)
+    rows = [attend_fp8(pages, b % 2, f64(q)[b], lens[b % 2], 0.1, WEIGHT) for b in range(8)]
+    ref, allowed = np.stack([r[0] for r in rows]), np.stack([r[1] for r in rows])
+    kc, vc, sc, table, cl = pages.cuda()
+    space = torch.empty(max(16, pkv.fp8_decode_workspace_size(8, hkv, hkv, 128, 1500)), dtype=torch.uint8, device="cuda")
+    for n in range(1, 9):
+        out = torch.empty(n, hkv, 128, dtype=torch.bfloat16, device="cuda")
+        pkv.paged_fp8_decode_attention(q[:n].cuda(), kc, vc, sc, table.repeat(4, 1)[:n], cl.repeat(4)[:n], 0.1, out, workspace=space)
+        assert_within(out, ref[:n], allowed[:n], f"{n} sequences")
+    assert device_errors() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(32, 8), (8, 8), (16, 4), (12, 6), (5, 5), (8, 1)])
+def test_more_pairs_than_clusters(hq, hkv, d):
+    """Long and short sequences, more than the GPU holds clusters for: pieces that begin and end inside of pairs."""
+    r = np.random.RandomState(hq)
+    lens = r.randint(0, 90, 310 // hkv + 1) + (r.rand(310 // hkv + 1) < 0.1) * 1500
+    run(lens, hq, hkv, d, seed=hq)
+
+
 def test_a_large_cache():
     """Blocks whose rows lie behind 2^32 bytes."""
     hkv, d, nb = 8, 128, 270_000

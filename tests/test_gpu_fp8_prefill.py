@@ -76,6 +76,16 @@ def test_one_sequence(past, chunk, hq, hkv):
     run((past,), (chunk,), hq, hkv, 128, seed=past + chunk)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv,most", [(8, 8, 9), (8, 8, 17), (8, 8, 24), (32, 8, 4), (32, 8, 6), (12, 6, 12), (16, 2, 3), (8, 4, 8),
+                                         (2, 1, 12)])
+def test_more_pairs_than_clusters(hq, hkv, most, d):
+    """Chunks of up to 24 rows, more (sequence, kv head) pairs than the GPU holds clusters for, some of them long."""
+    r = np.random.RandomState(most)
+    n = 310 // hkv + 1
+    run(r.randint(0, 90, n) + (r.rand(n) < 0.1) * 1500, np.append(r.randint(0, most + 1, n - 1), most), hq, hkv, d, most=most)
+
+
 def test_many_sequences():
     r = np.random.RandomState(1)
     chunks = r.randint(0, 9, 700)
