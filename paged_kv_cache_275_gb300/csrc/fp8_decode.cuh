@@ -12,8 +12,8 @@
 // brought to a largest value of 2^14 by a power of two, down to 2^-28 of it; smaller values lose bits that a score does not
 // show.  The exponents stay outside of the products: a score is S 2^(ke) scale, and a weight takes V's exponent with it,
 //   w_j = 2^((s_j - m) + ve_j - r),   O = 2^r sum_j w_j vc_j,   l = sum_j 2^(s_j - m),
-// with running references (base 2) m of s and r of (s - m) + ve, raised when some value passes them by 2^8, so that w is at
-// most 2^15 and the largest of a row is 2^7 or more: fp16's 11 bits hold for weights down to 2^-21 of the largest, and those
+// with running references (base 2) m of s and r of (s - m) + ve, seven below their largest value and raised when some value
+// passes them by fifteen, so that w is at most 2^15 and the largest of a row is 2^7 or more: fp16's 11 bits hold for weights down to 2^-21 of the largest, and those
 // below 2^-32 of it vanish.  (m comes off first: next to a large score an exponent would lose its bits.)
 //
 // Work.  The batch's blocks form one stream of units of 32 KB of K and V, eight (block, kv head) tiles of 128 dims or sixteen
@@ -49,8 +49,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMostCluster = 8;
 constexpr float kNone = -3.0e38f;  // the reference of a row that has seen no token
-constexpr float kSlack = 8.f;
-constexpr float kWeightShift = 7.f;  // the largest weight is brought to 2^7 .. 2^15
+constexpr float kTopLog = 7.f, kMostLog = 15.f;  // the largest of a row's weights is brought to 2^7 and may grow to 2^15
 
 template <int D, int NC>
 struct Few {
@@ -387,8 +386,8 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
     const int first_limit = rows.tokens - rows.count + 1;  // tokens that the first row sees
     const int count = kCluster ? n1 : min(at.units - at.unit, n1 - n);  // units of the pair here
     uint32_t q[NC][kSteps][2];  // B fragments of the rows
-    float q_scale[NC][2];       // of columns 2t, 2t + 1: what takes a product to a score
-    float m[NC][2], r[NC][2], l[NC][2];
+    float2 q_scale[NC];         // of columns 2t, 2t + 1: what takes a product to a score
+    float2 nm[NC], nr[NC], l[NC];  // of columns 2t, 2t + 1: -m, -r, and l
     float o[kSteps][NC][4];
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
@@ -420,12 +419,9 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
         for (int k = 0; k < 2; ++k)
           q[nc][c][k] = pack_f16(__uint_as_float(q[nc][c][k] << 16) * by, __uint_as_float(q[nc][c][k] & 0xffff0000u) * by);
       const float back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23) * p.qscale;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        q_scale[nc][k] = __shfl_sync(kAll, back, (2 * t + k) * 4);
-        m[nc][k] = r[nc][k] = kNone;
-        l[nc][k] = 0.f;
-      }
+      q_scale[nc] = make_float2(__shfl_sync(kAll, back, 2 * t * 4), __shfl_sync(kAll, back, (2 * t + 1) * 4));
+      nm[nc] = nr[nc] = make_float2(-kNone, -kNone);
+      l[nc] = make_float2(0.f, 0.f);
     }
 #pragma unroll
     for (int c = 0; c < kSteps; ++c)
@@ -434,156 +430,208 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[c][nc][k] = 0.f;
 
-    int first_token = (at.unit * nb + place_of * kTurns) * kBlockTokens;  // of this warp's blocks
-    for (int u = 0; u < count; ++u, first_token += stride * nb * kBlockTokens) {
+    int token0 = (at.unit * nb + place_of * kTurns) * kBlockTokens;  // of this warp's blocks
+    for (int u = 0; u < count; ++u, token0 += stride * nb * kBlockTokens) {
+      copies_wait<T::kStages - kTurns>();
+      __syncwarp();
+      const int place = stage;
+      if ((stage += kTurns) == T::kStages) stage = 0;
+      if (token0 >= rows.tokens) {
 #pragma unroll
-      for (int turn = 0; turn < kTurns; ++turn) {
-        const int token0 = first_token + turn * kBlockTokens;
-        copies_wait<T::kStages - 1>();
-        __syncwarp();
-        const uint32_t sk = ld_at + stage * T::kStage;
-        const unsigned char* sc = smem + T::kOffScales + (warp * T::kStages + stage) * T::kScales;
-        if (++stage == T::kStages) stage = 0;
-        if (token0 >= rows.tokens) {
-          send();
-          continue;
+        for (int turn = 0; turn < kTurns; ++turn) send();
+        continue;
+      }
+      // All of a warp's tiles of a unit at a time (D = 64: two, where one after the other XX).  What lies in the second one's
+      // place past the last token is masked like the rows past it.
+      // With few tiles a warp it is their latency that counts: V's codes, too, are taken into registers first, and the tiles'
+      // places are free for the next copies.  With many it is registers (V's codes first: 128 sequences 107 -> 110 us, drafts
+      // of up to five tokens 106 -> 128; one sequence 10.2 -> 8.9).
+      constexpr bool kEarly = kCluster;
+      float k_lo[kTurns], k_hi[kTurns], v_lo[kTurns], v_hi[kTurns];
+      uint32_t kx[kTurns][kSteps / 2][4], vx[kTurns][kSteps / 2][4];
+#pragma unroll
+      for (int y = 0; y < kTurns; ++y) {
+        const unsigned char* sc = smem + T::kOffScales + (warp * T::kStages + place + y) * T::kScales;
+        k_lo[y] = fp8_scale(sc[g]);
+        k_hi[y] = fp8_scale(sc[g + 8]);
+        v_lo[y] = fp8_power(sc[16 + g]);
+        v_hi[y] = fp8_power(sc[24 + g]);
+      }
+      const uint32_t tile_at = ld_at + place * T::kStage;
+      if constexpr (kEarly) {
+#pragma unroll
+        for (int y = 0; y < kTurns; ++y) {
+#pragma unroll
+          for (int c = 0; c < kSteps / 2; ++c) ldsm_x4((tile_at + y * T::kStage) ^ (32u * c), kx[y][c]);
+#pragma unroll
+          for (int c = 0; c < kSteps / 2; ++c) ldsm_x4_t(((tile_at + y * T::kStage) ^ (32u * c)) + T::kTile, vx[y][c]);
         }
-        // With few tiles a warp it is their latency that counts: V's codes, too, are taken into registers first, and the tile's
-        // place is free for the next copies.  With many it is registers (V's codes first: 128 sequences 107 -> 110 us, drafts
-        // of up to five tokens 106 -> 128; one sequence 10.2 -> 8.9).
-        constexpr bool kEarly = kCluster;
-        const float k_lo = fp8_scale(sc[g]), k_hi = fp8_scale(sc[g + 8]);
-        const float v_lo = static_cast<float>(static_cast<int>(sc[16 + g]) - 127);
-        const float v_hi = static_cast<float>(static_cast<int>(sc[24 + g]) - 127);
-        uint32_t kx[kSteps / 2][4], vx[kSteps / 2][4];
-        if constexpr (kEarly) {
+      }
+      // S^T = Kc q^T.  Chunk c of a row: its 16 codes are the product's depth, in the order 4t, 4t + 1, 4t + 2, 4t + 3 of
+      // a lane's four, as q's fragments are.  (In two sums where there would be a single chain of products.)
+      constexpr int kSums = NC * kTurns == 1 ? 2 : 1;
+      float s[kTurns][NC][4];
 #pragma unroll
-          for (int c = 0; c < kSteps / 2; ++c) ldsm_x4(sk ^ (32u * c), kx[c]);
+      for (int y = 0; y < kTurns; ++y) {
+        float sum[kSums][NC][4];
 #pragma unroll
-          for (int c = 0; c < kSteps / 2; ++c) ldsm_x4_t((sk ^ (32u * c)) + T::kTile, vx[c]);
-        }
-        // S^T = Kc q^T.  Chunk c of a row: its 16 codes are the product's depth, in the order 4t, 4t + 1, 4t + 2, 4t + 3 of
-        // a lane's four, as q's fragments are.
-        float s[NC][4], s2[NC][4];
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) s[nc][k] = s2[nc][k] = 0.f;
-#pragma unroll
-        for (int c = 0; c < kSteps / 2; ++c) {
-          uint32_t a[4][2];
-          if constexpr (!kEarly) ldsm_x4(sk ^ (32u * c), kx[c]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            a[k][0] = fp8_halves(static_cast<uint16_t>(kx[c][k]));
-            a[k][1] = fp8_halves(static_cast<uint16_t>(kx[c][k] >> 16));
-          }
-#pragma unroll
-          for (int nc = 0; nc < NC; ++nc) {
-            mma_f16(s[nc], a[0][0], a[1][0], a[0][1], a[1][1], q[nc][2 * c][0], q[nc][2 * c][1]);
-            mma_f16(s2[nc], a[2][0], a[3][0], a[2][1], a[3][1], q[nc][2 * c + 1][0], q[nc][2 * c + 1][1]);
-          }
-        }
-        if constexpr (kEarly) {
-          __syncwarp();  // the tile has been read
-          send();
-        }
-        const bool masked = token0 + kBlockTokens > first_limit;
-        bool raise = false;
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            s[nc][k] = (s[nc][k] + s2[nc][k]) * (q_scale[nc][k & 1] * (k < 2 ? k_lo : k_hi));
-          if (masked) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (token0 + g + (k < 2 ? 0 : 8) >= first_limit + ((nc * 8 + 2 * t + (k & 1)) >> group_bits)) s[nc][k] = -INFINITY;
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float d = s[nc][k] - m[nc][k & 1];
-            raise |= d > kSlack || d + (k < 2 ? v_lo : v_hi) > r[nc][k & 1] + kSlack;
-          }
-        }
-        if (__any_sync(kAll, raise)) {  // seldom but for a pair's first block
+        for (int x = 0; x < kSums; ++x)
 #pragma unroll
           for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float top = fmaxf(s[nc][k], s[nc][k + 2]);
-#pragma unroll
-              for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
-              top = fmaxf(top, m[nc][k]);
-              const float by = m[nc][k] - top;
-              m[nc][k] = top;
-              l[nc][k] *= ex2(by);
-              float top_w = fmaxf(s[nc][k] - top + v_lo, s[nc][k + 2] - top + v_hi);
-#pragma unroll
-              for (int off = 4; off < 32; off <<= 1) top_w = fmaxf(top_w, __shfl_xor_sync(kAll, top_w, off));
-              const float was = r[nc][k] + by;  // against the new m
-              r[nc][k] = fmaxf(top_w, was);
-              const float alpha = ex2(was - r[nc][k]);
-#pragma unroll
-              for (int c = 0; c < kSteps; ++c) {
-                o[c][nc][k] *= alpha;
-                o[c][nc][k + 2] *= alpha;
-              }
-            }
-        }
-        uint32_t w[NC][2];  // B fragments of the weights
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc) {
-          float wt[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float d = s[nc][k] - m[nc][k & 1];
-            l[nc][k & 1] += ex2(d);
-            wt[k] = ex2(d + ((k < 2 ? v_lo : v_hi) - r[nc][k & 1] + kWeightShift));
-          }
-          w[nc][0] = transpose8(pack_f16(wt[0], wt[1]));
-          w[nc][1] = transpose8(pack_f16(wt[2], wt[3]));
-        }
-        // Rows that nobody sees must not reach the product (0 times no number).
-        uint32_t keep_lo = kAll, keep_hi = kAll;  // of tokens 2t, 2t + 1 and of 2t + 8, 2t + 9
-        if (masked) {
-          const int left = rows.tokens - token0 - 2 * t;
-          keep_lo = left > 1 ? kAll : left > 0 ? 0xffffu : 0u;
-          keep_hi = left > 9 ? kAll : left > 8 ? 0xffffu : 0u;
-        }
-        // O^T += Vc^T W^T.  A lane's four codes of a chunk: tokens 2t and 2t + 1, dims 2g and 2g + 1; dims 2g are rows g of
-        // the product, dims 2g + 1 rows g + 8.
+            for (int k = 0; k < 4; ++k) sum[x][nc][k] = 0.f;
 #pragma unroll
         for (int c = 0; c < kSteps / 2; ++c) {
           uint32_t a[4][2];
-          if constexpr (!kEarly) ldsm_x4_t((sk ^ (32u * c)) + T::kTile, vx[c]);
+          if constexpr (!kEarly) ldsm_x4((tile_at + y * T::kStage) ^ (32u * c), kx[y][c]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint32_t y = __byte_perm(masked ? vx[c][k] & (k & 1 ? keep_hi : keep_lo) : vx[c][k], 0, 0x3120);
-            a[k][0] = fp8_halves(static_cast<uint16_t>(y));
-            a[k][1] = fp8_halves(static_cast<uint16_t>(y >> 16));
+            a[k][0] = fp8_halves(static_cast<uint16_t>(kx[y][c][k]));
+            a[k][1] = fp8_halves(static_cast<uint16_t>(kx[y][c][k] >> 16));
           }
 #pragma unroll
           for (int nc = 0; nc < NC; ++nc) {
-            mma_f16(o[2 * c][nc], a[0][0], a[0][1], a[1][0], a[1][1], w[nc][0], w[nc][1]);
-            mma_f16(o[2 * c + 1][nc], a[2][0], a[2][1], a[3][0], a[3][1], w[nc][0], w[nc][1]);
+            mma_f16(sum[0][nc], a[0][0], a[1][0], a[0][1], a[1][1], q[nc][2 * c][0], q[nc][2 * c][1]);
+            mma_f16(sum[kSums - 1][nc], a[2][0], a[3][0], a[2][1], a[3][1], q[nc][2 * c + 1][0], q[nc][2 * c + 1][1]);
           }
         }
-        if constexpr (!kEarly) {
-          __syncwarp();
-          send();
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // rows g and g + 8: tokens
+            float2 x = make_float2(sum[0][nc][2 * h], sum[0][nc][2 * h + 1]);
+            if (kSums == 2) x = __fadd2_rn(x, make_float2(sum[kSums - 1][nc][2 * h], sum[kSums - 1][nc][2 * h + 1]));
+            const float by = h ? k_hi[y] : k_lo[y];
+            x = __fmul2_rn(x, __fmul2_rn(q_scale[nc], make_float2(by, by)));
+            s[y][nc][2 * h] = x.x;
+            s[y][nc][2 * h + 1] = x.y;
+          }
+      }
+      if constexpr (kEarly) {
+        __syncwarp();  // the tiles have been read
+#pragma unroll
+        for (int turn = 0; turn < kTurns; ++turn) send();
+      }
+      const bool masked = token0 + kTurns * kBlockTokens > first_limit;
+      if (masked) {
+#pragma unroll
+        for (int y = 0; y < kTurns; ++y)
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (token0 + y * kBlockTokens + g + (k < 2 ? 0 : 8) >= first_limit + ((nc * 8 + 2 * t + (k & 1)) >> group_bits))
+                s[y][nc][k] = -INFINITY;
+      }
+      // Of tile y, column block nc and row half h: s - m, and (s - m) + ve - r.
+      auto logs = [&](int y, int nc, int h, float2& d, float2& e) {
+        const float v = h ? v_hi[y] : v_lo[y];
+        d = __fadd2_rn(make_float2(s[y][nc][2 * h], s[y][nc][2 * h + 1]), nm[nc]);
+        e = __fadd2_rn(d, __fadd2_rn(make_float2(v, v), nr[nc]));
+      };
+      float most = -INFINITY;
+#pragma unroll
+      for (int y = 0; y < kTurns; ++y)
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float2 d, e;
+            logs(y, nc, h, d, e);
+            most = fmaxf(fmaxf(most, fmaxf(d.x, d.y)), fmaxf(e.x, e.y));
+          }
+      if (__any_sync(kAll, most > kMostLog)) {  // seldom but for a pair's first block
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float top = -INFINITY, top_w = -INFINITY;
+#pragma unroll
+            for (int y = 0; y < kTurns; ++y) top = fmaxf(top, fmaxf(s[y][nc][k], s[y][nc][k + 2]));
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+            const float m = k ? -nm[nc].y : -nm[nc].x, r = k ? -nr[nc].y : -nr[nc].x;
+            const float mn = fmaxf(top - kTopLog, m), by = m - mn;
+#pragma unroll
+            for (int y = 0; y < kTurns; ++y) top_w = fmaxf(top_w, fmaxf(s[y][nc][k] - mn + v_lo[y], s[y][nc][k + 2] - mn + v_hi[y]));
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) top_w = fmaxf(top_w, __shfl_xor_sync(kAll, top_w, off));
+            const float was = r + by;  // against the new m
+            const float rn = fmaxf(top_w - kTopLog, was), alpha = ex2(was - rn), beta = ex2(by);
+            if (k) {
+              nm[nc].y = -mn;
+              nr[nc].y = -rn;
+              l[nc].y *= beta;
+            } else {
+              nm[nc].x = -mn;
+              nr[nc].x = -rn;
+              l[nc].x *= beta;
+            }
+#pragma unroll
+            for (int c = 0; c < kSteps; ++c) {
+              o[c][nc][k] *= alpha;
+              o[c][nc][k + 2] *= alpha;
+            }
+          }
+      }
+      uint32_t w[kTurns][NC][2];  // B fragments of the weights
+#pragma unroll
+      for (int y = 0; y < kTurns; ++y)
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float2 d, e;
+            logs(y, nc, h, d, e);
+            l[nc] = __fadd2_rn(l[nc], make_float2(ex2(d.x), ex2(d.y)));
+            w[y][nc][h] = transpose8(pack_f16(ex2(e.x), ex2(e.y)));
+          }
+      // O^T += Vc^T W^T.  A lane's four codes of a chunk: tokens 2t and 2t + 1, dims 2g and 2g + 1; dims 2g are rows g of
+      // the product, dims 2g + 1 rows g + 8.
+#pragma unroll
+      for (int y = 0; y < kTurns; ++y) {
+        // Rows that nobody sees must not reach the product (0 times no number).
+        uint32_t keep_lo = kAll, keep_hi = kAll;  // of tokens 2t, 2t + 1 and of 2t + 8, 2t + 9
+        if (masked) {
+          const int left = rows.tokens - token0 - y * kBlockTokens - 2 * t;
+          keep_lo = left > 1 ? kAll : left > 0 ? 0xffffu : 0u;
+          keep_hi = left > 9 ? kAll : left > 8 ? 0xffffu : 0u;
         }
+#pragma unroll
+        for (int c = 0; c < kSteps / 2; ++c) {
+          uint32_t a[4][2];
+          if constexpr (!kEarly) ldsm_x4_t(((tile_at + y * T::kStage) ^ (32u * c)) + T::kTile, vx[y][c]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t x = __byte_perm(masked ? vx[y][c][k] & (k & 1 ? keep_hi : keep_lo) : vx[y][c][k], 0, 0x3120);
+            a[k][0] = fp8_halves(static_cast<uint16_t>(x));
+            a[k][1] = fp8_halves(static_cast<uint16_t>(x >> 16));
+          }
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc) {
+            mma_f16(o[2 * c][nc], a[0][0], a[0][1], a[1][0], a[1][1], w[y][nc][0], w[y][nc][1]);
+            mma_f16(o[2 * c + 1][nc], a[2][0], a[2][1], a[3][0], a[3][1], w[y][nc][0], w[y][nc][1]);
+          }
+        }
+      }
+      if constexpr (!kEarly) {
+        __syncwarp();
+#pragma unroll
+        for (int turn = 0; turn < kTurns; ++turn) send();
       }
     }
 
     // The pair's end here: O against m, l summed over the lanes that share a column.
+    float m[NC][2], sum[NC][2];
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
+        m[nc][k] = (k ? -nm[nc].y : -nm[nc].x) + kTopLog;  // (up to where the largest weight may be 2^8, not 2^15)
+        sum[nc][k] = (k ? l[nc].y : l[nc].x) * ex2(-kTopLog);
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) l[nc][k] += __shfl_xor_sync(kAll, l[nc][k], off);
-        const float f = m[nc][k] == kNone ? 0.f : ex2(r[nc][k] - kWeightShift);
+        for (int off = 4; off < 32; off <<= 1) sum[nc][k] += __shfl_xor_sync(kAll, sum[nc][k], off);
+        const float f = m[nc][k] == kNone ? 0.f : ex2((k ? -nr[nc].y : -nr[nc].x) - kTopLog);
 #pragma unroll
         for (int c = 0; c < kSteps; ++c) {
           o[c][nc][k] *= f;
@@ -602,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
 #pragma unroll
           for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) s_ml[place * T::kCols + nc * 8 + 2 * t + k] = make_float2(m[nc][k], l[nc][k]);
+            for (int k = 0; k < 2; ++k) s_ml[place * T::kCols + nc * 8 + 2 * t + k] = make_float2(m[nc][k], sum[nc][k]);
 #pragma unroll
         for (int part = 0; part < kSteps * NC / 2; ++part) {
           if (gives)
@@ -622,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
                   const float top = fmaxf(m[nc][k], y.x);
                   mine[nc][k] = ex2(m[nc][k] - top);
                   other[nc][k] = ex2(y.x - top);
-                  l[nc][k] = l[nc][k] * mine[nc][k] + y.y * other[nc][k];
+                  sum[nc][k] = sum[nc][k] * mine[nc][k] + y.y * other[nc][k];
                   m[nc][k] = top;
                 }
 #pragma unroll
@@ -654,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
             const int col = nc * 8 + 2 * t + k, i = col >> group_bits;
             if (i >= rows.count) continue;
             if (started && ended) {
-              const float inv = 1.f / l[nc][k];
+              const float inv = 1.f / sum[nc][k];
               __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
                                    (static_cast<int64_t>(rows.first + i) * p.num_q_heads + kvh * group + (col & (group - 1))) * D;
 #pragma unroll
@@ -666,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
 #pragma unroll
               for (int c = 0; c < kSteps; ++c)
                 *reinterpret_cast<float2*>(dst + 16 * c + 2 * g) = make_float2(o[c][nc][k], o[c][nc][k + 2]);
-              if (g == 0) p.ws_ml[state] = make_float2(m[nc][k], l[nc][k]);
+              if (g == 0) p.ws_ml[state] = make_float2(m[nc][k], sum[nc][k]);
             }
           }
       }
@@ -690,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
 #pragma unroll
           for (int c = 0; c < kSteps; ++c)
             *reinterpret_cast<float2*>(s_o + warp * kRing + col * D + 16 * c + 2 * g) = make_float2(o[c][nc][k], o[c][nc][k + 2]);
-          if (g == 0) s_ml[warp * T::kCols + col] = make_float2(m[nc][k], l[nc][k]);
+          if (g == 0) s_ml[warp * T::kCols + col] = make_float2(m[nc][k], sum[nc][k]);
         }
       __syncthreads();
       constexpr int kQuads = D / 4;

@@ -15,7 +15,9 @@ namespace pkv {
 namespace {
 
 // 2^(e - 127); e = 255 gives infinity (the append writes none above 247).
-__device__ __forceinline__ float fp8_scale(uint32_t e) { return __uint_as_float(e ? e << 23 : 0x00400000u); }
+__device__ __forceinline__ float fp8_scale(uint32_t e) { return __uint_as_float(max(e << 23, 0x00400000u)); }
+// e - 127 as a number, by way of 2^23 + e, whose last bit is one.
+__device__ __forceinline__ float fp8_power(uint32_t e) { return __uint_as_float(0x4b000000u | e) - 8388735.f; }
 
 // The exponent byte of a row whose largest finite magnitude has the bf16 bits `top`: the least e >= 0 with
 // top <= 448 * 2^(e - 127).  448 = 1.75 * 2^8, so the mantissa is compared with 0.75 * 128.
