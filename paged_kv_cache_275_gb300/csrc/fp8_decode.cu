@@ -17,10 +17,12 @@ constexpr float kClusterUnitUs = (D == 128 ? 1.05f : 1.4f) + 0.4f * (NC - 1);
 
 template <int D, int NC>
 struct Instance {
-  static constexpr int kMost = Few<D, NC>::smem(kFp8LaunchSeqs);
-  static constexpr int kClusterSmem = Few<D, NC>::smem(0);
-  static_assert(Few<D, NC>::kCtas * (kMost + 1024 + 256) <= 228 * 1024, "shared memory of an SM's CTAs");
-  static_assert(Few<D, NC>::kCols * (D * 4 + 8) <= Few<D, NC>::kOffScales, "a cluster CTA's state lies in the rings");
+  using Stream = Few<D, NC, false>;
+  using Cluster = Few<D, NC, true>;
+  static constexpr int kMost = Stream::smem(kFp8LaunchSeqs);
+  static constexpr int kClusterSmem = Cluster::smem(0);
+  static_assert(Stream::kCtas * (kMost + 1024 + 256) <= 228 * 1024, "shared memory of an SM's CTAs");
+  static_assert(Cluster::kCols * (D * 4 + 8) <= Cluster::kOffScales, "a cluster CTA's state lies in the rings");
   static constexpr auto kStream = &few_rows_fp8_kernel<D, NC, false>;
   static constexpr auto kCluster = &few_rows_fp8_kernel<D, NC, true>;
 
@@ -69,12 +71,12 @@ struct Instance {
   }
 
   static int choose(const int* counts, int64_t pairs, int max_blocks_per_seq) {
-    const int units = (max_blocks_per_seq + Few<D, NC>::kUnitTiles - 1) / Few<D, NC>::kUnitTiles;
+    const int units = (max_blocks_per_seq + Cluster::kUnitTiles - 1) / Cluster::kUnitTiles;
     int k = 0;
     while (k < 3 && (1 << k) < units && pairs <= counts[k + 1]) ++k;
     if (pairs > counts[k]) return 0;
     const float bytes_us =
-        kFilled / kBytesPerUs * static_cast<float>(pairs) * units * (2.f * Few<D, NC>::kUnitTiles * Few<D, NC>::kTile);
+        kFilled / kBytesPerUs * static_cast<float>(pairs) * units * (2.f * Cluster::kUnitTiles * Cluster::kTile);
     const float units_us = kClusterUnitUs<D, NC> * static_cast<float>(units) / (1 << k);
     return kClusterUs + (units_us > bytes_us ? units_us : bytes_us) <= kStreamUs + bytes_us ? 1 << k : 0;
   }
@@ -107,7 +109,7 @@ struct Instance {
       const cudaLaunchConfig_t cfg = cluster_config(pairs, p.cluster_ctas, stream, attr);
       return cudaLaunchKernelEx(&cfg, kCluster, p);
     }
-    e = launch_pdl(kStream, dim3(p.num_pieces), dim3(kThreads), Few<D, NC>::smem(p.num_seqs), stream, p);
+    e = launch_pdl(kStream, dim3(p.num_pieces), dim3(kThreads), Stream::smem(p.num_seqs), stream, p);
     if (e != cudaSuccess) return e;
     const unsigned cols = p.state_rows;
     // A pair has about as many states as pieces come to it.  Up to twice the eight that a warp fetches at once it takes them

@@ -51,22 +51,26 @@ constexpr int kMostCluster = 8;
 constexpr float kNone = -3.0e38f;  // the reference of a row that has seen no token
 constexpr float kTopLog = 7.f, kMostLog = 15.f;  // the largest of a row's weights is brought to 2^7 and may grow to 2^15
 
-template <int D, int NC>
+template <int D, int NC, bool kCluster>
 struct Few {
   static constexpr int kCols = 8 * NC;
   static constexpr int kTile = kBlockTokens * D;           // bytes of one tile of K (or V)
   static constexpr int kTurns = 128 / D;                   // tiles of a unit that a warp takes, one after the other
   static constexpr int kUnitTiles = kWarps * kTurns;       // (block, kv head) tiles of a unit
   static constexpr int kCtas = NC == 1 ? 2 : 1;            // per SM
-  static constexpr int kStages = 6 * kTurns / kCtas;       // tiles of a warp's ring
+  static constexpr bool kAhead = D == 128 && NC == 3 && !kCluster;  // the next tile's scores beside this one's softmax
+  static constexpr int kStages = kAhead ? 5 : 6 * kTurns / kCtas;   // tiles of a warp's ring
   static constexpr int kStage = 2 * kTile;                 // K, V
   static constexpr int kScales = 2 * kBlockTokens;         // the exponents of both
   static constexpr int kOffScales = kWarps * kStages * kStage;
   static constexpr int kOffExchange = kOffScales + kWarps * kStages * kScales;
   static constexpr int kExchange = kWarps / 2 * 32 * 32;  // 8 values a lane of four warps
-  static constexpr int kOffMl = kOffExchange + kExchange;
+  static constexpr int kOffQ = kOffExchange + kExchange;  // a warp's fragments of q
+  static constexpr int kQ = kAhead ? NC * D / 16 * 2 * 32 * 4 : 0;
+  static constexpr int kOffMl = kOffQ + kWarps * kQ;
   static constexpr int kMl = (kWarps + 1) * kCols * 8;  // a cluster CTA's: of every warp, and joined
   static constexpr int kOffSeq = kOffMl + kMl;  // units before each sequence, [num_seqs + 1]; tokens, [num_seqs]
+  __device__ static int next(int place) { return place + kTurns == kStages ? 0 : place + kTurns; }  // of a unit's first tile
   static constexpr int smem(int num_seqs) { return kOffSeq + (2 * num_seqs + 1) * 4; }
 };
 
@@ -97,6 +101,11 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
+}
+__device__ __forceinline__ uint4 lds_128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -182,10 +191,255 @@ struct Walk {
   int b, heads, unit, units;
 };
 
+// A (sequence, kv head) in a warp's registers.
 template <int D, int NC, bool kCluster>
-__global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
+struct Pair {
+  using T = Few<D, NC, kCluster>;
+  static constexpr int kTurns = T::kTurns;
+  static constexpr int kSteps = D / 16;  // 16-byte chunks of a row of codes: 16 dims, the depth of a product
+  // With few tiles a warp it is their latency that counts: V's codes, too, are taken into registers first, and the tiles'
+  // places are free for the next copies.  With many it is registers (V's codes first: 128 sequences 107 -> 110 us, drafts of
+  // up to five tokens 106 -> 128; one sequence 10.2 -> 8.9).
+  static constexpr bool kEarly = kCluster;
+  // Scores come in two sums where there would be a single chain of products.
+  static constexpr int sums(int used) { return used * kTurns == 1 ? 2 : 1; }
+
+  uint32_t ld_at;               // this lane's address for ldmatrix in the ring's first tile
+  const unsigned char* scales;  // the ring's exponents
+  uint32_t q_at;                // kAhead: this lane's fragments of q in shared memory
+  int g, t;                     // lane / 4, lane % 4: row g and columns 2t, 2t + 1 of an accumulator
+  int group_bits;
+  int tokens, first_limit;    // tokens that the last and the first row see
+  uint32_t q[NC][kSteps][2];  // B fragments of the rows
+  float2 q_scale[NC];         // of columns 2t, 2t + 1: what takes a product to a score
+  float2 nm[NC], nr[NC], l[NC];  // of those columns: -m, -r, and l
+  float o[kSteps][NC][4];
+  uint32_t vx[kTurns][kSteps / 2][4];
+
+  // S^T = Kc q^T of the tiles at `place`.  Chunk c of a row: its 16 codes are the product's depth, in the order 4t, 4t + 1,
+  // 4t + 2, 4t + 3 of a lane's four, as q's fragments are.
+  template <int kUsed>
+  __device__ __forceinline__ void products(int place, float (&sum)[kTurns][sums(kUsed)][kUsed][4]) {
+    const uint32_t tile_at = ld_at + place * T::kStage;
+    uint32_t kx[kTurns][kSteps / 2][4];
+    if constexpr (kEarly) {
+#pragma unroll
+      for (int y = 0; y < kTurns; ++y) {
+#pragma unroll
+        for (int c = 0; c < kSteps / 2; ++c) ldsm_x4((tile_at + y * T::kStage) ^ (32u * c), kx[y][c]);
+#pragma unroll
+        for (int c = 0; c < kSteps / 2; ++c) ldsm_x4_t(((tile_at + y * T::kStage) ^ (32u * c)) + T::kTile, vx[y][c]);
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < kTurns; ++y) {
+#pragma unroll
+      for (int x = 0; x < sums(kUsed); ++x)
+#pragma unroll
+        for (int nc = 0; nc < kUsed; ++nc)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sum[y][x][nc][k] = 0.f;
+#pragma unroll
+      for (int c = 0; c < kSteps / 2; ++c) {
+        uint32_t a[4][2];
+        if constexpr (!kEarly) ldsm_x4((tile_at + y * T::kStage) ^ (32u * c), kx[y][c]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          a[k][0] = fp8_halves(static_cast<uint16_t>(kx[y][c][k]));
+          a[k][1] = fp8_halves(static_cast<uint16_t>(kx[y][c][k] >> 16));
+        }
+#pragma unroll
+        for (int nc = 0; nc < kUsed; ++nc) {
+          uint4 b = make_uint4(q[nc][2 * c][0], q[nc][2 * c][1], q[nc][2 * c + 1][0], q[nc][2 * c + 1][1]);
+          if constexpr (T::kAhead)
+            b = lds_128(q_at + (nc * kSteps / 2 + c) * 512);
+          mma_f16(sum[y][0][nc], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
+          mma_f16(sum[y][sums(kUsed) - 1][nc], a[2][0], a[3][0], a[2][1], a[3][1], b.z, b.w);
+        }
+      }
+    }
+  }
+  // The softmax of the tiles at `place`, from token0 on, and O^T += Vc^T W^T.
+  template <int kUsed, typename Send>
+  __device__ __forceinline__ void weigh(int place, int token0, const float (&sum)[kTurns][sums(kUsed)][kUsed][4], Send& send) {
+    const uint32_t tile_at = ld_at + place * T::kStage;
+    float v_lo[kTurns], v_hi[kTurns], s[kTurns][kUsed][4];
+#pragma unroll
+    for (int y = 0; y < kTurns; ++y) {
+      const unsigned char* sc = scales + (place + y) * T::kScales;
+      const float k_lo = fp8_scale(sc[g]), k_hi = fp8_scale(sc[g + 8]);
+      v_lo[y] = fp8_power(sc[16 + g]);
+      v_hi[y] = fp8_power(sc[24 + g]);
+#pragma unroll
+      for (int nc = 0; nc < kUsed; ++nc)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // rows g and g + 8: tokens
+          float2 x = make_float2(sum[y][0][nc][2 * h], sum[y][0][nc][2 * h + 1]);
+          if (sums(kUsed) == 2) x = __fadd2_rn(x, make_float2(sum[y][sums(kUsed) - 1][nc][2 * h], sum[y][sums(kUsed) - 1][nc][2 * h + 1]));
+          const float by = h ? k_hi : k_lo;
+          x = __fmul2_rn(x, __fmul2_rn(q_scale[nc], make_float2(by, by)));
+          s[y][nc][2 * h] = x.x;
+          s[y][nc][2 * h + 1] = x.y;
+        }
+    }
+    if constexpr (kEarly) {
+      __syncwarp();  // the tiles have been read
+#pragma unroll
+      for (int turn = 0; turn < kTurns; ++turn) send();
+    }
+    const bool masked = token0 + kTurns * kBlockTokens > first_limit;
+    if (masked) {
+#pragma unroll
+      for (int y = 0; y < kTurns; ++y)
+#pragma unroll
+        for (int nc = 0; nc < kUsed; ++nc)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (token0 + y * kBlockTokens + g + (k < 2 ? 0 : 8) >= first_limit + ((nc * 8 + 2 * t + (k & 1)) >> group_bits))
+              s[y][nc][k] = -INFINITY;
+    }
+    // Of tile y, column block nc and row half h: s - m, and (s - m) + ve - r.
+    auto logs = [&](int y, int nc, int h, float2& d, float2& e) {
+      const float v = h ? v_hi[y] : v_lo[y];
+      d = __fadd2_rn(make_float2(s[y][nc][2 * h], s[y][nc][2 * h + 1]), nm[nc]);
+      e = __fadd2_rn(d, __fadd2_rn(make_float2(v, v), nr[nc]));
+    };
+    float most = -INFINITY;
+#pragma unroll
+    for (int y = 0; y < kTurns; ++y)
+#pragma unroll
+      for (int nc = 0; nc < kUsed; ++nc)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float2 d, e;
+          logs(y, nc, h, d, e);
+          most = fmaxf(fmaxf(most, fmaxf(d.x, d.y)), fmaxf(e.x, e.y));
+        }
+    if (__any_sync(kAll, most > kMostLog)) {  // seldom but for a pair's first block
+#pragma unroll
+      for (int nc = 0; nc < kUsed; ++nc)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float top = -INFINITY, top_w = -INFINITY;
+#pragma unroll
+          for (int y = 0; y < kTurns; ++y) top = fmaxf(top, fmaxf(s[y][nc][k], s[y][nc][k + 2]));
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+          const float m = k ? -nm[nc].y : -nm[nc].x, r = k ? -nr[nc].y : -nr[nc].x;
+          const float mn = fmaxf(top - kTopLog, m), by = m - mn;
+#pragma unroll
+          for (int y = 0; y < kTurns; ++y) top_w = fmaxf(top_w, fmaxf(s[y][nc][k] - mn + v_lo[y], s[y][nc][k + 2] - mn + v_hi[y]));
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) top_w = fmaxf(top_w, __shfl_xor_sync(kAll, top_w, off));
+          const float was = r + by;  // against the new m
+          const float rn = fmaxf(top_w - kTopLog, was), alpha = ex2(was - rn), beta = ex2(by);
+          if (k) {
+            nm[nc].y = -mn;
+            nr[nc].y = -rn;
+            l[nc].y *= beta;
+          } else {
+            nm[nc].x = -mn;
+            nr[nc].x = -rn;
+            l[nc].x *= beta;
+          }
+#pragma unroll
+          for (int c = 0; c < kSteps; ++c) {
+            o[c][nc][k] *= alpha;
+            o[c][nc][k + 2] *= alpha;
+          }
+        }
+    }
+    uint32_t w[kTurns][kUsed][2];  // B fragments of the weights
+#pragma unroll
+    for (int y = 0; y < kTurns; ++y)
+#pragma unroll
+      for (int nc = 0; nc < kUsed; ++nc)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float2 d, e;
+          logs(y, nc, h, d, e);
+          l[nc] = __fadd2_rn(l[nc], make_float2(ex2(d.x), ex2(d.y)));
+          w[y][nc][h] = transpose8(pack_f16(ex2(e.x), ex2(e.y)));
+        }
+    // O^T += Vc^T W^T.  A lane's four codes of a chunk: tokens 2t and 2t + 1, dims 2g and 2g + 1; dims 2g are rows g of
+    // the product, dims 2g + 1 rows g + 8.
+#pragma unroll
+    for (int y = 0; y < kTurns; ++y) {
+      // Rows that nobody sees must not reach the product (0 times no number).
+      uint32_t keep_lo = kAll, keep_hi = kAll;  // of tokens 2t, 2t + 1 and of 2t + 8, 2t + 9
+      if (masked) {
+        const int left = tokens - token0 - y * kBlockTokens - 2 * t;
+        keep_lo = left > 1 ? kAll : left > 0 ? 0xffffu : 0u;
+        keep_hi = left > 9 ? kAll : left > 8 ? 0xffffu : 0u;
+      }
+#pragma unroll
+      for (int c = 0; c < kSteps / 2; ++c) {
+        uint32_t a[4][2];
+        if constexpr (!kEarly) ldsm_x4_t(((tile_at + y * T::kStage) ^ (32u * c)) + T::kTile, vx[y][c]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t x = __byte_perm(masked ? vx[y][c][k] & (k & 1 ? keep_hi : keep_lo) : vx[y][c][k], 0, 0x3120);
+          a[k][0] = fp8_halves(static_cast<uint16_t>(x));
+          a[k][1] = fp8_halves(static_cast<uint16_t>(x >> 16));
+        }
+#pragma unroll
+        for (int nc = 0; nc < kUsed; ++nc) {
+          mma_f16(o[2 * c][nc], a[0][0], a[0][1], a[1][0], a[1][1], w[y][nc][0], w[y][nc][1]);
+          mma_f16(o[2 * c + 1][nc], a[2][0], a[2][1], a[3][0], a[3][1], w[y][nc][0], w[y][nc][1]);
+        }
+      }
+    }
+    if constexpr (!kEarly) {
+      __syncwarp();
+#pragma unroll
+      for (int turn = 0; turn < kTurns; ++turn) send();
+    }
+  }
+  // The pair's units of this warp, `mine` of them from token0 on, `step` tokens apart.
+  template <int kUsed, typename Send>
+  __device__ __forceinline__ void units(int token0, int mine, int step, int& stage, Send& send) {
+    if constexpr (T::kAhead) {
+      float sum[kTurns][sums(kUsed)][kUsed][4];
+      if (mine > 0) {
+        copies_wait<T::kStages - kTurns>();
+        __syncwarp();
+        products<kUsed>(stage, sum);
+      }
+      for (int u = 0; u < mine; ++u, token0 += step) {
+        const int place = stage;
+        stage = T::next(stage);
+        float next[kTurns][sums(kUsed)][kUsed][4];
+        copies_wait<T::kStages - 2 * kTurns>();
+        __syncwarp();
+        products<kUsed>(u + 1 < mine ? stage : place, next);  // (without a branch, so that they run beside the softmax)
+        weigh<kUsed>(place, token0, sum, send);
+#pragma unroll
+        for (int y = 0; y < kTurns; ++y)
+#pragma unroll
+          for (int x = 0; x < sums(kUsed); ++x)
+#pragma unroll
+            for (int nc = 0; nc < kUsed; ++nc)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) sum[y][x][nc][k] = next[y][x][nc][k];
+      }
+    } else {
+      for (int u = 0; u < mine; ++u, token0 += step) {
+        const int place = stage;
+        stage = T::next(stage);
+        copies_wait<T::kStages - kTurns>();
+        __syncwarp();
+        float sum[kTurns][sums(kUsed)][kUsed][4];
+        products<kUsed>(place, sum);
+        weigh<kUsed>(place, token0, sum, send);
+      }
+    }
+  }
+};
+
+template <int D, int NC, bool kCluster>
+__global__ void __launch_bounds__(kThreads, Few<D, NC, kCluster>::kCtas)
     few_rows_fp8_kernel(const Fp8AttentionParams p) {
-  using T = Few<D, NC>;
+  using T = Few<D, NC, kCluster>;
   constexpr int kTurns = T::kTurns;
   constexpr int kSteps = D / 16;  // 16-byte chunks of a row of codes: 16 dims, the depth of a product
   extern __shared__ __align__(128) unsigned char smem[];
@@ -383,25 +637,31 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
   for (int n = kCluster ? 0 : n0; kCluster || n < n1;) {
     const Rows rows = kCluster ? pair : rows_of(p, at.b);
     const int kvh = at.heads * hc + head_of;
-    const int first_limit = rows.tokens - rows.count + 1;  // tokens that the first row sees
     const int count = kCluster ? n1 : min(at.units - at.unit, n1 - n);  // units of the pair here
-    uint32_t q[NC][kSteps][2];  // B fragments of the rows
-    float2 q_scale[NC];         // of columns 2t, 2t + 1: what takes a product to a score
-    float2 nm[NC], nr[NC], l[NC];  // of columns 2t, 2t + 1: -m, -r, and l
-    float o[kSteps][NC][4];
+    Pair<D, NC, kCluster> x;
+    x.ld_at = ld_at;
+    x.scales = smem + T::kOffScales + warp * T::kStages * T::kScales;
+    x.q_at = base + T::kOffQ + warp * T::kQ + lane * 16;
+    x.g = g;
+    x.t = t;
+    x.group_bits = group_bits;
+    x.tokens = rows.tokens;
+    x.first_limit = rows.tokens - rows.count + 1;
+    auto &q = x.q;
+    auto &o = x.o;
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
       const int col = nc * 8 + g, i = col >> group_bits;
       float top = 0.f;
 #pragma unroll
       for (int c = 0; c < kSteps; ++c) {
-        uint2 x = make_uint2(0u, 0u);
+        uint2 y = make_uint2(0u, 0u);
         if (i < rows.count)
-          x = __ldg(reinterpret_cast<const uint2*>(
+          y = __ldg(reinterpret_cast<const uint2*>(
               static_cast<const __nv_bfloat16*>(p.q) +
               (static_cast<int64_t>(rows.first + i) * p.num_q_heads + kvh * group + (col & (group - 1))) * D + 16 * c + 4 * t));
-        q[nc][c][0] = x.x;
-        q[nc][c][1] = x.y;
+        q[nc][c][0] = y.x;
+        q[nc][c][1] = y.y;
       }
 #pragma unroll
       for (int c = 0; c < kSteps; ++c)
@@ -419,9 +679,9 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
         for (int k = 0; k < 2; ++k)
           q[nc][c][k] = pack_f16(__uint_as_float(q[nc][c][k] << 16) * by, __uint_as_float(q[nc][c][k] & 0xffff0000u) * by);
       const float back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23) * p.qscale;
-      q_scale[nc] = make_float2(__shfl_sync(kAll, back, 2 * t * 4), __shfl_sync(kAll, back, (2 * t + 1) * 4));
-      nm[nc] = nr[nc] = make_float2(-kNone, -kNone);
-      l[nc] = make_float2(0.f, 0.f);
+      x.q_scale[nc] = make_float2(__shfl_sync(kAll, back, 2 * t * 4), __shfl_sync(kAll, back, (2 * t + 1) * 4));
+      x.nm[nc] = x.nr[nc] = make_float2(-kNone, -kNone);
+      x.l[nc] = make_float2(0.f, 0.f);
     }
 #pragma unroll
     for (int c = 0; c < kSteps; ++c)
@@ -430,195 +690,28 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[c][nc][k] = 0.f;
 
-    int token0 = (at.unit * nb + place_of * kTurns) * kBlockTokens;  // of this warp's blocks
-    for (int u = 0; u < count; ++u, token0 += stride * nb * kBlockTokens) {
-      copies_wait<T::kStages - kTurns>();
-      __syncwarp();
-      const int place = stage;
-      if ((stage += kTurns) == T::kStages) stage = 0;
-      if (token0 >= rows.tokens) {
+    if constexpr (T::kAhead) {
+      // The fragments of q make room for a second tile's scores.
+      uint4* own = reinterpret_cast<uint4*>(smem + T::kOffQ + warp * T::kQ) + lane;
 #pragma unroll
-        for (int turn = 0; turn < kTurns; ++turn) send();
-        continue;
-      }
-      // All of a warp's tiles of a unit at a time (D = 64: two, where one after the other XX).  What lies in the second one's
-      // place past the last token is masked like the rows past it.
-      // With few tiles a warp it is their latency that counts: V's codes, too, are taken into registers first, and the tiles'
-      // places are free for the next copies.  With many it is registers (V's codes first: 128 sequences 107 -> 110 us, drafts
-      // of up to five tokens 106 -> 128; one sequence 10.2 -> 8.9).
-      constexpr bool kEarly = kCluster;
-      float k_lo[kTurns], k_hi[kTurns], v_lo[kTurns], v_hi[kTurns];
-      uint32_t kx[kTurns][kSteps / 2][4], vx[kTurns][kSteps / 2][4];
+      for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
-      for (int y = 0; y < kTurns; ++y) {
-        const unsigned char* sc = smem + T::kOffScales + (warp * T::kStages + place + y) * T::kScales;
-        k_lo[y] = fp8_scale(sc[g]);
-        k_hi[y] = fp8_scale(sc[g + 8]);
-        v_lo[y] = fp8_power(sc[16 + g]);
-        v_hi[y] = fp8_power(sc[24 + g]);
-      }
-      const uint32_t tile_at = ld_at + place * T::kStage;
-      if constexpr (kEarly) {
+        for (int c = 0; c < kSteps / 2; ++c)
+          own[(nc * kSteps / 2 + c) * 32] = make_uint4(q[nc][2 * c][0], q[nc][2 * c][1], q[nc][2 * c + 1][0], q[nc][2 * c + 1][1]);
+    }
+
+    // All of a warp's tiles of a unit at a time.  What lies in the second one's place past the last token is masked like the rows
+    // past it.  Of the column blocks those that the sequence's rows fill (drafts of one to five tokens: XX us with all of them).
+    const int token0 = (at.unit * nb + place_of * kTurns) * kBlockTokens, step = stride * nb * kBlockTokens;
+    const int mine = token0 < rows.tokens ? min(count, (rows.tokens - token0 - 1) / step + 1) : 0;  // units with such blocks
+    const int cols = rows.count << group_bits;
+    if (NC == 1 || cols <= 8) x.template units<1>(token0, mine, step, stage, send);
+    else if (NC == 2 || cols <= 16) x.template units<NC < 2 ? NC : 2>(token0, mine, step, stage, send);
+    else x.template units<NC>(token0, mine, step, stage, send);
+    for (int u = mine; u < count; ++u) {  // at most one, the pair's last
+      stage = T::next(stage);
 #pragma unroll
-        for (int y = 0; y < kTurns; ++y) {
-#pragma unroll
-          for (int c = 0; c < kSteps / 2; ++c) ldsm_x4((tile_at + y * T::kStage) ^ (32u * c), kx[y][c]);
-#pragma unroll
-          for (int c = 0; c < kSteps / 2; ++c) ldsm_x4_t(((tile_at + y * T::kStage) ^ (32u * c)) + T::kTile, vx[y][c]);
-        }
-      }
-      // S^T = Kc q^T.  Chunk c of a row: its 16 codes are the product's depth, in the order 4t, 4t + 1, 4t + 2, 4t + 3 of
-      // a lane's four, as q's fragments are.  (In two sums where there would be a single chain of products.)
-      constexpr int kSums = NC * kTurns == 1 ? 2 : 1;
-      float s[kTurns][NC][4];
-#pragma unroll
-      for (int y = 0; y < kTurns; ++y) {
-        float sum[kSums][NC][4];
-#pragma unroll
-        for (int x = 0; x < kSums; ++x)
-#pragma unroll
-          for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) sum[x][nc][k] = 0.f;
-#pragma unroll
-        for (int c = 0; c < kSteps / 2; ++c) {
-          uint32_t a[4][2];
-          if constexpr (!kEarly) ldsm_x4((tile_at + y * T::kStage) ^ (32u * c), kx[y][c]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            a[k][0] = fp8_halves(static_cast<uint16_t>(kx[y][c][k]));
-            a[k][1] = fp8_halves(static_cast<uint16_t>(kx[y][c][k] >> 16));
-          }
-#pragma unroll
-          for (int nc = 0; nc < NC; ++nc) {
-            mma_f16(sum[0][nc], a[0][0], a[1][0], a[0][1], a[1][1], q[nc][2 * c][0], q[nc][2 * c][1]);
-            mma_f16(sum[kSums - 1][nc], a[2][0], a[3][0], a[2][1], a[3][1], q[nc][2 * c + 1][0], q[nc][2 * c + 1][1]);
-          }
-        }
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {  // rows g and g + 8: tokens
-            float2 x = make_float2(sum[0][nc][2 * h], sum[0][nc][2 * h + 1]);
-            if (kSums == 2) x = __fadd2_rn(x, make_float2(sum[kSums - 1][nc][2 * h], sum[kSums - 1][nc][2 * h + 1]));
-            const float by = h ? k_hi[y] : k_lo[y];
-            x = __fmul2_rn(x, __fmul2_rn(q_scale[nc], make_float2(by, by)));
-            s[y][nc][2 * h] = x.x;
-            s[y][nc][2 * h + 1] = x.y;
-          }
-      }
-      if constexpr (kEarly) {
-        __syncwarp();  // the tiles have been read
-#pragma unroll
-        for (int turn = 0; turn < kTurns; ++turn) send();
-      }
-      const bool masked = token0 + kTurns * kBlockTokens > first_limit;
-      if (masked) {
-#pragma unroll
-        for (int y = 0; y < kTurns; ++y)
-#pragma unroll
-          for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (token0 + y * kBlockTokens + g + (k < 2 ? 0 : 8) >= first_limit + ((nc * 8 + 2 * t + (k & 1)) >> group_bits))
-                s[y][nc][k] = -INFINITY;
-      }
-      // Of tile y, column block nc and row half h: s - m, and (s - m) + ve - r.
-      auto logs = [&](int y, int nc, int h, float2& d, float2& e) {
-        const float v = h ? v_hi[y] : v_lo[y];
-        d = __fadd2_rn(make_float2(s[y][nc][2 * h], s[y][nc][2 * h + 1]), nm[nc]);
-        e = __fadd2_rn(d, __fadd2_rn(make_float2(v, v), nr[nc]));
-      };
-      float most = -INFINITY;
-#pragma unroll
-      for (int y = 0; y < kTurns; ++y)
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float2 d, e;
-            logs(y, nc, h, d, e);
-            most = fmaxf(fmaxf(most, fmaxf(d.x, d.y)), fmaxf(e.x, e.y));
-          }
-      if (__any_sync(kAll, most > kMostLog)) {  // seldom but for a pair's first block
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float top = -INFINITY, top_w = -INFINITY;
-#pragma unroll
-            for (int y = 0; y < kTurns; ++y) top = fmaxf(top, fmaxf(s[y][nc][k], s[y][nc][k + 2]));
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
-            const float m = k ? -nm[nc].y : -nm[nc].x, r = k ? -nr[nc].y : -nr[nc].x;
-            const float mn = fmaxf(top - kTopLog, m), by = m - mn;
-#pragma unroll
-            for (int y = 0; y < kTurns; ++y) top_w = fmaxf(top_w, fmaxf(s[y][nc][k] - mn + v_lo[y], s[y][nc][k + 2] - mn + v_hi[y]));
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) top_w = fmaxf(top_w, __shfl_xor_sync(kAll, top_w, off));
-            const float was = r + by;  // against the new m
-            const float rn = fmaxf(top_w - kTopLog, was), alpha = ex2(was - rn), beta = ex2(by);
-            if (k) {
-              nm[nc].y = -mn;
-              nr[nc].y = -rn;
-              l[nc].y *= beta;
-            } else {
-              nm[nc].x = -mn;
-              nr[nc].x = -rn;
-              l[nc].x *= beta;
-            }
-#pragma unroll
-            for (int c = 0; c < kSteps; ++c) {
-              o[c][nc][k] *= alpha;
-              o[c][nc][k + 2] *= alpha;
-            }
-          }
-      }
-      uint32_t w[kTurns][NC][2];  // B fragments of the weights
-#pragma unroll
-      for (int y = 0; y < kTurns; ++y)
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float2 d, e;
-            logs(y, nc, h, d, e);
-            l[nc] = __fadd2_rn(l[nc], make_float2(ex2(d.x), ex2(d.y)));
-            w[y][nc][h] = transpose8(pack_f16(ex2(e.x), ex2(e.y)));
-          }
-      // O^T += Vc^T W^T.  A lane's four codes of a chunk: tokens 2t and 2t + 1, dims 2g and 2g + 1; dims 2g are rows g of
-      // the product, dims 2g + 1 rows g + 8.
-#pragma unroll
-      for (int y = 0; y < kTurns; ++y) {
-        // Rows that nobody sees must not reach the product (0 times no number).
-        uint32_t keep_lo = kAll, keep_hi = kAll;  // of tokens 2t, 2t + 1 and of 2t + 8, 2t + 9
-        if (masked) {
-          const int left = rows.tokens - token0 - y * kBlockTokens - 2 * t;
-          keep_lo = left > 1 ? kAll : left > 0 ? 0xffffu : 0u;
-          keep_hi = left > 9 ? kAll : left > 8 ? 0xffffu : 0u;
-        }
-#pragma unroll
-        for (int c = 0; c < kSteps / 2; ++c) {
-          uint32_t a[4][2];
-          if constexpr (!kEarly) ldsm_x4_t(((tile_at + y * T::kStage) ^ (32u * c)) + T::kTile, vx[y][c]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t x = __byte_perm(masked ? vx[y][c][k] & (k & 1 ? keep_hi : keep_lo) : vx[y][c][k], 0, 0x3120);
-            a[k][0] = fp8_halves(static_cast<uint16_t>(x));
-            a[k][1] = fp8_halves(static_cast<uint16_t>(x >> 16));
-          }
-#pragma unroll
-          for (int nc = 0; nc < NC; ++nc) {
-            mma_f16(o[2 * c][nc], a[0][0], a[0][1], a[1][0], a[1][1], w[y][nc][0], w[y][nc][1]);
-            mma_f16(o[2 * c + 1][nc], a[2][0], a[2][1], a[3][0], a[3][1], w[y][nc][0], w[y][nc][1]);
-          }
-        }
-      }
-      if constexpr (!kEarly) {
-        __syncwarp();
-#pragma unroll
-        for (int turn = 0; turn < kTurns; ++turn) send();
-      }
+      for (int turn = 0; turn < kTurns; ++turn) send();
     }
 
     // The pair's end here: O against m, l summed over the lanes that share a column.
@@ -627,11 +720,11 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
     for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        m[nc][k] = (k ? -nm[nc].y : -nm[nc].x) + kTopLog;  // (up to where the largest weight may be 2^8, not 2^15)
-        sum[nc][k] = (k ? l[nc].y : l[nc].x) * ex2(-kTopLog);
+        m[nc][k] = (k ? -x.nm[nc].y : -x.nm[nc].x) + kTopLog;  // (up to where the largest weight may be 2^8, not 2^15)
+        sum[nc][k] = (k ? x.l[nc].y : x.l[nc].x) * ex2(-kTopLog);
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) sum[nc][k] += __shfl_xor_sync(kAll, sum[nc][k], off);
-        const float f = m[nc][k] == kNone ? 0.f : ex2((k ? -nr[nc].y : -nr[nc].x) - kTopLog);
+        const float f = m[nc][k] == kNone ? 0.f : ex2((k ? -x.nr[nc].y : -x.nr[nc].x) - kTopLog);
 #pragma unroll
         for (int c = 0; c < kSteps; ++c) {
           o[c][nc][k] *= f;
@@ -742,7 +835,6 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC>::kCtas)
         }
       __syncthreads();
       constexpr int kQuads = D / 4;
-      const int cols = rows.count * group;
       for (int x = tid; x < cols * kQuads; x += kThreads) {
         const int dim = x % kQuads * 4, col = x / kQuads;
         float top = kNone, sum = 0.f;
