@@ -1275,6 +1275,7 @@ pkv_status few_rows_fp8(pkv::Fp8AttentionParams p, int32_t head_dim, void* works
     const pkv::Fp8FewPlan plan(s.num_seqs, p.num_kv_heads, head_dim, p.max_blocks_per_seq, rows, sms);
     s.unit_heads = plan.unit_heads;
     s.num_pieces = plan.num_pieces;
+    s.unit_costs = plan.unit_costs;
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     s.ws_records = reinterpret_cast<int*>(ws);
     s.ws_ml = reinterpret_cast<float2*>(ws + plan.ml);

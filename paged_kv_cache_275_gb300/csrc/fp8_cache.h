@@ -85,6 +85,7 @@ struct Fp8AttentionParams {
   int cluster_ctas;     // CTAs a (sequence, kv head), joined through their shared memory; 0: the stream form, all below
   int unit_heads;       // kv heads of a unit: 8, 4, 2 or 1
   int num_pieces;       // most pieces that the stream of units is cut into
+  int unit_costs;       // whether units cost by their rows, not all the same
   int state_rows;       // rows of a state: most query tokens * q heads per kv head
   int* ws_records;      // [num_seqs][head groups][2]: the piece of the first unit (times 2, plus its state slot), of the last
   float2* ws_ml;        // [piece][2 slots][unit_heads][state_rows]: (m in base 2, l)
@@ -102,6 +103,7 @@ inline int fp8_columns(int rows) { return rows <= kFp8MostRows ? (rows + 7) / 8 
 // Its workspace and how its work is cut.
 struct Fp8FewPlan {
   int unit_heads, num_pieces;
+  bool unit_costs;  // (their sum fits 31 bits)
   size_t ml, states, bytes;  // byte offsets of the parts behind the records, and the sum
   Fp8FewPlan(int num_seqs, int num_kv_heads, int head_dim, int max_blocks_per_seq, int state_rows, int sms) {
     const int seqs = num_seqs < kFp8LaunchSeqs ? num_seqs : kFp8LaunchSeqs;
@@ -109,6 +111,7 @@ struct Fp8FewPlan {
     while (num_kv_heads % unit_heads) unit_heads /= 2;
     const int blocks = (head_dim == 128 ? 8 : 16) / unit_heads;
     const int64_t units = static_cast<int64_t>(seqs) * (num_kv_heads / unit_heads) * ((max_blocks_per_seq + blocks - 1) / blocks);
+    unit_costs = units < (int64_t{1} << 27);
     const int64_t ctas = static_cast<int64_t>(sms) * (fp8_columns(state_rows) == 1 ? 2 : 1);
     num_pieces = static_cast<int>(units < 1 ? 1 : units < ctas ? units : ctas);
     const size_t rows = static_cast<size_t>(num_pieces) * 2 * unit_heads * state_rows;

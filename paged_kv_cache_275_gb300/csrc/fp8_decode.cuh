@@ -18,12 +18,13 @@
 //
 // Work.  The batch's blocks form one stream of units of 32 KB of K and V, eight (block, kv head) tiles of 128 dims or sixteen
 // of 64: all eight heads of a block (of two), or two (four) blocks of four heads, and so on.  The stream is cut into equal
-// contiguous pieces, one a CTA, so that every CTA moves the same bytes whatever the lengths.  Each of a CTA's eight warps takes
+// contiguous pieces, one a CTA (two an SM for up to eight rows), so that every CTA has the same work whatever the lengths: the
+// same bytes, or, where sequences differ in their rows, units that cost by them.  Each of a CTA's eight warps takes
 // its tile of every unit, which are neighbours in memory, through a ring of its own: the lanes copy it in 16-byte pieces
 // (cp.async), placed so that ldmatrix reads without bank conflicts.  So no warp waits for another, but where the warps of a
 // head join their states at a pair's end.  (By tensor copies, as large as a unit for eight heads, a CTA has to wait for all its
 // warps at every unit, and a unit of one head is 24 copies, whose number bounds an SM: 128 sequences of 2048 tokens of one head
-// took 28.7 us so, XX like this; of eight heads XX and XX.)  A (sequence, heads) pair cut by a piece's border leaves partial
+// took 28.7 us so, 17.7 like this; of eight heads 104 and 107.)  A (sequence, heads) pair cut by a piece's border leaves partial
 // states (m, l, O) that a second kernel joins.
 //
 // Few pairs.  A call of few (sequence, kv head) pairs takes a thread-block cluster a pair instead: its units, of one head, are
@@ -58,7 +59,9 @@ struct Few {
   static constexpr int kTurns = 128 / D;                   // tiles of a unit that a warp takes, one after the other
   static constexpr int kUnitTiles = kWarps * kTurns;       // (block, kv head) tiles of a unit
   static constexpr int kCtas = NC == 1 ? 2 : 1;            // per SM
-  static constexpr bool kAhead = D == 128 && NC == 3 && !kCluster;  // the next tile's scores beside this one's softmax
+  // The next tile's scores beside this one's softmax: with so many registers a warp is alone with one other on its scheduler
+  // (64 x 6 tokens 110 -> 103 us; with two column blocks 84.7 -> 86.2, with one 1000 short sequences 49.0 -> 50.8).
+  static constexpr bool kAhead = D == 128 && NC == 3 && !kCluster;
   static constexpr int kStages = kAhead ? 5 : 6 * kTurns / kCtas;   // tiles of a warp's ring
   static constexpr int kStage = 2 * kTile;                 // K, V
   static constexpr int kScales = 2 * kBlockTokens;         // the exponents of both
@@ -69,7 +72,10 @@ struct Few {
   static constexpr int kQ = kAhead ? NC * D / 16 * 2 * 32 * 4 : 0;
   static constexpr int kOffMl = kOffQ + kWarps * kQ;
   static constexpr int kMl = (kWarps + 1) * kCols * 8;  // a cluster CTA's: of every warp, and joined
-  static constexpr int kOffSeq = kOffMl + kMl;  // units before each sequence, [num_seqs + 1]; tokens, [num_seqs]
+  static constexpr int kOffSeq = kOffMl + kMl;  // costs before each sequence, [num_seqs + 1]; tokens, [num_seqs]
+  // What a unit costs by the column blocks that its sequence fills: 6, 7 or 8 (64 sequences with one to five tokens: 89.6 us;
+  // 4, 5, 6 92.2; 10, 11, 12 90.4; all the same 93.6).
+  __host__ __device__ static constexpr int cost(int blocks) { return NC == 1 ? 1 : 5 + blocks; }
   __device__ static int next(int place) { return place + kTurns == kStages ? 0 : place + kTurns; }  // of a unit's first tile
   static constexpr int smem(int num_seqs) { return kOffSeq + (2 * num_seqs + 1) * 4; }
 };
@@ -444,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC, kCluster>::kCtas)
   constexpr int kSteps = D / 16;  // 16-byte chunks of a row of codes: 16 dims, the depth of a product
   extern __shared__ __align__(128) unsigned char smem[];
   const uint32_t base = saddr(smem);
-  int* s_units = reinterpret_cast<int*>(smem + T::kOffSeq);
-  int* s_tokens = s_units + p.num_seqs + 1;
+  int* s_costs = reinterpret_cast<int*>(smem + T::kOffSeq);
+  int* s_tokens = s_costs + p.num_seqs + 1;
   __shared__ int s_sum[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hc = kCluster ? 1 : p.unit_heads, nb = T::kUnitTiles / hc;  // heads and blocks of a unit
@@ -455,11 +461,13 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC, kCluster>::kCtas)
 
   const int head_of = warp & (hc - 1), place_of = warp / hc;  // (hc is a power of two); of a unit's blocks place_of kTurns ..
 
-  // This CTA's units are numbers n0 .. n1 - 1 of the stream; of a cluster's pair, its rank and every stride-th from there on.
+  // This CTA's units are n1 of the stream from `at` on; of a cluster's pair, its rank and every stride-th from there on.
   const int piece = blockIdx.x;
-  int n0 = 0, n1 = 0, stride = 1;
+  int n1 = 0, stride = 1;
+  const int nb_bits = 31 - __clz(nb);
+  auto units_at = [&](int b) -> int { return ((s_tokens[b] + kBlockTokens - 1) / kBlockTokens + nb - 1) >> nb_bits; };
   Rows pair{};
-  Walk at{};  // unit n0
+  Walk at{};  // the first unit
   if constexpr (kCluster) {
     stride = static_cast<int>(cluster_size());
     const int number = static_cast<int>(blockIdx.x) / stride;
@@ -467,47 +475,59 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC, kCluster>::kCtas)
     at.heads = number - at.b * head_groups;
     at.unit = static_cast<int>(cluster_rank());
   } else {
-    // Units before each sequence.
-    if (tid == 0) s_units[0] = 0;
+    // What the units before each sequence cost.
+    if (tid == 0) s_costs[0] = 0;
     int running = 0;
     for (int first = 0; first < p.num_seqs; first += kThreads) {
       const int b = first + tid;
-      int units = 0;
+      int costs = 0;
       if (b < p.num_seqs) {
         const Rows r = rows_of(p, b);
         if (r.wrong && blockIdx.x == 0) atomicOr(p.err, r.wrong);
-        s_tokens[b] = r.tokens;
-        units = r.count > 0 ? ((r.tokens + kBlockTokens - 1) / kBlockTokens + nb - 1) / nb : 0;
+        s_tokens[b] = r.count > 0 ? r.tokens : 0;
+        const int blocks = (r.count * (p.num_q_heads / p.num_kv_heads) + 7) / 8;
+        costs = units_at(b) * (NC > 1 && p.unit_costs ? T::cost(blocks) : 1);
       }
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(kAll, units, off);
-        if (lane >= off) units += y;
+        const int y = __shfl_up_sync(kAll, costs, off);
+        if (lane >= off) costs += y;
       }
-      if (lane == 31) s_sum[warp] = units;
+      if (lane == 31) s_sum[warp] = costs;
       __syncthreads();
       int before = running;
       for (int w = 0; w < warp; ++w) before += s_sum[w];
-      if (b < p.num_seqs) s_units[b + 1] = before + units;
+      if (b < p.num_seqs) s_costs[b + 1] = before + costs;
       for (int w = 0; w < kThreads / 32; ++w) running += s_sum[w];
       __syncthreads();
     }
     const int total = running * head_groups;
-    const int pieces = min(total, p.num_pieces);
+    const int pieces = total == 0 ? 0 : min(max(total / T::cost(NC), 1), p.num_pieces);  // (a unit or more each)
     if (piece >= pieces) return;
-    n0 = static_cast<int>(static_cast<int64_t>(piece) * total / pieces);
-    n1 = static_cast<int>(static_cast<int64_t>(piece + 1) * total / pieces);
-    int lo = 0, hi = p.num_seqs - 1;  // unit n0's sequence: the last with units before it at or below
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s_units[mid] <= n0 / head_groups) lo = mid;
-      else hi = mid - 1;
+    // The sequence in which the cost x of the stream is reached, the last that begins there or before, and its unit there.
+    auto find = [&](int x, int& b) -> int {
+      int lo = 0, hi = p.num_seqs - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_costs[mid] <= x / head_groups) lo = mid;
+        else hi = mid - 1;
+      }
+      b = lo;
+      const int rest = x - s_costs[lo] * head_groups;
+      return NC == 1 || rest == 0 ? rest : rest / ((s_costs[lo + 1] - s_costs[lo]) / units_at(lo));
+    };
+    const int from = static_cast<int>(static_cast<int64_t>(piece) * total / pieces);
+    const int to = static_cast<int>(static_cast<int64_t>(piece + 1) * total / pieces);
+    const int begin = find(from, at.b);
+    n1 = to - from;
+    if (NC > 1) {
+      int last;
+      n1 = find(to, last) - begin;
+      for (int b = at.b; b < last; ++b) n1 += units_at(b) * head_groups;
     }
-    at.b = lo;
-    at.units = s_units[lo + 1] - s_units[lo];
-    const int rest = n0 - s_units[lo] * head_groups;
-    at.heads = rest / at.units;
-    at.unit = rest - at.heads * at.units;
+    at.units = units_at(at.b);
+    at.heads = begin / at.units;
+    at.unit = begin - at.heads * at.units;
   }
   // On to the pair that unit x.unit, past its own pair's end, lies in (there is one).
   auto carry = [&](Walk& x) {
@@ -517,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC, kCluster>::kCtas)
       x.heads = 0;
       do {
         ++x.b;
-        x.units = s_units[x.b + 1] - s_units[x.b];
+        x.units = units_at(x.b);
       } while (x.units == 0);
     }
   };
@@ -527,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC, kCluster>::kCtas)
   constexpr int kWindow = 32 / kTurns;  // units
   struct Window {
     Walk x;  // its first unit
-    int n;   // that one's number in the stream
+    int n;   // that one's number of the CTA's
   };
   auto block_at = [&](const Window& w) -> int {  // of this lane's tile
     return (w.x.unit + lane / kTurns * stride) * nb + place_of * kTurns + lane % kTurns;
@@ -540,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC, kCluster>::kCtas)
     atomicOr(p.err, kErrBlockId);
     return 0;
   };
-  Window window{at, n0}, next{};
+  Window window{at, 0}, next{};
   int ids = -1, next_ids = -1;  // -1: no tile
   int asked = 0;
   if constexpr (kCluster) {  // the first window's ids are asked for before the length is known
@@ -581,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC, kCluster>::kCtas)
     return w;
   };
   auto tiles_of = [&](const Window& w) -> int { return units_of(w) * kTurns; };
-  if (!kCluster && n0 < n1) ids = ids_of(window);
+  if (!kCluster) ids = ids_of(window);
   int sent = 0, tiles = tiles_of(window);  // of the window: tiles sent for, and all
   if (tiles > 0) {
     next = behind(window);
@@ -634,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC, kCluster>::kCtas)
   int stage = 0;
 
   // The piece's pairs of sequence and heads; a cluster's one, of which a CTA may have no unit.
-  for (int n = kCluster ? 0 : n0; kCluster || n < n1;) {
+  for (int n = 0; kCluster || n < n1;) {
     const Rows rows = kCluster ? pair : rows_of(p, at.b);
     const int kvh = at.heads * hc + head_of;
     const int count = kCluster ? n1 : min(at.units - at.unit, n1 - n);  // units of the pair here
@@ -701,7 +721,8 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC, kCluster>::kCtas)
     }
 
     // All of a warp's tiles of a unit at a time.  What lies in the second one's place past the last token is masked like the rows
-    // past it.  Of the column blocks those that the sequence's rows fill (drafts of one to five tokens: XX us with all of them).
+    // past it.  Of the column blocks those that the sequence's rows fill (64 sequences with one to five tokens: 96.1 us with all
+    // of them, 89.6 so).
     const int token0 = (at.unit * nb + place_of * kTurns) * kBlockTokens, step = stride * nb * kBlockTokens;
     const int mine = token0 < rows.tokens ? min(count, (rows.tokens - token0 - 1) / step + 1) : 0;  // units with such blocks
     const int cols = rows.count << group_bits;
@@ -781,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, NC, kCluster>::kCtas)
         }
       }
       const bool started = at.unit == 0, ended = at.unit + count == at.units;
-      const int slot = n == n0 ? 0 : 1;  // of the piece's states
+      const int slot = n == 0 ? 0 : 1;  // of the piece's states
       if (warp == 0 && lane == 0) {
         int* record = p.ws_records + 2 * (static_cast<int64_t>(at.b) * head_groups + at.heads);
         if (started) record[0] = piece * 2 + slot;
@@ -915,7 +936,7 @@ __global__ void __launch_bounds__(kSlices == 1 ? 128 : kSlices * 32) join_fp8_ke
   if (rows.count == 0) return;
   const int first = record.x >> 1;
   int states = rows.tokens > 0 ? record.y - first + 1 : 0;
-  if (rows.tokens > 0 && (first < 0 || states < 1 || record.y >= p.num_pieces)) return;  // (a piece timed out)
+  if (rows.tokens > 0 && (first < 0 || states < 1 || record.y >= p.num_pieces)) return;  // (the lengths were changed meanwhile)
   if (states == 1) return;  // whole in one piece, which wrote it
   for (int col = blockIdx.y * kRows + (kRows > 1 ? warp : 0); col < rows.count * group; col += gridDim.y * kRows) {
     float top = kNone, l = 0.f, acc[kPer];
