@@ -6,8 +6,9 @@ namespace {
 
 // Which form a call takes: clusters if those of all its pairs run at once and are expected to be done before the stream form.
 // Microseconds a call, measured (32 q and 8 kv heads of 128 dims, sequences of half a length to all of it; stream, clusters):
-//   1 x 128 8.4, 5.0; 1 x 8192 13.9, 13.4; 1 x 32768 23, 38; 8 x 2048 15.7, 9.9; 8 x 8192 29, 25; 32 x 2048 30, 25; 32 x 8192
-//   76, 81; of one kv head 16 x 8192 15.8, 14.0 and 16 x 32768 29, 38.
+//   1 x 128 8.4, 5.2; 1 x 8192 14.1, 10.1; 1 x 32768 22.7, 23.0; 8 x 2048 15.4, 9.7; 8 x 8192 29, 24; 32 x 2048 30, 24;
+//   32 x 8192 77, 77; of one kv head 16 x 8192 15.6, 13.4 and 16 x 32768 29, 35.
+// As large as the pairs leave room for, up to 16 CTAs (1 x 8192: 12.6 with 8).
 // A cluster's units come one after the other; the stream form has a second launch and a pass over the lengths; and either takes
 // the bytes' time, of a batch whose tables are filled to three quarters.
 constexpr float kClusterUs = 4.6f, kStreamUs = 10.5f;
@@ -23,6 +24,8 @@ struct Instance {
   static constexpr int kClusterSmem = Cluster::smem(0);
   static_assert(Stream::kCtas * (kMost + 1024 + 256) <= 228 * 1024, "shared memory of an SM's CTAs");
   static_assert(Cluster::kCols * (D * 4 + 8) <= Cluster::kOffScales, "a cluster CTA's state lies in the rings");
+  static constexpr int kSizes = 5;  // of clusters
+  static_assert(1 << (kSizes - 1) == kMostCluster, "the largest cluster");
   static constexpr auto kStream = &few_rows_fp8_kernel<D, NC, false>;
   static constexpr auto kCluster = &few_rows_fp8_kernel<D, NC, true>;
 
@@ -42,10 +45,10 @@ struct Instance {
     return cfg;
   }
 
-  // Clusters of 1, 2, 4 and 8 CTAs that the current device holds at once; both kernels' shared memory is set on the way.
+  // Clusters of 1, 2, 4, 8 and 16 CTAs that the current device holds at once; both kernels' attributes are set on the way.
   static cudaError_t prepare(const int** counts) {
     static std::mutex mu;
-    static int known[64][4];
+    static int known[64][kSizes];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -56,7 +59,8 @@ struct Instance {
       if ((e = cudaFuncSetAttribute(kStream, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess) return e;
       if ((e = cudaFuncSetAttribute(kCluster, cudaFuncAttributeMaxDynamicSharedMemorySize, kClusterSmem)) != cudaSuccess) return e;
       if ((e = cudaFuncSetAttribute(kCluster, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess) return e;
-      for (int k = 3; k >= 0; --k) {
+      if ((e = cudaFuncSetAttribute(kCluster, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
+      for (int k = kSizes - 1; k >= 0; --k) {
         cudaLaunchAttribute attr[2];
         cudaLaunchConfig_t cfg = cluster_config(1, 1 << k, nullptr, attr);
         cfg.numAttrs = 1;
@@ -73,7 +77,7 @@ struct Instance {
   static int choose(const int* counts, int64_t pairs, int max_blocks_per_seq) {
     const int units = (max_blocks_per_seq + Cluster::kUnitTiles - 1) / Cluster::kUnitTiles;
     int k = 0;
-    while (k < 3 && (1 << k) < units && pairs <= counts[k + 1]) ++k;
+    while (k < kSizes - 1 && (1 << k) < units && pairs <= counts[k + 1]) ++k;
     if (pairs > counts[k]) return 0;
     const float bytes_us =
         kFilled / kBytesPerUs * static_cast<float>(pairs) * units * (2.f * Cluster::kUnitTiles * Cluster::kTile);
@@ -92,7 +96,7 @@ struct Instance {
     auto takes = [&](int64_t seqs) { return choose(counts, seqs * num_kv_heads, max_blocks_per_seq); };
     *ctas = takes(num_seqs);
     *fewer = *ctas != 0 && takes(1) != 0;
-    for (int k = 1; k <= 3; ++k) {
+    for (int k = 1; k < kSizes; ++k) {
       const int64_t first = counts[k] / num_kv_heads + 1;  // the smallest batch whose pairs get no more than 2^(k - 1)
       if (first < num_seqs) *fewer = *fewer && takes(first) != 0;
     }
