@@ -679,14 +679,14 @@ def copy_blocks_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, kv_scales: tor
 
 def fp8_decode_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
                               max_blocks_per_seq: int) -> int:
-    """Bytes of the workspace of a decode call over an 8-bit cache on the current device."""
+    """Bytes that are enough for decode calls over an 8-bit cache of up to these sizes, on the current device."""
     return _query(ctypes.c_size_t, load().pkv_fp8_decode_workspace_size, num_seqs, num_q_heads, num_kv_heads, head_dim,
                   max_blocks_per_seq)
 
 
 def fp8_prefill_workspace_size(num_query_tokens: int, max_query_len: int, num_seqs: int, num_q_heads: int,
                                num_kv_heads: int, head_dim: int, max_blocks_per_seq: int) -> int:
-    """Bytes of the workspace of a chunk attention call over an 8-bit cache on the current device."""
+    """Bytes of the workspace of a chunk attention call over an 8-bit cache of these sizes, on the current device."""
     return _query(ctypes.c_size_t, load().pkv_fp8_prefill_workspace_size, num_query_tokens, max_query_len, num_seqs,
                   num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq)
 

@@ -1,5 +1,7 @@
 // The 8-bit cache's writes, reads and copies: quantising append (with or without the rotation of q and k), rows read back
-// as bf16, and whole-block copies.  All are bound by HBM: each row is read once and written once.
+// as bf16, and whole-block copies.  All are bound by HBM: each row is read once and written once.  Measured: 32773 tokens of 8
+// kv heads of 128 dims appended in 34.4 us (0.88 of the copy bandwidth), with the rotation of 32 q heads in 123 us (0.92);
+// 65536 of 64 dims read back in 35.3 us (0.86); 2048 blocks copied in 17.2 us (part of them from L2); the smallest calls 3 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -79,7 +81,9 @@ constexpr int kAppendCtas = 64;  // per SM at most; beyond that a warp takes sev
 
 // A lane owns two 16-byte chunks of a row, so that D / 16 lanes cover it and a warp takes 4 (D = 128) or 8 rows at a time:
 // the chunks c and c + D / 16, the rotation's two halves, or without rotation 2 c and 2 c + 1, whose codes are 16 bytes.
-// A warp takes a token, or a part of its rows, and has kAhead rows a lane in flight, the first while it looks up the slot.
+// A warp takes a token, or a part of its rows, and has kAhead rows a lane in flight, the first while it looks up the slot (up
+// to 37.8 us with other numbers of rows and CTAs where this takes 34.4).  Rows that hold an infinity or NaN look for their
+// largest finite value a second time.
 template <int D, bool kRotary>
 __global__ void __launch_bounds__(kAppendThreads) append_fp8_kernel(const Fp8AppendParams p) {
   pdl_trigger();
@@ -184,7 +188,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_fp8_kernel(const Fp8App
 }
 
 // A thread reads 8 codes of a row of K and of V, of kGatherTokens tokens at once, and writes 8 bf16 values of each: so the
-// loads and the stores of a warp are whole rows.
+// loads and the stores of a warp are whole rows.  A CTA's tokens are neighbours (39.4 us where this takes 35.3 without).
 constexpr int kGatherThreads = 256;
 constexpr int kGatherTokens = 2;
 constexpr int kGatherCtas = 64;  // per SM at most

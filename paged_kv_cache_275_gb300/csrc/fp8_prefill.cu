@@ -13,6 +13,11 @@
 //     zeros.
 //   * warp 8: issues the products, as there; it owns the tensor memory.
 //   * warps 0-7: softmax and epilogue, a row a thread, as there.
+// A chunk call that does not fill the GPU has each tile pair's key steps split over CTAs, as there, with a merge.
+// Measured: two prompts of 8192 tokens, 32 q and 8 kv heads of 128 dims, 950 us (1157 TFLOP/s, 0.60 of the bf16 burst rate; the
+// bf16 kernel over a bf16 cache runs at 1250 to 1300): seven converters and eight softmax warps share the issue slots.  512 tokens
+// behind 8192, 16 q heads, 50 us: four splits of 17 steps on 128 of 152 SMs, and the merge.  (A single query tile dealt to
+// both tiles' places by steps gained nothing: 64 sequences of 8 tokens 165 to 172 us.)
 // The softmax warps take 168 registers a thread and leave the others 88: 256 (168 + 88) is the block's 512 * 128.
 #include "paged_prefill_kernel.cuh"
 
@@ -331,161 +336,161 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     // ---------------- softmax / epilogue (thread = row of tile warp / 4) ----------------
     const int t = warp >> 2;
     if (t < n_tiles) {
-    const int r = tid & (kRows - 1);
-    constexpr int kChunks = D / 8;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t s_cols = lane_base + col_s(t), o_cols = lane_base + col_o(t);
-    const float qk = p.scale * kLog2e;
-    const int i = i0 + t * kTokens + r / G;
-    const bool row_ok = i < C;
-    cp_async_wait_all();
-    fence_async_smem();
-    bar_arrive(q_ready + 8 * t);
-    const int limit = row_ok ? prefix + i + 1 : 0;
-    // A warp without rows of the chunk leaves its part of P as it is: a row of O takes only its own row of P.
-    // (In a loop of its own: as a branch of the loop below it costs that a sixth of its speed.)
-    const bool idle = i0 + t * kTokens + (warp & 3) * 32 / G >= C;
-    for (int j = 0; idle && j < nsteps && !failed; ++j) {
-      if (!__all_sync(0xffffffffu, bar_wait(s_full + 8 * t, j & 1))) failed = true;
-      else bar_arrive(p_full + 8 * t);
-    }
-    const bool sees = kSplit ? limit > j0 * kKeys : row_ok;  // (a split's range may start behind the row's last key)
-    float m_used = -INFINITY, l = 0.f;
-    for (int j = idle ? nsteps : 0; j < nsteps && !failed; ++j) {
-      if (!__all_sync(0xffffffffu, bar_wait(s_full + 8 * t, j & 1))) {
-        failed = true;
-        break;
+      const int r = tid & (kRows - 1);
+      constexpr int kChunks = D / 8;
+      const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      const uint32_t s_cols = lane_base + col_s(t), o_cols = lane_base + col_o(t);
+      const float qk = p.scale * kLog2e;
+      const int i = i0 + t * kTokens + r / G;
+      const bool row_ok = i < C;
+      cp_async_wait_all();
+      fence_async_smem();
+      bar_arrive(q_ready + 8 * t);
+      const int limit = row_ok ? prefix + i + 1 : 0;
+      // A warp without rows of the chunk leaves its part of P as it is: a row of O takes only its own row of P.
+      // (In a loop of its own: as a branch of the loop below it costs that a sixth of its speed.)
+      const bool idle = i0 + t * kTokens + (warp & 3) * 32 / G >= C;
+      for (int j = 0; idle && j < nsteps && !failed; ++j) {
+        if (!__all_sync(0xffffffffu, bar_wait(s_full + 8 * t, j & 1))) failed = true;
+        else bar_arrive(p_full + 8 * t);
       }
-      tc_after_sync();
-      float s[kKeys];
-      tmem_ld64(s_cols, *reinterpret_cast<float(*)[64]>(&s[0]));
-      tmem_ld64(s_cols + 64, *reinterpret_cast<float(*)[64]>(&s[64]));
-      const int ja = j0 + j;
-      if (__any_sync(0xffffffffu, (ja + 1) * kKeys > limit)) {
-#pragma unroll
-        for (int x = 0; x < kKeys; ++x) s[x] = (ja * kKeys + x) < limit ? s[x] : -INFINITY;
-      }
-      float mc[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) mc[k] = fmax3(s[k], s[k + 8], s[k + 16]);
-      static_assert(kKeys == 128, "row max layout");
-#pragma unroll
-      for (int x = 24; x < 120; x += 16)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mc[k] = fmax3(mc[k], s[x + k], s[x + 8 + k]);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) mc[k] = fmaxf(mc[k], s[120 + k]);
-      const float bm = qk * fmax3(fmax3(mc[0], mc[1], mc[2]), fmax3(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7]));
-      const bool raise = sees && bm > m_used + kSlack;
-      const float m_new = raise ? bm : m_used;
-      const float alpha = raise ? ex2_approx(m_used - m_new) : 1.f;
-      const float neg_m = sees ? -m_new : 0.f;
-      float2 acc4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      uint32_t packed[kKeys / 2];
-      const float2 qk2 = make_float2(qk, qk), neg_m2 = make_float2(neg_m, neg_m);
-#pragma unroll
-      for (int x = 0; x < kKeys; x += 2) {
-        // The denominator sums the fp32 weights, within 2^-9 of the bf16 ones that P carries.
-        const float2 e = __ffma2_rn(make_float2(s[x], s[x + 1]), qk2, neg_m2);
-        const float p0 = ex2_approx(e.x), p1 = ex2_approx(e.y);
-        packed[x / 2] = pack_bf16(p0, p1);
-        acc4[(x / 2) & 3] = __fadd2_rn(acc4[(x / 2) & 3], make_float2(p0, p1));
-      }
-      const float2 a = __fadd2_rn(__fadd2_rn(acc4[0], acc4[1]), __fadd2_rn(acc4[2], acc4[3]));
-      l = l * alpha + (a.x + a.y);
-      m_used = m_new;
-      if (j >= 1 && __any_sync(0xffffffffu, raise)) {
-#pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          float o[32];
-          tmem_ld32(o_cols + c0, o);
-#pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] *= alpha;
-          tmem_st32(o_cols + c0, o);
+      const bool sees = kSplit ? limit > j0 * kKeys : row_ok;  // (a split's range may start behind the row's last key)
+      float m_used = -INFINITY, l = 0.f;
+      for (int j = idle ? nsteps : 0; j < nsteps && !failed; ++j) {
+        if (!__all_sync(0xffffffffu, bar_wait(s_full + 8 * t, j & 1))) {
+          failed = true;
+          break;
         }
-      }
-      tmem_st32_raw(s_cols, *reinterpret_cast<const uint32_t(*)[32]>(&packed[0]));
-      tmem_st32_raw(s_cols + 32, *reinterpret_cast<const uint32_t(*)[32]>(&packed[32]));
-      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-      tc_before_sync();
-      bar_arrive(p_full + 8 * t);
-    }
-    if constexpr (kSplit) {
-      // Partial states through the warp's own 4 KB of the tile's Q buffer, 32 columns at a time, so that each store writes
-      // four 128-byte row segments.
-      if (!failed && __all_sync(0xffffffffu, bar_wait(o_full + 8 * t, 0))) {
         tc_after_sync();
-        float* scratch = reinterpret_cast<float*>(smem + T::kOffQ + t * T::kQTile) + (warp & 3) * 32 * 32;
+        float s[kKeys];
+        tmem_ld64(s_cols, *reinterpret_cast<float(*)[64]>(&s[0]));
+        tmem_ld64(s_cols + 64, *reinterpret_cast<float(*)[64]>(&s[64]));
+        const int ja = j0 + j;
+        if (__any_sync(0xffffffffu, (ja + 1) * kKeys > limit)) {
 #pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          float o[32];
-          tmem_ld32(o_cols + c0, o);
-#pragma unroll
-          for (int q4 = 0; q4 < 8; ++q4)
-            *reinterpret_cast<float4*>(scratch + lane * 32 + ((q4 + lane) & 7) * 4) =
-                make_float4(o[4 * q4], o[4 * q4 + 1], o[4 * q4 + 2], o[4 * q4 + 3]);
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int rr = 4 * k + (lane >> 3), q4 = lane & 7;
-            const float4 v = *reinterpret_cast<const float4*>(scratch + rr * 32 + ((q4 + rr) & 7) * 4);
-            const int tr = (warp & 3) * 32 + rr, ii = i0 + t * kTokens + tr / G;
-            if (ii < C) *reinterpret_cast<float4*>(p.ws + ws_row(ii, tr % G) * D + c0 + q4 * 4) = v;
-          }
-          __syncwarp();
+          for (int x = 0; x < kKeys; ++x) s[x] = (ja * kKeys + x) < limit ? s[x] : -INFINITY;
         }
-        if (row_ok) ws_ml[ws_row(i, r % G)] = make_float2(m_used, l);
-      } else {
-        failed = true;
-      }
-    } else {
-      bool staged = false;
-      unsigned char* ot = smem + T::kOffQ + t * T::kQTile;  // (every S that read Q has retired)
-      if (!failed && __all_sync(0xffffffffu, bar_wait(o_full + 8 * t, 0))) {
-        tc_after_sync();
-        const float inv = l != 0.f ? 1.f / l : 0.f;
+        float mc[8];
 #pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          float o[32];
-          tmem_ld32(o_cols + c0, o);
+        for (int k = 0; k < 8; ++k) mc[k] = fmax3(s[k], s[k + 8], s[k + 16]);
+        static_assert(kKeys == 128, "row max layout");
 #pragma unroll
-          for (int x = 0; x < 32; x += 8) {
-            const int ch = (c0 + x) / 8;
-            *reinterpret_cast<uint4*>(ot + (ch / 8) * T::kQHalf + swz(r, ch % 8)) =
-                make_uint4(pack_bf16(o[x] * inv, o[x + 1] * inv), pack_bf16(o[x + 2] * inv, o[x + 3] * inv),
-                           pack_bf16(o[x + 4] * inv, o[x + 5] * inv), pack_bf16(o[x + 6] * inv, o[x + 7] * inv));
+        for (int x = 24; x < 120; x += 16)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mc[k] = fmax3(mc[k], s[x + k], s[x + 8 + k]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mc[k] = fmaxf(mc[k], s[120 + k]);
+        const float bm = qk * fmax3(fmax3(mc[0], mc[1], mc[2]), fmax3(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7]));
+        const bool raise = sees && bm > m_used + kSlack;
+        const float m_new = raise ? bm : m_used;
+        const float alpha = raise ? ex2_approx(m_used - m_new) : 1.f;
+        const float neg_m = sees ? -m_new : 0.f;
+        float2 acc4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t packed[kKeys / 2];
+        const float2 qk2 = make_float2(qk, qk), neg_m2 = make_float2(neg_m, neg_m);
+#pragma unroll
+        for (int x = 0; x < kKeys; x += 2) {
+          // The denominator sums the fp32 weights, within 2^-9 of the bf16 ones that P carries.
+          const float2 e = __ffma2_rn(make_float2(s[x], s[x + 1]), qk2, neg_m2);
+          const float p0 = ex2_approx(e.x), p1 = ex2_approx(e.y);
+          packed[x / 2] = pack_bf16(p0, p1);
+          acc4[(x / 2) & 3] = __fadd2_rn(acc4[(x / 2) & 3], make_float2(p0, p1));
+        }
+        const float2 a = __fadd2_rn(__fadd2_rn(acc4[0], acc4[1]), __fadd2_rn(acc4[2], acc4[3]));
+        l = l * alpha + (a.x + a.y);
+        m_used = m_new;
+        if (j >= 1 && __any_sync(0xffffffffu, raise)) {
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            float o[32];
+            tmem_ld32(o_cols + c0, o);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] *= alpha;
+            tmem_st32(o_cols + c0, o);
           }
         }
-        fence_async_smem();
-        staged = true;
-      } else {
-        failed = true;
+        tmem_st32_raw(s_cols, *reinterpret_cast<const uint32_t(*)[32]>(&packed[0]));
+        tmem_st32_raw(s_cols + 32, *reinterpret_cast<const uint32_t(*)[32]>(&packed[32]));
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_before_sync();
+        bar_arrive(p_full + 8 * t);
       }
-      bar_arrive(o_staged + 8 * t);  // (staged or not, so that the wait below ends)
-      if (__all_sync(0xffffffffu, staged && bar_wait(o_staged + 8 * t, 0))) {
-        const int tok0 = i0 + t * kTokens;
-        if (tok0 + kTokens <= C) {  // a whole tile leaves by tensor stores
-          if (r == 0) {
+      if constexpr (kSplit) {
+        // Partial states through the warp's own 4 KB of the tile's Q buffer, 32 columns at a time, so that each store writes
+        // four 128-byte row segments.
+        if (!failed && __all_sync(0xffffffffu, bar_wait(o_full + 8 * t, 0))) {
+          tc_after_sync();
+          float* scratch = reinterpret_cast<float*>(smem + T::kOffQ + t * T::kQTile) + (warp & 3) * 32 * 32;
 #pragma unroll
-            for (int h = 0; h < T::kHalves; ++h)
-              tma_store_3d(&map_out, 64 * h, kvh * G, q0 + tok0, s_base + T::kOffQ + t * T::kQTile + h * T::kQHalf);
-            tma_store_commit_and_wait_read();
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            float o[32];
+            tmem_ld32(o_cols + c0, o);
+#pragma unroll
+            for (int q4 = 0; q4 < 8; ++q4)
+              *reinterpret_cast<float4*>(scratch + lane * 32 + ((q4 + lane) & 7) * 4) =
+                  make_float4(o[4 * q4], o[4 * q4 + 1], o[4 * q4 + 2], o[4 * q4 + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int rr = 4 * k + (lane >> 3), q4 = lane & 7;
+              const float4 v = *reinterpret_cast<const float4*>(scratch + rr * 32 + ((q4 + rr) & 7) * 4);
+              const int tr = (warp & 3) * 32 + rr, ii = i0 + t * kTokens + tr / G;
+              if (ii < C) *reinterpret_cast<float4*>(p.ws + ws_row(ii, tr % G) * D + c0 + q4 * 4) = v;
+            }
+            __syncwarp();
+          }
+          if (row_ok) ws_ml[ws_row(i, r % G)] = make_float2(m_used, l);
+        } else {
+          failed = true;
+        }
+      } else {
+        bool staged = false;
+        unsigned char* ot = smem + T::kOffQ + t * T::kQTile;  // (every S that read Q has retired)
+        if (!failed && __all_sync(0xffffffffu, bar_wait(o_full + 8 * t, 0))) {
+          tc_after_sync();
+          const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            float o[32];
+            tmem_ld32(o_cols + c0, o);
+#pragma unroll
+            for (int x = 0; x < 32; x += 8) {
+              const int ch = (c0 + x) / 8;
+              *reinterpret_cast<uint4*>(ot + (ch / 8) * T::kQHalf + swz(r, ch % 8)) =
+                  make_uint4(pack_bf16(o[x] * inv, o[x + 1] * inv), pack_bf16(o[x + 2] * inv, o[x + 3] * inv),
+                             pack_bf16(o[x + 4] * inv, o[x + 5] * inv), pack_bf16(o[x + 6] * inv, o[x + 7] * inv));
+            }
+          }
+          fence_async_smem();
+          staged = true;
+        } else {
+          failed = true;
+        }
+        bar_arrive(o_staged + 8 * t);  // (staged or not, so that the wait below ends)
+        if (__all_sync(0xffffffffu, staged && bar_wait(o_staged + 8 * t, 0))) {
+          const int tok0 = i0 + t * kTokens;
+          if (tok0 + kTokens <= C) {  // a whole tile leaves by tensor stores
+            if (r == 0) {
+#pragma unroll
+              for (int h = 0; h < T::kHalves; ++h)
+                tma_store_3d(&map_out, 64 * h, kvh * G, q0 + tok0, s_base + T::kOffQ + t * T::kQTile + h * T::kQHalf);
+              tma_store_commit_and_wait_read();
+            }
+          } else {
+            __nv_bfloat16* og = static_cast<__nv_bfloat16*>(p.out);
+#pragma unroll 4
+            for (int c = r; c < kRows * kChunks; c += kRows) {
+              const int rr = c / kChunks, ch = c % kChunks, ii = tok0 + rr / G;
+              if (ii < C)
+                reinterpret_cast<uint4*>(og + (static_cast<size_t>(q0 + ii) * p.num_q_heads + kvh * G + rr % G) * D)[ch] =
+                    *reinterpret_cast<const uint4*>(ot + (ch / 8) * T::kQHalf + swz(rr, ch % 8));
+            }
           }
         } else {
-          __nv_bfloat16* og = static_cast<__nv_bfloat16*>(p.out);
-#pragma unroll 4
-          for (int c = r; c < kRows * kChunks; c += kRows) {
-            const int rr = c / kChunks, ch = c % kChunks, ii = tok0 + rr / G;
-            if (ii < C)
-              reinterpret_cast<uint4*>(og + (static_cast<size_t>(q0 + ii) * p.num_q_heads + kvh * G + rr % G) * D)[ch] =
-                  *reinterpret_cast<const uint4*>(ot + (ch / 8) * T::kQHalf + swz(rr, ch % 8));
-          }
+          failed = true;
         }
-      } else {
-        failed = true;
       }
-    }
-    if (failed && lane == 0) atomicOr(p.err, kErrTimeout);
+      if (failed && lane == 0) atomicOr(p.err, kErrTimeout);
     }
   }
 
