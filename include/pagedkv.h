@@ -552,7 +552,7 @@ pkv_status pkv_fp8_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, 
  * pkv_paged_prefill_attention over such a cache (q and out bf16), scale > 0: prompt chunks, and the few rows a sequence of
  * drafted tokens.  num_query_tokens is the number of rows of q and out (0: a no-op); a sequence whose chunk reaches outside
  * them, or is longer than its context, sets PKV_DEVERR_CONTEXT_LEN_TOO_LONG and is skipped; rows past max_query_len of a
- * chunk are not written, and set it too.  num_blocks * num_kv_heads * 16 must be below 2^31, max_blocks_per_seq at most 2^26
+ * chunk are unspecified, and set it too.  num_blocks * num_kv_heads * 16 must be below 2^31, max_blocks_per_seq at most 2^26
  * and num_seqs at most 65535.  A token that some rows of a sequence's chunk see has to be finite, or the rows of the chunk that
  * do not see it are unspecified.
  */
@@ -563,7 +563,8 @@ pkv_status pkv_paged_fp8_prefill_attention(const void* q, const void* k_cache, c
                                            int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                            int64_t num_blocks, int32_t block_size, float scale, void* out,
                                            void* workspace, size_t workspace_bytes, pkv_stream_t stream);
-/* Its workspace on the current device, for these sizes. */
+/* Its workspace on the current device, for these sizes.  Long chunks have their cache blocks turned into bf16 there, which takes
+   4 * num_seqs * max_blocks_per_seq * 16 * num_kv_heads * head_dim bytes, up to 2 GB (beyond that they do without). */
 pkv_status pkv_fp8_prefill_workspace_size(int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs,
                                           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                           int32_t max_blocks_per_seq, size_t* bytes);

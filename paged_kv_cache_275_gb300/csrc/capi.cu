@@ -6,6 +6,7 @@
 // word, and the per-thread error message.  No call allocates device memory.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -1317,6 +1318,50 @@ int32_t fp8_prefill_splits(int64_t num_query_tokens, int32_t max_query_len, int3
   if (num_seqs > 0 && n > 65535 / num_seqs) n = 65535 / num_seqs;
   return static_cast<int32_t>(n < 1 ? 1 : n);
 }
+
+// A chunk call's workspace: what it unpacks, if it does, then the states of its splits.
+struct Fp8ChunkPlan {
+  int32_t splits;
+  bool unpacks;
+  size_t v = 0, tables = 0, lens = 0, states = 0, bytes = 0;  // byte offsets, and the sum
+};
+
+// Whether the codes are turned into bf16 once, ahead of the bf16 kernel, or by every CTA that sees them.  A CTA's part of it
+// costs an SM 3.9 ns a token and head of 128 dims (2.6 of 64), of 152 SMs; unpacking costs the HBM 6 bytes an element, and a
+// launch.  Measured (32 q and 8 kv heads of 128 dims; by every CTA and ahead, us): 2 x 8192 946, 789; 1 x 2048 43.7, 42.7;
+// 1 x 1024 24.2, 27.1; 8 x 1024 119, 106; 8 x 512 behind 3584 271, 259; 8 x 256 behind 3840 147, 158; 1 x 512 behind 8192, 16 q
+// heads, 49.8, 56.2.
+// The context lengths are not known here: three quarters of the table, or the chunk.
+constexpr size_t kFp8MostUnpacked = size_t{2} << 30;
+bool fp8_unpacks(int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                 int32_t head_dim, int32_t max_blocks_per_seq) {
+  // (The bf16 kernel's map of the output ends behind so many rows.)
+  if (num_query_tokens > static_cast<int64_t>(num_seqs) * max_query_len) return false;
+  const int64_t slots = static_cast<int64_t>(num_seqs) * max_blocks_per_seq * PKV_BLOCK_SIZE * num_kv_heads;
+  if (slots >= (int64_t{1} << 31) || slots * head_dim * 4 > static_cast<int64_t>(kFp8MostUnpacked)) return false;
+  const double chunk = static_cast<double>(num_query_tokens) / num_seqs;
+  const double context = std::max(0.75 * PKV_BLOCK_SIZE * max_blocks_per_seq, chunk);
+  const double ctas = std::ceil(chunk / pkv::prefill_cta_tokens(num_q_heads / num_kv_heads)) * (1 - chunk / (2 * context));
+  const double each = head_dim == 128 ? 3.9e-3 / 152 : 2.6e-3 / 152, once = 6.0 * head_dim / 5.5e6;
+  return num_seqs * context * num_kv_heads * (ctas * each - once) > 3.5;
+}
+
+Fp8ChunkPlan fp8_chunk_plan(int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t max_blocks_per_seq, int sms) {
+  Fp8ChunkPlan plan{fp8_prefill_splits(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq, sms),
+                    fp8_unpacks(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq)};
+  if (plan.unpacks) {
+    auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    const size_t blocks = static_cast<size_t>(num_seqs) * max_blocks_per_seq;
+    plan.v = blocks * num_kv_heads * PKV_BLOCK_SIZE * head_dim * 2;
+    plan.tables = 2 * plan.v;
+    plan.lens = plan.tables + up(blocks * 4);
+    plan.states = plan.lens + up(static_cast<size_t>(num_seqs) * 4);
+  }
+  plan.bytes =
+      plan.states + pkv::prefill_workspace_bytes(num_seqs, max_query_len, num_q_heads, num_kv_heads, head_dim, plan.splits);
+  return plan;
+}
 }  // namespace
 
 pkv_status pkv_fp8_prefill_workspace_size(int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs,
@@ -1339,9 +1384,8 @@ pkv_status pkv_fp8_prefill_workspace_size(int64_t num_query_tokens, int32_t max_
         st != PKV_OK)
       return st;
   } else {
-    need = pkv::prefill_workspace_bytes(
-        num_seqs, max_query_len, num_q_heads, num_kv_heads, head_dim,
-        fp8_prefill_splits(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq, sms));
+    need = fp8_chunk_plan(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, sms)
+               .bytes;
   }
   *bytes = need;
   return ok();
@@ -1413,15 +1457,22 @@ pkv_status pkv_paged_fp8_prefill_attention(const void* q, const void* k_cache, c
     return few_rows_fp8(p, head_dim, workspace, workspace_bytes, stream);
   int sms = 0;
   if (pkv_status st = device_state(&p.err, &sms); st != PKV_OK) return st;
-  const int32_t splits =
-      fp8_prefill_splits(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq, sms);
-  const size_t need = pkv::prefill_workspace_bytes(num_seqs, max_query_len, num_q_heads, num_kv_heads, head_dim, splits);
-  if (need > 0 && (!workspace || workspace_bytes < need))
+  const Fp8ChunkPlan plan =
+      fp8_chunk_plan(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, sms);
+  if (plan.bytes > 0 && (!workspace || workspace_bytes < plan.bytes))
     return fail(PKV_ERR_INVALID_ARGUMENT, "workspace too small: %zu bytes given, %zu needed", workspace ? workspace_bytes : size_t{0},
-                need);
-  const cudaError_t e = pkv::launch_prefill_fp8(p, head_dim, splits, static_cast<float*>(workspace), reinterpret_cast<cudaStream_t>(stream));
+                plan.bytes);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  float* states = plan.splits > 1 ? reinterpret_cast<float*>(ws + plan.states) : nullptr;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      plan.unpacks ? pkv::launch_prefill_unpacked_fp8(p, head_dim, plan.splits,
+                                                      {ws, ws + plan.v, reinterpret_cast<int32_t*>(ws + plan.tables),
+                                                       reinterpret_cast<int32_t*>(ws + plan.lens)},
+                                                      states, sms, s)
+                   : pkv::launch_prefill_fp8(p, head_dim, plan.splits, states, s);
   if (e != cudaSuccess) return cuda_fail(e, "fp8 prefill launch");
-  g_launches.fetch_add(splits > 1 ? 2 : 1);
+  g_launches.fetch_add((plan.splits > 1 ? 2 : 1) + (plan.unpacks ? 1 : 0));
   return ok();
 }
 

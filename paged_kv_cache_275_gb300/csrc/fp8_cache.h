@@ -122,6 +122,14 @@ struct Fp8FewPlan {
   }
 };
 
+// What a chunk call unpacks to bf16 (fp8_prefill.cu).
+struct Fp8Unpacked {
+  void* k;  // bf16 [num_seqs][max_blocks_per_seq][num_kv_heads][16][head_dim]
+  void* v;
+  int32_t* block_tables;  // [num_seqs][max_blocks_per_seq]: 0, 1, 2, ...
+  int32_t* context_lens;  // [num_seqs]; -1: skipped
+};
+
 cudaError_t launch_append_fp8(const Fp8AppendParams& p, int head_dim, int num_sms, cudaStream_t stream);
 cudaError_t launch_gather_fp8(const Fp8GatherParams& p, int head_dim, int num_sms, cudaStream_t stream);
 cudaError_t launch_copy_blocks_fp8(const Fp8CopyParams& p, int num_pairs, cudaStream_t stream);
@@ -131,6 +139,8 @@ cudaError_t fp8_cluster_ctas(int head_dim, int rows, int num_seqs, int num_kv_he
                              bool* fewer);
 cudaError_t launch_few_rows_fp8(const Fp8AttentionParams& p, int head_dim, cudaStream_t stream);
 // Chunks on the 5th-generation tensor cores (fp8_prefill.cu); ws: prefill_workspace_bytes of num_splits > 1.
+cudaError_t launch_prefill_unpacked_fp8(const Fp8AttentionParams& p, int head_dim, int num_splits, const Fp8Unpacked& to, float* ws,
+                                        int num_sms, cudaStream_t stream);
 cudaError_t launch_prefill_fp8(const Fp8AttentionParams& p, int head_dim, int num_splits, float* ws, cudaStream_t stream);
 
 }  // namespace pkv

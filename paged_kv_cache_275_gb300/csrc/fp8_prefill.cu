@@ -1,5 +1,6 @@
 // Chunk attention over the 8-bit cache on the 5th-generation tensor cores: causal rows, as paged_prefill_kernel.cuh does it
-// over a bf16 cache, whose tiles, tensor-memory layout and products this kernel shares.
+// over a bf16 cache, whose tiles, tensor-memory layout and products this kernel shares.  Long chunks, whose blocks many CTAs see,
+// have them turned into bf16 once (unpack_fp8_kernel) and take the bf16 kernel itself.
 //
 // Bound by the products (bf16, 4 D flop a row and key it sees).  They stay bf16: q has eight significant bits and the softmax
 // weights need as many, so 8-bit products would take two parts of each and save nothing; and a code times its row's power of
@@ -14,10 +15,10 @@
 //   * warp 8: issues the products, as there; it owns the tensor memory.
 //   * warps 0-7: softmax and epilogue, a row a thread, as there.
 // A chunk call that does not fill the GPU has each tile pair's key steps split over CTAs, as there, with a merge.
-// Measured: two prompts of 8192 tokens, 32 q and 8 kv heads of 128 dims, 950 us (1157 TFLOP/s, 0.60 of the bf16 burst rate; the
-// bf16 kernel over a bf16 cache runs at 1250 to 1300): seven converters and eight softmax warps share the issue slots.  512 tokens
-// behind 8192, 16 q heads, 50 us: four splits of 17 steps on 128 of 152 SMs, and the merge.  (A single query tile dealt to
-// both tiles' places by steps gained nothing: 64 sequences of 8 tokens 165 to 172 us.)
+// Measured (8 kv heads of 128 dims): eight chunks of 256 behind 3840 tokens, 32 q heads, 147 us; 512 tokens behind 8192, 16 q
+// heads, 50 us: four splits of 17 steps on 128 of 152 SMs, and the merge.  Seven converters and eight softmax warps share the
+// issue slots, 1.3 times the bf16 kernel's time over a bf16 cache (two prompts of 8192 946 us, 789 unpacked).  A single query
+// tile dealt to both tiles' places by steps gained nothing (64 sequences of 8 tokens 165 to 172 us).
 // The softmax warps take 168 registers a thread and leave the others 88: 256 (168 + 88) is the block's 512 * 128.
 #include "paged_prefill_kernel.cuh"
 
@@ -578,6 +579,76 @@ __global__ void __launch_bounds__(256) merge_fp8_kernel(const Fp8PrefillParams p
   }
 }
 
+// Unpacked form: the blocks that a sequence's rows see, in order, as bf16 ([sequence][block of its table], both with all heads),
+// the table that numbers them so, and the context lengths, -1 for a sequence that the call skips.  Bound by HBM, two bytes
+// written for each read: 16384 tokens of 8 heads of 128 dims 23 us with cold caches.
+constexpr int kUnpackThreads = 256, kUnpackCtas = 8;  // CTAs an SM
+template <int D>
+__global__ void __launch_bounds__(kUnpackThreads) unpack_fp8_kernel(const Fp8AttentionParams p, const Fp8Unpacked to) {
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, ctas = static_cast<int>(gridDim.x);
+  const int64_t thread = static_cast<int64_t>(blockIdx.x) * kUnpackThreads + tid, threads = static_cast<int64_t>(ctas) * kUnpackThreads;
+  const int64_t slots = static_cast<int64_t>(p.num_seqs) * p.max_blocks_per_seq;
+  for (int64_t i = thread; i < slots; i += threads) to.block_tables[i] = static_cast<int32_t>(i);
+  auto blocks_of = [&](int b, bool& skipped) -> int {
+    const int q0 = __ldg(p.query_start + b), q1 = __ldg(p.query_start + b + 1), len = __ldg(p.context_lens + b);
+    const int64_t chunk = static_cast<int64_t>(q1) - q0;
+    skipped = chunk < 0 || len < chunk || len > p.max_blocks_per_seq * kBlockTokens || q0 < 0 || q1 > p.query_rows;
+    return skipped || chunk == 0 ? 0 : (len + kBlockTokens - 1) / kBlockTokens;
+  };
+  for (int64_t b = thread; b < p.num_seqs; b += threads) {
+    bool skipped;
+    blocks_of(static_cast<int>(b), skipped);
+    to.context_lens[b] = skipped ? -1 : __ldg(p.context_lens + b);
+  }
+  const int pieces = p.num_kv_heads * D;  // of 16 codes, in a block of K (or V)
+  const int parts = (pieces + kUnpackThreads - 1) / kUnpackThreads;
+  auto unpack = [&](int b, int64_t item) {  // a part of a block: a piece of K and of V a thread
+    const int j = static_cast<int>(item / parts), x = static_cast<int>(item % parts) * kUnpackThreads + tid;
+    if (x >= pieces) return;
+    const int64_t at = static_cast<int64_t>(b) * p.max_blocks_per_seq + j;
+    int id = __ldg(p.block_tables + at);
+    if (id < 0 || id >= p.num_blocks) {
+      if (tid == 0) atomicOr(p.err, kErrBlockId);
+      id = 0;
+    }
+    const int64_t from = static_cast<int64_t>(id) * pieces;
+    const int head = x / D, row = x % D / (D / 16);
+    const uint8_t* e = p.kv_scales + (static_cast<int64_t>(id) * p.num_kv_heads + head) * 2 * kBlockTokens + row;
+    const uint4 codes[2] = {load_codes(p.k_cache + (from + x) * 16), load_codes(p.v_cache + (from + x) * 16)};
+    const float scale[2] = {fp8_scale(__ldg(e)), fp8_scale(__ldg(e + kBlockTokens))};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+      uint32_t r[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 f = fp8_floats(static_cast<uint16_t>(w[k / 2] >> 16 * (k & 1)));
+        r[k] = pack_bf16(f.x * scale[i], f.y * scale[i]);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(i ? to.v : to.k) + (at * pieces + x) * 2;
+      dst[0] = make_uint4(r[0], r[1], r[2], r[3]);
+      dst[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    }
+  };
+  // The sequences' items are dealt to the CTAs in turns.
+  __shared__ int s_blocks[kUnpackThreads];
+  int64_t turn = blockIdx.x;  // items ahead until this CTA's next
+  for (int b0 = 0; b0 < p.num_seqs; b0 += kUnpackThreads) {
+    const int n = min(kUnpackThreads, p.num_seqs - b0);
+    bool skipped;
+    if (tid < n) s_blocks[tid] = blocks_of(b0 + tid, skipped);
+    __syncthreads();
+    for (int x = 0; x < n; ++x) {
+      const int64_t items = static_cast<int64_t>(s_blocks[x]) * parts;
+      for (; turn < items; turn += ctas) unpack(b0 + x, turn);
+      turn -= items;
+    }
+    __syncthreads();
+  }
+}
+
 template <int D, int G, bool kSplit>
 cudaError_t launch_fp8(Fp8PrefillParams p, cudaStream_t stream) {
   constexpr int kCtaTokens = kTiles * kRows / G;
@@ -623,6 +694,34 @@ cudaError_t dispatch_fp8(const Fp8PrefillParams& p, int head_dim, int group, cud
 }
 
 }  // namespace
+
+cudaError_t launch_prefill_unpacked_fp8(const Fp8AttentionParams& a, int head_dim, int num_splits, const Fp8Unpacked& to, float* ws,
+                                        int num_sms, cudaStream_t stream) {
+  const int64_t blocks = static_cast<int64_t>(a.num_seqs) * a.max_blocks_per_seq, most = static_cast<int64_t>(num_sms) * kUnpackCtas;
+  const int64_t items = blocks * ((a.num_kv_heads * head_dim + kUnpackThreads - 1) / kUnpackThreads);
+  const cudaError_t e = launch_pdl(head_dim == 128 ? unpack_fp8_kernel<128> : unpack_fp8_kernel<64>,
+                                   dim3(static_cast<unsigned>(items < most ? items : most)), dim3(kUnpackThreads), 0, stream, a, to);
+  if (e != cudaSuccess) return e;
+  PrefillParams p{};
+  p.q = a.q;
+  p.k_cache = to.k;
+  p.v_cache = to.v;
+  p.block_tables = to.block_tables;
+  p.context_lens = to.context_lens;
+  p.query_start = a.query_start;
+  p.out = a.out;
+  p.err = a.err;
+  p.num_blocks = blocks;
+  p.num_seqs = a.num_seqs;
+  p.num_q_heads = a.num_q_heads;
+  p.num_kv_heads = a.num_kv_heads;
+  p.max_blocks_per_seq = a.max_blocks_per_seq;
+  p.max_query_len = a.max_query_len;
+  p.scale = a.scale;
+  p.num_splits = num_splits;
+  p.ws = ws;
+  return launch_paged_prefill(p, head_dim, a.num_q_heads / a.num_kv_heads, a.max_query_len, stream);
+}
 
 cudaError_t launch_prefill_fp8(const Fp8AttentionParams& a, int head_dim, int num_splits, float* ws, cudaStream_t stream) {
   Fp8PrefillParams p{};
