@@ -707,7 +707,9 @@ def paged_fp8_prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
                                 stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """paged_prefill_attention over an 8-bit cache: prompt chunks, or the few rows a sequence of drafted tokens.
 
-    q and out [T, Hq, D] are bf16; max_query_len is at least every chunk's length.  Returns ``out``.
+    q and out [T, Hq, D] are bf16; max_query_len is at least every chunk's length.  The workspace of a call with long chunks
+    holds its cache blocks as bf16 (up to 2 GB, ``fp8_prefill_workspace_size``); without one given, the thread keeps its own.
+    Returns ``out``.
     """
     return (_binding or _native()).fp8_prefill(q, k_cache, v_cache, kv_scales, block_tables, context_lens, query_start,
                                                max_query_len, scale, out, workspace, stream)
