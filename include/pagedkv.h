@@ -534,7 +534,9 @@ pkv_status pkv_copy_blocks_fp8(void* k_cache, void* v_cache, void* kv_scales, co
                                int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks, pkv_stream_t stream);
 /*
  * pkv_paged_decode_attention over such a cache (q and out bf16).  num_blocks * num_kv_heads * 16 must be below 2^31,
- * max_blocks_per_seq at most 2^26 and num_seqs at most 65535.  A token that a sequence does not see does not matter, whatever its row and exponent hold.
+ * max_blocks_per_seq at most 2^26 and num_seqs at most 65535.  A token that a sequence does not see does not matter, whatever
+ * its row and exponent hold.  Sums are fp32; softmax weights enter the product with V in fp16 (eleven bits, the same ones
+ * wherever the batch is cut: a sequence's result does not depend on its batch beyond fp32 rounding).
  *
  *   workspace   device, 16-byte aligned, at least pkv_fp8_decode_workspace_size bytes (may be NULL if that is 0); scratch,
  *               as for pkv_paged_decode_attention

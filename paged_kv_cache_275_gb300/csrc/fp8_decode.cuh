@@ -12,10 +12,13 @@
 // brought to a largest value of 2^14 by a power of two, down to 2^-28 of it; smaller values lose bits that a score does not
 // show.  The exponents stay outside of the products: a score is S 2^(ke) scale, and a weight takes V's exponent with it,
 //   w_j = 2^((s_j - m) + ve_j - r),   O = 2^r sum_j w_j vc_j,   l = sum_j 2^(s_j - m),
-// with running references (base 2) m of s and r of (s - m) + ve, seven below their largest value and raised when some value
-// passes them by fifteen, so that w is at most 2^15 and the largest of a row is 2^7 or more: fp16's 11 bits hold for weights
-// down to 2^-21 of the largest, and those below 2^-32 of it vanish.  (m comes off first: next to a large score an exponent would
-// lose its bits.)
+// with running references (base 2) m of s and r of (s - m) + ve, seven to eight below their largest value and raised when some
+// value passes them by fifteen, so that w is at most 2^15 and the largest of a row is 2^7 or more: fp16's 11 bits (half a step is
+// 2^-11 of a weight) hold for weights down to 2^-21 of the largest, and those below 2^-32 of it vanish.  Eleven, for the values
+// that they weigh have four.  The references are whole numbers: a power of two moves no significant bit, so a weight is rounded
+// to the same eleven whatever the reference is, and a sequence's result does not depend on where its batch is cut.  (With the
+// largest value itself, 3 to 7 % of the results changed by a step with the cut; with whole numbers those that 32-bit sums
+// change.)  (m comes off first: next to a large score an exponent would lose its bits.)
 //
 // Work.  The batch's blocks form one stream of units of 32 KB of K and V, eight (block, kv head) tiles of 128 dims or sixteen
 // of 64: all eight heads of a block (of two), or two (four) blocks of four heads, and so on.  The stream is cut into equal
@@ -56,7 +59,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMostCluster = 16;
 constexpr float kNone = -3.0e38f;  // the reference of a row that has seen no token
-constexpr float kTopLog = 7.f, kMostLog = 15.f;  // the largest of a row's weights is brought to 2^7 and may grow to 2^15
+constexpr float kTopLog = 7.f, kMostLog = 15.f;  // the largest of a row's weights is brought to 2^7 .. 2^8, may grow to 2^15
 
 template <int D, int NC, bool kCluster>
 struct Few {
@@ -338,13 +341,13 @@ struct Pair {
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
           const float m = k ? -nm[nc].y : -nm[nc].x, r = k ? -nr[nc].y : -nr[nc].x;
-          const float mn = fmaxf(top - kTopLog, m), by = m - mn;
+          const float mn = fmaxf(floorf(top) - kTopLog, m), by = m - mn;
 #pragma unroll
           for (int y = 0; y < kTurns; ++y) top_w = fmaxf(top_w, fmaxf(s[y][nc][k] - mn + v_lo[y], s[y][nc][k + 2] - mn + v_hi[y]));
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) top_w = fmaxf(top_w, __shfl_xor_sync(kAll, top_w, off));
           const float was = r + by;  // against the new m
-          const float rn = fmaxf(top_w - kTopLog, was), alpha = ex2(was - rn), beta = ex2(by);
+          const float rn = fmaxf(floorf(top_w) - kTopLog, was), alpha = ex2(was - rn), beta = ex2(by);
           if (k) {
             nm[nc].y = -mn;
             nr[nc].y = -rn;
