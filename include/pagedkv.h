@@ -565,11 +565,18 @@ pkv_status pkv_paged_fp8_prefill_attention(const void* q, const void* k_cache, c
                                            int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                            int64_t num_blocks, int32_t block_size, float scale, void* out,
                                            void* workspace, size_t workspace_bytes, pkv_stream_t stream);
-/* Its workspace on the current device, for these sizes.  Long chunks have their cache blocks turned into bf16 there, which takes
-   4 * num_seqs * max_blocks_per_seq * 16 * num_kv_heads * head_dim bytes, up to 2 GB (beyond that they do without). */
+/*
+ * Its workspace on the current device, for calls of exactly these sizes (fewer sequences can be split and take more).  Long
+ * chunks have their cache blocks turned into bf16 there, which takes 4 * num_seqs * max_blocks_per_seq * 16 * num_kv_heads *
+ * head_dim bytes, up to 2 GB.  Beyond that, and with a smaller workspace, every CTA turns what it reads into bf16, for up to
+ * 1.2 times the time: pkv_fp8_prefill_least_workspace_size bytes are enough for that.
+ */
 pkv_status pkv_fp8_prefill_workspace_size(int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs,
                                           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                           int32_t max_blocks_per_seq, size_t* bytes);
+pkv_status pkv_fp8_prefill_least_workspace_size(int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs,
+                                                int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                                int32_t max_blocks_per_seq, size_t* bytes);
 
 /*
  * Copy whole KV blocks inside the pool: the copy half of copy-on-write for

@@ -71,6 +71,7 @@ EXPORTS = (
     "pkv_fp8_decode_workspace_size",
     "pkv_paged_fp8_prefill_attention",
     "pkv_fp8_prefill_workspace_size",
+    "pkv_fp8_prefill_least_workspace_size",
     "pkv_bm_create",
     "pkv_bm_destroy",
     "pkv_bm_num_free",
@@ -151,6 +152,7 @@ def load(path: Path | str | None = None) -> ctypes.CDLL:
         lib.pkv_paged_fp8_prefill_attention.argtypes = [V, V, V, V, V, I32, V, V, I64, I32, I32, I32, I32, I32, I64, I32, F32,
                                                         V, V, SZ, V]
         lib.pkv_fp8_prefill_workspace_size.argtypes = [I64] + [I32] * 6 + [ctypes.POINTER(SZ)]
+        lib.pkv_fp8_prefill_least_workspace_size.argtypes = [I64] + [I32] * 6 + [ctypes.POINTER(SZ)]
         lib.pkv_bm_create.argtypes = [I64, V, ctypes.POINTER(V)]
         lib.pkv_bm_destroy.argtypes = [V]
         lib.pkv_bm_num_free.argtypes = [V, ctypes.POINTER(I64)]
@@ -176,7 +178,7 @@ def load(path: Path | str | None = None) -> ctypes.CDLL:
                      "pkv_prefix_decode_workspace_size", "pkv_kv_append_fp8", "pkv_rope_append_fp8",
                      "pkv_kv_gather_fp8", "pkv_copy_blocks_fp8", "pkv_paged_fp8_decode_attention",
                      "pkv_fp8_decode_workspace_size", "pkv_paged_fp8_prefill_attention",
-                     "pkv_fp8_prefill_workspace_size"):
+                     "pkv_fp8_prefill_workspace_size", "pkv_fp8_prefill_least_workspace_size"):
             getattr(lib, name).restype = ctypes.c_int
         lib.pkv_last_error_message.argtypes = []
         lib.pkv_last_error_message.restype = ctypes.c_char_p
@@ -685,10 +687,14 @@ def fp8_decode_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int
 
 
 def fp8_prefill_workspace_size(num_query_tokens: int, max_query_len: int, num_seqs: int, num_q_heads: int,
-                               num_kv_heads: int, head_dim: int, max_blocks_per_seq: int) -> int:
-    """Bytes of the workspace of a chunk attention call over an 8-bit cache of these sizes, on the current device."""
-    return _query(ctypes.c_size_t, load().pkv_fp8_prefill_workspace_size, num_query_tokens, max_query_len, num_seqs,
-                  num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq)
+                               num_kv_heads: int, head_dim: int, max_blocks_per_seq: int, *, unpack: bool = True) -> int:
+    """Bytes of the workspace of a chunk attention call over an 8-bit cache of exactly these sizes, on the current device.
+
+    ``unpack=False``: of a call that is given that too.
+    """
+    lib = load()
+    return _query(ctypes.c_size_t, lib.pkv_fp8_prefill_workspace_size if unpack else lib.pkv_fp8_prefill_least_workspace_size,
+                  num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq)
 
 
 def paged_fp8_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, kv_scales: torch.Tensor,
@@ -703,13 +709,14 @@ def paged_fp8_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
 def paged_fp8_prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, kv_scales: torch.Tensor,
                                 block_tables: torch.Tensor, context_lens: torch.Tensor, query_start: torch.Tensor,
                                 max_query_len: int, scale: float, out: torch.Tensor, *,
-                                workspace: torch.Tensor | None = None,
+                                workspace: torch.Tensor | None = None, unpack: bool = True,
                                 stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """paged_prefill_attention over an 8-bit cache: prompt chunks, or the few rows a sequence of drafted tokens.
 
-    q and out [T, Hq, D] are bf16; max_query_len is at least every chunk's length.  The workspace of a call with long chunks
-    holds its cache blocks as bf16 (up to 2 GB, ``fp8_prefill_workspace_size``); without one given, the thread keeps its own.
-    Returns ``out``.
+    q and out [T, Hq, D] are bf16; max_query_len is at least every chunk's length.  A call with long chunks turns its cache
+    blocks into bf16 in the workspace (up to 2 GB, ``fp8_prefill_workspace_size``).  With ``unpack=False`` it converts them as
+    it goes, which takes up to 1.2 times as long and little workspace; so does a call that was given no workspace and finds no
+    memory for one.  Without a workspace given, each thread keeps one a stream.  Returns ``out``.
     """
     return (_binding or _native()).fp8_prefill(q, k_cache, v_cache, kv_scales, block_tables, context_lens, query_start,
-                                               max_query_len, scale, out, workspace, stream)
+                                               max_query_len, scale, out, workspace, unpack, stream)

@@ -8,6 +8,7 @@
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/util/Exception.h>
 #include <cuda_runtime.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -178,7 +179,7 @@ struct Workspace {
         raise(PyExc_ValueError, "workspace must hold " + std::to_string(need) + " bytes (got " + std::to_string(bytes) + ")");
       return;
     }
-    bytes = std::max<size_t>(need, 256);
+    const size_t size = std::max<size_t>(need, 256);
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(handle, &capture) != cudaSuccess) {
       (void)cudaGetLastError();
@@ -187,8 +188,9 @@ struct Workspace {
     // A call that is being captured takes a buffer of its own: the allocator gives it from the memory that torch reserves for
     // the graph, for as long as the graph lives, and what the graph's later calls are given there comes behind this call.
     if (capture != cudaStreamCaptureStatusNone) {
-      own = allocate(bytes, handle);
+      own = allocate(size, handle);
       data = own.get();
+      bytes = size;
       return;
     }
     Scratch* mine = nullptr;
@@ -201,8 +203,8 @@ struct Workspace {
     if (mine->bytes < need) {  // (the old buffer goes back first, to what runs behind it on its stream)
       mine->bytes = 0;
       mine->data.reset();
-      mine->data = allocate(bytes, handle);
-      mine->bytes = bytes;
+      mine->data = allocate(size, handle);
+      mine->bytes = size;
     }
     data = mine->data.get();
     bytes = mine->bytes;
@@ -561,7 +563,7 @@ PyObject* fp8_decode(PyObject*, PyObject* const* a, Py_ssize_t) {
 }
 
 // fp8_prefill(q, k_cache, v_cache, kv_scales, block_tables, context_lens, query_start, max_query_len, scale, out, workspace,
-// stream)
+// unpack, stream)
 PyObject* fp8_prefill(PyObject*, PyObject* const* a, Py_ssize_t) {
   return guarded([&]() -> PyObject* {
     Attention t(a[0], a[1], a[2], a[4], a[5], a[9], at::kFloat8_e4m3fn);
@@ -572,12 +574,21 @@ PyObject* fp8_prefill(PyObject*, PyObject* const* a, Py_ssize_t) {
     const int32_t most = int32(a[7], "max_query_len");
     const double scale = PyFloat_AsDouble(a[8]);
     if (PyErr_Occurred()) throw Raised{};
-    const pkv_stream_t stream = stream_of(a[11], t.dev);
+    const int unpack = PyObject_IsTrue(a[11]);
+    if (unpack < 0) throw Raised{};
+    const pkv_stream_t stream = stream_of(a[12], t.dev);
     const OnDevice guard(t.dev);
     size_t need = 0;
-    check(pkv_fp8_prefill_workspace_size(t.rows, most, t.batch, t.hq, t.hkv, t.d, t.width, &need));
+    auto size_of = [&](auto query) { check(query(t.rows, most, t.batch, t.hq, t.hkv, t.d, t.width, &need)); };
+    size_of(unpack ? pkv_fp8_prefill_workspace_size : pkv_fp8_prefill_least_workspace_size);
     Workspace ws;
-    if (need > 0) ws.take(a[10], t.dev, stream, need);
+    try {
+      if (need > 0) ws.take(a[10], t.dev, stream, need);
+    } catch (const c10::OutOfMemoryError&) {  // of a workspace that was not given: the form that needs least
+      size_of(pkv_fp8_prefill_least_workspace_size);
+      if (need > 0) ws.take(a[10], t.dev, stream, need);
+    }
+    ws.bytes = need;  // (what is larger chooses no other form)
     run([&] {
       return pkv_paged_fp8_prefill_attention(t.q, t.kc, t.vc, cache.scales, t.table, t.width, t.lens,
                                              static_cast<const int32_t*>(start.data_ptr()), t.rows, most, t.batch, t.hq,
@@ -619,7 +630,7 @@ PyMethodDef g_methods[] = {
     method<11, prefix_decode>("prefix_decode"), method<12, rope_append<true>>("rope_append_fp8"),
     method<7, kv_append_fp8>("kv_append_fp8"), method<7, kv_gather_fp8>("kv_gather_fp8"),
     method<5, copy_blocks_fp8>("copy_blocks_fp8"), method<10, fp8_decode>("fp8_decode"),
-    method<12, fp8_prefill>("fp8_prefill"), {nullptr, nullptr, 0, nullptr},
+    method<13, fp8_prefill>("fp8_prefill"), {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1346,10 +1346,12 @@ bool fp8_unpacks(int64_t num_query_tokens, int32_t max_query_len, int32_t num_se
   return num_seqs * context * num_kv_heads * (ctas * each - once) > 3.5;
 }
 
+// may_unpack: false for a call whose workspace is too small for that.
 Fp8ChunkPlan fp8_chunk_plan(int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs, int32_t num_q_heads,
-                            int32_t num_kv_heads, int32_t head_dim, int32_t max_blocks_per_seq, int sms) {
+                            int32_t num_kv_heads, int32_t head_dim, int32_t max_blocks_per_seq, int sms, bool may_unpack) {
   Fp8ChunkPlan plan{fp8_prefill_splits(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq, sms),
-                    fp8_unpacks(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq)};
+                    may_unpack && fp8_unpacks(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                              max_blocks_per_seq)};
   if (plan.unpacks) {
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     const size_t blocks = static_cast<size_t>(num_seqs) * max_blocks_per_seq;
@@ -1362,11 +1364,9 @@ Fp8ChunkPlan fp8_chunk_plan(int64_t num_query_tokens, int32_t max_query_len, int
       plan.states + pkv::prefill_workspace_bytes(num_seqs, max_query_len, num_q_heads, num_kv_heads, head_dim, plan.splits);
   return plan;
 }
-}  // namespace
 
-pkv_status pkv_fp8_prefill_workspace_size(int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs,
-                                          int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
-                                          int32_t max_blocks_per_seq, size_t* bytes) {
+pkv_status fp8_prefill_bytes(int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs, int32_t num_q_heads,
+                             int32_t num_kv_heads, int32_t head_dim, int32_t max_blocks_per_seq, bool may_unpack, size_t* bytes) {
   if (!bytes) return fail(PKV_ERR_INVALID_ARGUMENT, "bytes is null");
   if (num_query_tokens < 0 || max_query_len < 0)
     return fail(PKV_ERR_INVALID_ARGUMENT, "num_query_tokens and max_query_len must be >= 0");
@@ -1384,11 +1384,27 @@ pkv_status pkv_fp8_prefill_workspace_size(int64_t num_query_tokens, int32_t max_
         st != PKV_OK)
       return st;
   } else {
-    need = fp8_chunk_plan(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, sms)
+    need = fp8_chunk_plan(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, sms,
+                          may_unpack)
                .bytes;
   }
   *bytes = need;
   return ok();
+}
+}  // namespace
+
+pkv_status pkv_fp8_prefill_workspace_size(int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs,
+                                          int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                          int32_t max_blocks_per_seq, size_t* bytes) {
+  return fp8_prefill_bytes(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, true,
+                           bytes);
+}
+
+pkv_status pkv_fp8_prefill_least_workspace_size(int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs,
+                                                int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                                int32_t max_blocks_per_seq, size_t* bytes) {
+  return fp8_prefill_bytes(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, false,
+                           bytes);
 }
 
 pkv_status pkv_paged_fp8_decode_attention(const void* q, const void* k_cache, const void* v_cache, const void* kv_scales,
@@ -1457,8 +1473,12 @@ pkv_status pkv_paged_fp8_prefill_attention(const void* q, const void* k_cache, c
     return few_rows_fp8(p, head_dim, workspace, workspace_bytes, stream);
   int sms = 0;
   if (pkv_status st = device_state(&p.err, &sms); st != PKV_OK) return st;
-  const Fp8ChunkPlan plan =
-      fp8_chunk_plan(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, sms);
+  auto plan_of = [&](bool may_unpack) {
+    return fp8_chunk_plan(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, sms,
+                          may_unpack);
+  };
+  Fp8ChunkPlan plan = plan_of(true);
+  if (plan.unpacks && (!workspace || workspace_bytes < plan.bytes)) plan = plan_of(false);
   if (plan.bytes > 0 && (!workspace || workspace_bytes < plan.bytes))
     return fail(PKV_ERR_INVALID_ARGUMENT, "workspace too small: %zu bytes given, %zu needed", workspace ? workspace_bytes : size_t{0},
                 plan.bytes);
