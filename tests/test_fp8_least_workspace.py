@@ -32,15 +32,22 @@ def long_case(width=2000):
     return case, sizes
 
 
-def on_a_thread_without_memory(f, spare):
-    """f() on a thread of its own (which has kept no workspace), with so little memory left for this process."""
+def on_a_thread_without_memory(f, piece):
+    """f() on a thread of its own (which has kept no workspace), while this process can have no more than what it has and no
+    piece of that as large as `piece` is free."""
     from test_gpu_fp8_calls import on_a_thread
 
     torch.cuda.synchronize()
     torch.cuda.empty_cache()
     total = torch.cuda.get_device_properties(0).total_memory
-    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + spare) / total)
+    torch.cuda.set_per_process_memory_fraction(torch.cuda.memory_reserved() / total)
+    held = []
     try:
+        while True:
+            try:
+                held.append(torch.empty(piece, dtype=torch.uint8, device="cuda"))
+            except torch.OutOfMemoryError:
+                break
         thread, raised = on_a_thread(f)
         thread.join()
         torch.cuda.synchronize()
@@ -92,10 +99,10 @@ def test_asked_for_and_split():
 def test_no_memory_for_the_blocks():
     case, _ = long_case()
     want, got = case.call(), torch.empty_like(case.dq)
-    spare = 30 << 20
-    assert case.need > 2 * spare
+    piece = 30 << 20
+    assert case.need > piece
     on_a_thread_without_memory(
-        lambda: pkv.paged_fp8_prefill_attention(case.dq, *case.caches, case.dstart, case.most, 0.09, got), spare)
+        lambda: pkv.paged_fp8_prefill_attention(case.dq, *case.caches, case.dstart, case.most, 0.09, got), piece)
     assert torch.equal(got, want) and device_errors() == 0
 
 
@@ -105,7 +112,8 @@ def test_no_memory_for_a_split_call_s_states():
     from test_gpu_fp8_unpacked import Case
 
     case = Case((4096,), (1024,), 16, 2, 128, seed=9)
-    want = case.call()
+    want, got = case.call(), torch.empty_like(case.dq)
     with pytest.raises(torch.OutOfMemoryError):
-        on_a_thread_without_memory(lambda: case.call(), 4 << 20)
+        on_a_thread_without_memory(
+            lambda: pkv.paged_fp8_prefill_attention(case.dq, *case.caches, case.dstart, case.most, 0.09, got), 4 << 20)
     assert torch.equal(case.call(), want) and device_errors() == 0
