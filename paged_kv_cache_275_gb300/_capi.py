@@ -716,7 +716,8 @@ def paged_fp8_prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     q and out [T, Hq, D] are bf16; max_query_len is at least every chunk's length.  A call with long chunks turns its cache
     blocks into bf16 in the workspace (up to 2 GB, ``fp8_prefill_workspace_size``).  With ``unpack=False`` it converts them as
     it goes, which takes up to 1.2 times as long and little workspace; so does a call that was given no workspace and finds no
-    memory for one.  Without a workspace given, each thread keeps one a stream.  Returns ``out``.
+    memory for one.  Without a workspace given, each thread keeps one a stream, of up to 64 MB; a larger one is the call's own.
+    Returns ``out``.
     """
     return (_binding or _native()).fp8_prefill(q, k_cache, v_cache, kv_scales, block_tables, context_lens, query_start,
                                                max_query_len, scale, out, workspace, unpack, stream)

@@ -158,6 +158,10 @@ struct Scratch {
   Buffer data;
 };
 thread_local std::vector<Scratch> t_scratch;
+// Larger ones are not kept but go back to the allocator, for what runs behind the call on its stream.  The states of cut
+// streams and splits, which go by the GPU's CTAs, are smaller; what goes by the cache's size is not for every thread and stream
+// to hold.
+constexpr size_t kMostKept = size_t{64} << 20;
 
 // The caller's workspace (kept alive by `owner`), or one of this thread, device and stream.
 struct Workspace {
@@ -187,7 +191,7 @@ struct Workspace {
     }
     // A call that is being captured takes a buffer of its own: the allocator gives it from the memory that torch reserves for
     // the graph, for as long as the graph lives, and what the graph's later calls are given there comes behind this call.
-    if (capture != cudaStreamCaptureStatusNone) {
+    if (capture != cudaStreamCaptureStatusNone || need > kMostKept) {
       own = allocate(size, handle);
       data = own.get();
       bytes = size;
