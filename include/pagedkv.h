@@ -566,8 +566,9 @@ pkv_status pkv_paged_fp8_prefill_attention(const void* q, const void* k_cache, c
                                            int64_t num_blocks, int32_t block_size, float scale, void* out,
                                            void* workspace, size_t workspace_bytes, pkv_stream_t stream);
 /*
- * Its workspace on the current device, for calls of exactly these sizes (fewer sequences can be split and take more).  Long
- * chunks have their cache blocks turned into bf16 there, which takes 4 * num_seqs * max_blocks_per_seq * 16 * num_kv_heads *
+ * Its workspace on the current device, for calls of exactly these sizes (fewer sequences can be split and take more); with up
+ * to 24 rows a sequence and kv head (max_query_len * num_q_heads / num_kv_heads), for calls of up to num_seqs sequences and
+ * max_blocks_per_seq with that max_query_len, whatever num_query_tokens.  Long chunks have their cache blocks turned into bf16 there, which takes 4 * num_seqs * max_blocks_per_seq * 16 * num_kv_heads *
  * head_dim bytes, up to 2 GB.  Beyond that, and with a smaller workspace, every CTA turns what it reads into bf16, for up to
  * 1.2 times the time: pkv_fp8_prefill_least_workspace_size bytes are enough for that.
  */

@@ -1376,19 +1376,20 @@ pkv_status fp8_prefill_bytes(int64_t num_query_tokens, int32_t max_query_len, in
   int sms = 0;
   if (pkv_status st = device_state(nullptr, &sms); st != PKV_OK) return st;
   const int64_t rows = static_cast<int64_t>(max_query_len) * (num_q_heads / num_kv_heads);
-  int cluster = 0;
-  size_t need = 0, enough = 0;
+  size_t enough = 0;
   if (rows <= pkv::kFp8MostRows) {
+    int cluster = 0;
+    size_t need = 0;
     if (pkv_status st = few_rows_need(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, static_cast<int>(rows), &cluster,
                                       &need, &enough);
         st != PKV_OK)
       return st;
   } else {
-    need = fp8_chunk_plan(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, sms,
+    enough = fp8_chunk_plan(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, sms,
                           may_unpack)
                .bytes;
   }
-  *bytes = need;
+  *bytes = enough;
   return ok();
 }
 }  // namespace
