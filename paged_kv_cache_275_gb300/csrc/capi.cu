@@ -1327,22 +1327,27 @@ struct Fp8ChunkPlan {
 };
 
 // Whether the codes are turned into bf16 once, ahead of the bf16 kernel, or by every CTA that sees them.  A CTA's part of it
-// costs an SM 3.9 ns a token and head of 128 dims (2.6 of 64), of 152 SMs; unpacking costs the HBM 6 bytes an element, and a
-// launch.  Measured (32 q and 8 kv heads of 128 dims; by every CTA and ahead, us): 2 x 8192 946, 789; 1 x 2048 43.7, 42.7;
+// costs an SM 3.9 ns a token and head of 128 dims (2.6 of 64); unpacking costs the HBM 6 bytes an element, and a launch.
+// Measured (32 q and 8 kv heads of 128 dims; by every CTA and ahead, us): 2 x 8192 946, 789; 1 x 2048 43.7, 42.7;
 // 1 x 1024 24.2, 27.1; 8 x 1024 119, 106; 8 x 512 behind 3584 271, 259; 8 x 256 behind 3840 147, 158; 1 x 512 behind 8192, 16 q
 // heads, 49.8, 56.2.
-// The context lengths are not known here: three quarters of the table, or the chunk.
+// The context lengths are not known here.  A table of up to eight chunks is taken for one that was made for its sequences: three
+// quarters of it, or the chunk.  What a wider one holds is anything (a table as wide as the longest context that is served), and
+// the chunk alone is sure: what pays for it pays for any longer context.  (8 x 512 behind 3584 245 us in a table of 256 blocks,
+// 262 in one of 2048; trusting that one, eight fresh prompts of 512 would be given 1 GB for 17 MB of blocks and gain nothing.)
+constexpr int kFp8OwnTable = 8;
 constexpr size_t kFp8MostUnpacked = size_t{2} << 30;
 bool fp8_unpacks(int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
-                 int32_t head_dim, int32_t max_blocks_per_seq) {
+                 int32_t head_dim, int32_t max_blocks_per_seq, int sms) {
   // (The bf16 kernel's map of the output ends behind so many rows.)
   if (num_query_tokens > static_cast<int64_t>(num_seqs) * max_query_len) return false;
   const int64_t slots = static_cast<int64_t>(num_seqs) * max_blocks_per_seq * PKV_BLOCK_SIZE * num_kv_heads;
   if (slots >= (int64_t{1} << 31) || slots * head_dim * 4 > static_cast<int64_t>(kFp8MostUnpacked)) return false;
   const double chunk = static_cast<double>(num_query_tokens) / num_seqs;
-  const double context = std::max(0.75 * PKV_BLOCK_SIZE * max_blocks_per_seq, chunk);
+  const double table = static_cast<double>(PKV_BLOCK_SIZE) * max_blocks_per_seq;
+  const double context = table <= kFp8OwnTable * chunk ? std::max(0.75 * table, chunk) : chunk;
   const double ctas = std::ceil(chunk / pkv::prefill_cta_tokens(num_q_heads / num_kv_heads)) * (1 - chunk / (2 * context));
-  const double each = head_dim == 128 ? 3.9e-3 / 152 : 2.6e-3 / 152, once = 6.0 * head_dim / 5.5e6;
+  const double each = (head_dim == 128 ? 3.9e-3 : 2.6e-3) / sms, once = 6.0 * head_dim / 5.5e6;
   return num_seqs * context * num_kv_heads * (ctas * each - once) > 3.5;
 }
 
@@ -1351,7 +1356,7 @@ Fp8ChunkPlan fp8_chunk_plan(int64_t num_query_tokens, int32_t max_query_len, int
                             int32_t num_kv_heads, int32_t head_dim, int32_t max_blocks_per_seq, int sms, bool may_unpack) {
   Fp8ChunkPlan plan{fp8_prefill_splits(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq, sms),
                     may_unpack && fp8_unpacks(num_query_tokens, max_query_len, num_seqs, num_q_heads, num_kv_heads, head_dim,
-                                              max_blocks_per_seq)};
+                                              max_blocks_per_seq, sms)};
   if (plan.unpacks) {
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     const size_t blocks = static_cast<size_t>(num_seqs) * max_blocks_per_seq;
