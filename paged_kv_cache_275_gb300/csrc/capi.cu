@@ -376,7 +376,8 @@ pkv_status pkv_kv_append(const void* k, const void* v, const int64_t* slot_mappi
 pkv_status pkv_copy_blocks(void* k_cache, void* v_cache, const int64_t* src_dst, int32_t num_pairs,
                            int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks, pkv_stream_t stream) {
   if (num_pairs < 0) return fail(PKV_ERR_INVALID_ARGUMENT, "num_pairs must be >= 0 (got %d)", num_pairs);
-  if (num_pairs > (1 << 30)) return fail(PKV_ERR_UNSUPPORTED, "num_pairs %d too large", num_pairs);
+  if (num_pairs >= (1 << 30))  // two CTAs a pair, in a grid of up to 2^31 - 1
+    return fail(PKV_ERR_UNSUPPORTED, "num_pairs %d too large", num_pairs);
   if (num_kv_heads <= 0) return fail(PKV_ERR_INVALID_ARGUMENT, "num_kv_heads must be positive (got %d)", num_kv_heads);
   if (head_dim != 64 && head_dim != 128)
     return fail(PKV_ERR_UNSUPPORTED, "head_dim %d not built (64 or 128)", head_dim);
@@ -1199,7 +1200,8 @@ pkv_status pkv_kv_gather_fp8(const void* k_cache, const void* v_cache, const voi
 pkv_status pkv_copy_blocks_fp8(void* k_cache, void* v_cache, void* kv_scales, const int64_t* src_dst, int32_t num_pairs,
                                int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks, pkv_stream_t stream) {
   if (num_pairs < 0) return fail(PKV_ERR_INVALID_ARGUMENT, "num_pairs must be >= 0 (got %d)", num_pairs);
-  if (num_pairs > (1 << 30)) return fail(PKV_ERR_UNSUPPORTED, "num_pairs %d too large", num_pairs);
+  if (num_pairs >= (1 << 30))  // two CTAs a pair, in a grid of up to 2^31 - 1
+    return fail(PKV_ERR_UNSUPPORTED, "num_pairs %d too large", num_pairs);
   if (pkv_status st = check_fp8_rows(0, num_kv_heads, head_dim, num_blocks, PKV_BLOCK_SIZE); st != PKV_OK) return st;
   if (num_pairs == 0) return ok();
   if (!k_cache || !v_cache || !kv_scales || !src_dst) return fail(PKV_ERR_INVALID_ARGUMENT, "null pointer argument");
