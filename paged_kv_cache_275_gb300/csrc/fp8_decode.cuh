@@ -14,11 +14,17 @@
 //   w_j = 2^((s_j - m) + ve_j - r),   O = 2^r sum_j w_j vc_j,   l = sum_j 2^(s_j - m),
 // with running references (base 2) m of s and r of (s - m) + ve, seven to eight below their largest value and raised when some
 // value passes them by fifteen, so that w is at most 2^15 and the largest of a row is 2^7 or more: fp16's 11 bits (half a step is
-// 2^-11 of a weight) hold for weights down to 2^-21 of the largest, and those below 2^-32 of it vanish.  Eleven, for the values
-// that they weigh have four.  The references are whole numbers: a power of two moves no significant bit, so a weight is rounded
-// to the same eleven whatever the reference is, and a sequence's result does not depend on where its batch is cut.  (With the
-// largest value itself, 3 to 7 % of the results changed by a step with the cut; with whole numbers those that 32-bit sums
-// change.)  (m comes off first: next to a large score an exponent would lose its bits.)
+// 2^-11 of a weight) hold for weights down to 2^-21 of the largest, and those below 2^-32 of it vanish.  (m comes off first: next
+// to a large score an exponent would lose its bits.)
+//
+// Weights.  With one block of columns (decode, and chunks of up to eight rows) a weight enters its product in two parts, the
+// fp16 and what that rounded off, as the bf16 cache's decode has it, so that little but the output's own rounding is left (against
+// sums in 32 bits the results differ by 5e-5 of themselves, one part 4e-4).  128 sequences 105.9 -> 107.1 us, 61 long ones 104.9 -> 107.1, one 7.7 -> 7.9.
+// With two or three blocks, rows of chunks, it is one part: the chunk kernel beside it has eight bits, and the second part costs
+// 64 drafts 90 -> 100 us, 24 rows 106 -> 118.  There l sums the same eleven bits, for a row that one token outweighs then loses
+// none of them (without, 9e-4; 64 drafts 90.1 -> 92.2, 24 rows 106 -> 109).  And the references are whole numbers: a power of two moves no
+// significant bit, so a weight is rounded to the same eleven whatever the reference is, and a sequence's result does not depend
+// on where its batch is cut.  (With the largest value itself, 3 to 7 % of the results changed by a step with the cut.)
 //
 // Work.  The batch's blocks form one stream of units of 32 KB of K and V, eight (block, kv head) tiles of 128 dims or sixteen
 // of 64: all eight heads of a block (of two), or two (four) blocks of four heads, and so on.  The stream is cut into equal
@@ -36,9 +42,10 @@
 // joined through distributed shared memory.  One launch, no workspace, and no pass over the batch's lengths: one sequence of
 // 4097 tokens, 16 q and 8 kv heads, takes 7.8 us a call.
 //
-// Measured (32 q and 8 kv heads of 128 dims): 128 sequences of 512..4096 tokens 107 us, 5.7 TB/s with the second launch (0.85
-// of the copy bandwidth; 98 us with the products taken out); 61 sequences of up to 65536 tokens, 64 q heads of 64 dims, 106 us
-// (94 so), where the instructions count, 0.64 of the issue slots; 64 sequences with up to five tokens 89.6 us.
+// Measured (32 q and 8 kv heads of 128 dims; calls one after another over several inputs in turn): 128 sequences of 512..4096
+// tokens 107.1 us, 5.7 TB/s with the second launch (0.85 of the copy bandwidth); 61 sequences of up to 65536 tokens, 64 q heads
+// of 64 dims, 107.1 us, where the instructions count; 64 sequences with up to five tokens 92.2 us.  (Before weights came in two
+// parts and with the products taken out, over one input: 98 and 94.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -71,6 +78,7 @@ struct Few {
   // The next tile's scores beside this one's softmax: with so many registers a warp is alone with one other on its scheduler
   // (64 x 6 tokens 110 -> 103 us; with two column blocks 84.7 -> 86.2, with one 1000 short sequences 49.0 -> 50.8).
   static constexpr bool kAhead = D == 128 && NC == 3 && !kCluster;
+  static constexpr int kParts = NC == 1 ? 2 : 1;  // fp16 parts of a weight
   static constexpr int kStages = kAhead ? 5 : 6 * kTurns / kCtas;   // tiles of a warp's ring
   static constexpr int kStage = 2 * kTile;                 // K, V
   static constexpr int kScales = 2 * kBlockTokens;         // the exponents of both
@@ -172,6 +180,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ float2 unpack_f16(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -364,7 +373,7 @@ struct Pair {
           }
         }
     }
-    uint32_t w[kTurns][kUsed][2];  // B fragments of the weights
+    uint32_t w[T::kParts][kTurns][kUsed][2];  // B fragments of the weights
 #pragma unroll
     for (int y = 0; y < kTurns; ++y)
 #pragma unroll
@@ -373,8 +382,16 @@ struct Pair {
         for (int h = 0; h < 2; ++h) {
           float2 d, e;
           logs(y, nc, h, d, e);
-          l[nc] = __fadd2_rn(l[nc], make_float2(ex2(d.x), ex2(d.y)));
-          w[y][nc][h] = transpose8(pack_f16(ex2(e.x), ex2(e.y)));
+          const float2 p = make_float2(ex2(d.x), ex2(d.y)), x = make_float2(ex2(e.x), ex2(e.y));
+          const uint32_t high = pack_f16(x.x, x.y);
+          w[0][y][nc][h] = transpose8(high);
+          if constexpr (T::kParts == 2) {
+            const float2 of = unpack_f16(high);
+            w[1][y][nc][h] = transpose8(pack_f16(x.x - of.x, x.y - of.y));
+            l[nc] = __fadd2_rn(l[nc], p);
+          } else {
+            l[nc] = __fadd2_rn(l[nc], unpack_f16(pack_f16(p.x, p.y)));
+          }
         }
     // O^T += Vc^T W^T.  A lane's four codes of a chunk: tokens 2t and 2t + 1, dims 2g and 2g + 1; dims 2g are rows g of
     // the product, dims 2g + 1 rows g + 8.
@@ -398,10 +415,12 @@ struct Pair {
           a[k][1] = fp8_halves(static_cast<uint16_t>(x >> 16));
         }
 #pragma unroll
-        for (int nc = 0; nc < kUsed; ++nc) {
-          mma_f16(o[2 * c][nc], a[0][0], a[0][1], a[1][0], a[1][1], w[y][nc][0], w[y][nc][1]);
-          mma_f16(o[2 * c + 1][nc], a[2][0], a[2][1], a[3][0], a[3][1], w[y][nc][0], w[y][nc][1]);
-        }
+        for (int part = 0; part < T::kParts; ++part)
+#pragma unroll
+          for (int nc = 0; nc < kUsed; ++nc) {
+            mma_f16(o[2 * c][nc], a[0][0], a[0][1], a[1][0], a[1][1], w[part][y][nc][0], w[part][y][nc][1]);
+            mma_f16(o[2 * c + 1][nc], a[2][0], a[2][1], a[3][0], a[3][1], w[part][y][nc][0], w[part][y][nc][1]);
+          }
       }
     }
     if constexpr (!kEarly) {

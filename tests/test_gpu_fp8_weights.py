@@ -1,13 +1,19 @@
-"""What a sequence gets from the few-row attention over the 8-bit cache does not depend, beyond 32-bit arithmetic and the
-output's own rounding, on how its batch is cut into pieces: alone in a cluster, alone in the stream, in the middle of a batch,
-and as a chunk's one row beside sequences with more of them.
+"""Softmax weights of the few-row attention over the 8-bit cache.
 
-Softmax weights enter the product with V as fp16.  Against references that are whole numbers (base 2) a weight's eleven bits are
-the same whatever the reference, so that two cuts differ where 32-bit arithmetic does, by about 2^-22 of sum p |v|.  With n
-keys of independent values that is 2^-22 sqrt(n) of a result, against steps of 2^-8 of it and more: 0.1 % of the results round
-to the other side with 300 keys.  A weight whose 32 bits differ so may round to the other eleven, one in 2^11, which moves a
-result by 2^-10 / sqrt(n) of itself: less than another 0.1 %.  Ten times that is allowed.  References that are not whole
-numbers round every weight anew: 2^-11 of itself at most, 4e-4 of a result between two cuts, and 5 % of the results differ.
+Decode carries them to 16 bits and more, as the other decode calls do: the bound of fp8_plain.attend_fp8 without a term for
+weights that were rounded (its 2^-16 is the second part's).
+
+Chunks of more rows have eleven bits, half a step 2^-11 of a weight; the normaliser sums the same ones, so that both the
+product and its normaliser may be off by that.
+
+And what a sequence gets does not depend, beyond 32-bit arithmetic and the output's own rounding, on how its batch is cut into
+pieces: alone in a cluster, alone in the stream, first or in the middle of a batch.  Against references that are whole numbers
+(base 2) a weight's bits are the same whatever the reference, so that two cuts differ where 32-bit arithmetic does, by about
+2^-22 of sum p |v|.  With n keys of independent values that is 2^-22 sqrt(n) of a result, against steps of 2^-8 of it and more:
+0.1 % of the results round to the other side with 300 keys.  A weight whose 32 bits differ so may round to other eleven, one in
+2^11, which moves a result by 2^-10 / sqrt(n) of itself: less than another 0.1 %.  Ten times that is allowed.  References that
+are not whole numbers round every weight anew: 2^-11 of itself at most, 4e-4 of a result between two cuts, and 5 % of the
+results differ.
 """
 import numpy as np
 import pytest
@@ -23,47 +29,61 @@ pytestmark = pytest.mark.gpu
 MINE = (300, 77, 513, 160)
 
 
-def in_a_batch(caches, q, order, table, lens, scale):
-    """The rows of q in the given order, and then back in their own."""
-    at = torch.from_numpy(order).cuda()
-    out = torch.empty_like(q)
-    pkv.paged_fp8_decode_attention(q[at].contiguous(), *caches, table[at].contiguous(), lens[at].contiguous(), scale, out)
-    back = torch.empty_like(out)
-    back[at] = out
-    return back
+class Batch:
+    """Sequences of which the first are looked at; one query token each, as decode or as chunks of a call that allows more."""
+
+    def __init__(self, hq, hkv, d, drafts):
+        r = np.random.RandomState(hq)
+        self.lens = list(MINE) + list(r.randint(1, 700, 200))
+        self.pages = Fp8Pages(self.lens, hkv, d, hq)
+        self.q = self.pages.randn(len(self.lens), hq, d).cuda()
+        *self.caches, self.table, self.cl = self.pages.cuda()
+        self.scale, self.most = d ** -0.5, 24 // (hq // hkv) if drafts else 0
+        self.shuffled = torch.from_numpy(r.permutation(len(self.lens))).cuda()
+
+    def call(self, rows, wide=False):
+        q, table, cl = (x[rows].contiguous() for x in (self.q, self.table, self.cl))
+        if wide:
+            table = torch.nn.functional.pad(table, (0, 20000 - table.shape[1]), value=-1)
+        out = torch.empty_like(q)
+        if not self.most:
+            return pkv.paged_fp8_decode_attention(q, *self.caches, table, cl, self.scale, out)
+        start = torch.arange(len(q) + 1, dtype=torch.int32, device="cuda")
+        return pkv.paged_fp8_prefill_attention(q, *self.caches, table, cl, start, self.most, self.scale, out)
 
 
 @pytest.mark.parametrize("hq,hkv,d", [(8, 8, 128), (16, 2, 128), (16, 4, 64), (3, 3, 64)])
-def test_a_sequence_in_other_batches(hq, hkv, d):
-    r = np.random.RandomState(hq)
-    lens = list(MINE) + list(r.randint(1, 700, 200))
-    pages = Fp8Pages(lens, hkv, d, hq)
-    q, scale, n = pages.randn(len(lens), hq, d).cuda(), d ** -0.5, len(MINE)
-    kc, vc, sc, table, cl = pages.cuda()
-    caches = kc, vc, sc
-    wide = torch.full((1, 20000), -1, dtype=torch.int32, device="cuda")
-    outs = {"alone": [], "in the stream": [], "beside longer chunks": []}
-    for b in range(n):
-        out = torch.empty_like(q[:1])
-        pkv.paged_fp8_decode_attention(q[b:b + 1], *caches, table[b:b + 1], cl[b:b + 1], scale, out)
-        outs["alone"].append(out)
-        wide[0, :table.shape[1]] = table[b]
-        outs["in the stream"].append(pkv.paged_fp8_decode_attention(q[b:b + 1], *caches, wide, cl[b:b + 1], scale, torch.empty_like(out)))
-        # The query of a chunk of one token, in a call whose chunks may have up to 24 rows.
-        start = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
-        outs["beside longer chunks"].append(pkv.paged_fp8_prefill_attention(
-            q[b:b + 1], *caches, table[b:b + 1], cl[b:b + 1], start, 24 // (hq // hkv), scale, torch.empty_like(out)))
-    outs = {k: torch.cat(v) for k, v in outs.items()}
-    outs["first of a batch"] = in_a_batch(caches, q, np.arange(len(lens)), table, cl, scale)[:n]
-    outs["amid a batch"] = in_a_batch(caches, q, r.permutation(len(lens)), table, cl, scale)[:n]
+@pytest.mark.parametrize("drafts", [False, True], ids=["decode", "drafts"])
+def test_a_sequence_in_other_batches(hq, hkv, d, drafts):
+    batch, n = Batch(hq, hkv, d, drafts), len(MINE)
+    outs = {"alone": torch.cat([batch.call(slice(b, b + 1)) for b in range(n)]),
+            "in the stream": torch.cat([batch.call(slice(b, b + 1), wide=True) for b in range(n)]),
+            "first of a batch": batch.call(slice(None))[:n]}
+    back = torch.empty_like(batch.q)
+    back[batch.shuffled] = batch.call(batch.shuffled)
+    outs["amid a batch"] = back[:n]
     assert device_errors() == 0
     for b in range(n):
-        ref, allowed = attend_fp8(pages, b, f64(q[b]), MINE[b], scale, 2.0**-11)
+        ref, allowed = attend_fp8(batch.pages, b, f64(batch.q[b]), MINE[b], batch.scale, 2.0**-10 if drafts else 0.0)
         for what, out in outs.items():
             assert_within(out[b], ref, allowed, f"{what}, sequence {b}")
     differ = {what: float((out.view(torch.int16) != outs["alone"].view(torch.int16)).float().mean()) for what, out in outs.items()}
     print(hq, hkv, d, differ)
     assert max(differ.values()) <= 0.02, differ
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(2, 2, 128), (4, 2, 128), (16, 2, 128), (2, 2, 64), (16, 2, 64)])
+@pytest.mark.parametrize("seqs", [3, 400])  # in clusters and in the stream
+def test_weights_of_decode(hq, hkv, d, seqs):
+    """Few keys, whose weights' roundings cancel least, and a few more."""
+    lens = [2 + b % 61 for b in range(seqs)]
+    pages = Fp8Pages(lens, hkv, d, hq + seqs)
+    q = pages.randn(seqs, hq, d)
+    kc, vc, sc, table, cl = pages.cuda()
+    out = pkv.paged_fp8_decode_attention(q.cuda(), kc, vc, sc, table, cl, d ** -0.5, torch.empty(q.shape, dtype=q.dtype, device="cuda"))
+    assert device_errors() == 0
+    for b, n in enumerate(lens):
+        assert_within(out[b], *attend_fp8(pages, b, f64(q[b]), n, d ** -0.5, 0.0), f"sequence {b}")
 
 
 @pytest.mark.parametrize("spread", [1.0, 4.0])
