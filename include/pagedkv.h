@@ -501,11 +501,15 @@ pkv_status pkv_prefix_decode_workspace_size(int32_t num_seqs, int32_t num_q_head
  *
  * With a the row's largest finite magnitude, e - 127 is the least integer s >= -127 with a <= 448 * 2^s (-127 if a is 0),
  * and the codes are x * 2^-s rounded to nearest even; infinities and NaN become NaN.  The type keeps four significant bits
- * and a power of two takes none of them, so that codes and values are exact in any arithmetic.  16-byte alignment, streams
- * and errors are those of the bf16 calls.  Exponents of 248 and above, which no append writes, give unspecified results.
+ * and a power of two takes none of them, so that codes and values are exact in any arithmetic, but for a value of 2^128
+ * (stored for magnitudes above 3.29e38), which is infinity, and those below 2^-133, which are rounded, wherever rows become
+ * bf16 again: read back, and in attention of chunks of more than 24 rows.  16-byte alignment, streams and errors are those of
+ * the bf16 calls.  Exponents of 248 and above, which no append writes, give unspecified results.
  *
  * pkv_kv_append_fp8: pkv_kv_append into such a cache.  Rows t of k and v start t * (stride) elements behind the first and
  * hold [num_kv_heads][head_dim] contiguously; a stride is a multiple of 8 (rows may be slices of a projection's output).
+ * Slots must be distinct: a slot that comes twice is left with codes and exponents of either token, and so with values of
+ * neither.
  */
 pkv_status pkv_kv_append_fp8(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int64_t* slot_mapping,
                              int64_t num_tokens, int32_t num_kv_heads, int32_t head_dim, void* k_cache, void* v_cache,
@@ -520,9 +524,8 @@ pkv_status pkv_rope_append_fp8(const void* q, int64_t q_stride, const void* k, i
                                pkv_stream_t stream);
 /*
  * Cached rows read back as bf16: for every i in [0, num_tokens) with slot_mapping[i] >= 0, the rows of that slot go to
- * k[i][:][:] and v[i][:][:] (strides as for the append, at least num_kv_heads * head_dim; k and v must not overlap).  Exact:
- * bf16 holds every value, but that one of 2^128 (stored for magnitudes above 3.29e38) is infinity and those below 2^-133 are
- * rounded.  A negative slot leaves its rows as they are; a slot may come several times.  Device-side: a slot >= 16 *
+ * k[i][:][:] and v[i][:][:] (strides as for the append, at least num_kv_heads * head_dim; k and v must not overlap), exactly
+ * but for the values named above.  A negative slot leaves its rows as they are; a slot may come several times.  Device-side: a slot >= 16 *
  * num_blocks sets PKV_DEVERR_SLOT_OUT_OF_RANGE and its rows are left as they are.
  */
 pkv_status pkv_kv_gather_fp8(const void* k_cache, const void* v_cache, const void* kv_scales, int64_t num_blocks,
@@ -535,8 +538,7 @@ pkv_status pkv_copy_blocks_fp8(void* k_cache, void* v_cache, void* kv_scales, co
 /*
  * pkv_paged_decode_attention over such a cache (q and out bf16).  num_blocks * num_kv_heads * 16 must be below 2^31,
  * max_blocks_per_seq at most 2^26 and num_seqs at most 65535.  A token that a sequence does not see does not matter, whatever
- * its row and exponent hold.  Sums are fp32; softmax weights enter the product with V in fp16 (eleven bits, the same ones
- * wherever the batch is cut: a sequence's result does not depend on its batch beyond fp32 rounding).
+ * its row and exponent hold.  Sums are fp32; each softmax weight enters P.V as two fp16 parts, about 22 significant bits.
  *
  *   workspace   device, 16-byte aligned, at least pkv_fp8_decode_workspace_size bytes (may be NULL if that is 0); scratch,
  *               as for pkv_paged_decode_attention
@@ -557,6 +559,11 @@ pkv_status pkv_fp8_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, 
  * chunk are unspecified, and set it too.  num_blocks * num_kv_heads * 16 must be below 2^31, max_blocks_per_seq at most 2^26
  * and num_seqs at most 65535.  A token that some rows of a sequence's chunk see has to be finite, or the rows of the chunk that
  * do not see it are unspecified.
+ *
+ * Up to 24 rows a sequence and kv head (max_query_len * num_q_heads / num_kv_heads) are computed as decode is, up to 8 of them
+ * with its weights, more with one fp16 part (eleven bits, the same ones wherever the batch is cut).  So far a sequence's result
+ * does not depend on its batch beyond fp32 rounding.  With more than 24 the weights are rounded to bf16 against the running maximum, as in pkv_paged_prefill_attention, so the last bits of a row depend
+ * on the steps and splits that its keys fall into, which go by the whole call.
  */
 pkv_status pkv_paged_fp8_prefill_attention(const void* q, const void* k_cache, const void* v_cache, const void* kv_scales,
                                            const int32_t* block_tables, int32_t max_blocks_per_seq,
@@ -568,9 +575,10 @@ pkv_status pkv_paged_fp8_prefill_attention(const void* q, const void* k_cache, c
 /*
  * Its workspace on the current device, for calls of exactly these sizes (fewer sequences can be split and take more); with up
  * to 24 rows a sequence and kv head (max_query_len * num_q_heads / num_kv_heads), for calls of up to num_seqs sequences and
- * max_blocks_per_seq with that max_query_len, whatever num_query_tokens.  Long chunks have their cache blocks turned into bf16 there, which takes 4 * num_seqs * max_blocks_per_seq * 16 * num_kv_heads *
- * head_dim bytes, up to 2 GB.  Beyond that, and with a smaller workspace, every CTA turns what it reads into bf16, for up to
- * 1.2 times the time: pkv_fp8_prefill_least_workspace_size bytes are enough for that.
+ * max_blocks_per_seq with that max_query_len, whatever num_query_tokens.  Long chunks have their cache blocks turned into bf16
+ * there, which takes 4 * num_seqs * max_blocks_per_seq * 16 * num_kv_heads * head_dim bytes, up to 2 GB.  Beyond that, and with
+ * a smaller workspace, every CTA turns what it reads into bf16, for up to 1.25 times the time:
+ * pkv_fp8_prefill_least_workspace_size bytes are enough for that.
  */
 pkv_status pkv_fp8_prefill_workspace_size(int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs,
                                           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,

@@ -651,6 +651,7 @@ def kv_append_fp8(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, 
     """kv_append into an 8-bit cache: k/v [N, Hkv, D] bf16 are quantised as they are written (in place).
 
     k and v may be slices of wider rows, as of one projection's output: only a token's own [Hkv, D] has to be contiguous.
+    Slots that are not padding must be distinct: one that comes twice holds neither token's values.
     """
     (_binding or _native()).kv_append_fp8(k, v, slot_mapping, k_cache, v_cache, kv_scales, stream)
 
@@ -715,7 +716,7 @@ def paged_fp8_prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
 
     q and out [T, Hq, D] are bf16; max_query_len is at least every chunk's length.  A call with long chunks turns its cache
     blocks into bf16 in the workspace (up to 2 GB, ``fp8_prefill_workspace_size``).  With ``unpack=False`` it converts them as
-    it goes, which takes up to 1.2 times as long and little workspace; so does a call that was given no workspace and finds no
+    it goes, which takes up to 1.25 times as long and little workspace; so does a call that was given no workspace and finds no
     memory for one.  Without a workspace given, each thread keeps one a stream, of up to 64 MB; a larger one is the call's own.
     Returns ``out``.
     """

@@ -1307,7 +1307,8 @@ pkv_status pkv_fp8_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, 
 
 namespace {
 // CTAs that a tile pair's keys are split over: as many as leave every CTA an SM, at least two steps of 128 keys each (by the
-// longest context that the tables can hold).
+// longest context that the tables can hold: one fresh chunk of 64 tokens takes 8.3 us in a table of its own, 14.7 in a wide one,
+// where most of its splits have no step; one of 512 tokens 20.0 in either).
 int32_t fp8_prefill_splits(int64_t num_query_tokens, int32_t max_query_len, int32_t num_seqs, int32_t num_q_heads,
                            int32_t num_kv_heads, int32_t max_blocks_per_seq, int sms) {
   const int64_t cta = pkv::prefill_cta_tokens(num_q_heads / num_kv_heads);

@@ -93,8 +93,10 @@ struct Fp8AttentionParams {
 };
 
 constexpr int kFp8LaunchSeqs = 1024;
-// Above this the chunk kernel is faster (sequences of 512..8192 tokens, 64 of them: 24 rows 110 us here, 176 there; 32 rows 253
-// and 165), although it pads them to 128.
+// Above this the chunk kernel is faster, although it pads the rows to 128.  64 sequences of 512..8192 tokens, 8 kv heads, here
+// and there: 128 dims, 24 rows 104 and 171 us, 32 rows 253 and 163; 64 dims, 16 rows 61 and 138, 24 rows 72 and 138.  (With few
+// sequences the chunk kernel, whose splits fill the GPU, is the faster from some 16 rows on: eight of 2048 tokens, 128 dims, 24
+// rows 40 and 27, 16 rows 30 and 26; one of 8192, 24 rows 20 and 22.)
 constexpr int kFp8MostRows = 24;
 // Tables up to here keep every position, past the last unit's end too, below 2^31.
 constexpr int kFp8MostBlocks = 1 << 26;

@@ -9,6 +9,9 @@ namespace {
 //   1 x 128 8.4, 5.2; 1 x 8192 14.1, 10.1; 1 x 32768 22.7, 23.0; 8 x 2048 15.4, 9.7; 8 x 8192 29, 24; 32 x 2048 30, 24;
 //   32 x 8192 77, 77; of one kv head 16 x 8192 15.6, 13.4 and 16 x 32768 29, 35.
 // As large as the pairs leave room for, up to 16 CTAs (1 x 8192: 12.6 with 8).
+// The lengths are not known here, only the table's width.  In a table that is much wider than its sequences a call that clusters
+// would do in 5.1, 7.6 or 9.5 us (one of 512, one of 4097, eight of 2048 tokens; 8192 blocks wide) takes the stream form, 8.0,
+// 12.6 and 13.3; clusters over a context that does fill it would take, by the estimate, up to twice the stream form's time.
 // A cluster's units come one after the other; the stream form has a second launch and a pass over the lengths; and either takes
 // the bytes' time, of a batch whose tables are filled to three quarters.
 constexpr float kClusterUs = 4.6f, kStreamUs = 10.5f;

@@ -2,7 +2,7 @@
 //
 // The scale of a row is a power of two: e4m3 is a floating type, so a finer scale would keep no more significant bits, and
 // with a power of two the codes and the values they stand for are exact, in whatever arithmetic they are formed: bf16 holds
-// every value, a code times its scale (but those above its largest).
+// every value, a code times its scale (but that of 2^128, and those below 2^-133).
 #pragma once
 
 #include <cuda_bf16.h>

@@ -17,9 +17,11 @@
 // A chunk call that does not fill the GPU has each tile pair's key steps split over CTAs, as there, with a merge.
 // Measured (8 kv heads of 128 dims): eight chunks of 256 behind 3840 tokens, 32 q heads, 147 us; 512 tokens behind 8192, 16 q
 // heads, 50 us: four splits of 17 steps on 128 of 152 SMs, and the merge.  Seven converters and eight softmax warps share the
-// issue slots, 1.3 times the bf16 kernel's time over a bf16 cache (two prompts of 8192 946 us, 789 unpacked).  A single query
+// issue slots, 1.26 times the bf16 kernel's time over a bf16 cache (two prompts of 8192 925 us, 734 there, 746 unpacked, in one
+// loop over one input; 946 and 789 over several in turn).  A single query
 // tile dealt to both tiles' places by steps gained nothing (64 sequences of 8 tokens 165 to 172 us).
-// The softmax warps take 168 registers a thread and leave the others 88: 256 (168 + 88) is the block's 512 * 128.
+// The softmax warps take 168 registers a thread and leave the others 88: 256 (168 + 88) is the block's 512 * 128.  (The compiler
+// plans with 128 for all and spills 16 to 24 bytes a thread.)
 #include "paged_prefill_kernel.cuh"
 
 #include "fp8_cache.h"
@@ -581,7 +583,7 @@ __global__ void __launch_bounds__(256) merge_fp8_kernel(const Fp8PrefillParams p
 
 // Unpacked form: the blocks that a sequence's rows see, in order, as bf16 ([sequence][block of its table], both with all heads),
 // the table that numbers them so, and the context lengths, -1 for a sequence that the call skips.  Bound by HBM, two bytes
-// written for each read: 16384 tokens of 8 heads of 128 dims 23 us with cold caches.
+// written for each read: 16384 tokens of 8 heads of 128 dims 23 us with cold caches, 12 of the call's 746 us in a loop.
 constexpr int kUnpackThreads = 256, kUnpackCtas = 8;  // CTAs an SM
 template <int D>
 __global__ void __launch_bounds__(kUnpackThreads) unpack_fp8_kernel(const Fp8AttentionParams p, const Fp8Unpacked to) {
